@@ -1,4 +1,5 @@
-"""Fused Dynamic Tanh (DyT) forward/backward for NVIDIA B200 (sm_100a).
+"""Fused Dynamic Tanh (DyT) forward/backward for NVIDIA B200 (sm_100a), with the
+layer norm it takes the place of (``norm``) and a policy loss on the logits (``loss``).
 
 The computation lives in hand-written CUDA kernels behind a C ABI
 (``include/dyt.h``, built into ``libdyt.so``). This package is a thin layer
@@ -16,8 +17,14 @@ from . import _abi
 from ._abi import (DYT_BF16, DYT_F16, DYT_F32, MAX_RANKS, DytError, dyt_backward, dyt_backward_ex,
                    dyt_backward_noalloc, dyt_backward_partials, dyt_backward_strided, dyt_backward_workspace_bytes,
                    dyt_finalize_partials, dyt_forward, dyt_forward_ex, dyt_forward_strided, dyt_ipc_close,
-                   dyt_ipc_export, dyt_ipc_import, dyt_last_launch_info, dyt_partials_layout_query, dyt_plan_query,
-                   dyt_status_string)
+                   dyt_ipc_export, dyt_ipc_import, dyt_last_launch_info, dyt_layer_norm_backward,
+                   dyt_layer_norm_backward_workspace_bytes, dyt_layer_norm_forward, dyt_partials_layout_query,
+                   dyt_plan_query, dyt_policy_loss_backward, dyt_policy_loss_forward,
+                   dyt_policy_loss_workspace_bytes, dyt_status_string)
+from ._rows import DTYPE_CODE, _code, _cuda_contig, _rows, _stream, row_pitch
+from .loss import (PolicyLoss, PolicyLossFunction, policy_loss_backward, policy_loss_forward,
+                   policy_loss_workspace)
+from .norm import LayerNorm, LayerNormFunction, layer_norm_backward, layer_norm_forward, layer_norm_workspace
 
 __all__ = ["forward", "backward", "workspace", "backward_partials", "partials_layout", "finalize_partials", "DyT",
            "DyTFunction", "dyt_forward", "dyt_backward", "dyt_forward_strided", "dyt_backward_strided",
@@ -25,50 +32,11 @@ __all__ = ["forward", "backward", "workspace", "backward_partials", "partials_la
            "dyt_partials_layout_query", "dyt_finalize_partials", "dyt_ipc_export", "dyt_ipc_import",
            "dyt_ipc_close", "row_pitch", "dyt_backward_workspace_bytes", "dyt_status_string",
            "dyt_last_launch_info", "dyt_plan_query", "DytError", "DTYPE_CODE", "DYT_F32", "DYT_BF16", "DYT_F16",
-           "MAX_RANKS"]
-
-DTYPE_CODE = {torch.float32: DYT_F32, torch.bfloat16: DYT_BF16, torch.float16: DYT_F16}
-
-
-def _code(t: torch.Tensor, what: str) -> int:
-    try:
-        return DTYPE_CODE[t.dtype]
-    except KeyError:
-        raise TypeError(f"{what}: dtype {t.dtype} is not supported (float32, bfloat16, float16)") from None
-
-
-def _cuda_contig(t: torch.Tensor, what: str) -> None:
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-
-
-def row_pitch(t: torch.Tensor) -> int | None:
-    """Elements between consecutive rows when t's leading dimensions collapse into
-    one row index with a uniform pitch and its last dimension is dense; else None."""
-    if t.dim() == 0:
-        return None
-    if t.dim() == 1:
-        return t.shape[0] if t.shape[0] <= 1 or t.stride(0) == 1 else None
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        return None
-    ld = t.stride(-2)
-    for i in range(t.dim() - 2):  # dimension i must step over whole blocks of dimension i + 1
-        if t.shape[i] > 1 and t.stride(i) != t.shape[i + 1] * t.stride(i + 1):
-            return None
-    if t.numel() > t.shape[-1] and ld < t.shape[-1]:
-        return None
-    return max(ld, t.shape[-1])
-
-
-def _rows(t: torch.Tensor, what: str) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    ld = row_pitch(t)
-    if ld is None:
-        raise ValueError(f"{what}: rows must be dense and evenly spaced (stride 1 along the last dimension)")
-    return ld
+           "MAX_RANKS", "layer_norm_forward", "layer_norm_backward", "layer_norm_workspace", "LayerNorm",
+           "LayerNormFunction", "policy_loss_forward", "policy_loss_backward", "policy_loss_workspace", "PolicyLoss",
+           "PolicyLossFunction", "dyt_layer_norm_forward", "dyt_layer_norm_backward",
+           "dyt_layer_norm_backward_workspace_bytes", "dyt_policy_loss_forward", "dyt_policy_loss_backward",
+           "dyt_policy_loss_workspace_bytes"]
 
 
 def _shape(x: torch.Tensor, gamma: torch.Tensor):
@@ -77,12 +45,6 @@ def _shape(x: torch.Tensor, gamma: torch.Tensor):
         raise ValueError(f"x's last dimension {tuple(x.shape)} must equal gamma's length {N}")
     M = x.numel() // N if N else 0
     return M, N
-
-
-def _stream(device, stream):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return stream.cuda_stream
 
 
 def forward(x: torch.Tensor, alpha: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor,

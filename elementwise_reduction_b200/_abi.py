@@ -109,6 +109,22 @@ lib.dyt_ipc_close.argtypes = [_vp, ctypes.POINTER(IpcHandle)]
 lib.dyt_ipc_close.restype = _i32
 lib.dyt_backward_noalloc.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp]
 lib.dyt_backward_noalloc.restype = _i32
+_f32, _f64 = ctypes.c_float, ctypes.c_double
+lib.dyt_layer_norm_forward.argtypes = [_vp, _i64, _vp, _vp, _f32, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _i32, _i32,
+                                       _vp]
+lib.dyt_layer_norm_forward.restype = _i32
+lib.dyt_layer_norm_backward_workspace_bytes.argtypes = [_i64, _i64, _i32]
+lib.dyt_layer_norm_backward_workspace_bytes.restype = _sz
+lib.dyt_layer_norm_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i32,
+                                        _i32, _i32, _vp, _sz, _vp]
+lib.dyt_layer_norm_backward.restype = _i32
+lib.dyt_policy_loss_workspace_bytes.argtypes = [_i64, _i64, _i32]
+lib.dyt_policy_loss_workspace_bytes.restype = _sz
+lib.dyt_policy_loss_forward.argtypes = [_vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _f64, _f64, _f64, _f64, _vp, _vp,
+                                        _vp, _vp, _i64, _i64, _i32, _vp, _sz, _vp]
+lib.dyt_policy_loss_forward.restype = _i32
+lib.dyt_policy_loss_backward.argtypes = [_vp, _i64, _vp, _i32, _vp, _vp, _vp, _f64, _vp, _i64, _i64, _i64, _i32, _vp]
+lib.dyt_policy_loss_backward.restype = _i32
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # DYT_NOALLOC_SCRATCH_BYTES in include/dyt.h
 
 
@@ -206,6 +222,44 @@ def dyt_finalize_partials(workspaces, layouts, N, dgamma, dbeta, dalpha, alpha_d
     lays = (PartialsLayout * max(1, n))(*[PartialsLayout.from_dict(d) for d in layouts])
     return lib.dyt_finalize_partials(ws, lays, n, N, dgamma, dbeta, dalpha, alpha_dtype, gamma_dtype, beta_dtype,
                                      stream)
+
+
+def dyt_layer_norm_forward(x, ldx, gamma, beta, eps, y, ldy, mean, rstd, M, N, x_dtype, gamma_dtype, beta_dtype,
+                           stream) -> int:
+    """Raw C-ABI call: pointers as ints (gamma, beta, mean and rstd may be None). Returns the status code."""
+    return lib.dyt_layer_norm_forward(x, ldx, gamma, beta, eps, y, ldy, mean, rstd, M, N, x_dtype, gamma_dtype,
+                                      beta_dtype, stream)
+
+
+def dyt_layer_norm_backward_workspace_bytes(M, N, x_dtype) -> int:
+    return int(lib.dyt_layer_norm_backward_workspace_bytes(M, N, x_dtype))
+
+
+def dyt_layer_norm_backward(x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, dgamma, dbeta, M, N, x_dtype, gamma_dtype,
+                            beta_dtype, workspace, workspace_bytes, stream) -> int:
+    """Raw C-ABI call: pointers as ints (gamma, dgamma and dbeta may be None). Returns the status code."""
+    return lib.dyt_layer_norm_backward(x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, dgamma, dbeta, M, N, x_dtype,
+                                       gamma_dtype, beta_dtype, workspace, workspace_bytes, stream)
+
+
+def dyt_policy_loss_workspace_bytes(M, N, dtype) -> int:
+    return int(lib.dyt_policy_loss_workspace_bytes(M, N, dtype))
+
+
+def dyt_policy_loss_forward(logits, ld, tokens, token_bytes, old_logp, ref_logp, advantage, weight, clip_low,
+                            clip_high, kl_coef, temperature, loss, logp, stats, coef, M, N, dtype, workspace,
+                            workspace_bytes, stream) -> int:
+    """Raw C-ABI call: pointers as ints (ref_logp and weight may be None). Returns the status code."""
+    return lib.dyt_policy_loss_forward(logits, ld, tokens, token_bytes, old_logp, ref_logp, advantage, weight,
+                                       clip_low, clip_high, kl_coef, temperature, loss, logp, stats, coef, M, N,
+                                       dtype, workspace, workspace_bytes, stream)
+
+
+def dyt_policy_loss_backward(logits, ld, tokens, token_bytes, stats, coef, grad, temperature, dlogits, lddl, M, N,
+                             dtype, stream) -> int:
+    """Raw C-ABI call: pointers as ints (grad may be None). Returns the status code."""
+    return lib.dyt_policy_loss_backward(logits, ld, tokens, token_bytes, stats, coef, grad, temperature, dlogits,
+                                        lddl, M, N, dtype, stream)
 
 
 def dyt_ipc_export(ptr: int) -> bytes:

@@ -1,0 +1,99 @@
+"""What the tensor helpers share: dtype codes, row layouts, and the device and
+stream that a call runs on."""
+from __future__ import annotations
+
+import torch
+
+from ._abi import DYT_BF16, DYT_F16, DYT_F32
+
+DTYPE_CODE = {torch.float32: DYT_F32, torch.bfloat16: DYT_BF16, torch.float16: DYT_F16}
+
+
+def _code(t: torch.Tensor, what: str) -> int:
+    try:
+        return DTYPE_CODE[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what}: dtype {t.dtype} is not supported (float32, bfloat16, float16)") from None
+
+
+def _cuda_contig(t: torch.Tensor, what: str) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def row_pitch(t: torch.Tensor) -> int | None:
+    """Elements between consecutive rows when t's leading dimensions collapse into
+    one row index with a uniform pitch and its last dimension is dense; else None."""
+    if t.dim() == 0:
+        return None
+    if t.dim() == 1:
+        return t.shape[0] if t.shape[0] <= 1 or t.stride(0) == 1 else None
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        return None
+    ld = t.stride(-2)
+    for i in range(t.dim() - 2):  # dimension i must step over whole blocks of dimension i + 1
+        if t.shape[i] > 1 and t.stride(i) != t.shape[i + 1] * t.stride(i + 1):
+            return None
+    if t.numel() > t.shape[-1] and ld < t.shape[-1]:
+        return None
+    return max(ld, t.shape[-1])
+
+
+def _rows(t: torch.Tensor, what: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    ld = row_pitch(t)
+    if ld is None:
+        raise ValueError(f"{what}: rows must be dense and evenly spaced (stride 1 along the last dimension)")
+    return ld
+
+
+def _stream(device, stream):
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    return stream.cuda_stream
+
+
+def _elsewhere(t: torch.Tensor, stream: torch.cuda.Stream | None) -> bool:
+    """Whether a call on t's data has to switch the current device or stream (see _there)."""
+    if not t.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    return stream is not None or t.device.index != torch.cuda.current_device()
+
+
+def _there(t: torch.Tensor, stream: torch.cuda.Stream | None):
+    """A context in which t's device is the current one and `stream`, if given, the
+    current stream: what the call allocates then belongs to the stream that uses it."""
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _vector(t: torch.Tensor, what: str, n: int, device: torch.device, dtypes) -> int:
+    """The address of a contiguous tensor of n elements on `device`."""
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {t.dtype} is not supported ({', '.join(str(d)[6:] for d in dtypes)})")
+    if t.numel() != n:
+        raise ValueError(f"{what} must have {n} elements, not {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _like(t: torch.Tensor, what: str, x: torch.Tensor) -> int:
+    """The row pitch of a tensor of x's shape, dtype and device."""
+    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+        raise ValueError(f"{what} must match its input in shape, dtype and device")
+    return _rows(t, what)
+
+
+def _workspace(ws: torch.Tensor, device: torch.device) -> int:
+    if ws.device != device or not ws.is_contiguous() or ws.dtype != torch.uint8:
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    return ws.data_ptr()

@@ -14,16 +14,14 @@
 
 #include "dyt.h"
 #include "dyt_finalize.cuh"
+#include "dyt_host.h"
 #include "dyt_select.cuh"
 
-namespace {
-
-using dyt::Geom;
-using namespace dyt::launch;
+namespace dyt {
+namespace host {
 
 thread_local dyt_launch_info t_info = {};
 thread_local int t_cuda_err = 0;
-
 
 // A CUDA runtime call failed: keep its code for dyt_last_cuda_error and clear
 // the runtime's last-error state, so that the failure, reported by our status,
@@ -34,27 +32,22 @@ dyt_status cuda_fail(cudaError_t e) {
   return DYT_ERR_CUDA;
 }
 
-size_t dsize(int d) { return d == DYT_F32 ? 4 : 2; }
-bool valid_dtype(int d) { return d == DYT_F32 || d == DYT_BF16 || d == DYT_F16; }
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-// A pointer to whole elements of `bytes` bytes (the kernels' loads need it).
-bool elem_aligned(const void *p, size_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
-// Elements between the 16-byte boundary below p and p.
-int shift_of(const void *p, size_t elem) { return (int)(((uintptr_t)p & 15u) / elem); }
-// Two pointers at the same offset past a 16-byte boundary.
-bool same_offset(const void *a, const void *b) { return (((uintptr_t)a ^ (uintptr_t)b) & 15u) == 0; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+void record_info(const dyt_launch_info &i) { t_info = i; }
 
-// ---- per-device facts and per-kernel occupancy (cached, thread-safe) -------
+namespace {
 
 std::mutex g_mu;
 std::unordered_map<int, int> g_sms;                   // device -> SM count
-std::unordered_map<uint64_t, int> g_occ;              // (device, kernel) -> CTAs per SM
+std::unordered_map<uint64_t, int> g_occ;              // (device, kernel, block) -> CTAs per SM
 std::unordered_map<uint64_t, int> g_smem_ready;       // (device, kernel) -> dynamic shared memory opted in
 
 uint64_t kernel_key(int dev, const void *kernel) {
   return ((uint64_t)(uint32_t)dev << 48) ^ (uint64_t)(uintptr_t)kernel;
 }
+
+}  // namespace
+
+// ---- per-device facts and per-kernel occupancy (cached, thread-safe) -------
 
 dyt_status current_sms(int *dev_out, int *sms_out) {
   int dev = 0;
@@ -80,7 +73,7 @@ dyt_status current_sms(int *dev_out, int *sms_out) {
 }
 
 dyt_status occupancy(int dev, const void *kernel, int block, int *ctas) {
-  const uint64_t key = kernel_key(dev, kernel);
+  const uint64_t key = kernel_key(dev, kernel) * 1025u + (uint64_t)block;  // block <= 1024
   {
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_occ.find(key);
@@ -113,6 +106,31 @@ dyt_status prepare_smem(int dev, const void *kernel, int bytes) {
   g_smem_ready[key] = bytes;
   return DYT_OK;
 }
+
+dyt_status check_shape(int64_t M, int64_t N, int xd) {
+  if (!valid_dtype(xd)) return DYT_ERR_UNSUPPORTED_DTYPE;
+  if (M < 0 || N < 0 || N > INT32_MAX) return DYT_ERR_INVALID_VALUE;
+  if (N > 0 && M > INT64_MAX / N / 8) return DYT_ERR_INVALID_VALUE;
+  // group and item counts are ints
+  if (M > ((int64_t)1 << 40)) return DYT_ERR_INVALID_VALUE;
+  return DYT_OK;
+}
+
+// Row pitches: at least N, and the last element of every tensor addressable.
+dyt_status check_pitch(int64_t M, int64_t N, int64_t ld) {
+  if (ld < N) return DYT_ERR_INVALID_VALUE;
+  if (M > 1 && ld > 0 && (M - 1) > (INT64_MAX / 8 - N) / ld) return DYT_ERR_INVALID_VALUE;
+  return DYT_OK;
+}
+
+}  // namespace host
+}  // namespace dyt
+
+namespace {
+
+using dyt::Geom;
+using namespace dyt::launch;
+using namespace dyt::host;
 
 // ---- launch plan ---------------------------------------------------------------
 
@@ -280,28 +298,9 @@ dyt_status with_xtype(int xd, F &&f) {
   return DYT_ERR_UNSUPPORTED_DTYPE;
 }
 
-dyt_status check_shape(int64_t M, int64_t N, int xd) {
-  if (!valid_dtype(xd)) return DYT_ERR_UNSUPPORTED_DTYPE;
-  if (M < 0 || N < 0 || N > INT32_MAX) return DYT_ERR_INVALID_VALUE;
-  if (N > 0 && M > INT64_MAX / N / 8) return DYT_ERR_INVALID_VALUE;
-  // group and item counts are ints
-  if (M > ((int64_t)1 << 40)) return DYT_ERR_INVALID_VALUE;
-  return DYT_OK;
-}
-
 dyt_status check_param_dtypes(int ad, int gd, int bd) {
   return valid_dtype(ad) && valid_dtype(gd) && valid_dtype(bd) ? DYT_OK : DYT_ERR_UNSUPPORTED_DTYPE;
 }
-
-// Row pitches: at least N, and the last element of every tensor addressable.
-dyt_status check_pitch(int64_t M, int64_t N, int64_t ld) {
-  if (ld < N) return DYT_ERR_INVALID_VALUE;
-  if (M > 1 && ld > 0 && (M - 1) > (INT64_MAX / 8 - N) / ld) return DYT_ERR_INVALID_VALUE;
-  return DYT_OK;
-}
-
-// A row pitch of whole 16-byte vectors.
-bool vec_pitch(int64_t ld, size_t elem) { return ((uint64_t)ld * elem) % 16 == 0; }
 
 // Rows ld elements apart: a row's offset past a 16-byte boundary repeats
 // every 16 / (lowest set bit of ld * elem mod 16) rows (1, 2, 4 or 8).
@@ -418,25 +417,6 @@ dyt_status plan_for(int64_t M, int64_t N, bool aligned, bool pitched, bool adjac
   if (out->too_big) return DYT_ERR_INVALID_VALUE;
   return DYT_OK;
 }
-
-// Programmatic dependent launch: the kernel may be scheduled while its
-// predecessor in the stream drains; its first instruction waits
-// (griddepcontrol.wait) for that predecessor, so stream order holds.
-struct PdlConfig {
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg;
-  PdlConfig(unsigned grid, unsigned block, size_t smem, cudaStream_t s) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-};
 
 using MemGetAddressRangeFn = CUresult (*)(CUdeviceptr *, size_t *, CUdeviceptr);
 

@@ -1,0 +1,225 @@
+// Policy loss entry points (declared in include/dyt.h): argument checks, launch
+// plans and dispatch of the kernels in dyt_loss.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "dyt.h"
+#include "dyt_host.h"
+#include "dyt_loss.cuh"
+
+namespace {
+
+using namespace dyt::host;
+using dyt::loss::LossArgs;
+using dyt::loss::LossGradArgs;
+
+constexpr int kOpLossForward = 7, kOpLossBackward = 8;  // dyt_launch_info::op
+constexpr int kBlock = 256;
+constexpr int kCtasPerSm = 8;        // 2048 resident threads
+constexpr int64_t kWarpRow = 8192;   // rows of at most this many bytes take a warp
+constexpr int64_t kPartMin = 4096;   // the smallest part of a row, bytes
+constexpr int64_t kGradPart = 65536;  // the largest part of a row in the backward, bytes
+constexpr int kFinishBlock = 512, kFinishCtas = 8;
+
+template <typename F>
+dyt_status with_type(int xd, F &&f) {
+  switch (xd) {
+    case DYT_F32: return f(float{});
+    case DYT_BF16: return f(__nv_bfloat16{});
+    case DYT_F16: return f(__half{});
+  }
+  return DYT_ERR_UNSUPPORTED_DTYPE;
+}
+
+struct LossPlan {
+  bool cta;      // a part of a row is a CTA's, else a warp's
+  int S;         // parts of a row
+  int64_t grid;  // CTAs
+};
+
+// Few rows are split until every SM has its CTAs.
+LossPlan plan(int64_t M, int64_t N, size_t es, bool backward, int sms) {
+  LossPlan p;
+  const int64_t bytes = N * (int64_t)es;
+  const int64_t slots = (int64_t)sms * kCtasPerSm;
+  p.cta = bytes > kWarpRow || M < slots;
+  p.S = 1;
+  if (p.cta) {
+    int64_t s = M < slots ? std::min(slots / M, bytes / kPartMin) : 1;
+    if (backward) s = std::max(s, ceil_div(bytes, kGradPart));
+    p.S = (int)std::max<int64_t>(1, s);
+  }
+  const int64_t items = p.cta ? M * p.S : ceil_div(M, kBlock / 32);
+  p.grid = std::min<int64_t>(items, (int64_t)1 << 30);
+  return p;
+}
+
+size_t ws_bytes(int64_t M, const LossPlan &p) {
+  return ((size_t)M * (size_t)p.S * sizeof(float2) + 15) & ~(size_t)15;
+}
+
+void record(int op, const LossPlan *p, int vec, int kernels, size_t ws) {
+  dyt_launch_info i = {};
+  i.op = op;
+  i.kernels = kernels;
+  i.workspace_bytes = (int64_t)ws;
+  if (p) {
+    i.path = p->cta ? 2 : 1;
+    i.vec = vec;
+    i.block = kBlock;
+    i.grid = (int)p->grid;
+    i.row_lanes = i.rows_per_step = p->cta ? 1 : kBlock / 32;
+    i.col_chunks = p->S;
+    i.pack_rows = 1;
+  }
+  record_info(i);
+}
+
+bool finite_positive(double v) { return v > 0.0 && std::isfinite(v); }
+
+}  // namespace
+
+extern "C" {
+
+size_t dyt_policy_loss_workspace_bytes(int64_t M, int64_t N, dyt_dtype dtype) try {
+  if (check_shape(M, N, dtype) != DYT_OK || M == 0 || N == 0) return 0;
+  int dev = 0, sms = 0;
+  if (current_sms(&dev, &sms) != DYT_OK) return 0;
+  return ws_bytes(M, plan(M, N, dsize(dtype), false, sms));
+} catch (...) {
+  return 0;
+}
+
+dyt_status dyt_policy_loss_forward(const void *logits, int64_t ld, const void *tokens, int token_bytes,
+                                   const float *old_logp, const float *ref_logp, const float *advantage,
+                                   const float *weight, double clip_low, double clip_high, double kl_coef,
+                                   double temperature, float *loss, float *logp, float *stats, float *coef, int64_t M,
+                                   int64_t N, dyt_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   dyt_stream_t stream) try {
+  dyt_status st = check_shape(M, N, dtype);
+  if (st != DYT_OK) return st;
+  if (check_pitch(M, N, ld) != DYT_OK || (token_bytes != 4 && token_bytes != 8)) return DYT_ERR_INVALID_VALUE;
+  if (!(clip_low >= 0.0) || !std::isfinite(clip_low) || !(clip_high >= 0.0) || !std::isfinite(clip_high) ||
+      !std::isfinite(kl_coef) || !finite_positive(temperature))
+    return DYT_ERR_INVALID_VALUE;
+  if (!loss || !elem_aligned(loss, 4) || (M > 0 && N == 0)) return DYT_ERR_INVALID_VALUE;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (M == 0) {
+    const cudaError_t e = cudaMemsetAsync(loss, 0, sizeof(float), s);  // the empty sum
+    if (e != cudaSuccess) return cuda_fail(e);
+    record(kOpLossForward, nullptr, 0, 0, 0);
+    return DYT_OK;
+  }
+  const size_t es = dsize(dtype);
+  if (!logits || !tokens || !old_logp || !advantage || !logp || !stats || !coef || !workspace ||
+      !elem_aligned(logits, es) || !elem_aligned(tokens, token_bytes) || !elem_aligned(old_logp, 4) ||
+      !elem_aligned(ref_logp, 4) || !elem_aligned(advantage, 4) || !elem_aligned(weight, 4) ||
+      !elem_aligned(logp, 4) || !elem_aligned(stats, 8) || !elem_aligned(coef, 4) || !aligned16(workspace))
+    return DYT_ERR_INVALID_VALUE;
+  const float C = (float)(dyt::loss::kLog2eD / temperature);
+  if (!(C > 0.0f) || std::isinf(C)) return DYT_ERR_INVALID_VALUE;
+  int dev = 0, sms = 0;
+  st = current_sms(&dev, &sms);
+  if (st != DYT_OK) return st;
+  const LossPlan p = plan(M, N, es, false, sms);
+  const size_t need = ws_bytes(M, p);
+  if (workspace_bytes < need) return DYT_ERR_WORKSPACE_TOO_SMALL;
+  LossArgs a = {};
+  a.z = logits;
+  a.ld = ld;
+  a.tokens = tokens;
+  a.old_logp = old_logp;
+  a.ref_logp = ref_logp;
+  a.advantage = advantage;
+  a.weight = weight;
+  a.loss = loss;
+  a.logp = logp;
+  a.stats = (float2 *)stats;
+  a.coef = coef;
+  a.parts = (float2 *)workspace;
+  a.M = M;
+  a.N = N;
+  a.S = p.S;
+  a.wide_tokens = token_bytes == 8;
+  a.C = C;
+  a.inv_t = 1.0 / temperature;
+  a.lo = 1.0 - clip_low;
+  a.hi = 1.0 + clip_high;
+  a.kl = kl_coef;
+  return with_type(dtype, [&](auto t) -> dyt_status {
+    using T = decltype(t);
+    PdlConfig lc((unsigned)p.grid, kBlock, 0, s);
+    cudaError_t e = cudaLaunchKernelEx(
+        &lc.cfg, p.cta ? dyt::loss::loss_rows_kernel<T, true> : dyt::loss::loss_rows_kernel<T, false>, a);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const int64_t per = p.S == 1 ? kFinishBlock : kFinishBlock / 32;
+    const unsigned ctas = M > per ? kFinishCtas : 1;
+    PdlConfig lf(ctas, kFinishBlock, 0, s);
+    lf.cluster(ctas);
+    e = cudaLaunchKernelEx(&lf.cfg, dyt::loss::loss_finish_kernel<T>, a);
+    if (e != cudaSuccess) return cuda_fail(e);
+    record(kOpLossForward, &p, (int)(16 / sizeof(T)), 2, need);
+    return DYT_OK;
+  });
+} catch (...) {
+  return cuda_fail(cudaErrorMemoryAllocation);  // the host ran out of memory for the per-device facts
+}
+
+dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *tokens, int token_bytes,
+                                    const float *stats, const float *coef, const float *grad, double temperature,
+                                    void *dlogits, int64_t lddl, int64_t M, int64_t N, dyt_dtype dtype,
+                                    dyt_stream_t stream) try {
+  dyt_status st = check_shape(M, N, dtype);
+  if (st != DYT_OK) return st;
+  if (check_pitch(M, N, ld) != DYT_OK || check_pitch(M, N, lddl) != DYT_OK || (token_bytes != 4 && token_bytes != 8) ||
+      !finite_positive(temperature))
+    return DYT_ERR_INVALID_VALUE;
+  if (M == 0 || N == 0) {
+    record(kOpLossBackward, nullptr, 0, 0, 0);
+    return DYT_OK;
+  }
+  const size_t es = dsize(dtype);
+  if (!logits || !tokens || !stats || !coef || !dlogits || !elem_aligned(logits, es) ||
+      !elem_aligned(tokens, token_bytes) || !elem_aligned(stats, 8) || !elem_aligned(coef, 4) ||
+      !elem_aligned(grad, 4) || !elem_aligned(dlogits, es))
+    return DYT_ERR_INVALID_VALUE;
+  const float C = (float)(dyt::loss::kLog2eD / temperature);
+  if (!(C > 0.0f) || std::isinf(C)) return DYT_ERR_INVALID_VALUE;
+  int dev = 0, sms = 0;
+  st = current_sms(&dev, &sms);
+  if (st != DYT_OK) return st;
+  const LossPlan p = plan(M, N, es, true, sms);
+  LossGradArgs a = {};
+  a.z = logits;
+  a.ld = ld;
+  a.tokens = tokens;
+  a.stats = (const float2 *)stats;
+  a.coef = coef;
+  a.grad = grad;
+  a.dz = dlogits;
+  a.lddz = lddl;
+  a.M = M;
+  a.N = N;
+  a.S = p.S;
+  a.wide_tokens = token_bytes == 8;
+  a.C = C;
+  a.inv_t = 1.0 / temperature;
+  const bool shift = !same_offset(logits, dlogits) || (M > 1 && !vec_pitch(ld - lddl, es));
+  return with_type(dtype, [&](auto t) -> dyt_status {
+    using T = decltype(t);
+    PdlConfig lc((unsigned)p.grid, kBlock, 0, (cudaStream_t)stream);
+    const auto k = p.cta ? (shift ? dyt::loss::loss_grad_kernel<T, true, true> : dyt::loss::loss_grad_kernel<T, true, false>)
+                         : (shift ? dyt::loss::loss_grad_kernel<T, false, true> : dyt::loss::loss_grad_kernel<T, false, false>);
+    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
+    if (e != cudaSuccess) return cuda_fail(e);
+    record(kOpLossBackward, &p, (int)(16 / sizeof(T)), 1, 0);
+    return DYT_OK;
+  });
+} catch (...) {
+  return cuda_fail(cudaErrorMemoryAllocation);
+}
+
+}  // extern "C"

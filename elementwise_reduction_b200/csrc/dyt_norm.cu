@@ -1,0 +1,305 @@
+// Layer norm entry points (declared in include/dyt.h): argument checks, launch
+// plans and dispatch of the kernels in dyt_norm.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "dyt.h"
+#include "dyt_host.h"
+#include "dyt_norm.cuh"
+
+namespace {
+
+using namespace dyt::host;
+using dyt::norm::NormArgs;
+using dyt::norm::NormGradArgs;
+
+constexpr int kOpNormForward = 5, kOpNormBackward = 6;  // dyt_launch_info::op
+constexpr int kRowsBlock = 256;                         // threads of a CTA with several rows
+
+// How a row is spread over lanes: K vectors of V elements a lane.
+struct RowPlan {
+  int V = 1, K = 1, L = 1, NV = 0;
+  int block = 0;       // threads of a CTA
+  int rows = 1;        // rows side by side in a CTA
+  bool cta = false;    // a row is a whole CTA's
+  bool rowlong = false;  // too long for registers
+};
+
+int pow2_at_least(int64_t v) {
+  int p = 1;
+  while (p < v) p <<= 1;
+  return p;
+}
+
+// A lane holds at most max_elems elements of a row. Rows of up to 32 lanes
+// share a warp; longer ones take a CTA of up to max_block threads, with as few
+// vectors a thread as reach the end.
+RowPlan plan_rows(int64_t N, int V, int max_elems, int max_block) {
+  RowPlan p;
+  p.V = V;
+  const int64_t NV = ceil_div(N, V);
+  p.NV = (int)NV;
+  const int kmax = max_elems / V;
+  if (NV <= 32 * (int64_t)kmax && NV * V <= 512) {
+    p.K = NV <= 32 ? 1 : pow2_at_least(ceil_div(NV, 32));
+    p.L = pow2_at_least(ceil_div(NV, p.K));
+    p.block = kRowsBlock;
+    p.rows = p.block / p.L;
+    return p;
+  }
+  p.cta = true;
+  p.K = 1;
+  while (p.K < kmax && NV > (int64_t)p.K * max_block) p.K <<= 1;
+  if (NV > (int64_t)p.K * max_block) {
+    p.rowlong = true;
+    p.K = 1;
+    p.block = max_block;
+  } else {
+    p.block = (int)(ceil_div(ceil_div(NV, p.K), 32) * 32);
+  }
+  p.L = p.block;
+  return p;
+}
+
+constexpr int kFwdElems = 32, kFwdBlock = 1024;
+constexpr int kBwdElems = 16, kBwdBlock = 512;
+
+template <typename T>
+constexpr int vec_elems() {
+  return 16 / (int)sizeof(T);
+}
+
+template <typename F>
+dyt_status with_type(int xd, F &&f) {
+  switch (xd) {
+    case DYT_F32: return f(float{});
+    case DYT_BF16: return f(__nv_bfloat16{});
+    case DYT_F16: return f(__half{});
+  }
+  return DYT_ERR_UNSUPPORTED_DTYPE;
+}
+
+// ---- forward -------------------------------------------------------------------
+
+using FwdKernel = void (*)(NormArgs);
+
+template <typename T, int V, int K>
+FwdKernel fwd_at(const RowPlan &p) {
+  if constexpr (K * V <= kFwdElems) {
+    if (p.K == K) return p.cta ? dyt::norm::norm_fwd_kernel<T, V, K, true> : dyt::norm::norm_fwd_kernel<T, V, K, false>;
+    return fwd_at<T, V, K * 2>(p);
+  }
+  return nullptr;
+}
+template <typename T>
+FwdKernel fwd_kernel(const RowPlan &p) {
+  if (p.V == 1) return p.rowlong ? dyt::norm::norm_fwd_long_kernel<T, 1> : fwd_at<T, 1, 1>(p);
+  constexpr int V = vec_elems<T>();
+  return p.rowlong ? dyt::norm::norm_fwd_long_kernel<T, V> : fwd_at<T, V, 1>(p);
+}
+
+// ---- backward ------------------------------------------------------------------
+
+using BwdKernel = void (*)(NormGradArgs);
+
+template <typename T, int V, int K>
+BwdKernel bwd_at(const RowPlan &p) {
+  if constexpr (K * V <= kBwdElems) {
+    if (p.K == K) return p.cta ? dyt::norm::norm_bwd_kernel<T, V, K, true> : dyt::norm::norm_bwd_kernel<T, V, K, false>;
+    return bwd_at<T, V, K * 2>(p);
+  }
+  return nullptr;
+}
+template <typename T>
+BwdKernel bwd_kernel(const RowPlan &p) {
+  if (p.V == 1) return bwd_at<T, 1, 1>(p);
+  return bwd_at<T, vec_elems<T>(), 1>(p);
+}
+
+constexpr int kColumnsBlock = 256;  // vector-columns of a CTA in the long rows' second pass
+
+// Partial sums of a backward: one set per CTA (per row group for long rows).
+struct BwdPlan {
+  RowPlan r;
+  int64_t grid = 0;   // CTAs (the row pass's for long rows)
+  int64_t parts = 0;  // partial sets
+  int col_ctas = 0;   // long rows: CTAs across the columns
+  size_t off_c12 = 0, bytes = 0;
+};
+
+BwdPlan plan_bwd(int64_t M, int64_t N, int V, int sms) {
+  BwdPlan b;
+  b.r = plan_rows(N, V, kBwdElems, kBwdBlock);
+  if (b.r.rowlong) {
+    b.grid = std::min<int64_t>(M, (int64_t)sms * 2);
+    b.col_ctas = (int)ceil_div(b.r.NV, kColumnsBlock);
+    b.parts = std::max<int64_t>(1, std::min<int64_t>(M, (int64_t)sms * 4 / b.col_ctas));
+  } else {
+    const int per_sm = std::max(1, 512 / b.r.block);
+    b.grid = std::min<int64_t>(ceil_div(M, b.r.rows), (int64_t)sms * per_sm);
+    b.parts = b.grid;
+  }
+  b.off_c12 = ((size_t)b.parts * 2 * (size_t)N * sizeof(double) + 15) & ~(size_t)15;
+  b.bytes = b.off_c12 + (b.r.rowlong ? (size_t)M * sizeof(float2) : 0);
+  b.bytes = (b.bytes + 15) & ~(size_t)15;
+  return b;
+}
+
+size_t bwd_smem(const RowPlan &p) {
+  return p.cta ? 0 : (size_t)(p.block / 32) * 2 * p.L * p.K * p.V * sizeof(float);
+}
+
+void record(int op, const RowPlan *p, int64_t grid, int kernels, int64_t groups, size_t ws) {
+  dyt_launch_info i = {};
+  i.op = op;
+  i.kernels = kernels;
+  i.workspace_bytes = (int64_t)ws;
+  if (p) {
+    i.path = p->cta ? 2 : 1;
+    i.vec = p->V;
+    i.block = p->block;
+    i.grid = (int)grid;
+    i.row_lanes = p->rows;
+    i.rows_per_step = p->rows;
+    i.col_chunks = 1;
+    i.row_groups = (int)groups;
+    i.pack_rows = 1;
+  }
+  record_info(i);
+}
+
+bool param_ok(const void *p, int dt) { return p == nullptr || elem_aligned(p, dsize(dt)); }
+
+}  // namespace
+
+extern "C" {
+
+dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma, const void *beta, float eps, void *y,
+                                  int64_t ldy, float *mean, float *rstd, int64_t M, int64_t N, dyt_dtype x_dtype,
+                                  dyt_dtype gamma_dtype, dyt_dtype beta_dtype, dyt_stream_t stream) try {
+  dyt_status st = check_shape(M, N, x_dtype);
+  if (st != DYT_OK) return st;
+  if (!valid_dtype(gamma_dtype) || !valid_dtype(beta_dtype)) return DYT_ERR_UNSUPPORTED_DTYPE;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return DYT_ERR_INVALID_VALUE;
+  if (check_pitch(M, N, ldx) != DYT_OK || check_pitch(M, N, ldy) != DYT_OK) return DYT_ERR_INVALID_VALUE;
+  if (M == 0 || N == 0) {
+    record(kOpNormForward, nullptr, 0, 0, 0, 0);
+    return DYT_OK;
+  }
+  const size_t es = dsize(x_dtype);
+  if (!x || !y || !elem_aligned(x, es) || !elem_aligned(y, es) || !param_ok(gamma, gamma_dtype) ||
+      !param_ok(beta, beta_dtype) || !param_ok(mean, DYT_F32) || !param_ok(rstd, DYT_F32))
+    return DYT_ERR_INVALID_VALUE;
+  int dev = 0, sms = 0;
+  st = current_sms(&dev, &sms);
+  if (st != DYT_OK) return st;
+  return with_type(x_dtype, [&](auto t) -> dyt_status {
+    using T = decltype(t);
+    constexpr int VE = vec_elems<T>();
+    const bool vec = N % VE == 0 && aligned16(x) && aligned16(y) && (M == 1 || (vec_pitch(ldx, es) && vec_pitch(ldy, es)));
+    const RowPlan p = plan_rows(N, vec ? VE : 1, kFwdElems, kFwdBlock);
+    const FwdKernel k = fwd_kernel<T>(p);
+    int occ = 1;
+    const dyt_status s = occupancy(dev, (const void *)k, p.block, &occ);
+    if (s != DYT_OK) return s;
+    const int64_t grid = std::min<int64_t>(ceil_div(M, p.rows), (int64_t)sms * occ);
+    const NormArgs a = {x, ldx, gamma, beta, y, ldy, mean, rstd, M, N, p.NV, p.L, (int)gamma_dtype, (int)beta_dtype, eps};
+    PdlConfig lc((unsigned)grid, p.block, 0, (cudaStream_t)stream);
+    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
+    if (e != cudaSuccess) return cuda_fail(e);
+    record(kOpNormForward, &p, grid, 1, 0, 0);
+    return DYT_OK;
+  });
+} catch (...) {
+  return cuda_fail(cudaErrorMemoryAllocation);  // the host ran out of memory for the per-device facts
+}
+
+size_t dyt_layer_norm_backward_workspace_bytes(int64_t M, int64_t N, dyt_dtype x_dtype) try {
+  if (check_shape(M, N, x_dtype) != DYT_OK || M == 0 || N == 0) return 0;
+  int dev = 0, sms = 0;
+  if (current_sms(&dev, &sms) != DYT_OK) return 0;
+  const size_t one = plan_bwd(M, N, 1, sms).bytes;
+  const int v = 16 / (int)dsize(x_dtype);
+  return N % v == 0 ? std::max(one, plan_bwd(M, N, v, sms).bytes) : one;
+} catch (...) {
+  return 0;
+}
+
+dyt_status dyt_layer_norm_backward(const void *x, int64_t ldx, const void *dy, int64_t lddy, const void *gamma,
+                                   const float *mean, const float *rstd, void *dx, int64_t lddx, void *dgamma,
+                                   void *dbeta, int64_t M, int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype,
+                                   dyt_dtype beta_dtype, void *workspace, size_t workspace_bytes,
+                                   dyt_stream_t stream) try {
+  dyt_status st = check_shape(M, N, x_dtype);
+  if (st != DYT_OK) return st;
+  if (!valid_dtype(gamma_dtype) || !valid_dtype(beta_dtype)) return DYT_ERR_UNSUPPORTED_DTYPE;
+  if (check_pitch(M, N, ldx) != DYT_OK || check_pitch(M, N, lddy) != DYT_OK || check_pitch(M, N, lddx) != DYT_OK)
+    return DYT_ERR_INVALID_VALUE;
+  if (!param_ok(dgamma, gamma_dtype) || !param_ok(dbeta, beta_dtype)) return DYT_ERR_INVALID_VALUE;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (M == 0 || N == 0) {
+    cudaError_t e = cudaSuccess;  // empty sums
+    if (N > 0 && dgamma) e = cudaMemsetAsync(dgamma, 0, (size_t)N * dsize(gamma_dtype), s);
+    if (N > 0 && dbeta && e == cudaSuccess) e = cudaMemsetAsync(dbeta, 0, (size_t)N * dsize(beta_dtype), s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    record(kOpNormBackward, nullptr, 0, 0, 0, 0);
+    return DYT_OK;
+  }
+  const size_t es = dsize(x_dtype);
+  if (!x || !dy || !dx || !mean || !rstd || !workspace || !aligned16(workspace) || !elem_aligned(x, es) ||
+      !elem_aligned(dy, es) || !elem_aligned(dx, es) || !param_ok(gamma, gamma_dtype) || !param_ok(mean, DYT_F32) ||
+      !param_ok(rstd, DYT_F32))
+    return DYT_ERR_INVALID_VALUE;
+  int dev = 0, sms = 0;
+  st = current_sms(&dev, &sms);
+  if (st != DYT_OK) return st;
+  return with_type(x_dtype, [&](auto t) -> dyt_status {
+    using T = decltype(t);
+    constexpr int VE = vec_elems<T>();
+    const bool vec = N % VE == 0 && aligned16(x) && aligned16(dy) && aligned16(dx) &&
+                     (M == 1 || (vec_pitch(ldx, es) && vec_pitch(lddy, es) && vec_pitch(lddx, es)));
+    const BwdPlan b = plan_bwd(M, N, vec ? VE : 1, sms);
+    if (workspace_bytes < b.bytes) return DYT_ERR_WORKSPACE_TOO_SMALL;
+    double *parts = (double *)workspace;
+    const NormGradArgs a = {x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, parts, M, N, b.r.NV, b.r.L,
+                            (int)gamma_dtype};
+    int kernels = 2;
+    cudaError_t e;
+    if (b.r.rowlong) {
+      float2 *c12 = (float2 *)((char *)workspace + b.off_c12);
+      PdlConfig lr((unsigned)b.grid, 1024, 0, s);
+      e = cudaLaunchKernelEx(&lr.cfg, vec ? dyt::norm::norm_bwd_rows_kernel<T, VE> : dyt::norm::norm_bwd_rows_kernel<T, 1>,
+                             a, c12);
+      if (e != cudaSuccess) return cuda_fail(e);
+      PdlConfig lc((unsigned)b.col_ctas, kColumnsBlock, 0, s);
+      lc.cfg.gridDim.y = (unsigned)b.parts;
+      e = cudaLaunchKernelEx(&lc.cfg,
+                             vec ? dyt::norm::norm_bwd_columns_kernel<T, VE> : dyt::norm::norm_bwd_columns_kernel<T, 1>,
+                             a, (const float2 *)c12);
+      kernels = 3;
+    } else {
+      const BwdKernel k = bwd_kernel<T>(b.r);
+      PdlConfig lc((unsigned)b.grid, b.r.block, bwd_smem(b.r), s);
+      e = cudaLaunchKernelEx(&lc.cfg, k, a);
+    }
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dgamma || dbeta) {
+      PdlConfig lf((unsigned)ceil_div(N, dyt::norm::kSumCols), dyt::norm::kSumCols * dyt::norm::kSumLanes, 0, s);
+      lf.cfg.gridDim.y = 2;
+      e = cudaLaunchKernelEx(&lf.cfg, dyt::norm::norm_finalize_kernel, (const double *)parts, (int)b.parts, N, dgamma,
+                             (int)gamma_dtype, dbeta, (int)beta_dtype);
+      if (e != cudaSuccess) return cuda_fail(e);
+    } else {
+      --kernels;
+    }
+    record(kOpNormBackward, &b.r, b.grid, kernels, b.parts, b.bytes);
+    return DYT_OK;
+  });
+} catch (...) {
+  return cuda_fail(cudaErrorMemoryAllocation);
+}
+
+}  // extern "C"

@@ -1,0 +1,143 @@
+"""Layer norm, the layer that DyT takes the place of: forward, backward, autograd module.
+
+    y = gamma * (x - mean) * rstd + beta      (x: [..., N]; mean, rstd: per row; gamma/beta: [N])
+
+Row layouts, dtypes and streams are those of DyT's forward and backward.
+"""
+from __future__ import annotations
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _abi
+from ._rows import DTYPE_CODE, _code, _elsewhere, _like, _rows, _there, _vector, _workspace, row_pitch
+
+_F32 = (torch.float32,)
+_PARAM = tuple(DTYPE_CODE)
+
+
+def _shape(x: torch.Tensor) -> tuple[int, int]:
+    if x.dim() == 0:
+        raise ValueError("x must have at least one dimension")
+    N = x.shape[-1]
+    return (x.numel() // N if N else 0), N
+
+
+def layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+                       eps: float = 1e-5, out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                       rstd: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """(y, mean, rstd): y in x's dtype, the rows' statistics in float32 (one kernel
+    launch). x and out may be row-strided views (dense rows, evenly spaced): no copy
+    is made. gamma and beta may each have their own dtype, or be left out. out may
+    be x."""
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return layer_norm_forward(x, gamma, beta, eps, out, mean, rstd)
+    ldx, code = _rows(x, "x"), _code(x, "x")
+    M, N = _shape(x)
+    dev = x.device
+    gp = None if gamma is None else _vector(gamma, "gamma", N, dev, _PARAM)
+    bp = None if beta is None else _vector(beta, "beta", N, dev, _PARAM)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    ldy = _like(y, "out", x)
+    rows = x.shape[:-1]
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if mean is None else mean
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if rstd is None else rstd
+    st = _abi.dyt_layer_norm_forward(
+        x.data_ptr(), ldx, gp, bp, eps, y.data_ptr(), ldy, _vector(mean, "mean", mean.numel() if N == 0 else M, dev, _F32),
+        _vector(rstd, "rstd", rstd.numel() if N == 0 else M, dev, _F32), M, N, code,
+        code if gamma is None else DTYPE_CODE[gamma.dtype], code if beta is None else DTYPE_CODE[beta.dtype],
+        torch.cuda.current_stream().cuda_stream)
+    _abi._check(st, "dyt_layer_norm_forward")
+    return y, mean, rstd
+
+
+def layer_norm_workspace(x: torch.Tensor) -> torch.Tensor:
+    """A device workspace large enough for layer_norm_backward on x's shape and device."""
+    M, N = _shape(x)
+    with torch.cuda.device(x.device):
+        n = _abi.dyt_layer_norm_backward_workspace_bytes(M, N, _code(x, "x"))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
+
+
+def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+                        dx: torch.Tensor | None = None, dgamma: torch.Tensor | None = None,
+                        dbeta: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                        stream: torch.cuda.Stream | None = None):
+    """(dx, dgamma, dbeta) from the forward's statistics: dx in x's dtype and each
+    parameter's gradient in its parameter's dtype (None for a parameter that is not
+    given; beta's values are not read). x, dy and dx may be row-strided views; dx may
+    be x or dy."""
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return layer_norm_backward(x, dy, mean, rstd, gamma, beta, dx, dgamma, dbeta, ws)
+    ldx, code = _rows(x, "x"), _code(x, "x")
+    M, N = _shape(x)
+    dev = x.device
+    lddy = _like(dy, "dy", x)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
+    lddx = _like(dx, "dx", x)
+    gp = None if gamma is None else _vector(gamma, "gamma", N, dev, _PARAM)
+    if beta is not None:
+        _vector(beta, "beta", N, dev, _PARAM)
+    if (gamma is None and dgamma is not None) or (beta is None and dbeta is not None):
+        raise ValueError("dgamma and dbeta need their parameters")
+    if gamma is not None:
+        dgamma = torch.empty_like(gamma) if dgamma is None else dgamma
+    if beta is not None:
+        dbeta = torch.empty_like(beta) if dbeta is None else dbeta
+    ws = layer_norm_workspace(x) if ws is None else ws
+    st = _abi.dyt_layer_norm_backward(
+        x.data_ptr(), ldx, dy.data_ptr(), lddy, gp, _vector(mean, "mean", mean.numel() if N == 0 else M, dev, _F32),
+        _vector(rstd, "rstd", rstd.numel() if N == 0 else M, dev, _F32), dx.data_ptr(), lddx,
+        None if gamma is None else _vector(dgamma, "dgamma", N, dev, (gamma.dtype,)),
+        None if beta is None else _vector(dbeta, "dbeta", N, dev, (beta.dtype,)), M, N, code,
+        code if gamma is None else DTYPE_CODE[gamma.dtype], code if beta is None else DTYPE_CODE[beta.dtype],
+        _workspace(ws, dev), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    _abi._check(st, "dyt_layer_norm_backward")
+    return dx, dgamma, dbeta
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """Autograd wrapper: x and the rows' statistics are saved, the rest is recomputed."""
+
+    @staticmethod
+    def forward(ctx, x, gamma, beta, eps):
+        gamma, beta = (None if t is None else t.contiguous() for t in (gamma, beta))
+        x = x if row_pitch(x) is not None else x.contiguous()
+        y, mean, rstd = layer_norm_forward(x, gamma, beta, eps)
+        ctx.save_for_backward(x, mean, rstd, gamma, beta)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, mean, rstd, gamma, beta = ctx.saved_tensors
+        dy = dy if row_pitch(dy) is not None else dy.contiguous()
+        dx, dgamma, dbeta = layer_norm_backward(x, dy, mean, rstd, gamma, beta)
+        return dx, dgamma, dbeta, None
+
+
+class LayerNorm(torch.nn.Module):
+    """gamma * (x - mean) * rstd + beta over the last dimension.
+
+    gamma and beta have one entry per channel and live in ``param_dtype``; each
+    gradient comes back in that dtype. ``affine=False`` leaves both out,
+    ``bias=False`` beta alone.
+    """
+
+    def __init__(self, num_features: int, eps: float = 1e-5, affine: bool = True, bias: bool = True,
+                 param_dtype=torch.float32, device=None):
+        super().__init__()
+        self.eps = eps
+        make = lambda fill: torch.nn.Parameter(torch.full((num_features,), fill, dtype=param_dtype,  # noqa: E731
+                                                          device=device))
+        self.num_features = num_features
+        self.register_parameter("gamma", make(1.0) if affine else None)
+        self.register_parameter("beta", make(0.0) if affine and bias else None)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.shape[-1:] != (self.num_features,):
+            raise ValueError(f"x's last dimension {tuple(x.shape)} must be {self.num_features}")
+        return LayerNormFunction.apply(x, self.gamma, self.beta, self.eps)

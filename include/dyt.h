@@ -288,12 +288,15 @@ const char *dyt_status_string(dyt_status status);
 int dyt_last_cuda_error(void);
 
 /*
- * Launch geometry of the calling thread's last successful dyt_forward or
- * dyt_backward call, so tests can check which path ran.
+ * Launch geometry of the calling thread's last successful call, so tests can
+ * check which path ran. (Layer norm: path 1 = several rows per CTA, 2 = one;
+ * row_groups = partial sums per column. Policy loss: path 1 = a warp per row,
+ * 2 = a CTA per row or part of one; col_chunks = parts of a row.)
  */
 typedef struct dyt_launch_info {
   int op;            /* 1 = forward, 2 = backward, 3 = backward stage 1 (dyt_backward_partials),
-                        4 = finalize (dyt_finalize_partials), 0 = none yet */
+                        4 = finalize (dyt_finalize_partials), 5 / 6 = layer norm forward /
+                        backward, 7 / 8 = policy loss forward / backward, 0 = none yet */
   int path;          /* 0 = nothing launched, 1 = row-tiled (several rows per CTA step),
                         2 = row-per-CTA (one row per CTA step, columns across threads) */
   int vec;           /* elements per vector access (1 = the one-element kernels) */
@@ -377,6 +380,112 @@ dyt_status dyt_plan_query(int64_t M, int64_t N, dyt_dtype x_dtype, dyt_dtype par
 dyt_status dyt_backward_noalloc(const void *x, const void *dy, const void *alpha, const void *gamma,
                                 const void *beta, void *dx, void *dgamma, void *dbeta, void *dalpha, int64_t M,
                                 int64_t N, dyt_dtype x_dtype, dyt_dtype param_dtype, dyt_stream_t stream);
+
+/*
+ * Layer norm over the rows of x, the layer that DyT takes the place of:
+ *
+ *   mean[i] = sum_j x[i,j] / N      rstd[i] = (sum_j (x[i,j] - mean[i])^2 / N + eps)^(-1/2)
+ *   h[i,j]  = (x[i,j] - mean[i]) * rstd[i]
+ *   y[i,j]  = gamma[j] * h[i,j] + beta[j]
+ *
+ * One kernel launch. The conventions above hold (row pitches, any element
+ * alignment, dtypes, determinism, y may alias x with an equal pitch); a row's
+ * sums and its statistics are binary32, the squares are taken about the mean,
+ * and y is rounded once. No padding between rows is read or written.
+ *   gamma, beta  [N] gamma_dtype, beta_dtype, read; NULL for a layer without
+ *                (gamma = 1, beta = 0)
+ *   eps          >= 0 and finite, else DYT_ERR_INVALID_VALUE
+ *   mean, rstd   [M] binary32, written for the backward; each may be NULL
+ * Tensors whose rows are all whole aligned 16-byte vectors (N included) are
+ * read and written in vectors, others by elements. M * N == 0 launches nothing
+ * and writes nothing.
+ */
+dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma, const void *beta, float eps, void *y,
+                                  int64_t ldy, float *mean, float *rstd, int64_t M, int64_t N, dyt_dtype x_dtype,
+                                  dyt_dtype gamma_dtype, dyt_dtype beta_dtype, dyt_stream_t stream);
+
+/*
+ * Layer norm's gradients, from the statistics that the forward wrote:
+ *
+ *   g[i,j]    = gamma[j] * dy[i,j]
+ *   dx[i,j]   = rstd[i] * (g[i,j] - sum_k g[i,k] / N - h[i,j] * sum_k g[i,k] h[i,k] / N)
+ *   dgamma[j] = sum_i dy[i,j] * h[i,j]        dbeta[j] = sum_i dy[i,j]
+ *
+ * A kernel that writes dx and each CTA's column sums, and one that adds those
+ * in binary64 in a fixed order and rounds each gradient once (rows too long for
+ * a CTA's registers take a third). Columns are summed in binary32 over at most
+ * 128 rows and in binary64 beyond. dx may alias x or dy with an equal pitch.
+ *   gamma         NULL: 1
+ *   mean, rstd    [M] binary32, read
+ *   dgamma, dbeta [N] gamma_dtype, beta_dtype, written; NULL: not wanted
+ *   workspace     as for dyt_backward, of at least
+ *                 dyt_layer_norm_backward_workspace_bytes(M, N, x_dtype) bytes
+ * M * N == 0: dgamma and dbeta (when N > 0) are set to zero, and no workspace
+ * is used.
+ */
+size_t dyt_layer_norm_backward_workspace_bytes(int64_t M, int64_t N, dyt_dtype x_dtype);
+dyt_status dyt_layer_norm_backward(const void *x, int64_t ldx, const void *dy, int64_t lddy, const void *gamma,
+                                   const float *mean, const float *rstd, void *dx, int64_t lddx, void *dgamma,
+                                   void *dbeta, int64_t M, int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype,
+                                   dyt_dtype beta_dtype, void *workspace, size_t workspace_bytes,
+                                   dyt_stream_t stream);
+
+/*
+ * The clipped policy loss with a KL term, of M rows (tokens) of logits z over a
+ * vocabulary of N, T the temperature:
+ *
+ *   m = max_j z[i,j],  s = log sum_j exp((z[i,j] - m) / T)
+ *   lp = (z[i,tokens[i]] - m) / T - s                       (log probability)
+ *   r  = exp(lp - old_logp[i]),  c = min(max(r, 1 - clip_low), 1 + clip_high)
+ *   q  = ref_logp[i] - lp,       A = advantage[i],  w = weight[i]
+ *   loss    = sum_i w * (-min(r A, c A) + kl_coef * (exp(q) - q - 1))
+ *   coef[i] = w * (-(r A if r A <= c A else 0) + kl_coef * (1 - exp(q)))
+ *
+ * coef is the loss's derivative by lp; the backward needs it, and stats = (m, s).
+ * Two kernel launches. The logits are read once; the row sums are binary32, the
+ * rows' scalar arithmetic and the loss's sum binary64, each output rounded once.
+ *   logits    [M*N] dtype, row pitch ld, any element alignment
+ *   tokens    [M] int64 (token_bytes 8) or int32 (token_bytes 4). At a row that
+ *             counts, a token outside [0, N) makes lp, coef and the loss NaN;
+ *             nothing outside the row is read.
+ *   old_logp, advantage  [M] binary32
+ *   ref_logp  [M] binary32, or NULL: no KL term (nor with kl_coef 0)
+ *   weight    [M] binary32, or NULL: 1 / M each. A row of weight 0 does not
+ *             count: neither its logits nor its other values are used, and its
+ *             logp, stats and coef are 0.
+ *   loss      [1], logp [M], stats [M][2], coef [M]: binary32, written
+ *   workspace 16-byte aligned scratch of at least
+ *             dyt_policy_loss_workspace_bytes(M, N, dtype) bytes; two calls in
+ *             flight at once need two.
+ * clip_low and clip_high must be >= 0, temperature > 0, all finite. M == 0 sets
+ * the loss to 0; N == 0 with M > 0 gives DYT_ERR_INVALID_VALUE. A row whose
+ * logits are all -inf, or hold +inf or NaN, has lp NaN.
+ */
+size_t dyt_policy_loss_workspace_bytes(int64_t M, int64_t N, dyt_dtype dtype);
+dyt_status dyt_policy_loss_forward(const void *logits, int64_t ld, const void *tokens, int token_bytes,
+                                   const float *old_logp, const float *ref_logp, const float *advantage,
+                                   const float *weight, double clip_low, double clip_high, double kl_coef,
+                                   double temperature, float *loss, float *logp, float *stats, float *coef, int64_t M,
+                                   int64_t N, dyt_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   dyt_stream_t stream);
+
+/*
+ * The loss's gradient by the logits, from what the forward wrote:
+ *
+ *   dlogits[i,j] = (grad * coef[i] / T) * ((j == tokens[i]) - exp((z[i,j] - m) / T - s))
+ *
+ * One kernel launch, no workspace. Rows whose factor grad * coef / T is 0 (no
+ * weight, or the clipped side without a KL term) get zeros and are not read.
+ *   stats, coef  [M][2] and [M] binary32, read; temperature as in the forward
+ *   grad         [1] binary32, the loss's own gradient, on the device; NULL: 1
+ *   dlogits      [M*N] dtype, row pitch lddl, written; may alias logits with an
+ *                equal pitch
+ * M * N == 0 launches nothing.
+ */
+dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *tokens, int token_bytes,
+                                    const float *stats, const float *coef, const float *grad, double temperature,
+                                    void *dlogits, int64_t lddl, int64_t M, int64_t N, dyt_dtype dtype,
+                                    dyt_stream_t stream);
 
 #ifdef __cplusplus
 }
