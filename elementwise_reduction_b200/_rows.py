@@ -56,6 +56,19 @@ def _stream(device, stream):
     return stream.cuda_stream
 
 
+def _current(index: int) -> int:
+    """The current stream of a device, as the library takes it. (The raw handle: making a
+    torch.cuda.Stream object for it costs as much as a launch, 2 to 3 us.)"""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _pitch(t: torch.Tensor, what: str) -> int:
+    """The row pitch of a CUDA tensor; contiguous ones need no look at their strides."""
+    if t.is_contiguous() and t.dim():
+        return t.shape[-1]
+    return _rows(t, what)
+
+
 def _elsewhere(t: torch.Tensor, stream: torch.cuda.Stream | None) -> bool:
     """Whether a call on t's data has to switch the current device or stream (see _there)."""
     if not t.is_cuda:
@@ -90,7 +103,7 @@ def _like(t: torch.Tensor, what: str, x: torch.Tensor) -> int:
     """The row pitch of a tensor of x's shape, dtype and device."""
     if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
         raise ValueError(f"{what} must match its input in shape, dtype and device")
-    return _rows(t, what)
+    return _pitch(t, what)
 
 
 def _workspace(ws: torch.Tensor, device: torch.device) -> int:

@@ -19,13 +19,14 @@ using dyt::norm::NormGradArgs;
 constexpr int kOpNormForward = 5, kOpNormBackward = 6;  // dyt_launch_info::op
 constexpr int kRowsBlock = 256;                         // threads of a CTA with several rows
 
-// How a row is spread over lanes: K vectors of V elements a lane.
+// How a row is spread over lanes (see dyt_norm.cuh).
 struct RowPlan {
-  int V = 1, K = 1, L = 1, NV = 0;
-  int block = 0;       // threads of a CTA
-  int rows = 1;        // rows side by side in a CTA
-  bool cta = false;    // a row is a whole CTA's
-  bool rowlong = false;  // too long for registers
+  int V = 1, L = 1, NV = 0;
+  int block = 0;         // threads of a CTA
+  int rows = 1;          // rows side by side in a CTA
+  bool group = false;    // a row takes several warps
+  bool ragged = false;   // rows off 16-byte boundaries, or of no whole vectors
+  bool rowlong = false;  // too long for a CTA's registers
 };
 
 int pow2_at_least(int64_t v) {
@@ -34,38 +35,38 @@ int pow2_at_least(int64_t v) {
   return p;
 }
 
-// A lane holds at most max_elems elements of a row. Rows of up to 32 lanes
-// share a warp; longer ones take a CTA of up to max_block threads, with as few
-// vectors a thread as reach the end.
-RowPlan plan_rows(int64_t N, int V, int max_elems, int max_block) {
+// vec: elements of 16 bytes. aligned: every row of every tensor is whole aligned vectors. E: elements a lane holds.
+RowPlan plan_rows(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
   RowPlan p;
-  p.V = V;
-  const int64_t NV = ceil_div(N, V);
-  p.NV = (int)NV;
-  const int kmax = max_elems / V;
-  if (NV <= 32 * (int64_t)kmax && NV * V <= 512) {
-    p.K = NV <= 32 ? 1 : pow2_at_least(ceil_div(NV, 32));
-    p.L = pow2_at_least(ceil_div(NV, p.K));
-    p.block = kRowsBlock;
-    p.rows = p.block / p.L;
+  const int64_t lanes = aligned ? ceil_div(N / vec, E / vec) : ceil_div(N, E);
+  p.ragged = !aligned;
+  if (lanes > dyt::norm::kBlock) {
+    p.rowlong = true;
+    p.V = aligned ? vec : 1;
+    p.NV = (int)ceil_div(N, p.V);
+    p.block = p.L = 1024;
     return p;
   }
-  p.cta = true;
-  p.K = 1;
-  while (p.K < kmax && NV > (int64_t)p.K * max_block) p.K <<= 1;
-  if (NV > (int64_t)p.K * max_block) {
-    p.rowlong = true;
-    p.K = 1;
-    p.block = max_block;
-  } else {
-    p.block = (int)(ceil_div(ceil_div(NV, p.K), 32) * 32);
-  }
-  p.L = p.block;
+  p.V = aligned ? vec : 1;
+  p.NV = (int)ceil_div(N, p.V);
+  p.group = lanes > 32;
+  p.L = p.group ? (int)ceil_div(lanes, 32) * 32 : pow2_at_least(lanes);
+  // Ragged rows keep one slot more per row and warp: half the threads where that is up to half a slot per lane.
+  int block = p.ragged && p.L < 8 ? dyt::norm::kBlock / 2 : dyt::norm::kBlock;
+  // Few short rows: smaller CTAs, so that more SMs take part.
+  while (!p.group && block > 128 && ceil_div(M, block / p.L) < sms) block >>= 1;
+  p.rows = block / p.L;
+  p.block = p.rows * p.L;
   return p;
 }
 
-constexpr int kFwdElems = 32, kFwdBlock = 1024;
-constexpr int kBwdElems = 16, kBwdBlock = 512;
+// Rows at the tensor's ends whose chunks could reach 16 bytes past it: those
+// less than 16 bytes from its first or its last row.
+int64_t ends(const int64_t *lds, int n, size_t elem) {
+  int64_t f = 0;
+  for (int i = 0; i < n; ++i) f = std::max(f, ceil_div(16, std::max<int64_t>(1, lds[i] * (int64_t)elem)));
+  return f;
+}
 
 template <typename T>
 constexpr int vec_elems() {
@@ -82,41 +83,21 @@ dyt_status with_type(int xd, F &&f) {
   return DYT_ERR_UNSUPPORTED_DTYPE;
 }
 
-// ---- forward -------------------------------------------------------------------
-
 using FwdKernel = void (*)(NormArgs);
-
-template <typename T, int V, int K>
-FwdKernel fwd_at(const RowPlan &p) {
-  if constexpr (K * V <= kFwdElems) {
-    if (p.K == K) return p.cta ? dyt::norm::norm_fwd_kernel<T, V, K, true> : dyt::norm::norm_fwd_kernel<T, V, K, false>;
-    return fwd_at<T, V, K * 2>(p);
-  }
-  return nullptr;
-}
-template <typename T>
-FwdKernel fwd_kernel(const RowPlan &p) {
-  if (p.V == 1) return p.rowlong ? dyt::norm::norm_fwd_long_kernel<T, 1> : fwd_at<T, 1, 1>(p);
-  constexpr int V = vec_elems<T>();
-  return p.rowlong ? dyt::norm::norm_fwd_long_kernel<T, V> : fwd_at<T, V, 1>(p);
-}
-
-// ---- backward ------------------------------------------------------------------
-
 using BwdKernel = void (*)(NormGradArgs);
 
-template <typename T, int V, int K>
-BwdKernel bwd_at(const RowPlan &p) {
-  if constexpr (K * V <= kBwdElems) {
-    if (p.K == K) return p.cta ? dyt::norm::norm_bwd_kernel<T, V, K, true> : dyt::norm::norm_bwd_kernel<T, V, K, false>;
-    return bwd_at<T, V, K * 2>(p);
-  }
-  return nullptr;
+template <typename T>
+FwdKernel fwd_kernel(const RowPlan &p) {
+  using namespace dyt::norm;
+  if (p.rowlong) return p.V == 1 ? norm_fwd_long_kernel<T, 1> : norm_fwd_long_kernel<T, vec_elems<T>()>;
+  if (p.group) return p.ragged ? norm_fwd_kernel<T, true, true> : norm_fwd_kernel<T, true, false>;
+  return p.ragged ? norm_fwd_kernel<T, false, true> : norm_fwd_kernel<T, false, false>;
 }
 template <typename T>
 BwdKernel bwd_kernel(const RowPlan &p) {
-  if (p.V == 1) return bwd_at<T, 1, 1>(p);
-  return bwd_at<T, vec_elems<T>(), 1>(p);
+  using namespace dyt::norm;
+  if (p.group) return p.ragged ? norm_bwd_kernel<T, true, true> : norm_bwd_kernel<T, true, false>;
+  return p.ragged ? norm_bwd_kernel<T, false, true> : norm_bwd_kernel<T, false, false>;
 }
 
 constexpr int kColumnsBlock = 256;  // vector-columns of a CTA in the long rows' second pass
@@ -130,16 +111,15 @@ struct BwdPlan {
   size_t off_c12 = 0, bytes = 0;
 };
 
-BwdPlan plan_bwd(int64_t M, int64_t N, int V, int sms) {
+BwdPlan plan_bwd(int64_t M, int64_t N, int vec, bool aligned, int sms) {
   BwdPlan b;
-  b.r = plan_rows(N, V, kBwdElems, kBwdBlock);
+  b.r = plan_rows(M, N, vec, aligned, dyt::norm::kBwdElems, sms);
   if (b.r.rowlong) {
     b.grid = std::min<int64_t>(M, (int64_t)sms * 2);
     b.col_ctas = (int)ceil_div(b.r.NV, kColumnsBlock);
     b.parts = std::max<int64_t>(1, std::min<int64_t>(M, (int64_t)sms * 4 / b.col_ctas));
   } else {
-    const int per_sm = std::max(1, 512 / b.r.block);
-    b.grid = std::min<int64_t>(ceil_div(M, b.r.rows), (int64_t)sms * per_sm);
+    b.grid = std::min<int64_t>(ceil_div(M, b.r.rows), (int64_t)sms);
     b.parts = b.grid;
   }
   b.off_c12 = ((size_t)b.parts * 2 * (size_t)N * sizeof(double) + 15) & ~(size_t)15;
@@ -148,17 +128,13 @@ BwdPlan plan_bwd(int64_t M, int64_t N, int V, int sms) {
   return b;
 }
 
-size_t bwd_smem(const RowPlan &p) {
-  return p.cta ? 0 : (size_t)(p.block / 32) * 2 * p.L * p.K * p.V * sizeof(float);
-}
-
 void record(int op, const RowPlan *p, int64_t grid, int kernels, int64_t groups, size_t ws) {
   dyt_launch_info i = {};
   i.op = op;
   i.kernels = kernels;
   i.workspace_bytes = (int64_t)ws;
   if (p) {
-    i.path = p->cta ? 2 : 1;
+    i.path = p->group || p->rowlong ? 2 : 1;
     i.vec = p->V;
     i.block = p->block;
     i.grid = (int)grid;
@@ -167,6 +143,7 @@ void record(int op, const RowPlan *p, int64_t grid, int kernels, int64_t groups,
     i.col_chunks = 1;
     i.row_groups = (int)groups;
     i.pack_rows = 1;
+    i.shifted = p->ragged && !p->rowlong;
   }
   record_info(i);
 }
@@ -200,14 +177,16 @@ dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma,
     using T = decltype(t);
     constexpr int VE = vec_elems<T>();
     const bool vec = N % VE == 0 && aligned16(x) && aligned16(y) && (M == 1 || (vec_pitch(ldx, es) && vec_pitch(ldy, es)));
-    const RowPlan p = plan_rows(N, vec ? VE : 1, kFwdElems, kFwdBlock);
+    const RowPlan p = plan_rows(M, N, VE, vec, dyt::norm::fwd_elems(!vec), sms);
     const FwdKernel k = fwd_kernel<T>(p);
-    int occ = 1;
-    const dyt_status s = occupancy(dev, (const void *)k, p.block, &occ);
+    const size_t smem = p.rowlong ? 0 : dyt::norm::fwd_smem<T>(p.block, p.L, p.ragged);
+    const dyt_status s = prepare_smem(dev, (const void *)k, (int)smem);
     if (s != DYT_OK) return s;
-    const int64_t grid = std::min<int64_t>(ceil_div(M, p.rows), (int64_t)sms * occ);
-    const NormArgs a = {x, ldx, gamma, beta, y, ldy, mean, rstd, M, N, p.NV, p.L, (int)gamma_dtype, (int)beta_dtype, eps};
-    PdlConfig lc((unsigned)grid, p.block, 0, (cudaStream_t)stream);
+    const int64_t grid = std::min<int64_t>(ceil_div(M, p.rows), (int64_t)sms);
+    const int64_t lds[1] = {ldx};
+    const NormArgs a = {x, ldx, gamma, beta, y, ldy, mean, rstd, M, N, p.NV, p.L, p.rows, (int)gamma_dtype,
+                        (int)beta_dtype, p.ragged ? ends(lds, 1, es) : 0, eps};
+    PdlConfig lc((unsigned)grid, p.block, smem, (cudaStream_t)stream);
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
     if (e != cudaSuccess) return cuda_fail(e);
     record(kOpNormForward, &p, grid, 1, 0, 0);
@@ -221,9 +200,8 @@ size_t dyt_layer_norm_backward_workspace_bytes(int64_t M, int64_t N, dyt_dtype x
   if (check_shape(M, N, x_dtype) != DYT_OK || M == 0 || N == 0) return 0;
   int dev = 0, sms = 0;
   if (current_sms(&dev, &sms) != DYT_OK) return 0;
-  const size_t one = plan_bwd(M, N, 1, sms).bytes;
   const int v = 16 / (int)dsize(x_dtype);
-  return N % v == 0 ? std::max(one, plan_bwd(M, N, v, sms).bytes) : one;
+  return std::max(plan_bwd(M, N, v, false, sms).bytes, plan_bwd(M, N, v, true, sms).bytes);
 } catch (...) {
   return 0;
 }
@@ -261,11 +239,12 @@ dyt_status dyt_layer_norm_backward(const void *x, int64_t ldx, const void *dy, i
     constexpr int VE = vec_elems<T>();
     const bool vec = N % VE == 0 && aligned16(x) && aligned16(dy) && aligned16(dx) &&
                      (M == 1 || (vec_pitch(ldx, es) && vec_pitch(lddy, es) && vec_pitch(lddx, es)));
-    const BwdPlan b = plan_bwd(M, N, vec ? VE : 1, sms);
+    const BwdPlan b = plan_bwd(M, N, VE, vec, sms);
     if (workspace_bytes < b.bytes) return DYT_ERR_WORKSPACE_TOO_SMALL;
     double *parts = (double *)workspace;
-    const NormGradArgs a = {x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, parts, M, N, b.r.NV, b.r.L,
-                            (int)gamma_dtype};
+    const int64_t lds[2] = {ldx, lddy};
+    const NormGradArgs a = {x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, parts, M, N, b.r.NV, b.r.L, b.r.rows,
+                            (int)gamma_dtype, b.r.ragged ? ends(lds, 2, es) : 0};
     int kernels = 2;
     cudaError_t e;
     if (b.r.rowlong) {
@@ -282,7 +261,10 @@ dyt_status dyt_layer_norm_backward(const void *x, int64_t ldx, const void *dy, i
       kernels = 3;
     } else {
       const BwdKernel k = bwd_kernel<T>(b.r);
-      PdlConfig lc((unsigned)b.grid, b.r.block, bwd_smem(b.r), s);
+      const size_t smem = dyt::norm::bwd_smem<T>(b.r.block, b.r.L, b.r.ragged);
+      const dyt_status ready = prepare_smem(dev, (const void *)k, (int)smem);
+      if (ready != DYT_OK) return ready;
+      PdlConfig lc((unsigned)b.grid, b.r.block, smem, s);
       e = cudaLaunchKernelEx(&lc.cfg, k, a);
     }
     if (e != cudaSuccess) return cuda_fail(e);

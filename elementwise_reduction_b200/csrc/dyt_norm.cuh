@@ -7,15 +7,16 @@
 //   dgamma_j = sum_i dy_ij h_ij,  dbeta_j = sum_i dy_ij
 //
 // Both are bound by memory: a row is read once and kept in registers between
-// its sums and its outputs. A row belongs to L lanes: to part of a warp (L a
-// power of two up to 32, so that a warp holds 32 / L rows) or to a whole CTA.
-// Lane l owns the vectors l, l + L, ... (K of them) of V elements, the same
-// columns in every row, so gamma and beta are read once and the column sums of
-// the backward stay in registers. V is 16 bytes when every tensor's rows are
-// whole aligned vectors, else one element.
+// its sums and its outputs. A lane holds E elements of a row (32 in the
+// forward over aligned rows, else 16: the backward's column sums take twice
+// that many registers), the same columns in every row, so gamma and beta are read once and
+// the column sums of the backward stay in registers. A row has L lanes: 1 ..
+// 32 of a warp (32 / L rows side by side), or a group of whole warps that meet
+// at a barrier of their own, several groups to a CTA; rows beyond 512 lanes'
+// worth take the kernels for long rows.
 #pragma once
 
-#include "dyt_kernels.cuh"
+#include "dyt_async.cuh"
 
 namespace dyt {
 namespace norm {
@@ -31,9 +32,11 @@ struct NormArgs {
   float *rstd;
   int64_t M;
   int64_t N;
-  int NV;  // vectors of a row
-  int L;   // lanes of a row (blockDim.x when a CTA has one row)
+  int NV;    // vectors of a row
+  int L;     // lanes of a row
+  int rows;  // rows side by side in a CTA
   int gamma_dt, beta_dt;
+  int64_t fast;  // ragged rows: [fast, M - fast) are copied in whole 16-byte chunks
   float eps;
 };
 
@@ -52,13 +55,423 @@ struct NormGradArgs {
   int64_t N;
   int NV;
   int L;
+  int rows;
   int gamma_dt;
+  int64_t fast;
 };
 
+constexpr int kBlock = 512;  // threads of a CTA, at most
+// Elements of a row a lane holds.
+__host__ __device__ constexpr int fwd_elems(bool ragged) { return ragged ? 16 : 32; }
+constexpr int kBwdElems = 16;
 // Rows a lane adds in binary32 before its column sums move to binary64: the
 // run's rounding is at most 128 * 2^-24 of the sum of its terms' magnitudes.
 constexpr int kRunRows = 128;
 constexpr int kMaxWarps = 32;
+
+// Where a thread stands: lane `lane` of the L that share row `mine` of the
+// CTA's rows; `seg` of those lanes are in this warp, this is number `at` of them.
+struct Place {
+  int L, lane, mine, seg, at;
+  __device__ __forceinline__ Place(int L_) : L(L_) {
+    const int t = (int)threadIdx.x;
+    if (L <= 32) {  // a power of two
+      seg = L;
+      lane = at = t & (L - 1);
+      mine = t / L;
+    } else {
+      seg = 32;
+      mine = t / L;
+      lane = t - mine * L;
+      at = t & 31;
+    }
+  }
+};
+
+// The column of a lane's element i of E. Aligned rows: vectors lane, lane + L,
+// ... of 16 bytes; ragged ones: single elements seg apart, within a stretch of
+// seg E columns that belongs to the lanes of one warp.
+template <int V, int E, bool RAGGED>
+__device__ __forceinline__ int column(int L, int lane, int i) {
+  if constexpr (RAGGED) return L <= 32 ? lane + i * L : (lane >> 5) * (32 * E) + (lane & 31) + i * 32;
+  else return (lane + i / V * L) * V + i % V;
+}
+
+// ---- parameters ------------------------------------------------------------------
+
+// gamma or beta at columns c0 .. c0 + V - 1 (a NULL parameter is `none`).
+template <int V>
+__device__ __forceinline__ void load_columns(const void *p, int dt, int64_t c0, float none, float (&out)[V]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = none;
+    return;
+  }
+  int64_t col[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) col[e] = c0 + e;
+  load_params<V, void>(p, dt, col, 1.0f, out);
+}
+
+// gamma or beta for a lane's elements, as pairs (0 past the row's end, where the
+// backward relies on it). All loads are under way before the first value is
+// used. Aligned rows with parameters on 16-byte boundaries take wide loads.
+template <int V, int E, bool RAGGED>
+__device__ __forceinline__ void load_pairs(const void *p, int dt, const Place &at, int N, float none,
+                                           float2 (&out)[E / 2]) {
+  float f[E];
+  if (p == nullptr) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[i] = none;
+  } else if (!RAGGED && ((uintptr_t)p & 15u) == 0) {
+    if (dt == DYT_F32) {
+      float4 q[E / 4];
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        const int c = column<V, E, RAGGED>(at.L, at.lane, 4 * i);
+        q[i] = __ldg(static_cast<const float4 *>(p) + (c < N ? c : 0) / 4);
+      }
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        f[4 * i] = q[i].x;
+        f[4 * i + 1] = q[i].y;
+        f[4 * i + 2] = q[i].z;
+        f[4 * i + 3] = q[i].w;
+      }
+    } else {
+      uint2 q[E / 4];
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        const int c = column<V, E, RAGGED>(at.L, at.lane, 4 * i);
+        q[i] = __ldg(static_cast<const uint2 *>(p) + (c < N ? c : 0) / 4);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const uint32_t w = i & 2 ? q[i / 4].y : q[i / 4].x, u = i & 1 ? w >> 16 : w & 0xFFFFu;
+        f[i] = dt == DYT_BF16 ? __uint_as_float(u << 16) : __half2float(__ushort_as_half((unsigned short)u));
+      }
+    }
+  } else {
+    int64_t col[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = column<V, E, RAGGED>(at.L, at.lane, i);
+      col[i] = c < N ? c : 0;
+    }
+    load_params<E, void>(p, dt, col, 1.0f, f);
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (column<V, E, RAGGED>(at.L, at.lane, i) >= N) f[i] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) out[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+
+// ---- row input and output ------------------------------------------------------------
+
+// 16-byte slots of a block's lanes for one row of one tensor; RAGGED: one more
+// for the lanes of each row in a warp.
+template <typename T, int E>
+__host__ __device__ constexpr int row_slots(int block, int L, bool ragged) {
+  return E * (int)sizeof(T) / 16 * block + (ragged ? block / 32 * (L < 32 ? 32 / L : 1) : 0);
+}
+
+// The rows ahead, S - 1 of them under way in a ring of shared memory
+// (asynchronous 16-byte copies), read in the order they were copied.
+//  - Aligned rows: a thread copies its own vectors and reads them back; no
+//    thread reads another's.
+//  - RAGGED (rows at any element offset, any N): the lanes of a warp copy the
+//    aligned 16-byte chunks that hold their stretch of the row, one more than
+//    its bytes fill, and read single elements at the row's own offset (neighbouring
+//    lanes read neighbouring elements: no bank conflict at any offset, and
+//    single-element stores coalesce in the same way). A copied chunk holds at
+//    least one byte of the row and up to 15 of those around it; the first and
+//    the last `fast` rows, where those may lie outside the tensor, are read from
+//    global memory by elements instead.
+template <typename T, int E, int TENSORS, int S, bool RAGGED>
+struct RowFeed {
+  static constexpr int V = 16 / (int)sizeof(T);
+  static constexpr int K = E / V;
+  unsigned char *mine;      // this thread's slots (RAGGED: its row's in this warp) of stage 0, tensor 0
+  int plane;                // bytes from one tensor's (and stage's) slots to the next
+  const char *at[TENSORS];  // this lane's first vector (RAGGED: its warp's stretch) in the next row to copy
+  int64_t inc[TENSORS];     // bytes to the row after it
+  int64_t row;              // the next row to copy
+  int need;                 // RAGGED: bytes of the row in this warp's stretch
+  int wr = 0, rd = 0;       // byte offsets of the stages to copy to and to read
+
+  __device__ __forceinline__ RowFeed(unsigned char *ring, const T *const (&base)[TENSORS],
+                                     const int64_t (&ld)[TENSORS], const Place &p, int N, int64_t first,
+                                     int64_t step) {
+    const int t = (int)threadIdx.x;
+    plane = row_slots<T, E>((int)blockDim.x, p.L, RAGGED) * 16;
+    const int c0 = RAGGED ? column<V, E, true>(p.L, p.lane - p.at, 0) : p.lane * V;
+    mine = ring + (RAGGED ? t / p.seg * (p.seg * K + 1) : t) * 16;
+    need = (N - c0 < p.seg * E ? N - c0 : p.seg * E) * (int)sizeof(T);
+    row = first;
+#pragma unroll
+    for (int i = 0; i < TENSORS; ++i) {
+      at[i] = reinterpret_cast<const char *>(base[i] + first * ld[i] + c0);
+      inc[i] = step * ld[i] * (int64_t)sizeof(T);
+    }
+    if constexpr (!RAGGED) {  // vectors past the row's end are never copied and stay 0
+      for (int i = 0; i < S * TENSORS; ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          *reinterpret_cast<uint4 *>(mine + i * plane + k * (int)blockDim.x * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
+  __device__ __forceinline__ void issue(const Place &p, int64_t M, int NV, int64_t fast, int64_t step) {
+    if (RAGGED ? row >= fast && row < M - fast : row < M) {
+#pragma unroll
+      for (int t = 0; t < TENSORS; ++t) {
+        unsigned char *s = mine + wr + t * plane;
+        if constexpr (!RAGGED) {
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+            if (p.lane + k * p.L < NV) cp_async16(s + k * (int)blockDim.x * 16, at[t] + (int64_t)(k * p.L) * 16);
+        } else {
+          const int d = (int)((uintptr_t)at[t] & 15u);
+          const char *q = at[t] - d;
+          const int end = need + d;  // chunks that start before this hold bytes of the row
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const int o = (p.at + k * p.seg) * 16;
+            if (o < end) cp_async16(s + o, q + o);
+          }
+          const int o = p.seg * K * 16;
+          if (p.at == 0 && o < end) cp_async16(s + o, q + o);
+        }
+      }
+    }
+    cp_async_commit();
+    wr = wr == (S - 1) * TENSORS * plane ? 0 : wr + TENSORS * plane;
+    row += step;
+#pragma unroll
+    for (int t = 0; t < TENSORS; ++t) at[t] += inc[t];
+  }
+
+  // The oldest row has landed.
+  __device__ __forceinline__ void wait() const {
+    cp_async_wait<S - 2>();
+    if constexpr (RAGGED) __syncwarp();
+  }
+
+  // A lane's elements of row r (the oldest one) of tensor t; 0 past its end.
+  __device__ __forceinline__ void read(int t, const T *base, int64_t ld, int64_t r, const Place &p, int64_t M, int N,
+                                       int64_t fast, float2 (&f)[E / 2]) const {
+    const unsigned char *s = mine + rd + t * plane;
+    if constexpr (!RAGGED) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        VecIO<T, V>::unpack2(*reinterpret_cast<const uint4 *>(s + k * (int)blockDim.x * 16),
+                             *reinterpret_cast<float2(*)[V / 2]>(f + k * (V / 2)));
+    } else {
+      const int c0 = column<V, E, true>(p.L, p.lane, 0), left = N - c0;  // element i is inside while i seg < left
+      T v[E];
+      if (r >= fast && r < M - fast) {
+        const int d = (int)((uint32_t)(uintptr_t)base + ((uint32_t)r * (uint32_t)ld + (uint32_t)(c0 - p.at)) *
+                                                            (uint32_t)sizeof(T)) & 15;
+        const T *e = reinterpret_cast<const T *>(s + d) + p.at;
+        if (need == p.seg * E * (int)sizeof(T)) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[i] = e[i * p.seg];
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[i] = i * p.seg < left ? e[i * p.seg] : from_f32<T>(0.0f);
+        }
+      } else {
+        const T *g = base + (r < M ? r * ld + c0 : 0);
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = r < M && i * p.seg < left ? g[i * p.seg] : from_f32<T>(0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) f[i] = make_float2(to_f32<T>(v[2 * i]), to_f32<T>(v[2 * i + 1]));
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    rd = rd == (S - 1) * TENSORS * plane ? 0 : rd + TENSORS * plane;
+  }
+};
+
+// A lane's outputs, rounded once to T, to the row that starts at `out`.
+template <typename T, int E, bool RAGGED>
+__device__ __forceinline__ void store_pairs(T *out, const float2 (&f)[E / 2], const Place &p, int NV, int N) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if constexpr (!RAGGED) {
+#pragma unroll
+    for (int k = 0; k < E / V; ++k)
+      if (p.lane + k * p.L < NV)
+        VecIO<T, V>::store_raw(out + (p.lane + k * p.L) * V,
+                               VecIO<T, V>::pack2(*reinterpret_cast<const float2(*)[V / 2]>(f + k * (V / 2))));
+  } else {
+    const int c0 = column<V, E, true>(p.L, p.lane, 0), left = N - c0;
+    T *o = out + c0;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i * p.seg < left) o[i * p.seg] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
+  }
+}
+
+// ---- sums over a row's lanes -------------------------------------------------------
+
+__device__ __forceinline__ void group_barrier(int group, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+}
+
+// Over `width` lanes of a warp: every lane gets the same bits.
+__device__ __forceinline__ float lanes_sum(float v, int width) {
+  for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Sums over a CTA (the kernels for long rows): one barrier; `red` may still be
+// read from the call before the last one.
+template <int C>
+__device__ __forceinline__ void cta_sum(float (&v)[C], float *red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int c = 0; c < C; ++c) v[c] = warp_sum(v[c]);
+  if (lane == 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) red[c * kMaxWarps + warp] = v[c];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < C; ++c) v[c] = warp_sum(lane < warps ? red[c * kMaxWarps + lane] : 0.0f);
+}
+
+// s / n for n = N: the product with 1 / n, corrected once (exact for a row of equal values).
+__device__ __forceinline__ float div_n(float s, float n, float inv_n) {
+  const float q = s * inv_n;
+  return fabsf(q) < __int_as_float(0x7F800000) ? fmaf(fmaf(-q, n, s), inv_n, q) : q;
+}
+
+// ---- forward: a row in registers ---------------------------------------------
+
+// Ring stages: enough rows ahead to cover the memory's latency.
+#ifndef FST
+#define FST (sizeof(T) == 4 ? 3 : 4)
+#endif
+template <typename T>
+__host__ __device__ constexpr int fwd_stages() {
+  return FST;
+}
+template <typename T>
+__host__ __device__ constexpr size_t fwd_smem(int block, int L, bool ragged) {
+  return (size_t)fwd_stages<T>() * (ragged ? row_slots<T, fwd_elems(true)>(block, L, true) : row_slots<T, fwd_elems(false)>(block, L, false)) * 16;
+}
+
+// GROUP: a row takes several warps. A warp sums its part of the row, then the
+// squares about that part's own mean, so that one exchange joins the parts:
+// M2 = sum_w (M2_w + n_w (mean_w - mean)^2), with no cancellation.
+template <typename T, bool GROUP, bool RAGGED>
+__global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
+  constexpr int V = 16 / (int)sizeof(T);
+  constexpr int E = fwd_elems(RAGGED), P = E / 2;
+  constexpr int S = fwd_stages<T>();
+  __shared__ float2 red[2][kBlock / 32];
+  extern __shared__ __align__(16) unsigned char dyn[];
+  pdl_prologue();
+  const Place p(a.L);
+  if (dynamic_smem_bytes() < fwd_smem<T>((int)blockDim.x, p.L, RAGGED)) return;
+  const int N = (int)a.N, NV = a.NV;
+  const T *const x[1] = {static_cast<const T *>(a.x)};
+  const int64_t ld[1] = {a.ldx};
+  const int64_t step = (int64_t)gridDim.x * a.rows;
+  int64_t r0 = (int64_t)blockIdx.x * a.rows;
+  RowFeed<T, E, 1, S, RAGGED> feed(dyn, x, ld, p, N, r0 + p.mine, step);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.M, NV, a.fast, step);
+  float2 gam[P], bet[P];
+  load_pairs<V, E, RAGGED>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
+  load_pairs<V, E, RAGGED>(a.beta, a.beta_dt, p, N, 0.0f, bet);
+  const float n = (float)N, inv_n = 1.0f / n;
+  // elements of the row in a warp: in this one, and (GROUP) in warp `wl` of the group
+  const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31, w0 = GROUP ? p.mine * warps : 0;
+  auto part = [&](int w) {
+    int c = 0;
+    if constexpr (RAGGED) {
+      c = min(max(N - w * 32 * E, 0), 32 * E);
+    } else {
+#pragma unroll
+      for (int k = 0; k < E / V; ++k) c += min(max(N - (w * 32 + k * p.L) * V, 0), 32 * V);
+    }
+    return (float)c;
+  };
+  const float nw = GROUP ? part(p.lane / 32) : n, inv_nw = 1.0f / nw;
+  const float nl = GROUP && wl < warps ? part(wl) : 1.0f, inv_nl = 1.0f / nl;
+  const bool full = N == p.L * E;  // no lane holds anything past the row's end
+  T *yr = static_cast<T *>(a.y) + (r0 + p.mine) * a.ldy;
+  int par = 0;
+  for (; r0 < a.M; r0 += step, par ^= 1, yr += step * a.ldy) {
+    const int64_t row = r0 + p.mine;
+    feed.wait();
+    float2 v[P];
+    feed.read(0, x[0], ld[0], row, p, a.M, N, a.fast, v);
+    feed.advance();
+    feed.issue(p, a.M, NV, a.fast, step);
+    float2 t0 = v[0], t1 = v[1];  // what lies past the row's end is zero
+#pragma unroll
+    for (int i = 2; i < P; i += 2) {
+      t0 = add2(t0, v[i]);
+      t1 = add2(t1, v[i + 1]);
+    }
+    t0 = add2(t0, t1);
+    float s = t0.x + t0.y;
+    s = GROUP ? warp_sum(s) : lanes_sum(s, p.L);
+    float mean = div_n(s, nw, inv_nw);
+    t0 = t1 = make_float2(0.0f, 0.0f);
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float2 c = add2(v[i], f2(-mean));
+        if (i & 1) t1 = fma2(c, c, t1);
+        else t0 = fma2(c, c, t0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        float2 c = add2(v[i], f2(-mean));
+        if (column<V, E, RAGGED>(p.L, p.lane, 2 * i) >= N) c.x = 0.0f;
+        if (column<V, E, RAGGED>(p.L, p.lane, 2 * i + 1) >= N) c.y = 0.0f;
+        if (i & 1) t1 = fma2(c, c, t1);
+        else t0 = fma2(c, c, t0);
+      }
+    }
+    t0 = add2(t0, t1);
+    float q = t0.x + t0.y;
+    q = GROUP ? warp_sum(q) : lanes_sum(q, p.L);
+    if constexpr (GROUP) {
+      if (wl == 0) red[par][w0 + p.lane / 32] = make_float2(s, q);
+      group_barrier(p.mine, p.L);
+      // up to 16 warps, one a lane: the lower half of this warp has them
+      const float2 o = wl < warps ? red[par][w0 + wl] : make_float2(0.0f, 0.0f);
+      mean = div_n(__shfl_sync(0xFFFFFFFFu, lanes_sum(o.x, 16), 0), n, inv_n);
+      const float e = wl < warps ? div_n(o.x, nl, inv_nl) - mean : 0.0f;
+      q = __shfl_sync(0xFFFFFFFFu, lanes_sum(fmaf(e * e, nl, o.y), 16), 0);
+    }
+    const float rstd = rsqrtf(fmaf(q, inv_n, a.eps));
+    if (row < a.M) {
+      if (p.lane == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = fma2(mul2(add2(v[i], f2(-mean)), f2(rstd)), gam[i], bet[i]);
+      store_pairs<T, E, RAGGED>(yr, v, p, NV, N);
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// ---- forward: rows too long for registers --------------------------------------
 
 // V elements of T at p as stored: one element or 16 bytes.
 template <typename T, int V>
@@ -84,135 +497,6 @@ __device__ __forceinline__ void store_row(T *p, const float (&f)[V]) {
   }
 }
 
-// gamma or beta at columns c0 .. c0 + V - 1 (a NULL parameter is `none`).
-template <int V>
-__device__ __forceinline__ void load_columns(const void *p, int dt, int64_t c0, float none, float (&out)[V]) {
-  if (p == nullptr) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) out[e] = none;
-    return;
-  }
-  int64_t col[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) col[e] = c0 + e;
-  load_params<V, void>(p, dt, col, 1.0f, out);
-}
-
-// Sums over the lanes of a row. Part of a warp: a butterfly, every lane gets
-// the same bits. A CTA: the warps' sums meet in shared memory (`red`, a buffer
-// that the call before the last one may still be read from), one barrier.
-template <bool CTA, int C>
-__device__ __forceinline__ void row_sum(float (&v)[C], int L, float *red) {
-  if constexpr (!CTA) {
-    for (int o = L >> 1; o > 0; o >>= 1) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) v[c] += __shfl_xor_sync(0xFFFFFFFFu, v[c], o);
-    }
-  } else {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) v[c] += __shfl_xor_sync(0xFFFFFFFFu, v[c], o);
-    }
-    if (lane == 0) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) red[c * kMaxWarps + warp] = v[c];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; ++c) v[c] = lane < warps ? red[c * kMaxWarps + lane] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) v[c] += __shfl_xor_sync(0xFFFFFFFFu, v[c], o);
-    }
-  }
-}
-
-// ---- forward: a row in registers ---------------------------------------------
-
-template <typename T, int V, int K, bool CTA>
-__global__ void __launch_bounds__(CTA ? 1024 : 256) norm_fwd_kernel(NormArgs a) {
-  using IO = VecIO<T, V>;
-  __shared__ float red[2][kMaxWarps];
-  pdl_prologue();
-  const int L = CTA ? (int)blockDim.x : a.L;
-  const int lane = CTA ? (int)threadIdx.x : (int)threadIdx.x & (L - 1);
-  const int rows = CTA ? 1 : (int)blockDim.x / L;
-  const int mine = CTA ? 0 : (int)threadIdx.x / L;
-  const T *x = static_cast<const T *>(a.x);
-  T *y = static_cast<T *>(a.y);
-  float gam[K][V], bet[K][V];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int cv = lane + k * L;
-    if (cv < a.NV) {
-      load_columns<V>(a.gamma, a.gamma_dt, (int64_t)cv * V, 1.0f, gam[k]);
-      load_columns<V>(a.beta, a.beta_dt, (int64_t)cv * V, 0.0f, bet[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) gam[k][e] = bet[k][e] = 0.0f;
-    }
-  }
-  const float inv_n = 1.0f / (float)a.N;
-  const int64_t step = (int64_t)gridDim.x * rows;
-  typename IO::Raw next[K];
-  auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int cv = lane + k * L;
-      next[k] = row < a.M && cv < a.NV ? load_row<T, V>(x + row * a.ldx + (int64_t)cv * V) : typename IO::Raw{};
-    }
-  };
-  int64_t r0 = (int64_t)blockIdx.x * rows;  // every thread of a CTA makes the same steps
-  fetch(r0 + mine);
-  for (; r0 < a.M; r0 += step) {
-    const int64_t row = r0 + mine;
-    float v[K][V];
-#pragma unroll
-    for (int k = 0; k < K; ++k) IO::unpack(next[k], v[k]);
-    fetch(row + step);
-    float s[1] = {0.0f};  // the vectors past a row's end are zero
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int e = 0; e < V; ++e) s[0] += v[k][e];
-    row_sum<CTA, 1>(s, L, red[0]);
-    const float mean = s[0] / (float)a.N;  // exact for a constant row
-    float q[1] = {0.0f};
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const bool in = lane + k * L < a.NV;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        v[k][e] = in ? v[k][e] - mean : 0.0f;
-        q[0] = fmaf(v[k][e], v[k][e], q[0]);
-      }
-    }
-    row_sum<CTA, 1>(q, L, red[1]);
-    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv_n, a.eps));
-    if (row < a.M) {
-      if (lane == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
-      }
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int cv = lane + k * L;
-        if (cv < a.NV) {
-          float o[V];
-#pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = fmaf(v[k][e] * rstd, gam[k][e], bet[k][e]);
-          store_row<T, V>(y + row * a.ldy + (int64_t)cv * V, o);
-        }
-      }
-    }
-  }
-}
-
-// ---- forward: rows too long for registers --------------------------------------
-
 // One CTA reads each row three times (the second and third time mostly from
 // L2): its sum, its centred squares, its outputs.
 template <typename T, int V>
@@ -233,7 +517,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < V; ++e) s[0] += v[e];
     }
-    row_sum<true, 1>(s, B, red[0]);
+    cta_sum(s, red[0]);
     const float mean = s[0] / (float)a.N;  // exact for a constant row
     float q[1] = {0.0f};
 #pragma unroll 4
@@ -243,7 +527,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < V; ++e) q[0] = fmaf(v[e] - mean, v[e] - mean, q[0]);
     }
-    row_sum<true, 1>(q, B, red[1]);
+    cta_sum(q, red[1]);
     const float rstd = 1.0f / sqrtf(fmaf(q[0], inv_n, a.eps));
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -263,151 +547,173 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormArgs a) {
 
 // ---- backward: a row in registers ------------------------------------------------
 
-// A lane's column sums of one run of rows, moved to the CTA's partial sums in
-// binary64 (added to them after the first run). Rows side by side in a warp
-// are added by a butterfly over the lanes that own the same columns, the warps
-// in order.
-template <int V, int K, bool CTA>
-__device__ __forceinline__ void flush_columns(const NormGradArgs &a, float (&dg)[K][V], float (&db)[K][V], int lane,
-                                              int L, bool first, float *sh) {
-  double *pg = a.parts + (int64_t)blockIdx.x * 2 * a.N, *pb = pg + a.N;
-  if constexpr (CTA) {
+#ifndef BST
+#define BST (sizeof(T) == 4 ? 3 : 5)
+#endif
+template <typename T>
+__host__ __device__ constexpr int bwd_stages() {
+  return BST;
+}
+// Dynamic shared memory: the ring, then 16 bytes' worth of column sums of every thread.
+template <typename T>
+__host__ __device__ constexpr size_t bwd_ring(int block, int L, bool ragged) {
+  return (size_t)bwd_stages<T>() * 2 * row_slots<T, kBwdElems>(block, L, ragged) * 16;
+}
+template <typename T>
+__host__ __device__ constexpr size_t bwd_smem(int block, int L, bool ragged) {
+  return bwd_ring<T>(block, L, ragged) + (size_t)block * (16 / sizeof(T)) * 2 * sizeof(float);
+}
+
+// The column sums of one run of rows, added over the CTA's rows in a fixed
+// order and moved to its partial sums in binary64 (added to them after the
+// first run). Rows side by side in a warp are added by a butterfly first; `sh`
+// then holds a copy per warp (rows within a warp) or per group, V elements of
+// every lane at a time.
+template <int V, int E, bool RAGGED>
+__device__ __forceinline__ void flush_columns(const NormGradArgs &a, float2 (&dg)[E / 2], float2 (&db)[E / 2],
+                                              const Place &p, bool first, float *sh) {
+  double *pg = a.parts + (int64_t)blockIdx.x * 2 * a.N;
+  const int N = (int)a.N;
+  const int copies = p.L <= 32 ? (int)blockDim.x / 32 : a.rows;
+  const int copy = p.L <= 32 ? (int)threadIdx.x >> 5 : p.mine;
+  const int width = p.L * V;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int cv = lane + k * L;
-      if (cv < a.NV) {
+  for (int k = 0; k < E / V; ++k) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int64_t c = (int64_t)cv * V + e;
-          pg[c] = first ? (double)dg[k][e] : pg[c] + (double)dg[k][e];
-          pb[c] = first ? (double)db[k][e] : pb[c] + (double)db[k][e];
-        }
+    for (int e = 0; e < V; ++e) {
+      const int i = (k * V + e) / 2;
+      float u = e & 1 ? dg[i].y : dg[i].x, w = e & 1 ? db[i].y : db[i].x;
+      for (int o = p.L; o < 32; o <<= 1) {
+        u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+        w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
       }
-    }
-  } else {
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int width = L * K * V;  // columns, padded
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float u = dg[k][e], w = db[k][e];
-        for (int o = L; o < 32; o <<= 1) {
-          u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-          w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
-        }
-        if ((threadIdx.x & 31) < L) {
-          const int c = (lane + k * L) * V + e;
-          sh[(warp * 2) * width + c] = u;
-          sh[(warp * 2 + 1) * width + c] = w;
-        }
+      if (p.L >= 32 || ((int)threadIdx.x & 31) < p.L) {
+        sh[(copy * 2) * width + e * p.L + p.lane] = u;
+        sh[(copy * 2 + 1) * width + e * p.L + p.lane] = w;
       }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * width; i += blockDim.x) {
-      const int which = i >= width, c = i - which * width;
-      if (c < a.N) {
+      const int which = i >= width, j = i - which * width, e = j / p.L;
+      const int c = column<V, E, RAGGED>(p.L, j - e * p.L, 0) + (RAGGED ? (k * V + e) * p.seg : k * width + e);
+      if (c < N) {
         double t = 0.0;
-        for (int w = 0; w < warps; ++w) t += (double)sh[(w * 2 + which) * width + c];
-        double *p = which ? pb : pg;
-        p[c] = first ? t : p[c] + t;
+        for (int w = 0; w < copies; ++w) t += (double)sh[(w * 2 + which) * width + j];
+        double *o = pg + (int64_t)which * a.N + c;
+        *o = first ? t : *o + t;
       }
     }
     __syncthreads();
   }
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int e = 0; e < V; ++e) dg[k][e] = db[k][e] = 0.0f;
+  for (int i = 0; i < E / 2; ++i) dg[i] = db[i] = make_float2(0.0f, 0.0f);
 }
 
-template <typename T, int V, int K, bool CTA>
-__global__ void __launch_bounds__(CTA ? 512 : 256) norm_bwd_kernel(NormGradArgs a) {
-  using IO = VecIO<T, V>;
-  __shared__ float red[2][2 * kMaxWarps];
-  extern __shared__ float sh[];  // rows side by side: [warp][dgamma, dbeta][L K V]
+// Two sums over a warp at once: the halves of the warp take one each (the upper
+// half the second), in every lane of the half.
+__device__ __forceinline__ float half_sums(float u, float w) {
+  const bool up = (threadIdx.x & 16) != 0;
+  float v = (up ? w : u) + __shfl_xor_sync(0xFFFFFFFFu, up ? u : w, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+__device__ __forceinline__ void swap_halves(float v, float &u, float &w) {
+  const bool up = (threadIdx.x & 16) != 0;
+  const float other = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+  u = up ? other : v;
+  w = up ? v : other;
+}
+
+template <typename T, bool GROUP, bool RAGGED>
+__global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
+  constexpr int V = 16 / (int)sizeof(T);
+  constexpr int E = kBwdElems, P = E / 2;
+  constexpr int S = bwd_stages<T>();
+  __shared__ float red[2][2 * kBlock / 32];
+  extern __shared__ __align__(16) unsigned char dyn[];
   pdl_prologue();
-  const int L = CTA ? (int)blockDim.x : a.L;
-  const int lane = CTA ? (int)threadIdx.x : (int)threadIdx.x & (L - 1);
-  const int rows = CTA ? 1 : (int)blockDim.x / L;
-  const int mine = CTA ? 0 : (int)threadIdx.x / L;
-  const T *x = static_cast<const T *>(a.x);
-  const T *dy = static_cast<const T *>(a.dy);
-  T *dx = static_cast<T *>(a.dx);
-  float gam[K][V], dg[K][V], db[K][V];
+  const Place p(a.L);
+  if (dynamic_smem_bytes() < bwd_smem<T>((int)blockDim.x, p.L, RAGGED)) return;
+  float *sh = reinterpret_cast<float *>(dyn + bwd_ring<T>((int)blockDim.x, p.L, RAGGED));
+  const int N = (int)a.N, NV = a.NV;
+  const T *const src[2] = {static_cast<const T *>(a.x), static_cast<const T *>(a.dy)};
+  const int64_t ld[2] = {a.ldx, a.lddy};
+  const int64_t step = (int64_t)gridDim.x * a.rows;
+  int64_t r0 = (int64_t)blockIdx.x * a.rows;
+  RowFeed<T, E, 2, S, RAGGED> feed(dyn, src, ld, p, N, r0 + p.mine, step);
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int cv = lane + k * L;
+  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.M, NV, a.fast, step);
+  // The next row's statistics, loaded one row ahead: rows past M take the last
+  // one's, so that nothing waits for the loads before the next row.
+  auto clamp = [&](int64_t r) { return r < a.M ? r : a.M - 1; };
+  float nmean = a.mean[clamp(r0 + p.mine)], nrstd = a.rstd[clamp(r0 + p.mine)];
+  float2 gam[P], dg[P], db[P];
+  load_pairs<V, E, RAGGED>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
 #pragma unroll
-    for (int e = 0; e < V; ++e) gam[k][e] = dg[k][e] = db[k][e] = 0.0f;
-    if (cv < a.NV) load_columns<V>(a.gamma, a.gamma_dt, (int64_t)cv * V, 1.0f, gam[k]);
-  }
-  const float inv_n = 1.0f / (float)a.N;
-  const int64_t step = (int64_t)gridDim.x * rows;
-  typename IO::Raw nx[K], nd[K];
-  float nmean = 0.0f, nrstd = 0.0f;
-  auto fetch = [&](int64_t row) {
-    const bool in = row < a.M;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int cv = lane + k * L;
-      nx[k] = in && cv < a.NV ? load_row<T, V>(x + row * a.ldx + (int64_t)cv * V) : typename IO::Raw{};
-      nd[k] = in && cv < a.NV ? load_row<T, V>(dy + row * a.lddy + (int64_t)cv * V) : typename IO::Raw{};
-    }
-    nmean = in ? a.mean[row] : 0.0f;
-    nrstd = in ? a.rstd[row] : 0.0f;
-  };
-  int64_t r0 = (int64_t)blockIdx.x * rows;
-  fetch(r0 + mine);
+  for (int i = 0; i < P; ++i) dg[i] = db[i] = make_float2(0.0f, 0.0f);
+  const float inv_n = 1.0f / (float)N;
+  const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31, w0 = GROUP ? p.mine * warps : 0;
+  T *out = static_cast<T *>(a.dx) + (r0 + p.mine) * a.lddx;
   bool first = true;
   int run = 0, par = 0;
-  for (; r0 < a.M; r0 += step) {
-    const int64_t row = r0 + mine;
-    float h[K][V], d[K][V];
-    const float mean = nmean, rstd = nrstd;
+  for (; r0 < a.M; r0 += step, par ^= 1, out += step * a.lddx) {
+    const int64_t row = r0 + p.mine;
+    const bool in = row < a.M;
+    const float mean = in ? nmean : 0.0f, rstd = in ? nrstd : 0.0f;
+    feed.wait();
+    float2 h[P], d[P];
+    feed.read(0, src[0], ld[0], row, p, a.M, N, a.fast, h);
+    feed.read(1, src[1], ld[1], row, p, a.M, N, a.fast, d);
+    feed.advance();
+    feed.issue(p, a.M, NV, a.fast, step);
+    nmean = a.mean[clamp(row + step)];
+    nrstd = a.rstd[clamp(row + step)];
+    if (!RAGGED && !in) {  // the slots hold an older row
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      IO::unpack(nx[k], h[k]);
-      IO::unpack(nd[k], d[k]);
+      for (int i = 0; i < P; ++i) h[i] = d[i] = make_float2(0.0f, 0.0f);
     }
-    fetch(row + step);
-    float c[2] = {0.0f, 0.0f};
+    // Past the row's end d and gamma are 0, so nothing there enters a sum that is used.
+    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const bool in = row < a.M && lane + k * L < a.NV;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        h[k][e] = in ? (h[k][e] - mean) * rstd : 0.0f;
-        dg[k][e] = fmaf(d[k][e], h[k][e], dg[k][e]);
-        db[k][e] += d[k][e];
-        const float g = gam[k][e] * d[k][e];
-        c[0] += g;
-        c[1] = fmaf(g, h[k][e], c[1]);
-        d[k][e] = g;
-      }
+    for (int i = 0; i < P; ++i) {
+      h[i] = mul2(add2(h[i], f2(-mean)), f2(rstd));
+      dg[i] = fma2(d[i], h[i], dg[i]);
+      db[i] = add2(db[i], d[i]);
+      d[i] = mul2(gam[i], d[i]);
+      s1 = add2(s1, d[i]);
+      s2 = fma2(d[i], h[i], s2);
     }
-    row_sum<CTA, 2>(c, L, red[par]);
-    par ^= 1;
-    const float c1 = c[0] * inv_n, c2 = c[1] * inv_n;
-    if (row < a.M) {
+    float c1 = s1.x + s1.y, c2 = s2.x + s2.y;
+    if constexpr (GROUP) {
+      float v = half_sums(c1, c2);
+      if ((wl & 15) == 0) red[par][2 * (w0 + p.lane / 32) + (wl >> 4)] = v;
+      group_barrier(p.mine, p.L);
+      v = (wl & 15) < warps ? red[par][2 * (w0 + (wl & 15)) + (wl >> 4)] : 0.0f;
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int cv = lane + k * L;
-        if (cv < a.NV) {
-          float o[V];
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      swap_halves(v, c1, c2);
+    } else if (p.L == 32) {
+      swap_halves(half_sums(c1, c2), c1, c2);
+    } else {
+      c1 = lanes_sum(c1, p.L);
+      c2 = lanes_sum(c2, p.L);
+    }
+    if (in) {
+      c1 *= inv_n;
+      c2 *= inv_n;
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = rstd * (d[k][e] - fmaf(h[k][e], c2, c1));
-          store_row<T, V>(dx + row * a.lddx + (int64_t)cv * V, o);
-        }
-      }
+      for (int i = 0; i < P; ++i) d[i] = mul2(f2(rstd), add2(d[i], fma2(h[i], f2(-c2), f2(-c1))));
+      store_pairs<T, E, RAGGED>(out, d, p, NV, N);
     }
     if (++run == kRunRows) {
-      flush_columns<V, K, CTA>(a, dg, db, lane, L, first, sh);
+      flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
       first = false;
       run = 0;
     }
   }
-  if (run > 0 || first) flush_columns<V, K, CTA>(a, dg, db, lane, L, first, sh);
+  if (run > 0 || first) flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
+  cp_async_wait<0>();
 }
 
 // ---- backward: rows too long for registers ------------------------------------------
@@ -438,7 +744,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_rows_kernel(NormGradArgs a, flo
         c[1] = fmaf(gd, (v[e] - mean) * rstd, c[1]);
       }
     }
-    row_sum<true, 2>(c, (int)blockDim.x, red[par]);
+    cta_sum(c, red[par]);
     if (threadIdx.x == 0) c12[row] = make_float2(c[0] * inv_n, c[1] * inv_n);
   }
 }
@@ -499,11 +805,11 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(NormGradArgs a, c
 
 // ---- backward: the parameters' gradients ---------------------------------------------
 
-constexpr int kSumCols = 32, kSumLanes = 8;
+constexpr int kSumCols = 32, kSumLanes = 16, kSumBatch = 10;
 
 // The CTAs' column sums added in binary64 in a fixed order (lane l takes
-// partials l, l + 8, ...; the lanes are added in order) and rounded once.
-// blockIdx.y: 0 = dgamma, 1 = dbeta.
+// partials l, l + 16, ..., ten loads under way at a time; the lanes are added
+// in order) and rounded once. blockIdx.y: 0 = dgamma, 1 = dbeta.
 __global__ void __launch_bounds__(kSumCols *kSumLanes)
     norm_finalize_kernel(const double *__restrict__ parts, int nparts, int64_t N, void *dgamma, int gamma_dt,
                          void *dbeta, int beta_dt) {
@@ -516,8 +822,16 @@ __global__ void __launch_bounds__(kSumCols *kSumLanes)
   double t = 0.0;
   if (col < N) {
     const double *p = parts + blockIdx.y * N + col;
-#pragma unroll 4
-    for (int i = lane; i < nparts; i += kSumLanes) t += p[(int64_t)i * 2 * N];
+    for (int i = lane; i < nparts; i += kSumLanes * kSumBatch) {
+      double v[kSumBatch];
+#pragma unroll
+      for (int b = 0; b < kSumBatch; ++b) {
+        const int j = i + b * kSumLanes;
+        v[b] = j < nparts ? p[(int64_t)j * 2 * N] : 0.0;
+      }
+#pragma unroll
+      for (int b = 0; b < kSumBatch; ++b) t += v[b];
+    }
   }
   sh[lane][c] = t;
   __syncthreads();

@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._rows import _code, _elsewhere, _like, _rows, _there, _vector, _workspace, row_pitch
+from ._rows import _code, _current, _elsewhere, _like, _pitch, _there, _vector, _workspace, row_pitch
 
 _F32 = (torch.float32,)
 _TOKEN = (torch.int64, torch.int32)
@@ -28,9 +28,11 @@ def _shape(logits: torch.Tensor) -> tuple[int, int]:
 
 def policy_loss_workspace(logits: torch.Tensor) -> torch.Tensor:
     """A device workspace large enough for policy_loss_forward on the logits' shape and device."""
+    if _elsewhere(logits, None):
+        with _there(logits, None):
+            return policy_loss_workspace(logits)
     M, N = _shape(logits)
-    with torch.cuda.device(logits.device):
-        n = _abi.dyt_policy_loss_workspace_bytes(M, N, _code(logits, "logits"))
+    n = _abi.lib.dyt_policy_loss_workspace_bytes(M, N, _code(logits, "logits"))
     return torch.empty(max(n, 16), dtype=torch.uint8, device=logits.device)
 
 
@@ -49,23 +51,22 @@ def policy_loss_forward(logits: torch.Tensor, tokens: torch.Tensor, old_logp: to
         with _there(logits, stream):
             return policy_loss_forward(logits, tokens, old_logp, advantage, ref_logp, weight, clip_low, clip_high,
                                        kl_coef, temperature, ws)
-    ld, code = _rows(logits, "logits"), _code(logits, "logits")
     M, N = _shape(logits)
-    dev, rows = logits.device, logits.shape[:-1]
+    ld, code, dev, rows = _pitch(logits, "logits"), _code(logits, "logits"), logits.device, logits.shape[:-1]
     ws = policy_loss_workspace(logits) if ws is None else ws
     loss = torch.empty((), dtype=torch.float32, device=dev)
-    logp = torch.empty(rows, dtype=torch.float32, device=dev)
+    logp, coef = torch.empty((2, *rows), dtype=torch.float32, device=dev).unbind(0)
     stats = torch.empty((*rows, 2), dtype=torch.float32, device=dev)
-    coef = torch.empty(rows, dtype=torch.float32, device=dev)
-    st = _abi.dyt_policy_loss_forward(
+    st = _abi.lib.dyt_policy_loss_forward(
         logits.data_ptr(), ld, _vector(tokens, "tokens", M, dev, _TOKEN), tokens.element_size(),
         _vector(old_logp, "old_logp", M, dev, _F32),
         None if ref_logp is None else _vector(ref_logp, "ref_logp", M, dev, _F32),
         _vector(advantage, "advantage", M, dev, _F32),
         None if weight is None else _vector(weight, "weight", M, dev, _F32), clip_low, clip_high, kl_coef,
         temperature, loss.data_ptr(), logp.data_ptr(), stats.data_ptr(), coef.data_ptr(), M, N, code,
-        _workspace(ws, dev), ws.numel(), torch.cuda.current_stream().cuda_stream)
-    _abi._check(st, "dyt_policy_loss_forward")
+        _workspace(ws, dev), ws.numel(), _current(dev.index))
+    if st:
+        _abi._check(st, "dyt_policy_loss_forward")
     return loss, logp, stats, coef
 
 
@@ -79,17 +80,19 @@ def policy_loss_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: torc
     if _elsewhere(logits, stream):
         with _there(logits, stream):
             return policy_loss_backward(logits, tokens, stats, coef, grad, temperature, dlogits)
-    ld, code = _rows(logits, "logits"), _code(logits, "logits")
     M, N = _shape(logits)
-    dev = logits.device
-    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev) if dlogits is None else dlogits
-    lddl = _like(dlogits, "dlogits", logits)
-    st = _abi.dyt_policy_loss_backward(
+    ld, code, dev = _pitch(logits, "logits"), _code(logits, "logits"), logits.device
+    if dlogits is None:
+        dlogits, lddl = torch.empty(logits.shape, dtype=logits.dtype, device=dev), N
+    else:
+        lddl = _like(dlogits, "dlogits", logits)
+    st = _abi.lib.dyt_policy_loss_backward(
         logits.data_ptr(), ld, _vector(tokens, "tokens", M, dev, _TOKEN), tokens.element_size(),
         _vector(stats, "stats", 2 * M, dev, _F32), _vector(coef, "coef", M, dev, _F32),
         None if grad is None else _vector(grad, "grad", 1, dev, _F32), temperature, dlogits.data_ptr(), lddl, M, N,
-        code, torch.cuda.current_stream().cuda_stream)
-    _abi._check(st, "dyt_policy_loss_backward")
+        code, _current(dev.index))
+    if st:
+        _abi._check(st, "dyt_policy_loss_backward")
     return dlogits
 
 

@@ -10,7 +10,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._rows import DTYPE_CODE, _code, _elsewhere, _like, _rows, _there, _vector, _workspace, row_pitch
+from ._rows import DTYPE_CODE, _code, _current, _elsewhere, _like, _pitch, _there, _vector, _workspace, row_pitch
 
 _F32 = (torch.float32,)
 _PARAM = tuple(DTYPE_CODE)
@@ -33,30 +33,38 @@ def layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, beta:
     if _elsewhere(x, stream):
         with _there(x, stream):
             return layer_norm_forward(x, gamma, beta, eps, out, mean, rstd)
-    ldx, code = _rows(x, "x"), _code(x, "x")
     M, N = _shape(x)
-    dev = x.device
+    ldx, code, dev = _pitch(x, "x"), _code(x, "x"), x.device
     gp = None if gamma is None else _vector(gamma, "gamma", N, dev, _PARAM)
     bp = None if beta is None else _vector(beta, "beta", N, dev, _PARAM)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-    ldy = _like(y, "out", x)
-    rows = x.shape[:-1]
-    mean = torch.empty(rows, dtype=torch.float32, device=dev) if mean is None else mean
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if rstd is None else rstd
-    st = _abi.dyt_layer_norm_forward(
-        x.data_ptr(), ldx, gp, bp, eps, y.data_ptr(), ldy, _vector(mean, "mean", mean.numel() if N == 0 else M, dev, _F32),
-        _vector(rstd, "rstd", rstd.numel() if N == 0 else M, dev, _F32), M, N, code,
+    if out is None:
+        y, ldy = torch.empty(x.shape, dtype=x.dtype, device=dev), N
+    else:
+        y, ldy = out, _like(out, "out", x)
+    if mean is None and rstd is None:
+        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
+    else:
+        rows = x.shape[:-1]
+        mean = torch.empty(rows, dtype=torch.float32, device=dev) if mean is None else mean
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev) if rstd is None else rstd
+        for t, what in ((mean, "mean"), (rstd, "rstd")):
+            _vector(t, what, rows.numel(), dev, _F32)
+    st = _abi.lib.dyt_layer_norm_forward(
+        x.data_ptr(), ldx, gp, bp, eps, y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(), M, N, code,
         code if gamma is None else DTYPE_CODE[gamma.dtype], code if beta is None else DTYPE_CODE[beta.dtype],
-        torch.cuda.current_stream().cuda_stream)
-    _abi._check(st, "dyt_layer_norm_forward")
+        _current(dev.index))
+    if st:
+        _abi._check(st, "dyt_layer_norm_forward")
     return y, mean, rstd
 
 
 def layer_norm_workspace(x: torch.Tensor) -> torch.Tensor:
     """A device workspace large enough for layer_norm_backward on x's shape and device."""
+    if _elsewhere(x, None):
+        with _there(x, None):
+            return layer_norm_workspace(x)
     M, N = _shape(x)
-    with torch.cuda.device(x.device):
-        n = _abi.dyt_layer_norm_backward_workspace_bytes(M, N, _code(x, "x"))
+    n = _abi.lib.dyt_layer_norm_backward_workspace_bytes(M, N, _code(x, "x"))
     return torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
 
 
@@ -72,30 +80,38 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
     if _elsewhere(x, stream):
         with _there(x, stream):
             return layer_norm_backward(x, dy, mean, rstd, gamma, beta, dx, dgamma, dbeta, ws)
-    ldx, code = _rows(x, "x"), _code(x, "x")
     M, N = _shape(x)
-    dev = x.device
+    ldx, code, dev = _pitch(x, "x"), _code(x, "x"), x.device
     lddy = _like(dy, "dy", x)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
-    lddx = _like(dx, "dx", x)
+    if dx is None:
+        dx, lddx = torch.empty(x.shape, dtype=x.dtype, device=dev), N
+    else:
+        lddx = _like(dx, "dx", x)
     gp = None if gamma is None else _vector(gamma, "gamma", N, dev, _PARAM)
     if beta is not None:
         _vector(beta, "beta", N, dev, _PARAM)
     if (gamma is None and dgamma is not None) or (beta is None and dbeta is not None):
         raise ValueError("dgamma and dbeta need their parameters")
+    gd = bd = code
+    gg = bg = None
     if gamma is not None:
-        dgamma = torch.empty_like(gamma) if dgamma is None else dgamma
+        gd = DTYPE_CODE[gamma.dtype]
+        if dgamma is None:
+            dgamma = torch.empty_like(gamma)
+        gg = _vector(dgamma, "dgamma", N, dev, (gamma.dtype,))
     if beta is not None:
-        dbeta = torch.empty_like(beta) if dbeta is None else dbeta
+        bd = DTYPE_CODE[beta.dtype]
+        if dbeta is None:
+            dbeta = torch.empty_like(beta)
+        bg = _vector(dbeta, "dbeta", N, dev, (beta.dtype,))
+    rows = x.shape[:-1].numel()
     ws = layer_norm_workspace(x) if ws is None else ws
-    st = _abi.dyt_layer_norm_backward(
-        x.data_ptr(), ldx, dy.data_ptr(), lddy, gp, _vector(mean, "mean", mean.numel() if N == 0 else M, dev, _F32),
-        _vector(rstd, "rstd", rstd.numel() if N == 0 else M, dev, _F32), dx.data_ptr(), lddx,
-        None if gamma is None else _vector(dgamma, "dgamma", N, dev, (gamma.dtype,)),
-        None if beta is None else _vector(dbeta, "dbeta", N, dev, (beta.dtype,)), M, N, code,
-        code if gamma is None else DTYPE_CODE[gamma.dtype], code if beta is None else DTYPE_CODE[beta.dtype],
-        _workspace(ws, dev), ws.numel(), torch.cuda.current_stream().cuda_stream)
-    _abi._check(st, "dyt_layer_norm_backward")
+    st = _abi.lib.dyt_layer_norm_backward(
+        x.data_ptr(), ldx, dy.data_ptr(), lddy, gp, _vector(mean, "mean", rows, dev, _F32),
+        _vector(rstd, "rstd", rows, dev, _F32), dx.data_ptr(), lddx, gg, bg, M, N, code, gd, bd, _workspace(ws, dev),
+        ws.numel(), _current(dev.index))
+    if st:
+        _abi._check(st, "dyt_layer_norm_backward")
     return dx, dgamma, dbeta
 
 
