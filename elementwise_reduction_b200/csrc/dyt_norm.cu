@@ -60,12 +60,25 @@ RowPlan plan_rows(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
   return p;
 }
 
-// Rows at the tensor's ends whose chunks could reach 16 bytes past it: those
-// less than 16 bytes from its first or its last row.
-int64_t ends(const int64_t *lds, int n, size_t elem) {
-  int64_t f = 0;
-  for (int i = 0; i < n; ++i) f = std::max(f, ceil_div(16, std::max<int64_t>(1, lds[i] * (int64_t)elem)));
-  return f;
+// The walk of `grid` CTAs over the rows of tensors with pitches lds (the inputs, then the output).
+dyt::norm::Walk walk_of(const RowPlan &p, int64_t M, int64_t N, int64_t grid, const int64_t *lds, int n, size_t elem,
+                        int plane_slots) {
+  dyt::norm::Walk w = {};
+  w.M = M;
+  w.N = N;
+  w.NV = p.NV;
+  w.L = p.L;
+  w.rows = p.rows;
+  w.step = (int)(grid * p.rows);
+  for (int i = 0; i < n; ++i) w.inc[i] = (int64_t)w.step * lds[i] * (int64_t)elem;
+  // Rows at the tensors' ends whose chunks could reach past them: those less
+  // than 16 bytes from the first or the last row.
+  if (p.ragged)
+    for (int i = 0; i + 1 < n; ++i) w.fast = std::max(w.fast, ceil_div(16, std::max<int64_t>(1, lds[i] * (int64_t)elem)));
+  w.plane = plane_slots * 16;
+  w.n = (float)N;
+  w.inv_n = 1.0f / (float)N;
+  return w;
 }
 
 template <typename T>
@@ -90,14 +103,16 @@ template <typename T>
 FwdKernel fwd_kernel(const RowPlan &p) {
   using namespace dyt::norm;
   if (p.rowlong) return p.V == 1 ? norm_fwd_long_kernel<T, 1> : norm_fwd_long_kernel<T, vec_elems<T>()>;
-  if (p.group) return p.ragged ? norm_fwd_kernel<T, true, true> : norm_fwd_kernel<T, true, false>;
-  return p.ragged ? norm_fwd_kernel<T, false, true> : norm_fwd_kernel<T, false, false>;
+  if (p.group) return p.ragged ? norm_fwd_kernel<T, kGroup, true> : norm_fwd_kernel<T, kGroup, false>;
+  if (p.L == 32) return p.ragged ? norm_fwd_kernel<T, kWarp, true> : norm_fwd_kernel<T, kWarp, false>;
+  return p.ragged ? norm_fwd_kernel<T, kPart, true> : norm_fwd_kernel<T, kPart, false>;
 }
 template <typename T>
 BwdKernel bwd_kernel(const RowPlan &p) {
   using namespace dyt::norm;
-  if (p.group) return p.ragged ? norm_bwd_kernel<T, true, true> : norm_bwd_kernel<T, true, false>;
-  return p.ragged ? norm_bwd_kernel<T, false, true> : norm_bwd_kernel<T, false, false>;
+  if (p.group) return p.ragged ? norm_bwd_kernel<T, kGroup, true> : norm_bwd_kernel<T, kGroup, false>;
+  if (p.L == 32) return p.ragged ? norm_bwd_kernel<T, kWarp, true> : norm_bwd_kernel<T, kWarp, false>;
+  return p.ragged ? norm_bwd_kernel<T, kPart, true> : norm_bwd_kernel<T, kPart, false>;
 }
 
 constexpr int kColumnsBlock = 256;  // vector-columns of a CTA in the long rows' second pass
@@ -177,15 +192,15 @@ dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma,
     using T = decltype(t);
     constexpr int VE = vec_elems<T>();
     const bool vec = N % VE == 0 && aligned16(x) && aligned16(y) && (M == 1 || (vec_pitch(ldx, es) && vec_pitch(ldy, es)));
-    const RowPlan p = plan_rows(M, N, VE, vec, dyt::norm::fwd_elems(!vec), sms);
+    const RowPlan p = plan_rows(M, N, VE, vec, dyt::norm::fwd_elems<T>(!vec), sms);
     const FwdKernel k = fwd_kernel<T>(p);
     const size_t smem = p.rowlong ? 0 : dyt::norm::fwd_smem<T>(p.block, p.L, p.ragged);
     const dyt_status s = prepare_smem(dev, (const void *)k, (int)smem);
     if (s != DYT_OK) return s;
     const int64_t grid = std::min<int64_t>(ceil_div(M, p.rows), (int64_t)sms);
-    const int64_t lds[1] = {ldx};
-    const NormArgs a = {x, ldx, gamma, beta, y, ldy, mean, rstd, M, N, p.NV, p.L, p.rows, (int)gamma_dtype,
-                        (int)beta_dtype, p.ragged ? ends(lds, 1, es) : 0, eps};
+    const int64_t lds[2] = {ldx, ldy};
+    NormArgs a = {x, ldx, gamma, beta, y, ldy, mean, rstd, (int)gamma_dtype, (int)beta_dtype, eps, {}};
+    a.w = walk_of(p, M, N, grid, lds, 2, es, p.rowlong ? 0 : dyt::norm::fwd_plane<T>(p.block, p.L, p.ragged));
     PdlConfig lc((unsigned)grid, p.block, smem, (cudaStream_t)stream);
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -242,9 +257,10 @@ dyt_status dyt_layer_norm_backward(const void *x, int64_t ldx, const void *dy, i
     const BwdPlan b = plan_bwd(M, N, VE, vec, sms);
     if (workspace_bytes < b.bytes) return DYT_ERR_WORKSPACE_TOO_SMALL;
     double *parts = (double *)workspace;
-    const int64_t lds[2] = {ldx, lddy};
-    const NormGradArgs a = {x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, parts, M, N, b.r.NV, b.r.L, b.r.rows,
-                            (int)gamma_dtype, b.r.ragged ? ends(lds, 2, es) : 0};
+    const int64_t lds[3] = {ldx, lddy, lddx};
+    NormGradArgs a = {x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, parts, (int)gamma_dtype, {}};
+    a.w = walk_of(b.r, M, N, b.grid, lds, 3, es,
+                  b.r.rowlong ? 0 : dyt::norm::row_slots<T, dyt::norm::kBwdElems>(b.r.block, b.r.L, b.r.ragged));
     int kernels = 2;
     cudaError_t e;
     if (b.r.rowlong) {

@@ -8,8 +8,8 @@
 //
 // Both are bound by memory: a row is read once and kept in registers between
 // its sums and its outputs. A lane holds E elements of a row (32 in the
-// forward over aligned rows, else 16: the backward's column sums take twice
-// that many registers), the same columns in every row, so gamma and beta are read once and
+// forward over aligned 16-bit rows, else 16: the backward's column sums take
+// twice that many registers), the same columns in every row, so gamma and beta are read once and
 // the column sums of the backward stay in registers. A row has L lanes: 1 ..
 // 32 of a warp (32 / L rows side by side), or a group of whole warps that meet
 // at a barrier of their own, several groups to a CTA; rows beyond 512 lanes'
@@ -21,6 +21,21 @@
 namespace dyt {
 namespace norm {
 
+// How a launch walks the rows: the CTAs' rows side by side, `step` rows further
+// at every step. Computed on the host so that the loops keep it out of registers.
+struct Walk {
+  int64_t M;
+  int64_t N;
+  int NV;        // vectors of a row (elements, for ragged rows)
+  int L;         // lanes of a row
+  int rows;      // rows side by side in a CTA
+  int step;      // grid x rows
+  int64_t inc[3];  // bytes from a row to the one a step later: the inputs, the output
+  int64_t fast;  // ragged rows: [fast, M - fast) are copied in whole 16-byte chunks
+  int plane;     // bytes of a tensor's row in the ring, for the whole block
+  float n, inv_n;
+};
+
 struct NormArgs {
   const void *x;
   int64_t ldx;
@@ -30,14 +45,9 @@ struct NormArgs {
   int64_t ldy;
   float *mean;  // NULL: not written
   float *rstd;
-  int64_t M;
-  int64_t N;
-  int NV;    // vectors of a row
-  int L;     // lanes of a row
-  int rows;  // rows side by side in a CTA
   int gamma_dt, beta_dt;
-  int64_t fast;  // ragged rows: [fast, M - fast) are copied in whole 16-byte chunks
   float eps;
+  Walk w;
 };
 
 struct NormGradArgs {
@@ -51,50 +61,52 @@ struct NormGradArgs {
   void *dx;
   int64_t lddx;
   double *parts;  // [CTA][dgamma, dbeta][N] column sums
-  int64_t M;
-  int64_t N;
-  int NV;
-  int L;
-  int rows;
   int gamma_dt;
-  int64_t fast;
+  Walk w;
 };
 
 constexpr int kBlock = 512;  // threads of a CTA, at most
 // Elements of a row a lane holds.
-__host__ __device__ constexpr int fwd_elems(bool ragged) { return ragged ? 16 : 32; }
+template <typename T>
+__host__ __device__ constexpr int fwd_elems(bool ragged) {
+  return ragged || sizeof(T) == 4 ? 16 : 32;
+}
 constexpr int kBwdElems = 16;
 // Rows a lane adds in binary32 before its column sums move to binary64: the
 // run's rounding is at most 128 * 2^-24 of the sum of its terms' magnitudes.
 constexpr int kRunRows = 128;
 constexpr int kMaxWarps = 32;
 
+// How many lanes share a row: less than a warp (a power of two), a warp, or a group of warps.
+enum RowMode { kPart = 0, kWarp = 1, kGroup = 2 };
+
 // Where a thread stands: lane `lane` of the L that share row `mine` of the
-// CTA's rows; `seg` of those lanes are in this warp, this is number `at` of them.
+// CTA's rows; seg() of those lanes are in this warp, this is number `at` of them.
+template <int MODE>
 struct Place {
-  int L, lane, mine, seg, at;
-  __device__ __forceinline__ Place(int L_) : L(L_) {
+  int L, lane, mine, at;
+  __device__ __forceinline__ Place(int L_) : L(MODE == kWarp ? 32 : L_) {
     const int t = (int)threadIdx.x;
-    if (L <= 32) {  // a power of two
-      seg = L;
-      lane = at = t & (L - 1);
-      mine = t / L;
-    } else {
-      seg = 32;
+    if constexpr (MODE == kGroup) {
       mine = t / L;
       lane = t - mine * L;
       at = t & 31;
+    } else {
+      lane = at = t & (L - 1);
+      mine = MODE == kWarp ? t >> 5 : t / L;
     }
   }
+  __device__ __forceinline__ int seg() const { return MODE == kPart ? L : 32; }
 };
 
 // The column of a lane's element i of E. Aligned rows: vectors lane, lane + L,
 // ... of 16 bytes; ragged ones: single elements seg apart, within a stretch of
 // seg E columns that belongs to the lanes of one warp.
-template <int V, int E, bool RAGGED>
+template <int V, int E, bool RAGGED, int MODE>
 __device__ __forceinline__ int column(int L, int lane, int i) {
-  if constexpr (RAGGED) return L <= 32 ? lane + i * L : (lane >> 5) * (32 * E) + (lane & 31) + i * 32;
-  else return (lane + i / V * L) * V + i % V;
+  if constexpr (!RAGGED) return (lane + i / V * L) * V + i % V;
+  else if constexpr (MODE == kGroup) return (lane >> 5) * (32 * E) + (lane & 31) + i * 32;
+  else return lane + i * (MODE == kWarp ? 32 : L);
 }
 
 // ---- parameters ------------------------------------------------------------------
@@ -116,8 +128,8 @@ __device__ __forceinline__ void load_columns(const void *p, int dt, int64_t c0, 
 // gamma or beta for a lane's elements, as pairs (0 past the row's end, where the
 // backward relies on it). All loads are under way before the first value is
 // used. Aligned rows with parameters on 16-byte boundaries take wide loads.
-template <int V, int E, bool RAGGED>
-__device__ __forceinline__ void load_pairs(const void *p, int dt, const Place &at, int N, float none,
+template <int V, int E, bool RAGGED, int MODE>
+__device__ __forceinline__ void load_pairs(const void *p, int dt, const Place<MODE> &at, int N, float none,
                                            float2 (&out)[E / 2]) {
   float f[E];
   if (p == nullptr) {
@@ -128,7 +140,7 @@ __device__ __forceinline__ void load_pairs(const void *p, int dt, const Place &a
       float4 q[E / 4];
 #pragma unroll
       for (int i = 0; i < E / 4; ++i) {
-        const int c = column<V, E, RAGGED>(at.L, at.lane, 4 * i);
+        const int c = column<V, E, RAGGED, MODE>(at.L, at.lane, 4 * i);
         q[i] = __ldg(static_cast<const float4 *>(p) + (c < N ? c : 0) / 4);
       }
 #pragma unroll
@@ -142,7 +154,7 @@ __device__ __forceinline__ void load_pairs(const void *p, int dt, const Place &a
       uint2 q[E / 4];
 #pragma unroll
       for (int i = 0; i < E / 4; ++i) {
-        const int c = column<V, E, RAGGED>(at.L, at.lane, 4 * i);
+        const int c = column<V, E, RAGGED, MODE>(at.L, at.lane, 4 * i);
         q[i] = __ldg(static_cast<const uint2 *>(p) + (c < N ? c : 0) / 4);
       }
 #pragma unroll
@@ -155,14 +167,14 @@ __device__ __forceinline__ void load_pairs(const void *p, int dt, const Place &a
     int64_t col[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = column<V, E, RAGGED>(at.L, at.lane, i);
+      const int c = column<V, E, RAGGED, MODE>(at.L, at.lane, i);
       col[i] = c < N ? c : 0;
     }
     load_params<E, void>(p, dt, col, 1.0f, f);
   }
 #pragma unroll
   for (int i = 0; i < E; ++i)
-    if (column<V, E, RAGGED>(at.L, at.lane, i) >= N) f[i] = 0.0f;
+    if (column<V, E, RAGGED, MODE>(at.L, at.lane, i) >= N) f[i] = 0.0f;
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) out[i] = make_float2(f[2 * i], f[2 * i + 1]);
 }
@@ -188,68 +200,60 @@ __host__ __device__ constexpr int row_slots(int block, int L, bool ragged) {
 //    least one byte of the row and up to 15 of those around it; the first and
 //    the last `fast` rows, where those may lie outside the tensor, are read from
 //    global memory by elements instead.
-template <typename T, int E, int TENSORS, int S, bool RAGGED>
+template <typename T, int E, int TENSORS, int S, bool RAGGED, int MODE>
 struct RowFeed {
   static constexpr int V = 16 / (int)sizeof(T);
   static constexpr int K = E / V;
   unsigned char *mine;      // this thread's slots (RAGGED: its row's in this warp) of stage 0, tensor 0
-  int plane;                // bytes from one tensor's (and stage's) slots to the next
   const char *at[TENSORS];  // this lane's first vector (RAGGED: its warp's stretch) in the next row to copy
-  int64_t inc[TENSORS];     // bytes to the row after it
-  int64_t row;              // the next row to copy
   int need;                 // RAGGED: bytes of the row in this warp's stretch
   int wr = 0, rd = 0;       // byte offsets of the stages to copy to and to read
 
   __device__ __forceinline__ RowFeed(unsigned char *ring, const T *const (&base)[TENSORS],
-                                     const int64_t (&ld)[TENSORS], const Place &p, int N, int64_t first,
-                                     int64_t step) {
-    const int t = (int)threadIdx.x;
-    plane = row_slots<T, E>((int)blockDim.x, p.L, RAGGED) * 16;
-    const int c0 = RAGGED ? column<V, E, true>(p.L, p.lane - p.at, 0) : p.lane * V;
-    mine = ring + (RAGGED ? t / p.seg * (p.seg * K + 1) : t) * 16;
-    need = (N - c0 < p.seg * E ? N - c0 : p.seg * E) * (int)sizeof(T);
-    row = first;
+                                     const int64_t (&ld)[TENSORS], const Place<MODE> &p, const Walk &w,
+                                     int64_t first) {
+    const int t = (int)threadIdx.x, N = (int)w.N;
+    const int c0 = RAGGED ? column<V, E, true, MODE>(p.L, p.lane - p.at, 0) : p.lane * V;
+    mine = ring + (RAGGED ? t / p.seg() * (p.seg() * K + 1) : t) * 16;
+    need = (N - c0 < p.seg() * E ? N - c0 : p.seg() * E) * (int)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < TENSORS; ++i) {
-      at[i] = reinterpret_cast<const char *>(base[i] + first * ld[i] + c0);
-      inc[i] = step * ld[i] * (int64_t)sizeof(T);
-    }
+    for (int i = 0; i < TENSORS; ++i) at[i] = reinterpret_cast<const char *>(base[i] + first * ld[i] + c0);
     if constexpr (!RAGGED) {  // vectors past the row's end are never copied and stay 0
       for (int i = 0; i < S * TENSORS; ++i)
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          *reinterpret_cast<uint4 *>(mine + i * plane + k * (int)blockDim.x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4 *>(mine + i * w.plane + k * (int)blockDim.x * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
   }
 
-  __device__ __forceinline__ void issue(const Place &p, int64_t M, int NV, int64_t fast, int64_t step) {
-    if (RAGGED ? row >= fast && row < M - fast : row < M) {
+  // Starts the copies of the next row: in: there is one; row: which (RAGGED).
+  __device__ __forceinline__ void issue(const Place<MODE> &p, const Walk &w, bool in, int64_t row) {
+    if (RAGGED ? row >= w.fast && row < w.M - w.fast : in) {
 #pragma unroll
       for (int t = 0; t < TENSORS; ++t) {
-        unsigned char *s = mine + wr + t * plane;
+        unsigned char *s = mine + wr + t * w.plane;
         if constexpr (!RAGGED) {
 #pragma unroll
           for (int k = 0; k < K; ++k)
-            if (p.lane + k * p.L < NV) cp_async16(s + k * (int)blockDim.x * 16, at[t] + (int64_t)(k * p.L) * 16);
+            if (p.lane + k * p.L < w.NV) cp_async16(s + k * (int)blockDim.x * 16, at[t] + (int64_t)(k * p.L) * 16);
         } else {
           const int d = (int)((uintptr_t)at[t] & 15u);
           const char *q = at[t] - d;
           const int end = need + d;  // chunks that start before this hold bytes of the row
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            const int o = (p.at + k * p.seg) * 16;
+            const int o = (p.at + k * p.seg()) * 16;
             if (o < end) cp_async16(s + o, q + o);
           }
-          const int o = p.seg * K * 16;
+          const int o = p.seg() * K * 16;
           if (p.at == 0 && o < end) cp_async16(s + o, q + o);
         }
       }
     }
     cp_async_commit();
-    wr = wr == (S - 1) * TENSORS * plane ? 0 : wr + TENSORS * plane;
-    row += step;
+    wr = wr == (S - 1) * TENSORS * w.plane ? 0 : wr + TENSORS * w.plane;
 #pragma unroll
-    for (int t = 0; t < TENSORS; ++t) at[t] += inc[t];
+    for (int t = 0; t < TENSORS; ++t) at[t] += w.inc[t];
   }
 
   // The oldest row has landed.
@@ -259,45 +263,48 @@ struct RowFeed {
   }
 
   // A lane's elements of row r (the oldest one) of tensor t; 0 past its end.
-  __device__ __forceinline__ void read(int t, const T *base, int64_t ld, int64_t r, const Place &p, int64_t M, int N,
-                                       int64_t fast, float2 (&f)[E / 2]) const {
-    const unsigned char *s = mine + rd + t * plane;
+  __device__ __forceinline__ void read(int t, const T *base, int64_t ld, int64_t r, const Place<MODE> &p, const Walk &w,
+                                       float2 (&f)[E / 2]) const {
+    const int N = (int)w.N;
+    const unsigned char *s = mine + rd + t * w.plane;
     if constexpr (!RAGGED) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
         VecIO<T, V>::unpack2(*reinterpret_cast<const uint4 *>(s + k * (int)blockDim.x * 16),
                              *reinterpret_cast<float2(*)[V / 2]>(f + k * (V / 2)));
     } else {
-      const int c0 = column<V, E, true>(p.L, p.lane, 0), left = N - c0;  // element i is inside while i seg < left
+      const int c0 = column<V, E, true, MODE>(p.L, p.lane, 0), left = N - c0;  // element i is inside while i seg < left
       T v[E];
-      if (r >= fast && r < M - fast) {
+      if (r >= w.fast && r < w.M - w.fast) {
         const int d = (int)((uint32_t)(uintptr_t)base + ((uint32_t)r * (uint32_t)ld + (uint32_t)(c0 - p.at)) *
                                                             (uint32_t)sizeof(T)) & 15;
         const T *e = reinterpret_cast<const T *>(s + d) + p.at;
-        if (need == p.seg * E * (int)sizeof(T)) {
+        if (need == p.seg() * E * (int)sizeof(T)) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) v[i] = e[i * p.seg];
+          for (int i = 0; i < E; ++i) v[i] = e[i * p.seg()];
         } else {
 #pragma unroll
-          for (int i = 0; i < E; ++i) v[i] = i * p.seg < left ? e[i * p.seg] : from_f32<T>(0.0f);
+          for (int i = 0; i < E; ++i) v[i] = i * p.seg() < left ? e[i * p.seg()] : from_f32<T>(0.0f);
         }
       } else {
-        const T *g = base + (r < M ? r * ld + c0 : 0);
+        const T *g = base + (r < w.M ? r * ld + c0 : 0);
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = r < M && i * p.seg < left ? g[i * p.seg] : from_f32<T>(0.0f);
+        for (int i = 0; i < E; ++i) v[i] = r < w.M && i * p.seg() < left ? g[i * p.seg()] : from_f32<T>(0.0f);
       }
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) f[i] = make_float2(to_f32<T>(v[2 * i]), to_f32<T>(v[2 * i + 1]));
     }
   }
-  __device__ __forceinline__ void advance() {
-    rd = rd == (S - 1) * TENSORS * plane ? 0 : rd + TENSORS * plane;
+  __device__ __forceinline__ void advance(const Walk &w) {
+    rd = rd == (S - 1) * TENSORS * w.plane ? 0 : rd + TENSORS * w.plane;
   }
 };
 
-// A lane's outputs, rounded once to T, to the row that starts at `out`.
-template <typename T, int E, bool RAGGED>
-__device__ __forceinline__ void store_pairs(T *out, const float2 (&f)[E / 2], const Place &p, int NV, int N) {
+// A lane's outputs, rounded once to T, to the row that starts at `out`. full:
+// no lane of the warp holds anything past the row's end.
+template <typename T, int E, bool RAGGED, int MODE>
+__device__ __forceinline__ void store_pairs(T *out, const float2 (&f)[E / 2], const Place<MODE> &p, int NV, int N,
+                                            bool full) {
   constexpr int V = 16 / (int)sizeof(T);
   if constexpr (!RAGGED) {
 #pragma unroll
@@ -306,12 +313,22 @@ __device__ __forceinline__ void store_pairs(T *out, const float2 (&f)[E / 2], co
         VecIO<T, V>::store_raw(out + (p.lane + k * p.L) * V,
                                VecIO<T, V>::pack2(*reinterpret_cast<const float2(*)[V / 2]>(f + k * (V / 2))));
   } else {
-    const int c0 = column<V, E, true>(p.L, p.lane, 0), left = N - c0;
+    const int c0 = column<V, E, true, MODE>(p.L, p.lane, 0), left = N - c0;
     T *o = out + c0;
+    if (full) {
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i * p.seg < left) o[i * p.seg] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
+      for (int i = 0; i < E; ++i) o[i * p.seg()] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (i * p.seg() < left) o[i * p.seg()] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
+    }
   }
+}
+
+// Rows first, first + step, ... below M.
+__device__ __forceinline__ int row_count(int64_t M, int64_t first, int step) {
+  return first < M ? (int)((M - first + step - 1) / step) : 0;
 }
 
 // ---- sums over a row's lanes -------------------------------------------------------
@@ -357,43 +374,64 @@ __device__ __forceinline__ float div_n(float s, float n, float inv_n) {
 
 // Ring stages: enough rows ahead to cover the memory's latency.
 #ifndef FST
-#define FST (sizeof(T) == 4 ? 3 : 4)
+#define FST 4
 #endif
 template <typename T>
 __host__ __device__ constexpr int fwd_stages() {
   return FST;
 }
+// 32 elements a lane with gamma and beta in registers spill: beta stays in shared memory then.
+template <typename T>
+__host__ __device__ constexpr bool fwd_beta_shared(bool ragged) {
+  return fwd_elems<T>(ragged) == 32;
+}
+template <typename T>
+__host__ __device__ constexpr int fwd_plane(int block, int L, bool ragged) {
+  return ragged ? row_slots<T, fwd_elems<T>(true)>(block, L, true) : row_slots<T, fwd_elems<T>(false)>(block, L, false);
+}
 template <typename T>
 __host__ __device__ constexpr size_t fwd_smem(int block, int L, bool ragged) {
-  return (size_t)fwd_stages<T>() * (ragged ? row_slots<T, fwd_elems(true)>(block, L, true) : row_slots<T, fwd_elems(false)>(block, L, false)) * 16;
+  return (size_t)fwd_stages<T>() * fwd_plane<T>(block, L, ragged) * 16 +
+         (fwd_beta_shared<T>(ragged) ? (size_t)block * fwd_elems<T>(ragged) * sizeof(float) : 0);
 }
 
 // GROUP: a row takes several warps. A warp sums its part of the row, then the
 // squares about that part's own mean, so that one exchange joins the parts:
 // M2 = sum_w (M2_w + n_w (mean_w - mean)^2), with no cancellation.
-template <typename T, bool GROUP, bool RAGGED>
+template <typename T, int MODE, bool RAGGED>
 __global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
+  constexpr bool GROUP = MODE == kGroup;
   constexpr int V = 16 / (int)sizeof(T);
-  constexpr int E = fwd_elems(RAGGED), P = E / 2;
+  constexpr int E = fwd_elems<T>(RAGGED), P = E / 2;
   constexpr int S = fwd_stages<T>();
-  __shared__ float2 red[2][kBlock / 32];
+  __shared__ float4 red[2][kBlock / 32];
   extern __shared__ __align__(16) unsigned char dyn[];
   pdl_prologue();
-  const Place p(a.L);
+  const Place<MODE> p(a.w.L);
   if (dynamic_smem_bytes() < fwd_smem<T>((int)blockDim.x, p.L, RAGGED)) return;
-  const int N = (int)a.N, NV = a.NV;
+  const int N = (int)a.w.N;
   const T *const x[1] = {static_cast<const T *>(a.x)};
   const int64_t ld[1] = {a.ldx};
-  const int64_t step = (int64_t)gridDim.x * a.rows;
-  int64_t r0 = (int64_t)blockIdx.x * a.rows;
-  RowFeed<T, E, 1, S, RAGGED> feed(dyn, x, ld, p, N, r0 + p.mine, step);
+  const int64_t r0 = (int64_t)blockIdx.x * a.w.rows;
+  int64_t row = r0 + p.mine;
+  const int steps = row_count(a.w.M, r0, a.w.step), left = row_count(a.w.M, row, a.w.step);  // the CTA's, this row's
+  RowFeed<T, E, 1, S, RAGGED, MODE> feed(dyn, x, ld, p, a.w, row);
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.M, NV, a.fast, step);
-  float2 gam[P], bet[P];
-  load_pairs<V, E, RAGGED>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
-  load_pairs<V, E, RAGGED>(a.beta, a.beta_dt, p, N, 0.0f, bet);
-  const float n = (float)N, inv_n = 1.0f / n;
+  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.w, i < left, row + (int64_t)i * a.w.step);
+  constexpr bool BS = fwd_beta_shared<T>(RAGGED);
+  float4 *bslot = reinterpret_cast<float4 *>(dyn + S * a.w.plane) + threadIdx.x;  // this thread's own
+  float2 gam[P], bet[BS ? 1 : P];
+  if constexpr (BS) {
+    load_pairs<V, E, RAGGED, MODE>(a.beta, a.beta_dt, p, N, 0.0f, gam);
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i)
+      bslot[i * blockDim.x] = make_float4(gam[2 * i].x, gam[2 * i].y, gam[2 * i + 1].x, gam[2 * i + 1].y);
+  } else {
+    load_pairs<V, E, RAGGED, MODE>(a.beta, a.beta_dt, p, N, 0.0f, bet);
+  }
+  load_pairs<V, E, RAGGED, MODE>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
   // elements of the row in a warp: in this one, and (GROUP) in warp `wl` of the group
+  const float n = a.w.n, inv_n = a.w.inv_n;
   const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31, w0 = GROUP ? p.mine * warps : 0;
   auto part = [&](int w) {
     int c = 0;
@@ -406,17 +444,18 @@ __global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
     return (float)c;
   };
   const float nw = GROUP ? part(p.lane / 32) : n, inv_nw = 1.0f / nw;
-  const float nl = GROUP && wl < warps ? part(wl) : 1.0f, inv_nl = 1.0f / nl;
-  const bool full = N == p.L * E;  // no lane holds anything past the row's end
-  T *yr = static_cast<T *>(a.y) + (r0 + p.mine) * a.ldy;
-  int par = 0;
-  for (; r0 < a.M; r0 += step, par ^= 1, yr += step * a.ldy) {
-    const int64_t row = r0 + p.mine;
+  const float nl = GROUP && wl < warps ? part(wl) : 0.0f;
+  // no lane of the warp holds anything past the row's end
+  const bool full = RAGGED ? feed.need == p.seg() * E * (int)sizeof(T) : N == p.L * E;
+  char *out = reinterpret_cast<char *>(static_cast<T *>(a.y) + row * a.ldy);
+#pragma unroll 1
+  for (int it = 0; it < steps; ++it) {
+    const int par = it & 1;
     feed.wait();
     float2 v[P];
-    feed.read(0, x[0], ld[0], row, p, a.M, N, a.fast, v);
-    feed.advance();
-    feed.issue(p, a.M, NV, a.fast, step);
+    feed.read(0, x[0], ld[0], row, p, a.w, v);
+    feed.advance(a.w);
+    feed.issue(p, a.w, it + S - 1 < left, row + (int64_t)(S - 1) * a.w.step);
     float2 t0 = v[0], t1 = v[1];  // what lies past the row's end is zero
 #pragma unroll
     for (int i = 2; i < P; i += 2) {
@@ -439,8 +478,12 @@ __global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         float2 c = add2(v[i], f2(-mean));
-        if (column<V, E, RAGGED>(p.L, p.lane, 2 * i) >= N) c.x = 0.0f;
-        if (column<V, E, RAGGED>(p.L, p.lane, 2 * i + 1) >= N) c.y = 0.0f;
+        if constexpr (RAGGED) {
+          if (column<V, E, RAGGED, MODE>(p.L, p.lane, 2 * i) >= N) c.x = 0.0f;
+          if (column<V, E, RAGGED, MODE>(p.L, p.lane, 2 * i + 1) >= N) c.y = 0.0f;
+        } else {
+          if (p.lane + 2 * i / V * p.L >= a.w.NV) c = make_float2(0.0f, 0.0f);
+        }
         if (i & 1) t1 = fma2(c, c, t1);
         else t0 = fma2(c, c, t0);
       }
@@ -449,24 +492,35 @@ __global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
     float q = t0.x + t0.y;
     q = GROUP ? warp_sum(q) : lanes_sum(q, p.L);
     if constexpr (GROUP) {
-      if (wl == 0) red[par][w0 + p.lane / 32] = make_float2(s, q);
+      if (wl == 0) red[par][w0 + p.lane / 32] = make_float4(s, q, mean, 0.0f);
       group_barrier(p.mine, p.L);
       // up to 16 warps, one a lane: the lower half of this warp has them
-      const float2 o = wl < warps ? red[par][w0 + wl] : make_float2(0.0f, 0.0f);
+      const float4 o = wl < warps ? red[par][w0 + wl] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       mean = div_n(__shfl_sync(0xFFFFFFFFu, lanes_sum(o.x, 16), 0), n, inv_n);
-      const float e = wl < warps ? div_n(o.x, nl, inv_nl) - mean : 0.0f;
-      q = __shfl_sync(0xFFFFFFFFu, lanes_sum(fmaf(e * e, nl, o.y), 16), 0);
+      const float e = o.z - mean;
+      q = __shfl_sync(0xFFFFFFFFu, lanes_sum(wl < warps ? fmaf(e * e, nl, o.y) : 0.0f, 16), 0);
     }
     const float rstd = rsqrtf(fmaf(q, inv_n, a.eps));
-    if (row < a.M) {
+    if (it < left) {
       if (p.lane == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
       }
 #pragma unroll
-      for (int i = 0; i < P; ++i) v[i] = fma2(mul2(add2(v[i], f2(-mean)), f2(rstd)), gam[i], bet[i]);
-      store_pairs<T, E, RAGGED>(yr, v, p, NV, N);
+      for (int i = 0; i < P; ++i) {
+        float2 b;
+        if constexpr (BS) {
+          const float2 *q = reinterpret_cast<const float2 *>(bslot + i / 2 * blockDim.x);
+          b = q[i & 1];
+        } else {
+          b = bet[i];
+        }
+        v[i] = fma2(mul2(add2(v[i], f2(-mean)), f2(rstd)), gam[i], b);
+      }
+      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), v, p, a.w.NV, N, full);
     }
+    row += a.w.step;
+    out += a.w.inc[1];
   }
   cp_async_wait<0>();
 }
@@ -504,24 +558,24 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormArgs a) {
   using IO = VecIO<T, V>;
   __shared__ float red[2][kMaxWarps];
   pdl_prologue();
-  const float inv_n = 1.0f / (float)a.N;
+  const float inv_n = 1.0f / (float)a.w.N;
   const int B = blockDim.x;
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+  for (int64_t row = blockIdx.x; row < a.w.M; row += gridDim.x) {
     const T *x = static_cast<const T *>(a.x) + row * a.ldx;
     T *y = static_cast<T *>(a.y) + row * a.ldy;
     float s[1] = {0.0f};
 #pragma unroll 4
-    for (int64_t cv = threadIdx.x; cv < a.NV; cv += B) {
+    for (int64_t cv = threadIdx.x; cv < a.w.NV; cv += B) {
       float v[V];
       IO::unpack(load_row<T, V>(x + cv * V), v);
 #pragma unroll
       for (int e = 0; e < V; ++e) s[0] += v[e];
     }
     cta_sum(s, red[0]);
-    const float mean = s[0] / (float)a.N;  // exact for a constant row
+    const float mean = s[0] / (float)a.w.N;  // exact for a constant row
     float q[1] = {0.0f};
 #pragma unroll 4
-    for (int64_t cv = threadIdx.x; cv < a.NV; cv += B) {
+    for (int64_t cv = threadIdx.x; cv < a.w.NV; cv += B) {
       float v[V];
       IO::unpack(load_row<T, V>(x + cv * V), v);
 #pragma unroll
@@ -533,7 +587,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormArgs a) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
-    for (int64_t cv = threadIdx.x; cv < a.NV; cv += B) {
+    for (int64_t cv = threadIdx.x; cv < a.w.NV; cv += B) {
       float v[V], g[V], b[V];
       IO::unpack(load_row<T, V>(x + cv * V), v);
       load_columns<V>(a.gamma, a.gamma_dt, cv * V, 1.0f, g);
@@ -569,13 +623,13 @@ __host__ __device__ constexpr size_t bwd_smem(int block, int L, bool ragged) {
 // first run). Rows side by side in a warp are added by a butterfly first; `sh`
 // then holds a copy per warp (rows within a warp) or per group, V elements of
 // every lane at a time.
-template <int V, int E, bool RAGGED>
+template <int V, int E, bool RAGGED, int MODE>
 __device__ __forceinline__ void flush_columns(const NormGradArgs &a, float2 (&dg)[E / 2], float2 (&db)[E / 2],
-                                              const Place &p, bool first, float *sh) {
-  double *pg = a.parts + (int64_t)blockIdx.x * 2 * a.N;
-  const int N = (int)a.N;
-  const int copies = p.L <= 32 ? (int)blockDim.x / 32 : a.rows;
-  const int copy = p.L <= 32 ? (int)threadIdx.x >> 5 : p.mine;
+                                              const Place<MODE> &p, bool first, float *sh) {
+  double *pg = a.parts + (int64_t)blockIdx.x * 2 * a.w.N;
+  const int N = (int)a.w.N;
+  const int copies = MODE != kGroup ? (int)blockDim.x / 32 : a.w.rows;
+  const int copy = MODE != kGroup ? (int)threadIdx.x >> 5 : p.mine;
   const int width = p.L * V;
 #pragma unroll
   for (int k = 0; k < E / V; ++k) {
@@ -583,11 +637,11 @@ __device__ __forceinline__ void flush_columns(const NormGradArgs &a, float2 (&dg
     for (int e = 0; e < V; ++e) {
       const int i = (k * V + e) / 2;
       float u = e & 1 ? dg[i].y : dg[i].x, w = e & 1 ? db[i].y : db[i].x;
-      for (int o = p.L; o < 32; o <<= 1) {
+      for (int o = p.seg(); o < 32; o <<= 1) {
         u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
         w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
       }
-      if (p.L >= 32 || ((int)threadIdx.x & 31) < p.L) {
+      if (MODE != kPart || ((int)threadIdx.x & 31) < p.L) {
         sh[(copy * 2) * width + e * p.L + p.lane] = u;
         sh[(copy * 2 + 1) * width + e * p.L + p.lane] = w;
       }
@@ -595,11 +649,11 @@ __device__ __forceinline__ void flush_columns(const NormGradArgs &a, float2 (&dg
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * width; i += blockDim.x) {
       const int which = i >= width, j = i - which * width, e = j / p.L;
-      const int c = column<V, E, RAGGED>(p.L, j - e * p.L, 0) + (RAGGED ? (k * V + e) * p.seg : k * width + e);
+      const int c = column<V, E, RAGGED, MODE>(p.L, j - e * p.L, 0) + (RAGGED ? (k * V + e) * p.seg() : k * width + e);
       if (c < N) {
         double t = 0.0;
         for (int w = 0; w < copies; ++w) t += (double)sh[(w * 2 + which) * width + j];
-        double *o = pg + (int64_t)which * a.N + c;
+        double *o = pg + (int64_t)which * a.w.N + c;
         *o = first ? t : *o + t;
       }
     }
@@ -625,50 +679,57 @@ __device__ __forceinline__ void swap_halves(float v, float &u, float &w) {
   w = up ? v : other;
 }
 
-template <typename T, bool GROUP, bool RAGGED>
+template <typename T, int MODE, bool RAGGED>
 __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
+  constexpr bool GROUP = MODE == kGroup;
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int E = kBwdElems, P = E / 2;
   constexpr int S = bwd_stages<T>();
   __shared__ float red[2][2 * kBlock / 32];
   extern __shared__ __align__(16) unsigned char dyn[];
   pdl_prologue();
-  const Place p(a.L);
+  const Place<MODE> p(a.w.L);
   if (dynamic_smem_bytes() < bwd_smem<T>((int)blockDim.x, p.L, RAGGED)) return;
   float *sh = reinterpret_cast<float *>(dyn + bwd_ring<T>((int)blockDim.x, p.L, RAGGED));
-  const int N = (int)a.N, NV = a.NV;
+  const int N = (int)a.w.N;
   const T *const src[2] = {static_cast<const T *>(a.x), static_cast<const T *>(a.dy)};
   const int64_t ld[2] = {a.ldx, a.lddy};
-  const int64_t step = (int64_t)gridDim.x * a.rows;
-  int64_t r0 = (int64_t)blockIdx.x * a.rows;
-  RowFeed<T, E, 2, S, RAGGED> feed(dyn, src, ld, p, N, r0 + p.mine, step);
+  const int64_t r0 = (int64_t)blockIdx.x * a.w.rows;
+  int64_t row = r0 + p.mine;
+  const int steps = row_count(a.w.M, r0, a.w.step), left = row_count(a.w.M, row, a.w.step);  // the CTA's, this row's
+  RowFeed<T, E, 2, S, RAGGED, MODE> feed(dyn, src, ld, p, a.w, row);
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.M, NV, a.fast, step);
-  // The next row's statistics, loaded one row ahead: rows past M take the last
-  // one's, so that nothing waits for the loads before the next row.
-  auto clamp = [&](int64_t r) { return r < a.M ? r : a.M - 1; };
-  float nmean = a.mean[clamp(r0 + p.mine)], nrstd = a.rstd[clamp(r0 + p.mine)];
+  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.w, i < left, row + (int64_t)i * a.w.step);
+  // The next row's statistics, loaded one row ahead and used as they are: past
+  // its last row a lane stays at that row (at M - 1 if it has none), so that
+  // nothing waits for the loads before the next row.
+  int64_t stat = left > 0 ? row : a.w.M - 1;
+  float nmean = a.mean[stat], nrstd = a.rstd[stat];
   float2 gam[P], dg[P], db[P];
-  load_pairs<V, E, RAGGED>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
+  load_pairs<V, E, RAGGED, MODE>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
 #pragma unroll
   for (int i = 0; i < P; ++i) dg[i] = db[i] = make_float2(0.0f, 0.0f);
-  const float inv_n = 1.0f / (float)N;
+  const float inv_n = a.w.inv_n;
   const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31, w0 = GROUP ? p.mine * warps : 0;
-  T *out = static_cast<T *>(a.dx) + (r0 + p.mine) * a.lddx;
+  // no lane of the warp holds anything past the row's end
+  const bool full = RAGGED ? feed.need == p.seg() * E * (int)sizeof(T) : N == p.L * E;
+  char *out = reinterpret_cast<char *>(static_cast<T *>(a.dx) + row * a.lddx);
   bool first = true;
-  int run = 0, par = 0;
-  for (; r0 < a.M; r0 += step, par ^= 1, out += step * a.lddx) {
-    const int64_t row = r0 + p.mine;
-    const bool in = row < a.M;
+  int run = 0;
+#pragma unroll 1
+  for (int it = 0; it < steps; ++it) {
+    const bool in = it < left;
+    const int par = it & 1;
     const float mean = in ? nmean : 0.0f, rstd = in ? nrstd : 0.0f;
     feed.wait();
     float2 h[P], d[P];
-    feed.read(0, src[0], ld[0], row, p, a.M, N, a.fast, h);
-    feed.read(1, src[1], ld[1], row, p, a.M, N, a.fast, d);
-    feed.advance();
-    feed.issue(p, a.M, NV, a.fast, step);
-    nmean = a.mean[clamp(row + step)];
-    nrstd = a.rstd[clamp(row + step)];
+    feed.read(0, src[0], ld[0], row, p, a.w, h);
+    feed.read(1, src[1], ld[1], row, p, a.w, d);
+    feed.advance(a.w);
+    feed.issue(p, a.w, it + S - 1 < left, row + (int64_t)(S - 1) * a.w.step);
+    if (it + 1 < left) stat += a.w.step;
+    nmean = a.mean[stat];
+    nrstd = a.rstd[stat];
     if (!RAGGED && !in) {  // the slots hold an older row
 #pragma unroll
       for (int i = 0; i < P; ++i) h[i] = d[i] = make_float2(0.0f, 0.0f);
@@ -693,7 +754,7 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
       swap_halves(v, c1, c2);
-    } else if (p.L == 32) {
+    } else if constexpr (MODE == kWarp) {
       swap_halves(half_sums(c1, c2), c1, c2);
     } else {
       c1 = lanes_sum(c1, p.L);
@@ -704,8 +765,10 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
       c2 *= inv_n;
 #pragma unroll
       for (int i = 0; i < P; ++i) d[i] = mul2(f2(rstd), add2(d[i], fma2(h[i], f2(-c2), f2(-c1))));
-      store_pairs<T, E, RAGGED>(out, d, p, NV, N);
+      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), d, p, a.w.NV, N, full);
     }
+    row += a.w.step;
+    out += a.w.inc[2];
     if (++run == kRunRows) {
       flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
       first = false;
@@ -724,15 +787,15 @@ __global__ void __launch_bounds__(1024) norm_bwd_rows_kernel(NormGradArgs a, flo
   using IO = VecIO<T, V>;
   __shared__ float red[2][2 * kMaxWarps];
   pdl_prologue();
-  const float inv_n = 1.0f / (float)a.N;
+  const float inv_n = 1.0f / (float)a.w.N;
   int par = 0;
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, par ^= 1) {
+  for (int64_t row = blockIdx.x; row < a.w.M; row += gridDim.x, par ^= 1) {
     const T *x = static_cast<const T *>(a.x) + row * a.ldx;
     const T *dy = static_cast<const T *>(a.dy) + row * a.lddy;
     const float mean = a.mean[row], rstd = a.rstd[row];
     float c[2] = {0.0f, 0.0f};
 #pragma unroll 2
-    for (int64_t cv = threadIdx.x; cv < a.NV; cv += blockDim.x) {
+    for (int64_t cv = threadIdx.x; cv < a.w.NV; cv += blockDim.x) {
       float v[V], d[V], g[V];
       IO::unpack(load_row<T, V>(x + cv * V), v);
       IO::unpack(load_row<T, V>(dy + cv * V), d);
@@ -756,7 +819,7 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(NormGradArgs a, c
   using IO = VecIO<T, V>;
   pdl_prologue();
   const int64_t cv = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (cv >= a.NV) return;
+  if (cv >= a.w.NV) return;
   const T *x = static_cast<const T *>(a.x) + cv * V;
   const T *dy = static_cast<const T *>(a.dy) + cv * V;
   T *dx = static_cast<T *>(a.dx) + cv * V;
@@ -771,7 +834,7 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(NormGradArgs a, c
   }
   int run = 0;
 #pragma unroll 2
-  for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
+  for (int64_t row = blockIdx.y; row < a.w.M; row += gridDim.y) {
     float v[V], d[V], o[V];
     IO::unpack(load_row<T, V>(x + row * a.ldx), v);
     IO::unpack(load_row<T, V>(dy + row * a.lddy), d);
@@ -795,7 +858,7 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(NormGradArgs a, c
       }
     }
   }
-  double *pg = a.parts + (int64_t)blockIdx.y * 2 * a.N + cv * V, *pb = pg + a.N;
+  double *pg = a.parts + (int64_t)blockIdx.y * 2 * a.w.N + cv * V, *pb = pg + a.w.N;
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     pg[e] = sg[e] + (double)dg[e];
