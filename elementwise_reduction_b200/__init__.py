@@ -21,7 +21,7 @@ from ._abi import (DYT_BF16, DYT_F16, DYT_F32, MAX_RANKS, DytError, dyt_backward
                    dyt_layer_norm_backward_workspace_bytes, dyt_layer_norm_forward, dyt_partials_layout_query,
                    dyt_plan_query, dyt_policy_loss_backward, dyt_policy_loss_forward,
                    dyt_policy_loss_workspace_bytes, dyt_status_string)
-from ._rows import DTYPE_CODE, _code, _cuda_contig, _rows, _stream, row_pitch
+from ._tensors import DTYPE_CODE, _code, _cuda_contig, _rows, _stream, row_pitch
 from .loss import (PolicyLoss, PolicyLossFunction, policy_loss_backward, policy_loss_forward,
                    policy_loss_workspace)
 from .norm import LayerNorm, LayerNormFunction, layer_norm_backward, layer_norm_forward, layer_norm_workspace

@@ -69,6 +69,17 @@ def _pitch(t: torch.Tensor, what: str) -> int:
     return _rows(t, what)
 
 
+def _fresh(t: torch.Tensor) -> torch.Tensor:
+    """An uninitialised contiguous tensor of t's shape, dtype and device. (empty_like of a
+    contiguous tensor takes 1.3 us, torch.empty of its shape 3.3.)"""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _fresh_rows(rows: torch.Size, device: torch.device) -> torch.Tensor:
+    """An uninitialised float32 value per row. (A single int as the shape halves the call's time.)"""
+    return torch.empty(rows[0] if len(rows) == 1 else rows, dtype=torch.float32, device=device)
+
+
 def _elsewhere(t: torch.Tensor, stream: torch.cuda.Stream | None) -> bool:
     """Whether a call on t's data has to switch the current device or stream (see _there)."""
     if not t.is_cuda:

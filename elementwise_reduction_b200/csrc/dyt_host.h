@@ -46,7 +46,7 @@ inline bool vec_pitch(int64_t ld, size_t elem) { return ((uint64_t)ld * elem) % 
 // predecessor in the stream drains; its first instruction waits
 // (griddepcontrol.wait) for that predecessor, so stream order holds.
 struct PdlConfig {
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg;
   PdlConfig(unsigned grid, unsigned block, size_t smem, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -58,14 +58,6 @@ struct PdlConfig {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-  }
-  // CTAs in clusters of `size` along x.
-  void cluster(unsigned size) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = size;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
   }
 };
 

@@ -17,12 +17,18 @@ using dyt::loss::LossArgs;
 using dyt::loss::LossGradArgs;
 
 constexpr int kOpLossForward = 7, kOpLossBackward = 8;  // dyt_launch_info::op
-constexpr int kBlock = 256;
-constexpr int kCtasPerSm = 8;        // 2048 resident threads
-constexpr int64_t kWarpRow = 8192;   // rows of at most this many bytes take a warp
-constexpr int64_t kPartMin = 4096;   // the smallest part of a row, bytes
-constexpr int64_t kGradPart = 65536;  // the largest part of a row in the backward, bytes
-constexpr int kFinishBlock = 512, kFinishCtas = 8;
+// The forward: 512 threads on an SM, their rings full of shared memory. A warp
+// gets several items, so that the last ones do not leave most of the SMs idle;
+// parts of less than kPartMin bytes would be mostly set-up.
+constexpr int kRowsPerSm = 512;
+constexpr int kItemsPerWarp = 2;
+constexpr int64_t kPartMin = 4096;
+constexpr int kFinishCtasPerSm = 2;
+
+constexpr int kGradBlock = 256;
+constexpr int kGradCtasPerSm = 8;     // 2048 resident threads
+constexpr int64_t kWarpRow = 8192;    // rows of at most this many bytes take a warp
+constexpr int64_t kGradPart = 65536;  // the largest part of a row, bytes
 
 template <typename F>
 dyt_status with_type(int xd, F &&f) {
@@ -34,31 +40,61 @@ dyt_status with_type(int xd, F &&f) {
   return DYT_ERR_UNSUPPORTED_DTYPE;
 }
 
+// Parts of a row and CTAs.
 struct LossPlan {
-  bool cta;      // a part of a row is a CTA's, else a warp's
+  bool cta;      // backward: a part of a row is a CTA's, else a warp's
   int S;         // parts of a row
+  int block;
   int64_t grid;  // CTAs
+  int finish;    // forward: CTAs of the second kernel
+  size_t off_sums, off_done, bytes;  // forward: the workspace
 };
 
-// Few rows are split until every SM has its CTAs.
-LossPlan plan(int64_t M, int64_t N, size_t es, bool backward, int sms) {
-  LossPlan p;
-  const int64_t bytes = N * (int64_t)es;
-  const int64_t slots = (int64_t)sms * kCtasPerSm;
-  p.cta = bytes > kWarpRow || M < slots;
+LossPlan plan_forward(int64_t M, int64_t N, size_t es, int sms) {
+  LossPlan p = {};
+  const int64_t bytes = N * (int64_t)es, warps = (int64_t)sms * (kRowsPerSm / 32);
+  // At least kItemsPerWarp items a warp, in as nearly whole rounds as a few
+  // parts more can make them: 4096 rows over 2368 warps are 1.73 rounds whole,
+  // 6.92 in four parts.
+  const int64_t most = std::max<int64_t>(1, bytes / kPartMin);
   p.S = 1;
-  if (p.cta) {
-    int64_t s = M < slots ? std::min(slots / M, bytes / kPartMin) : 1;
-    if (backward) s = std::max(s, ceil_div(bytes, kGradPart));
-    p.S = (int)std::max<int64_t>(1, s);
+  const int64_t least = std::min(most, ceil_div(warps * kItemsPerWarp, M));
+  double best = -1.0;
+  for (int64_t S = least; S <= std::min(most, least + 8); ++S) {
+    const double rounds = (double)M * (double)S / (double)warps, even = rounds / std::ceil(rounds);
+    if (even > best + 0.02) {
+      best = even;
+      p.S = (int)S;
+    }
+    if (S == 1 && rounds > 8.0) break;
   }
-  const int64_t items = p.cta ? M * p.S : ceil_div(M, kBlock / 32);
-  p.grid = std::min<int64_t>(items, (int64_t)1 << 30);
+  const int64_t items = M * p.S;
+  // few items: small CTAs, one warp's work after the other over all SMs
+  p.block = dyt::loss::kRowsBlock;
+  while (p.block > 32 && ceil_div(items, p.block / 32) < 2 * (int64_t)sms) p.block >>= 1;
+  p.grid = std::min<int64_t>(ceil_div(items, p.block / 32), (int64_t)sms * (kRowsPerSm / p.block));
+  const int64_t per = p.S > dyt::loss::kThreadParts ? dyt::loss::kFinishBlock / 32 : dyt::loss::kFinishBlock;
+  p.finish = (int)std::min<int64_t>(ceil_div(M, per), (int64_t)sms * kFinishCtasPerSm);
+  p.off_sums = ((size_t)items * sizeof(float2) + 15) & ~(size_t)15;
+  p.off_done = p.off_sums + (size_t)p.finish * sizeof(double);
+  p.bytes = (p.off_done + sizeof(unsigned) + 15) & ~(size_t)15;
   return p;
 }
 
-size_t ws_bytes(int64_t M, const LossPlan &p) {
-  return ((size_t)M * (size_t)p.S * sizeof(float2) + 15) & ~(size_t)15;
+// Few rows are split until every SM has its CTAs, long ones into parts of kGradPart bytes.
+LossPlan plan_backward(int64_t M, int64_t N, size_t es, int sms) {
+  LossPlan p = {};
+  const int64_t bytes = N * (int64_t)es;
+  const int64_t slots = (int64_t)sms * kGradCtasPerSm;
+  p.cta = bytes > kWarpRow || M < slots;
+  p.S = 1;
+  p.block = kGradBlock;
+  if (p.cta)
+    p.S = (int)std::max<int64_t>(M < slots ? std::max<int64_t>(1, std::min(slots / M, bytes / kPartMin)) : 1,
+                                 ceil_div(bytes, kGradPart));
+  const int64_t items = p.cta ? M * p.S : ceil_div(M, kGradBlock / 32);
+  p.grid = std::min<int64_t>(items, (int64_t)1 << 30);
+  return p;
 }
 
 void record(int op, const LossPlan *p, int vec, int kernels, size_t ws) {
@@ -69,9 +105,9 @@ void record(int op, const LossPlan *p, int vec, int kernels, size_t ws) {
   if (p) {
     i.path = p->cta ? 2 : 1;
     i.vec = vec;
-    i.block = kBlock;
+    i.block = p->block;
     i.grid = (int)p->grid;
-    i.row_lanes = i.rows_per_step = p->cta ? 1 : kBlock / 32;
+    i.row_lanes = i.rows_per_step = p->cta ? 1 : p->block / 32;
     i.col_chunks = p->S;
     i.pack_rows = 1;
   }
@@ -88,7 +124,7 @@ size_t dyt_policy_loss_workspace_bytes(int64_t M, int64_t N, dyt_dtype dtype) tr
   if (check_shape(M, N, dtype) != DYT_OK || M == 0 || N == 0) return 0;
   int dev = 0, sms = 0;
   if (current_sms(&dev, &sms) != DYT_OK) return 0;
-  return ws_bytes(M, plan(M, N, dsize(dtype), false, sms));
+  return plan_forward(M, N, dsize(dtype), sms).bytes;
 } catch (...) {
   return 0;
 }
@@ -124,9 +160,8 @@ dyt_status dyt_policy_loss_forward(const void *logits, int64_t ld, const void *t
   int dev = 0, sms = 0;
   st = current_sms(&dev, &sms);
   if (st != DYT_OK) return st;
-  const LossPlan p = plan(M, N, es, false, sms);
-  const size_t need = ws_bytes(M, p);
-  if (workspace_bytes < need) return DYT_ERR_WORKSPACE_TOO_SMALL;
+  const LossPlan p = plan_forward(M, N, es, sms);
+  if (workspace_bytes < p.bytes) return DYT_ERR_WORKSPACE_TOO_SMALL;
   LossArgs a = {};
   a.z = logits;
   a.ld = ld;
@@ -140,9 +175,17 @@ dyt_status dyt_policy_loss_forward(const void *logits, int64_t ld, const void *t
   a.stats = (float2 *)stats;
   a.coef = coef;
   a.parts = (float2 *)workspace;
+  a.sums = (double *)((char *)workspace + p.off_sums);
+  a.done = (unsigned *)((char *)workspace + p.off_done);
   a.M = M;
   a.N = N;
   a.S = p.S;
+  const int64_t vecs = ceil_div(N, 16 / (int64_t)es), batch = dyt::loss::kBatch * 32;
+  a.part_vecs = (int)(ceil_div(ceil_div(vecs, batch), p.S) * batch);
+  a.aligned = N % (16 / (int64_t)es) == 0 && aligned16(logits) && (M == 1 || vec_pitch(ld, es));
+  const int64_t warps = p.grid * (p.block / 32);
+  a.row_step = warps % M;
+  a.part_step = (int)(warps / M);
   a.wide_tokens = token_bytes == 8;
   a.C = C;
   a.inv_t = 1.0 / temperature;
@@ -151,17 +194,16 @@ dyt_status dyt_policy_loss_forward(const void *logits, int64_t ld, const void *t
   a.kl = kl_coef;
   return with_type(dtype, [&](auto t) -> dyt_status {
     using T = decltype(t);
-    PdlConfig lc((unsigned)p.grid, kBlock, 0, s);
-    cudaError_t e = cudaLaunchKernelEx(
-        &lc.cfg, p.cta ? dyt::loss::loss_rows_kernel<T, true> : dyt::loss::loss_rows_kernel<T, false>, a);
+    const size_t smem = dyt::loss::rows_smem(p.block);
+    const dyt_status ready = prepare_smem(dev, (const void *)dyt::loss::loss_rows_kernel<T>, (int)smem);
+    if (ready != DYT_OK) return ready;
+    PdlConfig lc((unsigned)p.grid, p.block, smem, s);
+    cudaError_t e = cudaLaunchKernelEx(&lc.cfg, dyt::loss::loss_rows_kernel<T>, a);
     if (e != cudaSuccess) return cuda_fail(e);
-    const int64_t per = p.S == 1 ? kFinishBlock : kFinishBlock / 32;
-    const unsigned ctas = M > per ? kFinishCtas : 1;
-    PdlConfig lf(ctas, kFinishBlock, 0, s);
-    lf.cluster(ctas);
+    PdlConfig lf((unsigned)p.finish, dyt::loss::kFinishBlock, 0, s);
     e = cudaLaunchKernelEx(&lf.cfg, dyt::loss::loss_finish_kernel<T>, a);
     if (e != cudaSuccess) return cuda_fail(e);
-    record(kOpLossForward, &p, (int)(16 / sizeof(T)), 2, need);
+    record(kOpLossForward, &p, (int)(16 / sizeof(T)), 2, p.bytes);
     return DYT_OK;
   });
 } catch (...) {
@@ -191,7 +233,7 @@ dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *
   int dev = 0, sms = 0;
   st = current_sms(&dev, &sms);
   if (st != DYT_OK) return st;
-  const LossPlan p = plan(M, N, es, true, sms);
+  const LossPlan p = plan_backward(M, N, es, sms);
   LossGradArgs a = {};
   a.z = logits;
   a.ld = ld;
@@ -210,7 +252,7 @@ dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *
   const bool shift = !same_offset(logits, dlogits) || (M > 1 && !vec_pitch(ld - lddl, es));
   return with_type(dtype, [&](auto t) -> dyt_status {
     using T = decltype(t);
-    PdlConfig lc((unsigned)p.grid, kBlock, 0, (cudaStream_t)stream);
+    PdlConfig lc((unsigned)p.grid, p.block, 0, (cudaStream_t)stream);
     const auto k = p.cta ? (shift ? dyt::loss::loss_grad_kernel<T, true, true> : dyt::loss::loss_grad_kernel<T, true, false>)
                          : (shift ? dyt::loss::loss_grad_kernel<T, false, true> : dyt::loss::loss_grad_kernel<T, false, false>);
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);

@@ -7,19 +7,18 @@
 //   coef = w (-(r A where r A <= c A, else 0) + kl (1 - exp(q)))   (d loss / d lp)
 //   dz_j = (grad coef / T) ([j = t] - exp((z_j - m) / T - s))
 //
-// Both passes are bound by reading (and writing) the logits once. The forward
-// keeps a running maximum and sum per thread; rows are split over several CTAs
-// when there are few of them, and the second kernel joins the parts, does the
-// rows' scalar arithmetic in binary64 and adds the loss in a fixed order. Rows
-// of weight 0 are not read.
+// Both passes are bound by reading (and writing) the logits once. In the
+// forward a warp takes one row, or one of S parts of it, at a time, keeps a
+// running maximum and sum per lane, and reads ahead into its next item, so that
+// the memory never waits for the end of a row. The second kernel joins the
+// parts, does the rows' scalar arithmetic in binary64 and adds the loss in a
+// fixed order. Rows of weight 0 are not read.
 //
 // Exponentials are 2^((z - m) C) with C = log2(e) / T in binary32: the maximum is
 // taken out before anything is rounded to its size, and its own term is exactly 1.
 #pragma once
 
-#include <cooperative_groups.h>
-
-#include "dyt_kernels.cuh"
+#include "dyt_async.cuh"
 
 namespace dyt {
 namespace loss {
@@ -41,9 +40,15 @@ struct LossArgs {
   float2 *stats;           // [M] (m, s)
   float *coef;             // [M]
   float2 *parts;           // [M][S] (maximum, sum of 2^((z - maximum) C)) of each part of a row
+  double *sums;            // [CTA of the second kernel] what its rows add to the loss
+  unsigned *done;          // how many of those CTAs have finished
   int64_t M;
   int64_t N;
   int S;                   // parts of a row
+  int part_vecs;           // 16-byte vectors of each, the last one's may be fewer
+  int aligned;             // every row is whole aligned 16-byte vectors
+  int64_t row_step;        // a warp's next item lies part_step parts and row_step rows further on
+  int part_step;
   int wide_tokens;
   float C;                 // log2(e) / T
   double inv_t;
@@ -87,13 +92,20 @@ __device__ __forceinline__ Run join(const Run &a, const Run &b, float C) {
   return r;
 }
 
+// The largest of three (one instruction on sm_100); a NaN passes over.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // 2 n values more. NaN passes over the maximum and reaches the sum.
 template <int n>
 __device__ __forceinline__ void add_pairs(Run &r, const float2 (&v)[n], float C) {
-  float2 t = v[0];
+  float t[2] = {fmaxf(v[0].x, v[0].y), kNegInf};
 #pragma unroll
-  for (int i = 1; i < n; ++i) t = make_float2(fmaxf(t.x, v[i].x), fmaxf(t.y, v[i].y));
-  const float top = fmaxf(t.x, t.y);
+  for (int i = 1; i < n; ++i) t[i & 1] = max3(t[i & 1], v[i].x, v[i].y);
+  const float top = fmaxf(t[0], t[1]);
   if (top > r.m) {
     r.s *= ex2_approx((r.m - top) * C);  // 0 for the first values: 2^-inf
     r.m = top;
@@ -109,168 +121,289 @@ __device__ __forceinline__ void add_pairs(Run &r, const float2 (&v)[n], float C)
   r.s += s[0].x + s[0].y;
 }
 
-__device__ __forceinline__ void add_one(Run &r, float v, float C) {
-  const float2 p[1] = {make_float2(v, kNegInf)};
-  add_pairs(r, p, C);
-}
-
 template <typename T>
 __device__ __forceinline__ int head_elems(const T *p, int64_t N) {
   const int h = (int)((16u - (uint32_t)((uintptr_t)p & 15u)) & 15u) / (int)sizeof(T);
   return h < N ? h : (int)N;
 }
 
-// One part of one row per G threads (a warp, or the CTA): the row's whole
-// 16-byte vectors are cut into S parts, its first and last elements off those
-// vectors go with the first and the last part.
-template <typename T, bool CTA>
-__global__ void __launch_bounds__(256) loss_rows_kernel(LossArgs a) {
-  constexpr int V = 16 / (int)sizeof(T);
-  constexpr int U = 4;
-  using IO = VecIO<T, V>;
-  __shared__ Run sh[8];
-  pdl_prologue();
-  const int G = CTA ? (int)blockDim.x : 32;
-  const int t = CTA ? (int)threadIdx.x : (int)threadIdx.x & 31;
-  const int64_t items = a.M * a.S;
-  const int64_t step = CTA ? gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
-  int64_t item = CTA ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  for (; item < items; item += step) {
-    const int64_t row = a.S == 1 ? item : item / a.S;
-    const int part = (int)(item - row * a.S);
-    if (a.weight && a.weight[row] == 0.0f) continue;
-    const T *z = static_cast<const T *>(a.z) + row * a.ld;
-    const int head = head_elems(z, a.N);
-    const int64_t nb = (a.N - head) / V;
-    const int tail = (int)(a.N - head - nb * V);
-    const int64_t b0 = nb * part / a.S, b1 = nb * (part + 1) / a.S;
-    Run r;
-    if (part == 0 && t < head) add_one(r, to_f32<T>(z[t]), a.C);
-    if (part == a.S - 1 && t < tail) add_one(r, to_f32<T>(z[a.N - tail + t]), a.C);
-    const uint4 *zv = reinterpret_cast<const uint4 *>(z + head);
-    int64_t i = b0 + t;
-    for (; i + (U - 1) * G < b1; i += U * G) {
-      uint4 raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = __ldcs(zv + i + u * G);
-      float2 v[U * V / 2];
-#pragma unroll
-      for (int u = 0; u < U; ++u) IO::unpack2(raw[u], *reinterpret_cast<float2(*)[V / 2]>(v + u * V / 2));
-      add_pairs(r, v, a.C);
-    }
-    for (; i < b1; i += G) {
-      float2 v[V / 2];
-      IO::unpack2(__ldcs(zv + i), v);
-      add_pairs(r, v, a.C);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      Run other;
-      other.m = __shfl_xor_sync(0xFFFFFFFFu, r.m, o);
-      other.s = __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
-      // the lower lane's part first, on both sides: the same bits
-      r = (threadIdx.x & o) ? join(other, r, a.C) : join(r, other, a.C);
-    }
-    if constexpr (CTA) {
-      if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = r;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        for (int w = 1; w < G / 32; ++w) r = join(r, sh[w], a.C);
-      }
-      __syncthreads();
-    }
-    if (t == 0) a.parts[item] = make_float2(r.m, r.s);
+constexpr int kRowsBlock = 256;        // threads of a CTA of the forward, at most
+constexpr int kBatch = 8, kStages = 3;  // a lane's 16-byte vectors in a batch, and batches in its ring
+constexpr int kQueue = 4;               // items that a warp has begun to read, at most kStages
+
+__host__ __device__ constexpr size_t rows_smem(int block) { return (size_t)block * kBatch * kStages * 16; }
+
+// The items (row, part) a warp reads, all rows' first parts before their second
+// ones: item, item + warps, ... without those of weight 0. Weights are looked
+// up 32 items at a time, one per lane.
+struct Items {
+  int64_t row;
+  int part;
+  uint32_t mask;  // which of the items looked up count, from the current one on
+  int left;       // how many of them there are
+
+  __device__ __forceinline__ bool any(const LossArgs &a) const { return part < a.S; }
+  __device__ __forceinline__ void load(const LossArgs &a) {
+    const int k = threadIdx.x & 31;
+    const int64_t r = row + k * a.row_step, over = r / a.M;
+    const int64_t p = part + (int64_t)k * a.part_step + over;
+    mask = __ballot_sync(0xFFFFFFFFu, p < a.S && (a.weight == nullptr || a.weight[r - over * a.M] != 0.0f));
+    left = 32;
   }
+  __device__ __forceinline__ void step(const LossArgs &a) {
+    row += a.row_step;
+    part += a.part_step;
+    if (row >= a.M) {
+      row -= a.M;
+      ++part;
+    }
+    mask >>= 1;
+    if (--left == 0 && any(a)) load(a);
+  }
+  // To the first item that counts, from the current one on; false: there is none.
+  __device__ __forceinline__ bool find(const LossArgs &a) {
+    while (any(a) && !(mask & 1u)) step(a);
+    return any(a);
+  }
+};
+
+struct Item {
+  int64_t row;
+  int part;
+  int nv;  // whole 16-byte vectors of the part
+};
+
+// A warp's items, one after the other: the row's whole 16-byte vectors are cut
+// into S parts, the elements before and after them go with the first and the
+// last part. Every lane keeps kStages batches of vectors in a ring of its own
+// (asynchronous copies), also across items.
+template <typename T>
+__global__ void __launch_bounds__(kRowsBlock, 2) loss_rows_kernel(LossArgs a) {
+  constexpr int V = 16 / (int)sizeof(T);
+  constexpr int P = V / 2;
+  using IO = VecIO<T, V>;
+  __shared__ Item queue[kRowsBlock / 32][kQueue];
+  extern __shared__ __align__(16) unsigned char dyn[];
+  pdl_prologue();
+  if (dynamic_smem_bytes() < rows_smem((int)blockDim.x)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0u;
+  uint4 *ring = reinterpret_cast<uint4 *>(dyn) + warp * (kStages * kBatch * 32) + lane;
+  Items it;
+  {
+    const int64_t first = (int64_t)blockIdx.x * ((int)blockDim.x >> 5) + warp;
+    it.part = (int)(first / a.M);
+    it.row = first - it.part * a.M;
+    it.load(a);
+  }
+  const uint4 *src = nullptr;  // this lane's next vector of the item being read
+  int ahead = 0;               // vectors of it not yet asked for
+  int put = 0, wr = 0;         // items begun, the ring's first slot to fill
+  bool reading = false;
+  auto issue = [&]() {
+    if (!reading && it.find(a)) {
+      const T *z = static_cast<const T *>(a.z) + it.row * a.ld;
+      const int head = a.aligned ? 0 : head_elems(z, a.N);
+      const int nb = (int)((a.N - head) / V);
+      // cut at whole batches, so that only a row's last one is not full
+      const int b0 = min(it.part * a.part_vecs, nb), b1 = it.part == a.S - 1 ? nb : min(b0 + a.part_vecs, nb);
+      src = reinterpret_cast<const uint4 *>(z + head) + b0 + lane;
+      ahead = b1 - b0;
+      if (lane == 0) queue[warp][put % kQueue] = Item{it.row, it.part, ahead};
+      __syncwarp();
+      ++put;
+      reading = true;
+      it.step(a);
+    }
+    if (reading) {
+      uint4 *slot = ring + wr;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (u * 32 + lane < ahead) cp_async16(slot + u * 32, src + u * 32);
+      src += kBatch * 32;
+      ahead -= kBatch * 32;
+      reading = ahead > 0;
+    }
+    cp_async_commit();
+    wr = wr == (kStages - 1) * kBatch * 32 ? 0 : wr + kBatch * 32;
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue();
+  int rd = 0;
+  const float C = a.C;
+  for (int got = 0; got < put; ++got) {
+    const Item item = queue[warp][got % kQueue];
+    // The elements off the vectors: used only after those, so that nothing waits for them.
+    float first = kNegInf, last = kNegInf;
+    if (!a.aligned) {
+      const T *z = static_cast<const T *>(a.z) + item.row * a.ld;
+      const int head = head_elems(z, a.N), tail = (int)((a.N - head) % V);
+      if (item.part == 0 && lane < head) first = to_f32<T>(z[lane]);
+      if (item.part == a.S - 1 && lane < tail) last = to_f32<T>(z[a.N - tail + lane]);
+    }
+    Run r;
+    int n = item.nv;
+    do {
+      cp_async_wait<kStages - 2>();
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) raw[u] = ring[rd + u * 32];
+      rd = rd == (kStages - 1) * kBatch * 32 ? 0 : rd + kBatch * 32;
+      issue();
+      if (n >= kBatch * 32) {
+        float2 v[kBatch * P];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) IO::unpack2(raw[u], *reinterpret_cast<float2(*)[P]>(v + u * P));
+        add_pairs(r, v, C);
+      } else {
+        float2 v[kBatch * P];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          IO::unpack2(raw[u], *reinterpret_cast<float2(*)[P]>(v + u * P));
+          if (u * 32 + lane >= n)
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[u * P + i] = f2(kNegInf);
+        }
+        add_pairs(r, v, C);
+      }
+      n -= kBatch * 32;
+    } while (n > 0);
+    if (!a.aligned) {
+      const float2 p[1] = {make_float2(first, last)};
+      add_pairs(r, p, C);
+    }
+    float m = r.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    // equal maxima keep their sum as it is (infinities included)
+    float s = r.m == m ? r.s : r.s * ex2_approx((r.m - m) * a.C);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0) a.parts[item.row * a.S + item.part] = make_float2(m, s);
+  }
+  cp_async_wait<0>();
 }
 
-// What row i adds to the loss; writes its outputs.
+// What the second kernel needs of a row besides its parts.
+struct RowInput {
+  double w, hit, old_logp, advantage, ref_logp;
+};
+
 template <typename T>
-__device__ __forceinline__ double finish_row(const LossArgs &a, int64_t row, const Run &r, double w) {
-  const T *z = static_cast<const T *>(a.z) + row * a.ld;
-  const int64_t tok = token_at(a.tokens, a.wide_tokens, row);
-  // a token outside the vocabulary has no probability: NaN, here and in the loss
-  const double hit = tok >= 0 && tok < a.N ? (double)to_f32<T>(z[tok]) : (double)__int_as_float(0x7FC00000);
+__device__ __forceinline__ RowInput row_input(const LossArgs &a, int64_t row) {
+  RowInput in = {};
+  in.w = a.weight ? (double)a.weight[row] : 1.0 / (double)a.M;
+  if (in.w != 0.0) {
+    const int64_t tok = token_at(a.tokens, a.wide_tokens, row);
+    in.old_logp = (double)a.old_logp[row];
+    in.advantage = (double)a.advantage[row];
+    if (a.ref_logp) in.ref_logp = (double)a.ref_logp[row];
+    // a token outside the vocabulary has no probability: NaN, here and in the loss
+    in.hit = tok >= 0 && tok < a.N ? (double)to_f32<T>((static_cast<const T *>(a.z) + row * a.ld)[tok])
+                                   : (double)__int_as_float(0x7FC00000);
+  }
+  return in;
+}
+
+// What a row adds to the loss; writes its outputs.
+__device__ __forceinline__ double finish_row(const LossArgs &a, int64_t row, const Run &r, const RowInput &in) {
+  if (in.w == 0.0) {
+    a.logp[row] = 0.0f;
+    a.stats[row] = make_float2(0.0f, 0.0f);
+    a.coef[row] = 0.0f;
+    return 0.0;
+  }
   const double s = log((double)r.s);
-  const double lp = (hit - (double)r.m) * a.inv_t - s;
-  const double A = (double)a.advantage[row];
-  const double ratio = exp(lp - (double)a.old_logp[row]);
+  const double lp = (in.hit - (double)r.m) * a.inv_t - s;
+  const double A = in.advantage;
+  const double ratio = exp(lp - in.old_logp);
   const double ra = ratio * A, ca = fmin(fmax(ratio, a.lo), a.hi) * A;
   const bool held = ra > ca;  // the clipped side is the smaller one: no gradient
   double each = held ? -ca : -ra, d = held ? 0.0 : -ra;
   if (a.ref_logp && a.kl != 0.0) {
-    const double q = (double)a.ref_logp[row] - lp, em = expm1(q);
+    const double q = in.ref_logp - lp, em = expm1(q);
     each += a.kl * (em - q);
     d -= a.kl * em;
   }
   a.logp[row] = (float)lp;
   a.stats[row] = make_float2(r.m, (float)s);
-  a.coef[row] = (float)(w * d);
-  return w * each;
+  a.coef[row] = (float)(in.w * d);
+  return in.w * each;
 }
 
-// Joins the rows' parts, finishes the rows and adds the loss: one cluster, a
-// thread per row (S = 1) or a warp per row, each CTA's sum added in order.
+constexpr int kFinishBlock = 128;
+constexpr int kThreadParts = 16;  // rows of at most this many parts take a thread each, others a warp
+
+// Joins the rows' parts, finishes the rows and adds the loss: each CTA adds its
+// rows in a fixed order, and the CTA that finishes last adds the CTAs' sums in
+// order (the count of finished CTAs starts at 0: the first kernel sets it).
+// Before the wait for the first kernel a CTA reads its first rows' inputs: that
+// kernel lets this one start only after its own wait for what came before, and
+// writes none of them.
 template <typename T>
-__global__ void __launch_bounds__(512) loss_finish_kernel(LossArgs a) {
-  namespace cg = cooperative_groups;
-  __shared__ double sh[16];
-  __shared__ double total;
+__global__ void __launch_bounds__(kFinishBlock) loss_finish_kernel(LossArgs a) {
+  __shared__ double sh[kFinishBlock / 32];
+  __shared__ bool last;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool wide = a.S > kThreadParts;
+  const int64_t per = wide ? kFinishBlock / 32 : kFinishBlock;  // rows of a CTA step
+  int64_t row = blockIdx.x * per + (wide ? tid >> 5 : tid);
+  RowInput in = {};
+  if (row < a.M) in = row_input<T>(a, row);
   pdl_prologue();
-  cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = (int)gridDim.x, tid = threadIdx.x;
   double sum = 0.0;
-  const int64_t per = (a.S == 1 ? blockDim.x : blockDim.x / 32);  // rows of a CTA step
-  for (int64_t row = (int64_t)blockIdx.x * per + (a.S == 1 ? tid : tid >> 5); row < a.M; row += per * ctas) {
-    const double w = a.weight ? (double)a.weight[row] : 1.0 / (double)a.M;
+  while (row < a.M) {
     Run r;
-    if (w != 0.0) {
-      if (a.S == 1) {
-        const float2 p = a.parts[row];
-        r.m = p.x;
-        r.s = p.y;
-      } else {
-        for (int i = tid & 31; i < a.S; i += 32) {
-          const float2 p = a.parts[row * a.S + i];
-          Run o;
-          o.m = p.x;
-          o.s = p.y;
-          r = join(r, o, a.C);
-        }
+    if (in.w != 0.0) {
+      for (int i = wide ? lane : 0; i < a.S; i += wide ? 32 : 1) {
+        const float2 p = a.parts[row * a.S + i];
+        Run o;
+        o.m = p.x;
+        o.s = p.y;
+        r = join(r, o, a.C);
+      }
+    }
+    if (wide) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          Run other;
-          other.m = __shfl_xor_sync(0xFFFFFFFFu, r.m, o);
-          other.s = __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
-          r = (tid & o) ? join(other, r, a.C) : join(r, other, a.C);
-        }
+      for (int o = 16; o > 0; o >>= 1) {
+        Run other;
+        other.m = __shfl_xor_sync(0xFFFFFFFFu, r.m, o);
+        other.s = __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
+        // the lower lane's part first, on both sides: the same bits
+        r = (tid & o) ? join(other, r, a.C) : join(r, other, a.C);
       }
     }
-    if (a.S == 1 || (tid & 31) == 0) {
-      if (w != 0.0) {
-        sum += finish_row<T>(a, row, r, w);
-      } else {
-        a.logp[row] = 0.0f;
-        a.stats[row] = make_float2(0.0f, 0.0f);
-        a.coef[row] = 0.0f;
-      }
-    }
+    if (!wide || lane == 0) sum += finish_row(a, row, r, in);
+    row += per * gridDim.x;
+    if (row < a.M) in = row_input<T>(a, row);
   }
+  auto cta_sum = [&](double v) {  // to thread 0
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if ((tid & 31) == 0) sh[tid >> 5] = sum;
-  __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (lane == 0) sh[tid >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+    if (tid == 0)
+      for (int w = 0; w < kFinishBlock / 32; ++w) v += sh[w];
+    return v;
+  };
+  sum = cta_sum(sum);
+  if (gridDim.x == 1) {
+    if (tid == 0) *a.loss = (float)sum;
+    return;
+  }
   if (tid == 0) {
-    double s = 0.0;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) s += sh[w];
-    total = s;
+    a.sums[blockIdx.x] = sum;
+    __threadfence();
+    last = atomicAdd(a.done, 1u) == gridDim.x - 1;
   }
-  cluster.sync();
-  if (blockIdx.x == 0 && tid == 0) {
-    double s = 0.0;
-    for (int c = 0; c < ctas; ++c) s += *cluster.map_shared_rank(&total, c);
-    *a.loss = (float)s;
-  }
-  cluster.sync();  // every CTA's shared memory stays until it has been read
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double s = 0.0;
+  for (unsigned i = tid; i < gridDim.x; i += kFinishBlock) s += __ldcg(a.sums + i);
+  s = cta_sum(s);
+  if (tid == 0) *a.loss = (float)s;
 }
 
 // ---- backward -------------------------------------------------------------------------

@@ -14,7 +14,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._rows import _code, _current, _elsewhere, _like, _pitch, _there, _vector, _workspace, row_pitch
+from ._tensors import (_code, _current, _elsewhere, _fresh, _fresh_rows, _like, _pitch, _there, _vector, _workspace,
+                       row_pitch)
 
 _F32 = (torch.float32,)
 _TOKEN = (torch.int64, torch.int32)
@@ -53,9 +54,14 @@ def policy_loss_forward(logits: torch.Tensor, tokens: torch.Tensor, old_logp: to
                                        kl_coef, temperature, ws)
     M, N = _shape(logits)
     ld, code, dev, rows = _pitch(logits, "logits"), _code(logits, "logits"), logits.device, logits.shape[:-1]
-    ws = policy_loss_workspace(logits) if ws is None else ws
+    if ws is None:
+        n = _abi.lib.dyt_policy_loss_workspace_bytes(M, N, code)
+        ws = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
+        wp = ws.data_ptr()
+    else:
+        wp, n = _workspace(ws, dev), ws.numel()
     loss = torch.empty((), dtype=torch.float32, device=dev)
-    logp, coef = torch.empty((2, *rows), dtype=torch.float32, device=dev).unbind(0)
+    logp, coef = _fresh_rows(rows, dev), _fresh_rows(rows, dev)
     stats = torch.empty((*rows, 2), dtype=torch.float32, device=dev)
     st = _abi.lib.dyt_policy_loss_forward(
         logits.data_ptr(), ld, _vector(tokens, "tokens", M, dev, _TOKEN), tokens.element_size(),
@@ -64,7 +70,7 @@ def policy_loss_forward(logits: torch.Tensor, tokens: torch.Tensor, old_logp: to
         _vector(advantage, "advantage", M, dev, _F32),
         None if weight is None else _vector(weight, "weight", M, dev, _F32), clip_low, clip_high, kl_coef,
         temperature, loss.data_ptr(), logp.data_ptr(), stats.data_ptr(), coef.data_ptr(), M, N, code,
-        _workspace(ws, dev), ws.numel(), _current(dev.index))
+        wp, n, _current(dev.index))
     if st:
         _abi._check(st, "dyt_policy_loss_forward")
     return loss, logp, stats, coef
@@ -83,7 +89,7 @@ def policy_loss_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: torc
     M, N = _shape(logits)
     ld, code, dev = _pitch(logits, "logits"), _code(logits, "logits"), logits.device
     if dlogits is None:
-        dlogits, lddl = torch.empty(logits.shape, dtype=logits.dtype, device=dev), N
+        dlogits, lddl = _fresh(logits), N
     else:
         lddl = _like(dlogits, "dlogits", logits)
     st = _abi.lib.dyt_policy_loss_backward(

@@ -10,7 +10,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._rows import DTYPE_CODE, _code, _current, _elsewhere, _like, _pitch, _there, _vector, _workspace, row_pitch
+from ._tensors import (DTYPE_CODE, _code, _current, _elsewhere, _fresh, _fresh_rows, _like, _pitch, _there, _vector,
+                       _workspace, row_pitch)
 
 _F32 = (torch.float32,)
 _PARAM = tuple(DTYPE_CODE)
@@ -38,17 +39,18 @@ def layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, beta:
     gp = None if gamma is None else _vector(gamma, "gamma", N, dev, _PARAM)
     bp = None if beta is None else _vector(beta, "beta", N, dev, _PARAM)
     if out is None:
-        y, ldy = torch.empty(x.shape, dtype=x.dtype, device=dev), N
+        y, ldy = _fresh(x), N
     else:
         y, ldy = out, _like(out, "out", x)
-    if mean is None and rstd is None:
-        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
+    rows = x.shape[:-1]
+    if mean is None:
+        mean = _fresh_rows(rows, dev)
     else:
-        rows = x.shape[:-1]
-        mean = torch.empty(rows, dtype=torch.float32, device=dev) if mean is None else mean
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev) if rstd is None else rstd
-        for t, what in ((mean, "mean"), (rstd, "rstd")):
-            _vector(t, what, rows.numel(), dev, _F32)
+        _vector(mean, "mean", rows.numel(), dev, _F32)
+    if rstd is None:
+        rstd = _fresh_rows(rows, dev)
+    else:
+        _vector(rstd, "rstd", rows.numel(), dev, _F32)
     st = _abi.lib.dyt_layer_norm_forward(
         x.data_ptr(), ldx, gp, bp, eps, y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(), M, N, code,
         code if gamma is None else DTYPE_CODE[gamma.dtype], code if beta is None else DTYPE_CODE[beta.dtype],
@@ -84,7 +86,7 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
     ldx, code, dev = _pitch(x, "x"), _code(x, "x"), x.device
     lddy = _like(dy, "dy", x)
     if dx is None:
-        dx, lddx = torch.empty(x.shape, dtype=x.dtype, device=dev), N
+        dx, lddx = _fresh(x), N
     else:
         lddx = _like(dx, "dx", x)
     gp = None if gamma is None else _vector(gamma, "gamma", N, dev, _PARAM)
@@ -98,18 +100,27 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
         gd = DTYPE_CODE[gamma.dtype]
         if dgamma is None:
             dgamma = torch.empty_like(gamma)
-        gg = _vector(dgamma, "dgamma", N, dev, (gamma.dtype,))
+            gg = dgamma.data_ptr()
+        else:
+            gg = _vector(dgamma, "dgamma", N, dev, (gamma.dtype,))
     if beta is not None:
         bd = DTYPE_CODE[beta.dtype]
         if dbeta is None:
             dbeta = torch.empty_like(beta)
-        bg = _vector(dbeta, "dbeta", N, dev, (beta.dtype,))
+            bg = dbeta.data_ptr()
+        else:
+            bg = _vector(dbeta, "dbeta", N, dev, (beta.dtype,))
     rows = x.shape[:-1].numel()
-    ws = layer_norm_workspace(x) if ws is None else ws
+    if ws is None:
+        n = _abi.lib.dyt_layer_norm_backward_workspace_bytes(M, N, code)
+        ws = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
+        wp = ws.data_ptr()
+    else:
+        wp, n = _workspace(ws, dev), ws.numel()
     st = _abi.lib.dyt_layer_norm_backward(
         x.data_ptr(), ldx, dy.data_ptr(), lddy, gp, _vector(mean, "mean", rows, dev, _F32),
-        _vector(rstd, "rstd", rows, dev, _F32), dx.data_ptr(), lddx, gg, bg, M, N, code, gd, bd, _workspace(ws, dev),
-        ws.numel(), _current(dev.index))
+        _vector(rstd, "rstd", rows, dev, _F32), dx.data_ptr(), lddx, gg, bg, M, N, code, gd, bd, wp, n,
+        _current(dev.index))
     if st:
         _abi._check(st, "dyt_layer_norm_backward")
     return dx, dgamma, dbeta

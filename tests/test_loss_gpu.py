@@ -97,13 +97,17 @@ def test_row_counts(M, N, dtype):
 
 
 def test_paths():
-    # a warp per row, a CTA per row, and a row over several CTAs are all taken
-    info = Case(3000, 1000, "bf16").check_forward()[1]
-    assert info["path"] == 1
-    info = Case(1500, 8200, "bf16").check_forward()[1]
-    assert info["path"] == 2 and info["col_chunks"] == 1
-    info = Case(2, 60000, "bf16").check_forward()[1]
-    assert info["path"] == 2 and info["col_chunks"] > 8
+    # many short rows are whole items, few or long ones are split; the backward gives a warp or a CTA to a row
+    def both(M, N):
+        c = Case(M, N, "bf16")
+        got, fwd = c.check_forward()
+        return fwd, c.check_backward(got)
+    fwd, bwd = both(3000, 1000)
+    assert fwd["col_chunks"] == 1 and bwd["path"] == 1
+    fwd, bwd = both(1500, 8200)
+    assert 1 < fwd["col_chunks"] <= 8 and bwd["path"] == 2 and bwd["col_chunks"] == 1
+    fwd, bwd = both(2, 60000)
+    assert fwd["col_chunks"] > 8 and bwd["col_chunks"] > 8
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
