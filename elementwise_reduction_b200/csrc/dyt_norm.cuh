@@ -69,7 +69,7 @@ constexpr int kBlock = 512;  // threads of a CTA, at most
 // Elements of a row a lane holds.
 template <typename T>
 __host__ __device__ constexpr int fwd_elems(bool ragged) {
-  return ragged || sizeof(T) == 4 ? 16 : 32;
+  return sizeof(T) == 4 ? 16 : 32;
 }
 constexpr int kBwdElems = 16;
 // Rows a lane adds in binary32 before its column sums move to binary64: the
@@ -275,6 +275,11 @@ struct RowFeed {
     for (int t = 0; t < TENSORS; ++t) at[t] += w.inc[t];
   }
 
+  // RAGGED: elements g .. g + 7 of every lane of the warp lie inside the row.
+  __device__ __forceinline__ bool whole(const Place<MODE> &p, int g) const {
+    return (g + 8) * p.seg() * (int)sizeof(T) <= need;
+  }
+
   // The oldest row (PAIR: the two oldest) has landed.
   __device__ __forceinline__ void wait() const {
     cp_async_wait<S - 2>();
@@ -298,12 +303,15 @@ struct RowFeed {
         const int d = (int)((uint32_t)(uintptr_t)base + ((uint32_t)r * (uint32_t)ld + (uint32_t)(c0 - p.at)) *
                                                             (uint32_t)sizeof(T)) & 15;
         const T *e = reinterpret_cast<const T *>(s + d) + p.at;
-        if (need == p.seg() * E * (int)sizeof(T)) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) v[i] = e[i * p.seg()];
-        } else {
+        for (int g = 0; g < E; g += 8) {
+          if (whole(p, g)) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) v[i] = i * p.seg() < left ? e[i * p.seg()] : from_f32<T>(0.0f);
+            for (int i = g; i < g + 8; ++i) v[i] = e[i * p.seg()];
+          } else {
+#pragma unroll
+            for (int i = g; i < g + 8; ++i) v[i] = i * p.seg() < left ? e[i * p.seg()] : from_f32<T>(0.0f);
+          }
         }
       } else {
         const T *g = base + (r < w.M ? r * ld + c0 : 0);
@@ -322,11 +330,10 @@ struct RowFeed {
   }
 };
 
-// A lane's outputs, rounded once to T, to the row that starts at `out`. full:
-// no lane of the warp holds anything past the row's end.
-template <typename T, int E, bool RAGGED, int MODE>
-__device__ __forceinline__ void store_pairs(T *out, const float2 (&f)[E / 2], const Place<MODE> &p, int NV, int N,
-                                            bool full) {
+// A lane's outputs, rounded once to T, to the row that starts at `out`.
+template <typename T, int E, bool RAGGED, int MODE, typename Feed>
+__device__ __forceinline__ void store_pairs(T *out, const float2 (&f)[E / 2], const Place<MODE> &p, const Feed &feed,
+                                            int NV, int N) {
   constexpr int V = 16 / (int)sizeof(T);
   if constexpr (!RAGGED) {
 #pragma unroll
@@ -336,13 +343,16 @@ __device__ __forceinline__ void store_pairs(T *out, const float2 (&f)[E / 2], co
   } else {
     const int c0 = column<V, E, true, MODE>(p.L, p.lane, 0), left = N - c0;
     T *o = out + c0;
-    if (full) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) o[i * p.seg()] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
-    } else {
+    for (int g = 0; g < E; g += 8) {
+      if (feed.whole(p, g)) {
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (i * p.seg() < left) o[i * p.seg()] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
+        for (int i = g; i < g + 8; ++i) o[i * p.seg()] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
+      } else {
+#pragma unroll
+        for (int i = g; i < g + 8; ++i)
+          if (i * p.seg() < left) o[i * p.seg()] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
+      }
     }
   }
 }
@@ -466,8 +476,7 @@ __global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
   };
   const float nw = GROUP ? part(p.lane / 32) : n, inv_nw = 1.0f / nw;
   const float nl = GROUP && wl < warps ? part(wl) : 0.0f;
-  // no lane of the warp holds anything past the row's end
-  const bool full = RAGGED ? feed.need == p.seg() * E * (int)sizeof(T) : N == p.L * E;
+  const bool full = N == p.L * E;  // no lane holds anything past the row's end
   char *out = reinterpret_cast<char *>(static_cast<T *>(a.y) + row * a.ldy);
 #pragma unroll 1
   for (int it = 0; it < steps; ++it) {
@@ -488,25 +497,28 @@ __global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
     s = GROUP ? warp_sum(s) : lanes_sum(s, p.L);
     float mean = div_n(s, nw, inv_nw);
     t0 = t1 = make_float2(0.0f, 0.0f);
-    if (full) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float2 c = add2(v[i], f2(-mean));
-        if (i & 1) t1 = fma2(c, c, t1);
-        else t0 = fma2(c, c, t0);
-      }
-    } else {
+    for (int g = 0; g < E; g += 8) {
+      if (RAGGED ? feed.whole(p, g) : full) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        float2 c = add2(v[i], f2(-mean));
-        if constexpr (RAGGED) {
-          if (column<V, E, RAGGED, MODE>(p.L, p.lane, 2 * i) >= N) c.x = 0.0f;
-          if (column<V, E, RAGGED, MODE>(p.L, p.lane, 2 * i + 1) >= N) c.y = 0.0f;
-        } else {
-          if (p.lane + 2 * i / V * p.L >= a.w.NV) c = make_float2(0.0f, 0.0f);
+        for (int i = g / 2; i < g / 2 + 4; ++i) {
+          const float2 c = add2(v[i], f2(-mean));
+          if (i & 1) t1 = fma2(c, c, t1);
+          else t0 = fma2(c, c, t0);
         }
-        if (i & 1) t1 = fma2(c, c, t1);
-        else t0 = fma2(c, c, t0);
+      } else {
+#pragma unroll
+        for (int i = g / 2; i < g / 2 + 4; ++i) {
+          float2 c = add2(v[i], f2(-mean));
+          if constexpr (RAGGED) {
+            if (column<V, E, RAGGED, MODE>(p.L, p.lane, 2 * i) >= N) c.x = 0.0f;
+            if (column<V, E, RAGGED, MODE>(p.L, p.lane, 2 * i + 1) >= N) c.y = 0.0f;
+          } else {
+            if (p.lane + 2 * i / V * p.L >= a.w.NV) c = make_float2(0.0f, 0.0f);
+          }
+          if (i & 1) t1 = fma2(c, c, t1);
+          else t0 = fma2(c, c, t0);
+        }
       }
     }
     t0 = add2(t0, t1);
@@ -538,7 +550,7 @@ __global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
         }
         v[i] = fma2(mul2(add2(v[i], f2(-mean)), f2(rstd)), gam[i], b);
       }
-      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), v, p, a.w.NV, N, full);
+      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), v, p, feed, a.w.NV, N);
     }
     row += a.w.step;
     out += a.w.inc[1];
@@ -752,8 +764,6 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
   for (int i = 0; i < P; ++i) dg[i] = db[i] = make_float2(0.0f, 0.0f);
   const float inv_n = a.w.inv_n;
   const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31, w0 = GROUP ? p.mine * warps : 0;
-  // no lane of the warp holds anything past the row's end
-  const bool full = RAGGED ? feed.need == p.seg() * E * (int)sizeof(T) : N == p.L * E;
   char *out = reinterpret_cast<char *>(static_cast<T *>(a.dx) + row * a.lddx);
   bool first = true;
   int run = 0;
@@ -823,7 +833,7 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
           const float2 t = mul2(add2(h[i], f2(-mean)), f2(rstd));
           d[i] = mul2(f2(rstd), fma2(gam[i], d[i], fma2(t, f2(-c2), f2(-c1))));
         }
-        store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(o), d, p, in ? a.w.NV : 0, in ? N : 0, full && in);
+        store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(o), d, p, feed, in ? a.w.NV : 0, N);
       };
       finish(row, m0, r0, c[0], c[1], out, true);
       feed.advance(a.w);
@@ -888,7 +898,7 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
         c2 *= inv_n;
 #pragma unroll
         for (int i = 0; i < P; ++i) d[i] = mul2(f2(rstd), add2(d[i], fma2(h[i], f2(-c2), f2(-c1))));
-        store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), d, p, a.w.NV, N, full);
+        store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), d, p, feed, a.w.NV, N);
       }
       row += a.w.step;
       out += a.w.inc[2];
