@@ -214,7 +214,7 @@ __host__ __device__ constexpr int row_slots(int block, int L, bool ragged) {
 //    least one byte of the row and up to 15 of those around it; the first and
 //    the last `fast` rows, where those may lie outside the tensor, are read from
 //    global memory by elements instead.
-template <typename T, int E, int TENSORS, int S, bool RAGGED, int MODE, bool PAIR = false>
+template <typename T, int E, int TENSORS, int S, bool RAGGED, int MODE>
 struct RowFeed {
   static constexpr int V = 16 / (int)sizeof(T);
   static constexpr int K = E / V;
@@ -263,7 +263,7 @@ struct RowFeed {
           cp_async16_if(p.at == 0 && o < end, s + o, q + o);
         }
       }
-    } else if (!RAGGED && (MODE == kPart || PAIR)) {  // lanes without a row take part in the sums: with zeros
+    } else if (!RAGGED && MODE == kPart) {  // lanes without a row take part in the warp's sums: with zeros
 #pragma unroll
       for (int i = 0; i < TENSORS * K; ++i)
         *reinterpret_cast<uint4 *>(mine + wr + i / K * w.plane + i % K * (int)blockDim.x * 16) =
@@ -280,7 +280,7 @@ struct RowFeed {
     return (g + 8) * p.seg() * (int)sizeof(T) <= need;
   }
 
-  // The oldest row (PAIR: the two oldest) has landed.
+  // The oldest row has landed.
   __device__ __forceinline__ void wait() const {
     cp_async_wait<S - 2>();
     if constexpr (RAGGED) __syncwarp();
@@ -321,9 +321,6 @@ struct RowFeed {
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) f[i] = make_float2(to_f32<T>(v[2 * i]), to_f32<T>(v[2 * i + 1]));
     }
-  }
-  __device__ __forceinline__ void back(const Walk &w) {
-    rd = rd == 0 ? (S - 1) * TENSORS * w.plane : rd - TENSORS * w.plane;
   }
   __device__ __forceinline__ void advance(const Walk &w) {
     rd = rd == (S - 1) * TENSORS * w.plane ? 0 : rd + TENSORS * w.plane;
@@ -637,11 +634,6 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormArgs a) {
 #ifndef BST
 #define BST (sizeof(T) == 4 ? 3 : 5)
 #endif
-// Whether groups take two rows a step.
-template <typename T>
-constexpr __host__ __device__ bool bwd_pairs(bool group, bool ragged) {
-  return group && !ragged && sizeof(T) == 2;
-}
 template <typename T>
 __host__ __device__ constexpr int bwd_stages() {
   return BST;
@@ -717,28 +709,13 @@ __device__ __forceinline__ void swap_halves(float v, float &u, float &w) {
   w = up ? v : other;
 }
 
-// Four sums over a warp at once: each quarter of the warp takes one, in every lane of the quarter.
-__device__ __forceinline__ float quarter_sums(float u0, float u1, float u2, float u3) {
-  const bool h = (threadIdx.x & 16) != 0, q = (threadIdx.x & 8) != 0;
-  const float k0 = (h ? u2 : u0) + __shfl_xor_sync(0xFFFFFFFFu, h ? u0 : u2, 16);
-  const float k1 = (h ? u3 : u1) + __shfl_xor_sync(0xFFFFFFFFu, h ? u1 : u3, 16);
-  float v = (q ? k1 : k0) + __shfl_xor_sync(0xFFFFFFFFu, q ? k0 : k1, 8);
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
 template <typename T, int MODE, bool RAGGED>
 __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
   constexpr bool GROUP = MODE == kGroup;
-  // Measured, one row a step and two: 32768 x 8192 bf16 301 and 290 us, 32768 x
-  // 1024 43.9 and 41.7; 16384 x 2048 fp32 70.9 and 74.8, ragged 8191 x 1001
-  // fp16 22.9 and 32.9 (single elements are read twice there).
-  constexpr bool PAIR = bwd_pairs<T>(GROUP, RAGGED);
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int E = kBwdElems, P = E / 2;
   constexpr int S = bwd_stages<T>();
-  __shared__ float red[2][4 * kBlock / 32];
+  __shared__ float red[2][2 * kBlock / 32];
   extern __shared__ __align__(16) unsigned char dyn[];
   pdl_prologue();
   const Place<MODE> p(a.w.L);
@@ -750,9 +727,9 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
   const int64_t r0 = (int64_t)blockIdx.x * a.w.rows;
   int64_t row = r0 + p.mine;
   const int steps = row_count(a.w.M, r0, a.w.step), left = row_count(a.w.M, row, a.w.step);  // the CTA's, this row's
-  RowFeed<T, E, 2, S, RAGGED, MODE, PAIR> feed(dyn, src, ld, p, a.w, row);
+  RowFeed<T, E, 2, S, RAGGED, MODE> feed(dyn, src, ld, p, a.w, row);
 #pragma unroll
-  for (int i = 0; i < (PAIR ? S : S - 1); ++i) feed.issue(p, a.w, i < left, row + (int64_t)i * a.w.step);
+  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.w, i < left, row + (int64_t)i * a.w.step);
   // The next row's statistics, loaded one row ahead and used as they are: past
   // its last row a lane stays at that row (at M - 1 if it has none), so that
   // nothing waits for the loads before the next row.
@@ -767,153 +744,67 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
   char *out = reinterpret_cast<char *>(static_cast<T *>(a.dx) + row * a.lddx);
   bool first = true;
   int run = 0;
-  if constexpr (PAIR) {
-    // Two rows a step: their sums meet at one barrier, and each fills the other's
-    // waits. The rows stay in the ring and are read twice.
-    float nmean1 = 0.0f, nrstd1 = 0.0f;
-    if (left > 1) {
-      nmean1 = a.mean[stat + a.w.step];
-      nrstd1 = a.rstd[stat + a.w.step];
-    }
 #pragma unroll 1
-    for (int it = 0; it < steps; it += 2) {
-      if (it >= left) break;  // the group has no row: only at the CTA's last step
-      const bool two = it + 1 < left;
-      const float m0 = nmean, r0 = nrstd, m1 = two ? nmean1 : 0.0f, r1 = two ? nrstd1 : 0.0f;
-      const int64_t row1 = row + a.w.step;
-      feed.wait();
-      // the next two rows' statistics (past the last row: its own again)
-      if (it + 2 < left) stat += 2 * (int64_t)a.w.step;
-      const int64_t stat1 = it + 3 < left ? stat + a.w.step : stat;
-      nmean = a.mean[stat];
-      nrstd = a.rstd[stat];
-      nmean1 = a.mean[stat1];
-      nrstd1 = a.rstd[stat1];
-      float c[4];
-      // Past the row's end dy and gamma are 0, so nothing there enters a sum that is used.
-      auto sums = [&](int64_t r, float mean, float rstd, float &c1, float &c2) {
-        float2 h[P], d[P], s1 = make_float2(0.0f, 0.0f), s2 = s1;
-        feed.read(0, src[0], ld[0], r, p, a.w, h);
-        feed.read(1, src[1], ld[1], r, p, a.w, d);
+  for (int it = 0; it < steps; ++it) {
+    const bool in = it < left;
+    const float mean = in ? nmean : 0.0f, rstd = in ? nrstd : 0.0f;
+    if (MODE != kPart && !in) break;  // whole warps without a row: only at the CTA's last step
+    feed.wait();
+    float2 h[P], d[P];
+    feed.read(0, src[0], ld[0], row, p, a.w, h);
+    feed.read(1, src[1], ld[1], row, p, a.w, d);
+    feed.advance(a.w);
+    feed.issue(p, a.w, it + S - 1 < left, row + (int64_t)(S - 1) * a.w.step);
+    if (it + 1 < left) stat += a.w.step;
+    nmean = a.mean[stat];
+    nrstd = a.rstd[stat];
+    // Past the row's end d and gamma are 0, so nothing there enters a sum that is used.
+    float2 s1[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)}, s2[2] = {s1[0], s1[0]};
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float2 t = mul2(d[i], mul2(add2(h[i], f2(-mean)), f2(rstd)));
-          dg[i] = add2(dg[i], t);
-          db[i] = add2(db[i], d[i]);
-          s1 = fma2(gam[i], d[i], s1);
-          s2 = fma2(gam[i], t, s2);
-        }
-        c1 = s1.x + s1.y;
-        c2 = s2.x + s2.y;
-      };
-      sums(row, m0, r0, c[0], c[1]);
-      feed.advance(a.w);
-      sums(row1, m1, r1, c[2], c[3]);
-      feed.back(a.w);
-      const int par = (it >> 1) & 1;
-      float v = quarter_sums(c[0], c[1], c[2], c[3]);
-      if ((wl & 7) == 0) red[par][4 * (w0 + p.lane / 32) + (wl >> 3)] = v;
+    for (int i = 0; i < P; ++i) {
+      h[i] = mul2(add2(h[i], f2(-mean)), f2(rstd));
+      dg[i] = fma2(d[i], h[i], dg[i]);
+      db[i] = add2(db[i], d[i]);
+      d[i] = mul2(gam[i], d[i]);
+      s1[i & 1] = add2(s1[i & 1], d[i]);
+      s2[i & 1] = fma2(d[i], h[i], s2[i & 1]);
+    }
+    s1[0] = add2(s1[0], s1[1]);
+    s2[0] = add2(s2[0], s2[1]);
+    float c1 = s1[0].x + s1[0].y, c2 = s2[0].x + s2[0].y;
+    if constexpr (GROUP) {
+      const int par = it & 1;
+      float v = half_sums(c1, c2);
+      if ((wl & 15) == 0) red[par][2 * (w0 + p.lane / 32) + (wl >> 4)] = v;
       group_barrier(p.mine, p.L);
-      {
-        const int i = wl & 7;
-        const float *q = red[par] + 4 * (w0 + i) + (wl >> 3);
-        v = (i < warps ? q[0] : 0.0f) + (i + 8 < warps ? q[32] : 0.0f);
-      }
+      v = (wl & 15) < warps ? red[par][2 * (w0 + (wl & 15)) + (wl >> 4)] : 0.0f;
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      v *= inv_n;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = __shfl_sync(0xFFFFFFFFu, v, 8 * i);
-      auto finish = [&](int64_t r, float mean, float rstd, float c1, float c2, char *o, bool in) {
-        float2 h[P], d[P];
-        feed.read(0, src[0], ld[0], r, p, a.w, h);
-        feed.read(1, src[1], ld[1], r, p, a.w, d);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float2 t = mul2(add2(h[i], f2(-mean)), f2(rstd));
-          d[i] = mul2(f2(rstd), fma2(gam[i], d[i], fma2(t, f2(-c2), f2(-c1))));
-        }
-        store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(o), d, p, feed, in ? a.w.NV : 0, N);
-      };
-      finish(row, m0, r0, c[0], c[1], out, true);
-      feed.advance(a.w);
-      finish(row1, m1, r1, c[2], c[3], out + a.w.inc[2], two);
-      feed.advance(a.w);
-      feed.issue(p, a.w, it + S < left, row + (int64_t)S * a.w.step);
-      feed.issue(p, a.w, it + S + 1 < left, row + (int64_t)(S + 1) * a.w.step);
-      row += 2 * (int64_t)a.w.step;
-      out += 2 * a.w.inc[2];
-      if ((run += 2) == kRunRows) {
-        flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
-        first = false;
-        run = 0;
-      }
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      swap_halves(v, c1, c2);
+    } else if constexpr (MODE == kWarp) {
+      swap_halves(half_sums(c1, c2), c1, c2);
+    } else {
+      c1 = lanes_sum(c1, p.L);
+      c2 = lanes_sum(c2, p.L);
     }
-  } else {
-#pragma unroll 1
-    for (int it = 0; it < steps; ++it) {
-      const bool in = it < left;
-      const float mean = in ? nmean : 0.0f, rstd = in ? nrstd : 0.0f;
-      if (MODE != kPart && !in) break;  // whole warps without a row: only at the CTA's last step
-      feed.wait();
-      float2 h[P], d[P];
-      feed.read(0, src[0], ld[0], row, p, a.w, h);
-      feed.read(1, src[1], ld[1], row, p, a.w, d);
-      feed.advance(a.w);
-      feed.issue(p, a.w, it + S - 1 < left, row + (int64_t)(S - 1) * a.w.step);
-      if (it + 1 < left) stat += a.w.step;
-      nmean = a.mean[stat];
-      nrstd = a.rstd[stat];
-      // Past the row's end d and gamma are 0, so nothing there enters a sum that is used.
-      float2 s1[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)}, s2[2] = {s1[0], s1[0]};
+    if (MODE != kPart || in) {
+      c1 *= inv_n;
+      c2 *= inv_n;
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        h[i] = mul2(add2(h[i], f2(-mean)), f2(rstd));
-        dg[i] = fma2(d[i], h[i], dg[i]);
-        db[i] = add2(db[i], d[i]);
-        d[i] = mul2(gam[i], d[i]);
-        s1[i & 1] = add2(s1[i & 1], d[i]);
-        s2[i & 1] = fma2(d[i], h[i], s2[i & 1]);
-      }
-      s1[0] = add2(s1[0], s1[1]);
-      s2[0] = add2(s2[0], s2[1]);
-      float c1 = s1[0].x + s1[0].y, c2 = s2[0].x + s2[0].y;
-      if constexpr (GROUP) {
-        const int par = it & 1;
-        float v = half_sums(c1, c2);
-        if ((wl & 15) == 0) red[par][2 * (w0 + p.lane / 32) + (wl >> 4)] = v;
-        group_barrier(p.mine, p.L);
-        v = (wl & 15) < warps ? red[par][2 * (w0 + (wl & 15)) + (wl >> 4)] : 0.0f;
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        swap_halves(v, c1, c2);
-      } else if constexpr (MODE == kWarp) {
-        swap_halves(half_sums(c1, c2), c1, c2);
-      } else {
-        c1 = lanes_sum(c1, p.L);
-        c2 = lanes_sum(c2, p.L);
-      }
-      if (MODE != kPart || in) {
-        c1 *= inv_n;
-        c2 *= inv_n;
-#pragma unroll
-        for (int i = 0; i < P; ++i) d[i] = mul2(f2(rstd), add2(d[i], fma2(h[i], f2(-c2), f2(-c1))));
-        store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), d, p, feed, a.w.NV, N);
-      }
-      row += a.w.step;
-      out += a.w.inc[2];
-      if (++run == kRunRows) {
-        flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
-        first = false;
-        run = 0;
-      }
+      for (int i = 0; i < P; ++i) d[i] = mul2(f2(rstd), add2(d[i], fma2(h[i], f2(-c2), f2(-c1))));
+      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), d, p, feed, a.w.NV, N);
+    }
+    row += a.w.step;
+    out += a.w.inc[2];
+    if (++run == kRunRows) {
+      flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
+      first = false;
+      run = 0;
     }
   }
   // Every warp of the CTA flushes equally often: one that left at the last step
   // joins the flush that the others make in it or here.
-  const int odd = PAIR ? (steps + 1) / 2 * 2 % kRunRows : steps % kRunRows;
-  const bool gone = PAIR ? left <= (steps - 1) / 2 * 2 : MODE != kPart && left < steps;
-  if (odd != 0 || gone) flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
+  if (steps % kRunRows != 0 || (MODE != kPart && left < steps)) flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
   cp_async_wait<0>();
 }
 
