@@ -17,18 +17,16 @@ using dyt::loss::LossArgs;
 using dyt::loss::LossGradArgs;
 
 constexpr int kOpLossForward = 7, kOpLossBackward = 8;  // dyt_launch_info::op
-// The forward: 512 threads on an SM, their rings full of shared memory. A warp
-// gets several items, so that the last ones do not leave most of the SMs idle;
-// parts of less than kPartMin bytes would be mostly set-up.
+// The forward: 512 threads on an SM, their rings full of shared memory.
 constexpr int kRowsPerSm = 512;
-constexpr int kItemsPerWarp = 2;
-constexpr int64_t kPartMin = 4096;
+constexpr int kMostParts = 256;  // parts of a row, at most
 constexpr int kFinishCtasPerSm = 2;
 
 constexpr int kGradBlock = 256;
 constexpr int kGradCtasPerSm = 8;     // 2048 resident threads
 constexpr int64_t kWarpRow = 8192;    // rows of at most this many bytes take a warp
 constexpr int64_t kGradPart = 65536;  // the largest part of a row, bytes
+constexpr int64_t kGradPartMin = 4096;  // and the smallest
 
 template <typename F>
 dyt_status with_type(int xd, F &&f) {
@@ -44,6 +42,7 @@ dyt_status with_type(int xd, F &&f) {
 struct LossPlan {
   bool cta;      // backward: a part of a row is a CTA's, else a warp's
   int S;         // parts of a row
+  int most;      // forward: the parts that there is room for
   int block;
   int64_t grid;  // CTAs
   int finish;    // forward: CTAs of the second kernel
@@ -53,31 +52,19 @@ struct LossPlan {
 LossPlan plan_forward(int64_t M, int64_t N, size_t es, int sms) {
   LossPlan p = {};
   const int64_t bytes = N * (int64_t)es, warps = (int64_t)sms * (kRowsPerSm / 32);
-  // At least kItemsPerWarp items a warp, in as nearly whole rounds as a few
-  // parts more can make them: 4096 rows over 2368 warps are 1.73 rounds whole,
-  // 6.92 in four parts.
-  const int64_t most = std::max<int64_t>(1, bytes / kPartMin);
-  p.S = 1;
-  const int64_t least = std::min(most, ceil_div(warps * kItemsPerWarp, M));
-  double best = -1.0;
-  for (int64_t S = least; S <= std::min(most, least + 8); ++S) {
-    const double rounds = (double)M * (double)S / (double)warps, even = rounds / std::ceil(rounds);
-    if (even > best + 0.02) {
-      best = even;
-      p.S = (int)S;
-    }
-    if (S == 1 && rounds > 8.0) break;
-  }
+  const int64_t batches = std::max<int64_t>(1, ceil_div(bytes, 16) / (dyt::loss::kBatch * 32));
+  p.S = dyt::loss::choose_parts((float)M, (float)warps, (int)std::min<int64_t>(batches, kMostParts));
+  p.most = (int)std::max<int64_t>(p.S, std::min<int64_t>(batches, dyt::loss::kListedParts));
   const int64_t items = M * p.S;
   // few items: small CTAs, one warp's work after the other over all SMs
   p.block = dyt::loss::kRowsBlock;
   while (p.block > 32 && ceil_div(items, p.block / 32) < 2 * (int64_t)sms) p.block >>= 1;
   p.grid = std::min<int64_t>(ceil_div(items, p.block / 32), (int64_t)sms * (kRowsPerSm / p.block));
-  const int64_t per = p.S > dyt::loss::kThreadParts ? dyt::loss::kFinishBlock / 32 : dyt::loss::kFinishBlock;
+  const int64_t per = p.most > dyt::loss::kThreadParts ? dyt::loss::kFinishBlock / 32 : dyt::loss::kFinishBlock;
   p.finish = (int)std::min<int64_t>(ceil_div(M, per), (int64_t)sms * kFinishCtasPerSm);
-  p.off_sums = ((size_t)items * sizeof(float2) + 15) & ~(size_t)15;
+  p.off_sums = ((size_t)M * (size_t)p.most * sizeof(float2) + 15) & ~(size_t)15;
   p.off_done = p.off_sums + (size_t)p.finish * sizeof(double);
-  p.bytes = (p.off_done + sizeof(unsigned) + 15) & ~(size_t)15;
+  p.bytes = (p.off_done + 2 * sizeof(unsigned) + 15) & ~(size_t)15;
   return p;
 }
 
@@ -90,7 +77,7 @@ LossPlan plan_backward(int64_t M, int64_t N, size_t es, int sms) {
   p.S = 1;
   p.block = kGradBlock;
   if (p.cta)
-    p.S = (int)std::max<int64_t>(M < slots ? std::max<int64_t>(1, std::min(slots / M, bytes / kPartMin)) : 1,
+    p.S = (int)std::max<int64_t>(M < slots ? std::max<int64_t>(1, std::min(slots / M, bytes / kGradPartMin)) : 1,
                                  ceil_div(bytes, kGradPart));
   const int64_t items = p.cta ? M * p.S : ceil_div(M, kGradBlock / 32);
   p.grid = std::min<int64_t>(items, (int64_t)1 << 30);
@@ -149,6 +136,7 @@ dyt_status dyt_policy_loss_forward(const void *logits, int64_t ld, const void *t
     record(kOpLossForward, nullptr, 0, 0, 0);
     return DYT_OK;
   }
+  if (M == 1) ld = N;  // one row has no pitch
   const size_t es = dsize(dtype);
   if (!logits || !tokens || !old_logp || !advantage || !logp || !stats || !coef || !workspace ||
       !elem_aligned(logits, es) || !elem_aligned(tokens, token_bytes) || !elem_aligned(old_logp, 4) ||
@@ -180,12 +168,13 @@ dyt_status dyt_policy_loss_forward(const void *logits, int64_t ld, const void *t
   a.M = M;
   a.N = N;
   a.S = p.S;
-  const int64_t vecs = ceil_div(N, 16 / (int64_t)es), batch = dyt::loss::kBatch * 32;
-  a.part_vecs = (int)(ceil_div(ceil_div(vecs, batch), p.S) * batch);
-  a.aligned = N % (16 / (int64_t)es) == 0 && aligned16(logits) && (M == 1 || vec_pitch(ld, es));
-  const int64_t warps = p.grid * (p.block / 32);
-  a.row_step = warps % M;
-  a.part_step = (int)(warps / M);
+  a.most = p.most;
+  a.batches = (int)ceil_div(ceil_div(N * (int64_t)es, 16), dyt::loss::kBatch * 32);
+  // A list for few rows only: every CTA reads all the weights, and a warp looks
+  // up at most 32 items in it. Small CTAs have little work to spread.
+  a.listed = weight != nullptr && M <= dyt::loss::kMaxListed && p.block == dyt::loss::kRowsBlock &&
+             M * p.most <= 32 * p.grid * (p.block / 32);
+  a.aligned = N % (16 / (int64_t)es) == 0 && aligned16(logits) && vec_pitch(ld, es);
   a.wide_tokens = token_bytes == 8;
   a.C = C;
   a.inv_t = 1.0 / temperature;
@@ -223,6 +212,7 @@ dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *
     record(kOpLossBackward, nullptr, 0, 0, 0);
     return DYT_OK;
   }
+  if (M == 1) ld = lddl = N;  // one row has no pitch
   const size_t es = dsize(dtype);
   if (!logits || !tokens || !stats || !coef || !dlogits || !elem_aligned(logits, es) ||
       !elem_aligned(tokens, token_bytes) || !elem_aligned(stats, 8) || !elem_aligned(coef, 4) ||
@@ -249,7 +239,7 @@ dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *
   a.wide_tokens = token_bytes == 8;
   a.C = C;
   a.inv_t = 1.0 / temperature;
-  const bool shift = !same_offset(logits, dlogits) || (M > 1 && !vec_pitch(ld - lddl, es));
+  const bool shift = !same_offset(logits, dlogits) || !vec_pitch(ld - lddl, es);
   return with_type(dtype, [&](auto t) -> dyt_status {
     using T = decltype(t);
     PdlConfig lc((unsigned)p.grid, p.block, 0, (cudaStream_t)stream);

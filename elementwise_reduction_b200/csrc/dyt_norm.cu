@@ -177,6 +177,7 @@ dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma,
   if (!valid_dtype(gamma_dtype) || !valid_dtype(beta_dtype)) return DYT_ERR_UNSUPPORTED_DTYPE;
   if (!(eps >= 0.0f) || std::isinf(eps)) return DYT_ERR_INVALID_VALUE;
   if (check_pitch(M, N, ldx) != DYT_OK || check_pitch(M, N, ldy) != DYT_OK) return DYT_ERR_INVALID_VALUE;
+  if (M == 1) ldx = ldy = N;  // one row has no pitch
   if (M == 0 || N == 0) {
     record(kOpNormForward, nullptr, 0, 0, 0, 0);
     return DYT_OK;
@@ -191,7 +192,7 @@ dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma,
   return with_type(x_dtype, [&](auto t) -> dyt_status {
     using T = decltype(t);
     constexpr int VE = vec_elems<T>();
-    const bool vec = N % VE == 0 && aligned16(x) && aligned16(y) && (M == 1 || (vec_pitch(ldx, es) && vec_pitch(ldy, es)));
+    const bool vec = N % VE == 0 && aligned16(x) && aligned16(y) && vec_pitch(ldx, es) && vec_pitch(ldy, es);
     const RowPlan p = plan_rows(M, N, VE, vec, dyt::norm::fwd_elems<T>(!vec), sms);
     const FwdKernel k = fwd_kernel<T>(p);
     const size_t smem = p.rowlong ? 0 : dyt::norm::fwd_smem<T>(p.block, p.L, p.ragged);
@@ -232,6 +233,7 @@ dyt_status dyt_layer_norm_backward(const void *x, int64_t ldx, const void *dy, i
   if (check_pitch(M, N, ldx) != DYT_OK || check_pitch(M, N, lddy) != DYT_OK || check_pitch(M, N, lddx) != DYT_OK)
     return DYT_ERR_INVALID_VALUE;
   if (!param_ok(dgamma, gamma_dtype) || !param_ok(dbeta, beta_dtype)) return DYT_ERR_INVALID_VALUE;
+  if (M == 1) ldx = lddy = lddx = N;  // one row has no pitch
   const cudaStream_t s = (cudaStream_t)stream;
   if (M == 0 || N == 0) {
     cudaError_t e = cudaSuccess;  // empty sums
@@ -253,7 +255,7 @@ dyt_status dyt_layer_norm_backward(const void *x, int64_t ldx, const void *dy, i
     using T = decltype(t);
     constexpr int VE = vec_elems<T>();
     const bool vec = N % VE == 0 && aligned16(x) && aligned16(dy) && aligned16(dx) &&
-                     (M == 1 || (vec_pitch(ldx, es) && vec_pitch(lddy, es) && vec_pitch(lddx, es)));
+                     vec_pitch(ldx, es) && vec_pitch(lddy, es) && vec_pitch(lddx, es);
     const BwdPlan b = plan_bwd(M, N, VE, vec, sms);
     if (workspace_bytes < b.bytes) return DYT_ERR_WORKSPACE_TOO_SMALL;
     double *parts = (double *)workspace;

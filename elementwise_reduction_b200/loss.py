@@ -14,8 +14,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._tensors import (_code, _current, _elsewhere, _fresh, _fresh_rows, _like, _pitch, _there, _vector, _workspace,
-                       row_pitch)
+from ._tensors import (_code, _current, _elsewhere, _fresh, _fresh_rows, _like, _pitch, _scratch, _there, _vector,
+                       _workspace, row_pitch)
 
 _F32 = (torch.float32,)
 _TOKEN = (torch.int64, torch.int32)
@@ -34,7 +34,7 @@ def policy_loss_workspace(logits: torch.Tensor) -> torch.Tensor:
             return policy_loss_workspace(logits)
     M, N = _shape(logits)
     n = _abi.lib.dyt_policy_loss_workspace_bytes(M, N, _code(logits, "logits"))
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=logits.device)
+    return _scratch(n, logits.device)
 
 
 def policy_loss_forward(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch.Tensor, advantage: torch.Tensor,
@@ -56,13 +56,14 @@ def policy_loss_forward(logits: torch.Tensor, tokens: torch.Tensor, old_logp: to
     ld, code, dev, rows = _pitch(logits, "logits"), _code(logits, "logits"), logits.device, logits.shape[:-1]
     if ws is None:
         n = _abi.lib.dyt_policy_loss_workspace_bytes(M, N, code)
-        ws = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
+        ws = _scratch(n, dev)
         wp = ws.data_ptr()
     else:
         wp, n = _workspace(ws, dev), ws.numel()
-    loss = torch.empty((), dtype=torch.float32, device=dev)
+    loss = torch.empty_strided((), (), dtype=torch.float32, device=dev)
     logp, coef = _fresh_rows(rows, dev), _fresh_rows(rows, dev)
-    stats = torch.empty((*rows, 2), dtype=torch.float32, device=dev)
+    stats = (torch.empty_strided((M, 2), (2, 1), dtype=torch.float32, device=dev) if len(rows) == 1 else
+             torch.empty((*rows, 2), dtype=torch.float32, device=dev))
     st = _abi.lib.dyt_policy_loss_forward(
         logits.data_ptr(), ld, _vector(tokens, "tokens", M, dev, _TOKEN), tokens.element_size(),
         _vector(old_logp, "old_logp", M, dev, _F32),

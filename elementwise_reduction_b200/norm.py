@@ -10,8 +10,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._tensors import (DTYPE_CODE, _code, _current, _elsewhere, _fresh, _fresh_rows, _like, _pitch, _there, _vector,
-                       _workspace, row_pitch)
+from ._tensors import (DTYPE_CODE, _code, _current, _elsewhere, _fresh, _fresh_rows, _like, _pitch, _scratch, _there,
+                       _vector, _workspace, row_pitch)
 
 _F32 = (torch.float32,)
 _PARAM = tuple(DTYPE_CODE)
@@ -67,7 +67,7 @@ def layer_norm_workspace(x: torch.Tensor) -> torch.Tensor:
             return layer_norm_workspace(x)
     M, N = _shape(x)
     n = _abi.lib.dyt_layer_norm_backward_workspace_bytes(M, N, _code(x, "x"))
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
+    return _scratch(n, x.device)
 
 
 def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -113,7 +113,7 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
     rows = x.shape[:-1].numel()
     if ws is None:
         n = _abi.lib.dyt_layer_norm_backward_workspace_bytes(M, N, code)
-        ws = torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=dev)
+        ws = _scratch(n, dev)
         wp = ws.data_ptr()
     else:
         wp, n = _workspace(ws, dev), ws.numel()
