@@ -201,7 +201,7 @@ dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma,
     const int64_t grid = std::min<int64_t>(ceil_div(M, p.rows), (int64_t)sms);
     const int64_t lds[2] = {ldx, ldy};
     NormArgs a = {x, ldx, gamma, beta, y, ldy, mean, rstd, (int)gamma_dtype, (int)beta_dtype, eps, {}};
-    a.w = walk_of(p, M, N, grid, lds, 2, es, p.rowlong ? 0 : dyt::norm::fwd_plane<T>(p.block, p.L, p.ragged));
+    a.w = walk_of(p, M, N, grid, lds, 2, es, p.rowlong ? 0 : dyt::norm::fwd_plane<T>(32, p.L, p.ragged));
     PdlConfig lc((unsigned)grid, p.block, smem, (cudaStream_t)stream);
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -262,7 +262,7 @@ dyt_status dyt_layer_norm_backward(const void *x, int64_t ldx, const void *dy, i
     const int64_t lds[3] = {ldx, lddy, lddx};
     NormGradArgs a = {x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, parts, (int)gamma_dtype, {}};
     a.w = walk_of(b.r, M, N, b.grid, lds, 3, es,
-                  b.r.rowlong ? 0 : dyt::norm::row_slots<T, dyt::norm::kBwdElems>(b.r.block, b.r.L, b.r.ragged));
+                  b.r.rowlong ? 0 : dyt::norm::row_slots<T, dyt::norm::kBwdElems>(32, b.r.L, b.r.ragged));
     int kernels = 2;
     cudaError_t e;
     if (b.r.rowlong) {

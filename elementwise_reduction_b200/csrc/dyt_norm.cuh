@@ -32,7 +32,7 @@ struct Walk {
   int step;      // grid x rows
   int64_t inc[3];  // bytes from a row to the one a step later: the inputs, the output
   int64_t fast;  // ragged rows: [fast, M - fast) are copied in whole 16-byte chunks
-  int plane;     // bytes of a tensor's row in the ring, for the whole block
+  int plane;     // bytes of the slots that a warp has for one tensor's rows (read for ragged rows of part of a warp)
   float n, inv_n;
 };
 
@@ -223,12 +223,19 @@ struct RowFeed {
   int need;                 // RAGGED: bytes of the row in this warp's stretch
   int wr = 0, rd = 0;       // byte offsets of the stages to copy to and to read
 
+  // Bytes of a warp's slots for one tensor's rows; its ring is S x TENSORS of them.
+  static __device__ __forceinline__ int plane(const Walk &w) {
+    if constexpr (!RAGGED) return K * 512;
+    else if constexpr (MODE != kPart) return (32 * K + 1) * 16;
+    else return w.plane;
+  }
+
   __device__ __forceinline__ RowFeed(unsigned char *ring, const T *const (&base)[TENSORS],
                                      const int64_t (&ld)[TENSORS], const Place<MODE> &p, const Walk &w,
                                      int64_t first) {
     const int t = (int)threadIdx.x, N = (int)w.N;
     const int c0 = RAGGED ? column<V, E, true, MODE>(p.L, p.lane - p.at, 0) : p.lane * V;
-    mine = ring + (RAGGED ? t / p.seg() * (p.seg() * K + 1) : t) * 16;
+    mine = ring + (t >> 5) * (S * TENSORS * plane(w)) + (RAGGED ? (t & 31) / p.seg() * (p.seg() * K + 1) : t & 31) * 16;
     need = (N - c0 < p.seg() * E ? N - c0 : p.seg() * E) * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < TENSORS; ++i) at[i] = reinterpret_cast<const char *>(base[i] + first * ld[i] + c0);
@@ -236,7 +243,7 @@ struct RowFeed {
       for (int i = 0; i < S * TENSORS; ++i)
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          *reinterpret_cast<uint4 *>(mine + i * w.plane + k * (int)blockDim.x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4 *>(mine + i * plane(w) + k * 512) = make_uint4(0u, 0u, 0u, 0u);
     }
   }
 
@@ -245,11 +252,11 @@ struct RowFeed {
     if (RAGGED ? row >= w.fast && row < w.M - w.fast : in) {
 #pragma unroll
       for (int t = 0; t < TENSORS; ++t) {
-        unsigned char *s = mine + wr + t * w.plane;
+        unsigned char *s = mine + wr + t * plane(w);
         if constexpr (!RAGGED) {
 #pragma unroll
           for (int k = 0; k < K; ++k)
-            cp_async16_if(p.lane + k * p.L < w.NV, s + k * (int)blockDim.x * 16, at[t] + (int64_t)(k * p.L) * 16);
+            cp_async16_if(p.lane + k * p.L < w.NV, s + k * 512, at[t] + (int64_t)(k * p.L) * 16);
         } else {
           const int d = (int)((uintptr_t)at[t] & 15u);
           const char *q = at[t] - d;
@@ -266,11 +273,10 @@ struct RowFeed {
     } else if (!RAGGED && MODE == kPart) {  // lanes without a row take part in the warp's sums: with zeros
 #pragma unroll
       for (int i = 0; i < TENSORS * K; ++i)
-        *reinterpret_cast<uint4 *>(mine + wr + i / K * w.plane + i % K * (int)blockDim.x * 16) =
-            make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(mine + wr + i / K * plane(w) + i % K * 512) = make_uint4(0u, 0u, 0u, 0u);
     }
     cp_async_commit();
-    wr = wr == (S - 1) * TENSORS * w.plane ? 0 : wr + TENSORS * w.plane;
+    wr = wr == (S - 1) * TENSORS * plane(w) ? 0 : wr + TENSORS * plane(w);
 #pragma unroll
     for (int t = 0; t < TENSORS; ++t) at[t] += w.inc[t];
   }
@@ -290,11 +296,11 @@ struct RowFeed {
   __device__ __forceinline__ void read(int t, const T *base, int64_t ld, int64_t r, const Place<MODE> &p, const Walk &w,
                                        float2 (&f)[E / 2]) const {
     const int N = (int)w.N;
-    const unsigned char *s = mine + rd + t * w.plane;
+    const unsigned char *s = mine + rd + t * plane(w);
     if constexpr (!RAGGED) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        VecIO<T, V>::unpack2(*reinterpret_cast<const uint4 *>(s + k * (int)blockDim.x * 16),
+        VecIO<T, V>::unpack2(*reinterpret_cast<const uint4 *>(s + k * 512),
                              *reinterpret_cast<float2(*)[V / 2]>(f + k * (V / 2)));
     } else {
       const int c0 = column<V, E, true, MODE>(p.L, p.lane, 0), left = N - c0;  // element i is inside while i seg < left
@@ -323,7 +329,7 @@ struct RowFeed {
     }
   }
   __device__ __forceinline__ void advance(const Walk &w) {
-    rd = rd == (S - 1) * TENSORS * w.plane ? 0 : rd + TENSORS * w.plane;
+    rd = rd == (S - 1) * TENSORS * plane(w) ? 0 : rd + TENSORS * plane(w);
   }
 };
 
@@ -416,8 +422,12 @@ __host__ __device__ constexpr int fwd_plane(int block, int L, bool ragged) {
   return ragged ? row_slots<T, fwd_elems<T>(true)>(block, L, true) : row_slots<T, fwd_elems<T>(false)>(block, L, false);
 }
 template <typename T>
+__host__ __device__ constexpr size_t fwd_ring(int block, int L, bool ragged) {
+  return (size_t)fwd_stages<T>() * fwd_plane<T>(block, L, ragged) * 16;
+}
+template <typename T>
 __host__ __device__ constexpr size_t fwd_smem(int block, int L, bool ragged) {
-  return (size_t)fwd_stages<T>() * fwd_plane<T>(block, L, ragged) * 16 +
+  return fwd_ring<T>(block, L, ragged) +
          (fwd_beta_shared<T>(ragged) ? (size_t)block * fwd_elems<T>(ragged) * sizeof(float) : 0);
 }
 
@@ -445,13 +455,15 @@ __global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) feed.issue(p, a.w, i < left, row + (int64_t)i * a.w.step);
   constexpr bool BS = fwd_beta_shared<T>(RAGGED);
-  float4 *bslot = reinterpret_cast<float4 *>(dyn + S * a.w.plane) + threadIdx.x;  // this thread's own
+  // this thread's own slots, 32 apart
+  float4 *bslot = reinterpret_cast<float4 *>(dyn + fwd_ring<T>((int)blockDim.x, p.L, RAGGED)) +
+                  (threadIdx.x >> 5) * (P / 2 * 32) + (threadIdx.x & 31);
   float2 gam[P], bet[BS ? 1 : P];
   if constexpr (BS) {
     load_pairs<V, E, RAGGED, MODE>(a.beta, a.beta_dt, p, N, 0.0f, gam);
 #pragma unroll
     for (int i = 0; i < P / 2; ++i)
-      bslot[i * blockDim.x] = make_float4(gam[2 * i].x, gam[2 * i].y, gam[2 * i + 1].x, gam[2 * i + 1].y);
+      bslot[i * 32] = make_float4(gam[2 * i].x, gam[2 * i].y, gam[2 * i + 1].x, gam[2 * i + 1].y);
   } else {
     load_pairs<V, E, RAGGED, MODE>(a.beta, a.beta_dt, p, N, 0.0f, bet);
   }
@@ -538,7 +550,7 @@ __global__ void __launch_bounds__(kBlock, 1) norm_fwd_kernel(NormArgs a) {
       for (int i = 0; i < P; ++i) {
         float2 b;
         if constexpr (BS) {
-          const float2 *q = reinterpret_cast<const float2 *>(bslot + i / 2 * blockDim.x);
+          const float2 *q = reinterpret_cast<const float2 *>(bslot + i / 2 * 32);
           b = q[i & 1];
         } else {
           b = bet[i];
