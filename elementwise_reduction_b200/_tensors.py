@@ -87,11 +87,12 @@ def _scratch(n: int, device: torch.device) -> torch.Tensor:
     return torch.empty_strided((n if n > 16 else 16,), (1,), dtype=torch.uint8, device=device)
 
 
-def _elsewhere(t: torch.Tensor, stream: torch.cuda.Stream | None) -> bool:
-    """Whether a call on t's data has to switch the current device or stream (see _there)."""
-    if not t.is_cuda:
+def _elsewhere(index: int, stream: torch.cuda.Stream | None) -> bool:
+    """Whether a call on the data of device `index` (a tensor's get_device()) has to
+    switch the current device or stream (see _there)."""
+    if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    return stream is not None or t.device.index != torch.cuda.current_device()
+    return stream is not None or index != torch._C._cuda_getDevice()
 
 
 def _there(t: torch.Tensor, stream: torch.cuda.Stream | None):
@@ -104,27 +105,27 @@ def _there(t: torch.Tensor, stream: torch.cuda.Stream | None):
     return torch.cuda.stream(stream)
 
 
-def _vector(t: torch.Tensor, what: str, n: int, device: torch.device, dtypes) -> int:
-    """The address of a contiguous tensor of n elements on `device`."""
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}")
+def _vector(t: torch.Tensor, what: str, n: int, index: int, dtypes) -> int:
+    """The address of a contiguous tensor of n elements on device `index`."""
+    if t.get_device() == index and t.dtype in dtypes and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{what} must be on cuda:{index}")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype} is not supported ({', '.join(str(d)[6:] for d in dtypes)})")
     if t.numel() != n:
         raise ValueError(f"{what} must have {n} elements, not {t.numel()}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be contiguous")
 
 
 def _like(t: torch.Tensor, what: str, x: torch.Tensor) -> int:
     """The row pitch of a tensor of x's shape, dtype and device."""
-    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+    if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != x.get_device():
         raise ValueError(f"{what} must match its input in shape, dtype and device")
     return _pitch(t, what)
 
 
-def _workspace(ws: torch.Tensor, device: torch.device) -> int:
-    if ws.device != device or not ws.is_contiguous() or ws.dtype != torch.uint8:
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+def _workspace(ws: torch.Tensor, index: int) -> int:
+    if ws.get_device() != index or not ws.is_contiguous() or ws.dtype != torch.uint8:
+        raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{index}")
     return ws.data_ptr()

@@ -29,7 +29,7 @@ def _shape(logits: torch.Tensor) -> tuple[int, int]:
 
 def policy_loss_workspace(logits: torch.Tensor) -> torch.Tensor:
     """A device workspace large enough for policy_loss_forward on the logits' shape and device."""
-    if _elsewhere(logits, None):
+    if _elsewhere(logits.get_device(), None):
         with _there(logits, None):
             return policy_loss_workspace(logits)
     M, N = _shape(logits)
@@ -48,7 +48,8 @@ def policy_loss_forward(logits: torch.Tensor, tokens: torch.Tensor, old_logp: to
     logits may be a row-strided view; tokens are int64 or int32, the other inputs
     float32, contiguous. Without weight every row weighs 1 / rows; without ref_logp
     (or with kl_coef 0) there is no KL term."""
-    if _elsewhere(logits, stream):
+    index = logits.get_device()
+    if _elsewhere(index, stream):
         with _there(logits, stream):
             return policy_loss_forward(logits, tokens, old_logp, advantage, ref_logp, weight, clip_low, clip_high,
                                        kl_coef, temperature, ws)
@@ -59,19 +60,19 @@ def policy_loss_forward(logits: torch.Tensor, tokens: torch.Tensor, old_logp: to
         ws = _scratch(n, dev)
         wp = ws.data_ptr()
     else:
-        wp, n = _workspace(ws, dev), ws.numel()
+        wp, n = _workspace(ws, index), ws.numel()
     loss = torch.empty_strided((), (), dtype=torch.float32, device=dev)
     logp, coef = _fresh_rows(rows, dev), _fresh_rows(rows, dev)
     stats = (torch.empty_strided((M, 2), (2, 1), dtype=torch.float32, device=dev) if len(rows) == 1 else
              torch.empty((*rows, 2), dtype=torch.float32, device=dev))
     st = _abi.lib.dyt_policy_loss_forward(
-        logits.data_ptr(), ld, _vector(tokens, "tokens", M, dev, _TOKEN), tokens.element_size(),
-        _vector(old_logp, "old_logp", M, dev, _F32),
-        None if ref_logp is None else _vector(ref_logp, "ref_logp", M, dev, _F32),
-        _vector(advantage, "advantage", M, dev, _F32),
-        None if weight is None else _vector(weight, "weight", M, dev, _F32), clip_low, clip_high, kl_coef,
+        logits.data_ptr(), ld, _vector(tokens, "tokens", M, index, _TOKEN), tokens.element_size(),
+        _vector(old_logp, "old_logp", M, index, _F32),
+        None if ref_logp is None else _vector(ref_logp, "ref_logp", M, index, _F32),
+        _vector(advantage, "advantage", M, index, _F32),
+        None if weight is None else _vector(weight, "weight", M, index, _F32), clip_low, clip_high, kl_coef,
         temperature, loss.data_ptr(), logp.data_ptr(), stats.data_ptr(), coef.data_ptr(), M, N, code,
-        wp, n, _current(dev.index))
+        wp, n, _current(index))
     if st:
         _abi._check(st, "dyt_policy_loss_forward")
     return loss, logp, stats, coef
@@ -84,7 +85,8 @@ def policy_loss_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: torc
     policy_loss_forward returned at the same temperature. grad: the loss's own gradient
     (one float32 value on the device; left out: 1). logits and dlogits may be
     row-strided views; dlogits may be logits."""
-    if _elsewhere(logits, stream):
+    index = logits.get_device()
+    if _elsewhere(index, stream):
         with _there(logits, stream):
             return policy_loss_backward(logits, tokens, stats, coef, grad, temperature, dlogits)
     M, N = _shape(logits)
@@ -94,10 +96,10 @@ def policy_loss_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: torc
     else:
         lddl = _like(dlogits, "dlogits", logits)
     st = _abi.lib.dyt_policy_loss_backward(
-        logits.data_ptr(), ld, _vector(tokens, "tokens", M, dev, _TOKEN), tokens.element_size(),
-        _vector(stats, "stats", 2 * M, dev, _F32), _vector(coef, "coef", M, dev, _F32),
-        None if grad is None else _vector(grad, "grad", 1, dev, _F32), temperature, dlogits.data_ptr(), lddl, M, N,
-        code, _current(dev.index))
+        logits.data_ptr(), ld, _vector(tokens, "tokens", M, index, _TOKEN), tokens.element_size(),
+        _vector(stats, "stats", 2 * M, index, _F32), _vector(coef, "coef", M, index, _F32),
+        None if grad is None else _vector(grad, "grad", 1, index, _F32), temperature, dlogits.data_ptr(), lddl, M, N,
+        code, _current(index))
     if st:
         _abi._check(st, "dyt_policy_loss_backward")
     return dlogits

@@ -14,7 +14,7 @@ from ._tensors import (DTYPE_CODE, _code, _current, _elsewhere, _fresh, _fresh_r
                        _vector, _workspace, row_pitch)
 
 _F32 = (torch.float32,)
-_PARAM = tuple(DTYPE_CODE)
+_PARAM = DTYPE_CODE
 
 
 def _shape(x: torch.Tensor) -> tuple[int, int]:
@@ -31,13 +31,14 @@ def layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, beta:
     launch). x and out may be row-strided views (dense rows, evenly spaced): no copy
     is made. gamma and beta may each have their own dtype, or be left out. out may
     be x."""
-    if _elsewhere(x, stream):
+    index = x.get_device()
+    if _elsewhere(index, stream):
         with _there(x, stream):
             return layer_norm_forward(x, gamma, beta, eps, out, mean, rstd)
     M, N = _shape(x)
     ldx, code, dev = _pitch(x, "x"), _code(x, "x"), x.device
-    gp = None if gamma is None else _vector(gamma, "gamma", N, dev, _PARAM)
-    bp = None if beta is None else _vector(beta, "beta", N, dev, _PARAM)
+    gp = None if gamma is None else _vector(gamma, "gamma", N, index, _PARAM)
+    bp = None if beta is None else _vector(beta, "beta", N, index, _PARAM)
     if out is None:
         y, ldy = _fresh(x), N
     else:
@@ -46,15 +47,15 @@ def layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, beta:
     if mean is None:
         mean = _fresh_rows(rows, dev)
     else:
-        _vector(mean, "mean", rows.numel(), dev, _F32)
+        _vector(mean, "mean", rows.numel(), index, _F32)
     if rstd is None:
         rstd = _fresh_rows(rows, dev)
     else:
-        _vector(rstd, "rstd", rows.numel(), dev, _F32)
+        _vector(rstd, "rstd", rows.numel(), index, _F32)
     st = _abi.lib.dyt_layer_norm_forward(
         x.data_ptr(), ldx, gp, bp, eps, y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(), M, N, code,
         code if gamma is None else DTYPE_CODE[gamma.dtype], code if beta is None else DTYPE_CODE[beta.dtype],
-        _current(dev.index))
+        _current(index))
     if st:
         _abi._check(st, "dyt_layer_norm_forward")
     return y, mean, rstd
@@ -62,7 +63,7 @@ def layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, beta:
 
 def layer_norm_workspace(x: torch.Tensor) -> torch.Tensor:
     """A device workspace large enough for layer_norm_backward on x's shape and device."""
-    if _elsewhere(x, None):
+    if _elsewhere(x.get_device(), None):
         with _there(x, None):
             return layer_norm_workspace(x)
     M, N = _shape(x)
@@ -79,7 +80,8 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
     parameter's gradient in its parameter's dtype (None for a parameter that is not
     given; beta's values are not read). x, dy and dx may be row-strided views; dx may
     be x or dy."""
-    if _elsewhere(x, stream):
+    index = x.get_device()
+    if _elsewhere(index, stream):
         with _there(x, stream):
             return layer_norm_backward(x, dy, mean, rstd, gamma, beta, dx, dgamma, dbeta, ws)
     M, N = _shape(x)
@@ -89,9 +91,9 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
         dx, lddx = _fresh(x), N
     else:
         lddx = _like(dx, "dx", x)
-    gp = None if gamma is None else _vector(gamma, "gamma", N, dev, _PARAM)
+    gp = None if gamma is None else _vector(gamma, "gamma", N, index, _PARAM)
     if beta is not None:
-        _vector(beta, "beta", N, dev, _PARAM)
+        _vector(beta, "beta", N, index, _PARAM)
     if (gamma is None and dgamma is not None) or (beta is None and dbeta is not None):
         raise ValueError("dgamma and dbeta need their parameters")
     gd = bd = code
@@ -102,25 +104,25 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
             dgamma = torch.empty_like(gamma)
             gg = dgamma.data_ptr()
         else:
-            gg = _vector(dgamma, "dgamma", N, dev, (gamma.dtype,))
+            gg = _vector(dgamma, "dgamma", N, index, (gamma.dtype,))
     if beta is not None:
         bd = DTYPE_CODE[beta.dtype]
         if dbeta is None:
             dbeta = torch.empty_like(beta)
             bg = dbeta.data_ptr()
         else:
-            bg = _vector(dbeta, "dbeta", N, dev, (beta.dtype,))
+            bg = _vector(dbeta, "dbeta", N, index, (beta.dtype,))
     rows = x.shape[:-1].numel()
     if ws is None:
         n = _abi.lib.dyt_layer_norm_backward_workspace_bytes(M, N, code)
         ws = _scratch(n, dev)
         wp = ws.data_ptr()
     else:
-        wp, n = _workspace(ws, dev), ws.numel()
+        wp, n = _workspace(ws, index), ws.numel()
     st = _abi.lib.dyt_layer_norm_backward(
-        x.data_ptr(), ldx, dy.data_ptr(), lddy, gp, _vector(mean, "mean", rows, dev, _F32),
-        _vector(rstd, "rstd", rows, dev, _F32), dx.data_ptr(), lddx, gg, bg, M, N, code, gd, bd, wp, n,
-        _current(dev.index))
+        x.data_ptr(), ldx, dy.data_ptr(), lddy, gp, _vector(mean, "mean", rows, index, _F32),
+        _vector(rstd, "rstd", rows, index, _F32), dx.data_ptr(), lddx, gg, bg, M, N, code, gd, bd, wp, n,
+        _current(index))
     if st:
         _abi._check(st, "dyt_layer_norm_backward")
     return dx, dgamma, dbeta
