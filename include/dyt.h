@@ -289,9 +289,10 @@ int dyt_last_cuda_error(void);
 
 /*
  * Launch geometry of the calling thread's last successful call, so tests can
- * check which path ran. (Layer norm: path 1 = several rows per CTA, 2 = one;
- * row_groups = partial sums per column. Policy loss: path 1 = a warp per row,
- * 2 = a CTA per row or part of one; col_chunks = parts of a row.)
+ * check which path ran. (Layer norm: path 1 = a row in a warp, 2 = in several
+ * warps; row_groups = partial sums per column; shifted = 1 for ragged rows.
+ * Policy loss: path 1 = a warp per row or part of one, 2 = a CTA; col_chunks =
+ * parts of a row. The other fields that do not apply are 0.)
  */
 typedef struct dyt_launch_info {
   int op;            /* 1 = forward, 2 = backward, 3 = backward stage 1 (dyt_backward_partials),
@@ -391,14 +392,17 @@ dyt_status dyt_backward_noalloc(const void *x, const void *dy, const void *alpha
  * One kernel launch. The conventions above hold (row pitches, any element
  * alignment, dtypes, determinism, y may alias x with an equal pitch); a row's
  * sums and its statistics are binary32, the squares are taken about the mean,
- * and y is rounded once. No padding between rows is read or written.
+ * and y is rounded once.
  *   gamma, beta  [N] gamma_dtype, beta_dtype, read; NULL for a layer without
  *                (gamma = 1, beta = 0)
  *   eps          >= 0 and finite, else DYT_ERR_INVALID_VALUE
  *   mean, rstd   [M] binary32, written for the backward; each may be NULL
- * Tensors whose rows are all whole aligned 16-byte vectors (N included) are
- * read and written in vectors, others by elements. M * N == 0 launches nothing
- * and writes nothing.
+ * A row is read once and kept on the SM when N is at most 16384 (16-bit) or
+ * 8192 (binary32); longer rows are read three times, the second and third time
+ * mostly from L2. Ragged rows (off 16-byte boundaries, or of no whole 16-byte
+ * vectors) are copied in aligned 16-byte chunks, which reads up to 15 bytes on
+ * either side of a row, always between the tensor's first and last elements;
+ * their values reach no result. M * N == 0 launches nothing and writes nothing.
  */
 dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma, const void *beta, float eps, void *y,
                                   int64_t ldy, float *mean, float *rstd, int64_t M, int64_t N, dyt_dtype x_dtype,
@@ -411,10 +415,12 @@ dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma,
  *   dx[i,j]   = rstd[i] * (g[i,j] - sum_k g[i,k] / N - h[i,j] * sum_k g[i,k] h[i,k] / N)
  *   dgamma[j] = sum_i dy[i,j] * h[i,j]        dbeta[j] = sum_i dy[i,j]
  *
- * A kernel that writes dx and each CTA's column sums, and one that adds those
- * in binary64 in a fixed order and rounds each gradient once (rows too long for
- * a CTA's registers take a third). Columns are summed in binary32 over at most
- * 128 rows and in binary64 beyond. dx may alias x or dy with an equal pitch.
+ * Two kernel launches: one writes dx and each CTA's column sums, one adds those
+ * in binary64 in a fixed order and rounds each gradient once (not launched when
+ * neither gradient is wanted; rows of more than 8192 elements take a kernel
+ * more and read x and dy twice). Columns are summed in binary32 over at most
+ * 128 rows a lane and in binary64 beyond. Ragged rows are read as in the
+ * forward. dx may alias x or dy with an equal pitch.
  *   gamma         NULL: 1
  *   mean, rstd    [M] binary32, read
  *   dgamma, dbeta [N] gamma_dtype, beta_dtype, written; NULL: not wanted
@@ -442,8 +448,9 @@ dyt_status dyt_layer_norm_backward(const void *x, int64_t ldx, const void *dy, i
  *   coef[i] = w * (-(r A if r A <= c A else 0) + kl_coef * (1 - exp(q)))
  *
  * coef is the loss's derivative by lp; the backward needs it, and stats = (m, s).
- * Two kernel launches. The logits are read once; the row sums are binary32, the
- * rows' scalar arithmetic and the loss's sum binary64, each output rounded once.
+ * Two kernel launches. The logits are read once (nothing outside a row is); the
+ * row sums are binary32, the rows' scalar arithmetic and the loss's sum
+ * binary64, each output rounded once.
  *   logits    [M*N] dtype, row pitch ld, any element alignment
  *   tokens    [M] int64 (token_bytes 8) or int32 (token_bytes 4). At a row that
  *             counts, a token outside [0, N) makes lp, coef and the loss NaN;

@@ -160,6 +160,64 @@ def test_rows_without_weight_are_not_used(M, N):
     assert all(torch.equal(t, torch.zeros_like(t)) for t in c.forward())
 
 
+@pytest.mark.parametrize("M,N", [(8192, 2100), (8193, 2100), (8191, 517), (20000, 260), (3000, 9001)])
+@pytest.mark.parametrize("masked", [0.5, 0.97])
+def test_many_rows_of_which_few_count(M, N, masked):
+    # up to 8192 rows the kernel lists those that count, beyond it looks their weights up
+    c = Case(M, N, "bf16", masked=masked)
+    got, _ = c.check_forward()
+    c.check_backward(got, grad=1000.0)
+    last = torch.zeros(M, device="cuda")
+    last[-1] = 1.0
+    c.weight, c.tokens = last, torch.where(last != 0, torch.full_like(c.tokens, N - 1), c.tokens)
+    got, _ = c.check_forward()
+    assert int((got[1] != 0).sum()) == 1
+
+
+def test_runs_of_padding():
+    # sequences of a padded batch: the first rows of each count
+    M, N = 16 * 200, 1300
+    c = Case(M, N, "bf16")
+    lens = torch.tensor([200, 3, 150, 1, 0, 77, 200, 20, 0, 0, 9, 199, 64, 128, 32, 31], device="cuda")
+    on = (torch.arange(200, device="cuda") < lens[:, None]).reshape(-1)
+    c.weight = on.float() / on.sum()
+    got, _ = c.check_forward()
+    c.check_backward(got, grad=100.0)
+
+
+def test_offsets_beyond_32_bits():
+    # rows 2^30 + 1 elements apart: the last one starts past 2^31 elements, off 16-byte boundaries
+    pitch, N = (1 << 30) + 1, 5000
+    g = torch.Generator("cuda").manual_seed(2)
+    z, dz = (torch.empty(2 * pitch + N + 8, dtype=torch.bfloat16, device="cuda").as_strided((3, N), (pitch, 1))
+             for _ in range(2))
+    z.copy_(torch.randn(3, N, device="cuda", generator=g))
+    tokens = torch.tensor([0, 77, N - 1], device="cuda")
+    lp = z.double().log_softmax(-1).gather(1, tokens[:, None])[:, 0].float()
+    adv = torch.tensor([1.0, -2.0, 0.5], device="cuda")
+    got = dyt().policy_loss_forward(z, tokens, lp - 0.03, adv)
+    want, tol = R.loss_forward(z, tokens, lp - 0.03, adv)
+    for a, b, t, name in zip(got, want, tol, ("loss", "logp", "stats", "coef")):
+        R.assert_close(a, b, t, name)
+    for out in (dz, torch.empty(3, N, dtype=torch.bfloat16, device="cuda")):
+        dyt().policy_loss_backward(z, tokens, got[2], got[3], dlogits=out)
+        want, tol = R.loss_backward(z, tokens, got[2], got[3])
+        R.assert_close(out, want, tol + R.half_step(out.dtype, want), "dlogits")
+
+
+def test_two_calls_at_once():
+    c = Case(900, 6001, "bf16", masked=0.2)
+    want = c.forward()
+    dwant = dyt().policy_loss_backward(c.z.t, c.tokens, want[2], want[3])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [(c.forward(stream=s), dyt().policy_loss_backward(c.z.t, c.tokens, want[2], want[3], stream=s))
+           for _ in range(8) for s in streams]
+    torch.cuda.synchronize()
+    for f, b in got:
+        assert all(torch.equal(x, y) for x, y in zip(f, want)) and torch.equal(b, dwant)
+
+
 @pytest.mark.parametrize("N,low", [(50, -INF), (5000, -INF), (5000, torch.finfo(torch.float32).min)])
 def test_masked_vocabulary(N, low):
     # all but a few logits masked, by -inf or the type's lowest value, in whole vectors and single places

@@ -66,7 +66,7 @@ def test_widths(N, xd):
 
 
 @pytest.mark.parametrize("xd", ["f32", "bf16"])
-@pytest.mark.parametrize("N", [8200, 16384, 16385, 32776, 40001])
+@pytest.mark.parametrize("N", [8200, 12001, 16383, 16384, 16385, 32776, 40001])
 def test_long_rows(N, xd):
     check(5, N, xd)
 
@@ -81,6 +81,34 @@ def test_row_counts(M, N, xd):
 def test_rows_beyond_one_run(N):
     # several runs of 128 rows per lane
     check(160000 if N == 16 else 90000 if N == 1024 else 3000, N, "bf16" if N != 16 else "f32")
+
+
+@pytest.mark.parametrize("N,lanes", [(1024, 64), (512, 32), (1021, 64), (96, 8)])
+def test_some_rows_short_of_a_full_run(N, lanes):
+    # 128 steps, a run of column sums, of which some rows of one CTA do not make the last one
+    rows = 512 // lanes
+    step = torch.cuda.get_device_properties(0).multi_processor_count * rows
+    for extra in (5 * rows + 3, 1):
+        check(127 * step + extra, N, "bf16")
+        assert dyt().dyt_last_launch_info()["rows_per_step"] == rows
+
+
+def test_offsets_beyond_32_bits():
+    # rows 2^30 + 8 elements apart: the last one starts past 2^31 elements
+    pitch, N = (1 << 30) + 8, 1000
+    g = torch.Generator("cuda").manual_seed(5)
+    x, dy, y = (torch.empty(2 * pitch + N + 8, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    xv, dv, yv = (t.as_strided((3, N), (pitch, 1)) for t in (x, dy, y))
+    xv.copy_(torch.randn(3, N, device="cuda", generator=g))
+    dv.copy_(torch.randn(3, N, device="cuda", generator=g))
+    gamma = torch.rand(N, device="cuda", generator=g)
+    _, mean, rstd = dyt().layer_norm_forward(xv, gamma, gamma, EPS, out=yv)
+    want, tol = R.norm_forward(xv, gamma, gamma, EPS)
+    R.assert_close(yv, want[0], tol[0] + R.half_step(yv.dtype, want[0]), "y")
+    dx, dgamma, _ = dyt().layer_norm_backward(xv, dv, mean, rstd, gamma, gamma, dx=yv)
+    want, tol = R.norm_backward(xv, dv, mean, rstd, gamma)
+    R.assert_close(dx, want[0], tol[0] + R.half_step(dx.dtype, want[0]), "dx")
+    R.assert_close(dgamma, want[1], tol[1] + R.half_step(dgamma.dtype, want[1]), "dgamma")
 
 
 @pytest.mark.parametrize("xd,pd", [(a, b) for a in ("f32", "bf16", "f16") for b in ("f32", "bf16", "f16")])
@@ -270,6 +298,20 @@ def test_captured_and_replayed():
         y2, m2, r2 = dyt().layer_norm_forward(xs, gamma, beta, EPS)
         want = dyt().layer_norm_backward(xs, ds, m2, r2, gamma, beta)
         assert torch.equal(y, y2) and all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+def test_two_calls_at_once():
+    # on two streams, each with its own workspace
+    x, dy, gamma, beta = inputs(3000, 520, "bf16")
+    _, mean, rstd = dyt().layer_norm_forward(x.t, gamma, beta, EPS)
+    want = dyt().layer_norm_backward(x.t, dy.t, mean, rstd, gamma, beta)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[dyt().layer_norm_backward(x.t, dy.t, mean, rstd, gamma, beta, stream=s) for s in streams] for _ in range(8)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for one in pair:
+            assert all(torch.equal(a, b) for a, b in zip(one, want))
 
 
 def test_refusals():
