@@ -17,7 +17,6 @@ using dyt::norm::NormArgs;
 using dyt::norm::NormGradArgs;
 
 constexpr int kOpNormForward = 5, kOpNormBackward = 6;  // dyt_launch_info::op
-constexpr int kRowsBlock = 256;                         // threads of a CTA with several rows
 
 // How a row is spread over lanes (see dyt_norm.cuh).
 struct RowPlan {
@@ -193,7 +192,7 @@ dyt_status dyt_layer_norm_forward(const void *x, int64_t ldx, const void *gamma,
     using T = decltype(t);
     constexpr int VE = vec_elems<T>();
     const bool vec = N % VE == 0 && aligned16(x) && aligned16(y) && vec_pitch(ldx, es) && vec_pitch(ldy, es);
-    const RowPlan p = plan_rows(M, N, VE, vec, dyt::norm::fwd_elems<T>(!vec), sms);
+    const RowPlan p = plan_rows(M, N, VE, vec, dyt::norm::fwd_elems<T>(), sms);
     const FwdKernel k = fwd_kernel<T>(p);
     const size_t smem = p.rowlong ? 0 : dyt::norm::fwd_smem<T>(p.block, p.L, p.ragged);
     const dyt_status s = prepare_smem(dev, (const void *)k, (int)smem);
