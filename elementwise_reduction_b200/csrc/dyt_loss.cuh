@@ -69,6 +69,7 @@ struct LossGradArgs {
   int64_t N;
   int S;
   int wide_tokens;
+  int lines;          // every row is whole 128-byte lines: they are not needed again
   float C;
   double inv_t;
 };
@@ -504,15 +505,16 @@ __device__ __forceinline__ uint4 cut16(const uint4 &lo, const uint4 &hi, uint32_
                     __funnelshift_r(w[3], w[4], b));
 }
 
-// Measured: 8192 x 131072 bf16 630 us (6.8 TB/s), 4096 x 32003 fp16 with a
-// quarter of the rows without weight 82 us; rows at different offsets, 4096 x
-// 32003 bf16, 114 us. Bound by memory.
+// Measured: 8192 x 131072 bf16 629 us (6.8 TB/s), 4096 x 32003 fp16 with a
+// quarter of the rows without weight 79 us (5.8 TB/s); rows at different
+// offsets, 4096 x 32003 bf16, 98 us. Bound by memory. Five CTAs an SM, 48
+// registers, took 78.9 / 97.7 us on the last two, four CTAs 82.1 / 106.5.
 // G threads (a warp, or the CTA) per part of a row. The vectors are those of
 // the output row; SHIFT: the input row lies at another offset past a 16-byte
 // boundary, and each of its vectors is cut out of two aligned ones inside the
 // row. The elements before and after those vectors are taken one by one.
 template <typename T, bool CTA, bool SHIFT>
-__global__ void __launch_bounds__(256) loss_grad_kernel(LossGradArgs a) {
+__global__ void __launch_bounds__(256, 5) loss_grad_kernel(LossGradArgs a) {
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int U = SHIFT ? 2 : 4;
   using IO = VecIO<T, V>;
@@ -528,7 +530,11 @@ __global__ void __launch_bounds__(256) loss_grad_kernel(LossGradArgs a) {
     const int part = (int)(item - row * a.S);
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
     T *dz = static_cast<T *>(a.dz) + row * a.lddz;
-    const float A = (float)(gt * (double)a.coef[row]);
+    // (all of the row's numbers are asked for at once, whichever are used)
+    const float coef = a.coef[row];
+    const int64_t tok = token_at(a.tokens, a.wide_tokens, row);
+    const float2 st = a.stats[row];
+    const float A = (float)(gt * (double)coef);
     // whole output vectors [head, head + nb V): with SHIFT, those whose two
     // input vectors lie inside the row
     int64_t head = head_elems(dz, a.N);
@@ -554,8 +560,6 @@ __global__ void __launch_bounds__(256) loss_grad_kernel(LossGradArgs a) {
       for (int64_t i = b0 + t; i < b1; i += G) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
       continue;
     }
-    const int64_t tok = token_at(a.tokens, a.wide_tokens, row);
-    const float2 st = a.stats[row];
     // p = 2^(z C - K), K = m C + s log2(e); K's rounding, |k - K| <= 2^-24 |K|,
     // goes into the factor as 1 + (k - K) ln 2 (its square is below 2^-34 for |K| < 100)
     const double K = (double)st.x * (double)a.C + (double)st.y * kLog2eD;
@@ -590,7 +594,7 @@ __global__ void __launch_bounds__(256) loss_grad_kernel(LossGradArgs a) {
       uint4 raw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        raw[u] = __ldcs(in + i + u * G);
+        raw[u] = a.lines ? __ldcs(in + i + u * G) : in[i + u * G];
         if constexpr (SHIFT) {
           if (d > 0) raw[u] = cut16(raw[u], in[i + u * G + 1], (uint32_t)d * sizeof(T));
         }
