@@ -24,7 +24,6 @@ namespace dyt {
 namespace loss {
 
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr double kLn2 = 0.693147180559945309417232121458;
 constexpr double kLog2eD = 1.44269504088896340735992468100;
 
 struct LossArgs {
@@ -75,7 +74,7 @@ struct LossGradArgs {
 };
 
 __device__ __forceinline__ int64_t token_at(const void *p, int wide, int64_t row) {
-  return wide ? static_cast<const int64_t *>(p)[row] : (int64_t) static_cast<const int32_t *>(p)[row];
+  return wide ? __ldcg(static_cast<const long long *>(p) + row) : (int64_t)__ldcg(static_cast<const int *>(p) + row);
 }
 
 // ---- running maximum and sum -----------------------------------------------------
@@ -371,14 +370,14 @@ struct RowInput {
 template <typename T>
 __device__ __forceinline__ RowInput row_input(const LossArgs &a, int64_t row) {
   RowInput in = {};
-  in.w = a.weight ? (double)a.weight[row] : 1.0 / (double)a.M;
+  in.w = a.weight ? (double)__ldcg(a.weight + row) : 1.0 / (double)a.M;
   if (in.w != 0.0) {
     const int64_t tok = token_at(a.tokens, a.wide_tokens, row);
-    in.old_logp = (double)a.old_logp[row];
-    in.advantage = (double)a.advantage[row];
-    if (a.ref_logp) in.ref_logp = (double)a.ref_logp[row];
+    in.old_logp = (double)__ldcg(a.old_logp + row);
+    in.advantage = (double)__ldcg(a.advantage + row);
+    if (a.ref_logp) in.ref_logp = (double)__ldcg(a.ref_logp + row);
     // a token outside the vocabulary has no probability: NaN, here and in the loss
-    in.hit = tok >= 0 && tok < a.N ? (double)to_f32<T>((static_cast<const T *>(a.z) + row * a.ld)[tok])
+    in.hit = tok >= 0 && tok < a.N ? (double)to_f32<T>(__ldcg(static_cast<const T *>(a.z) + row * a.ld + tok))
                                    : (double)__int_as_float(0x7FC00000);
   }
   return in;
@@ -418,7 +417,7 @@ constexpr int kThreadParts = 16;  // rows of at most this many parts take a thre
 // order (the count of finished CTAs starts at 0: the first kernel sets it).
 // Before the wait for the first kernel a CTA reads its first rows' inputs: that
 // kernel lets this one start only after its own wait for what came before, and
-// writes none of them.
+// writes none of them. (Those loads pass by L1, which may be older than that.)
 template <typename T>
 __global__ void __launch_bounds__(kFinishBlock) loss_finish_kernel(LossArgs a) {
   __shared__ double sh[kFinishBlock / 32];
@@ -560,13 +559,14 @@ __global__ void __launch_bounds__(256, 5) loss_grad_kernel(LossGradArgs a) {
       for (int64_t i = b0 + t; i < b1; i += G) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
       continue;
     }
-    // p = 2^(z C - K), K = m C + s log2(e); K's rounding, |k - K| <= 2^-24 |K|,
-    // goes into the factor as 1 + (k - K) ln 2 (its square is below 2^-34 for |K| < 100)
-    const double K = (double)st.x * (double)a.C + (double)st.y * kLog2eD;
-    const float k = (float)K;
-    const float B = -A * fmaf((float)((double)k - K), (float)kLn2, 1.0f);
+    // p = 2^((z - m) C) e^-s: the maximum leaves first, as in the forward
+    const float B = -A * expf(-st.y);
+    auto power = [&](float2 z2) {
+      const float2 e = mul2(add2(z2, f2(-st.x)), f2(a.C));
+      return make_float2(ex2_approx(e.x), ex2_approx(e.y));
+    };
     auto one = [&](int64_t j) {
-      const float p = ex2_approx(fmaf(to_f32<T>(z[j]), a.C, -k));
+      const float p = power(f2(to_f32<T>(z[j]))).x;
       dz[j] = from_f32<T>(j == tok ? fmaf(B, p, A) : B * p);
     };
     if (part == 0)
@@ -575,18 +575,18 @@ __global__ void __launch_bounds__(256, 5) loss_grad_kernel(LossGradArgs a) {
       for (int64_t j = t; j < rest; j += G) one(a.N - rest + j);
     const uint4 *in = reinterpret_cast<const uint4 *>(z + (head - d));
     auto vec = [&](int64_t i, const uint4 &raw) {
-      float v[V];
-      IO::unpack(raw, v);
+      float2 f[V / 2];
+      IO::unpack2(raw, f);
       const int64_t j0 = head + i * V;
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = B * ex2_approx(fmaf(v[e], a.C, -k));
+      for (int e = 0; e < V / 2; ++e) f[e] = mul2(f2(B), power(f[e]));
       if (tok >= j0 && tok < j0 + V) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] += j0 + e == tok ? A : 0.0f;
+        for (int e = 0; e < V / 2; ++e) {
+          f[e].x += j0 + 2 * e == tok ? A : 0.0f;
+          f[e].y += j0 + 2 * e + 1 == tok ? A : 0.0f;
+        }
       }
-      float2 f[V / 2];
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) f[e] = make_float2(v[2 * e], v[2 * e + 1]);
       __stcs(out + i, IO::pack2(f));
     };
     int64_t i = b0 + t;

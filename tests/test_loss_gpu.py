@@ -271,6 +271,35 @@ def test_large_logits_keep_their_differences():
         c.check_backward(got)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [1.0, 0.25])
+def test_rows_at_the_lowest_value_and_far_from_zero(dtype, T):
+    # the backward takes the maximum out too before anything is rounded to its size:
+    # rows all at the type's lowest value (equal probabilities), all but one there,
+    # rows around the type's largest values, ordinary rows
+    N, t = 1003, R.DT[dtype]
+    c = Case(6, N, dtype, T=T, ref=False)
+    big = torch.finfo(t)
+    c.z.t[0] = big.min
+    c.z.t[1] = big.min
+    c.z.t[1, 5] = 1.0
+    c.z.t[2] = big.max
+    c.z.t[3] = big.max / 2 * (1 - torch.arange(N, device="cuda") % 4 * big.eps)  # neighbours there
+    c.z.t[4] += 1000.0
+    c.tokens[:5] = torch.tensor([N - 1, 6, 0, 4, 8], device="cuda")
+    c.tokens[1] = 5
+    lp = R.loss_forward(c.z.t, c.tokens, c.old, c.adv, T=T)[0][1]
+    c.old = lp.float()
+    got, _ = c.check_forward()
+    for row in (0, 2):
+        assert abs(float(got[1][row]) + float(torch.log(torch.tensor(float(N))))) < 1e-4
+    c.check_backward(got)
+    shifted = R.Guarded(6, N, t, offset=3)  # the input at another offset than the output
+    shifted.set(c.z.t)
+    c.z = shifted
+    c.check_backward(got, out_pitch=N + 5, out_offset=1)
+
+
 def test_clipped_rows_have_no_gradient():
     c = Case(8, 900, ref=False)
     got, _ = c.check_forward()
