@@ -507,7 +507,7 @@ __device__ __forceinline__ uint4 cut16(const uint4 &lo, const uint4 &hi, uint32_
 // Measured: 8192 x 131072 bf16 629 us (6.8 TB/s), 4096 x 32003 fp16 with a
 // quarter of the rows without weight 79 us (5.8 TB/s); rows at different
 // offsets, 4096 x 32003 bf16, 98 us. Bound by memory. Five CTAs an SM, 48
-// registers, took 78.9 / 97.7 us on the last two, four CTAs 82.1 / 106.5.
+// registers, gain 4% over four on ragged rows (78.9 and 82.1 us).
 // G threads (a warp, or the CTA) per part of a row. The vectors are those of
 // the output row; SHIFT: the input row lies at another offset past a 16-byte
 // boundary, and each of its vectors is cut out of two aligned ones inside the
@@ -515,7 +515,7 @@ __device__ __forceinline__ uint4 cut16(const uint4 &lo, const uint4 &hi, uint32_
 template <typename T, bool CTA, bool SHIFT>
 __global__ void __launch_bounds__(256, 5) loss_grad_kernel(LossGradArgs a) {
   constexpr int V = 16 / (int)sizeof(T);
-  constexpr int U = SHIFT ? 2 : 4;
+  constexpr int U = SHIFT ? 1 : 4;  // vectors under way (SHIFT, 1, 2 and 4: 98, 111 and 106 us for the case above)
   using IO = VecIO<T, V>;
   pdl_prologue();
   const int G = CTA ? (int)blockDim.x : 32;
