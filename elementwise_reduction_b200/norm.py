@@ -58,6 +58,9 @@ def layer_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, beta:
         _current(index))
     if st:
         _abi._check(st, "dyt_layer_norm_forward")
+    if N == 0:  # no elements: no statistics, and no kernel that would write them
+        mean.fill_(float("nan"))
+        rstd.fill_(float("nan"))
     return y, mean, rstd
 
 

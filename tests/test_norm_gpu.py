@@ -198,6 +198,12 @@ def test_empty_shapes():
     assert y.shape == (3, 0)
 
 
+def test_rows_without_elements_have_no_statistics():
+    mean, rstd = torch.zeros(3, device="cuda"), torch.zeros(3, device="cuda")
+    dyt().layer_norm_forward(torch.empty(3, 0, device="cuda"), mean=mean, rstd=rstd)
+    assert torch.isnan(mean).all() and torch.isnan(rstd).all()
+
+
 @pytest.mark.parametrize("M,N,xd", [(5000, 64, "f32"), (3000, 1001, "f16"), (1000, 4096, "bf16"), (40, 20000, "bf16")])
 def test_deterministic_with_a_garbage_workspace(M, N, xd):
     x, dy, gamma, beta = inputs(M, N, xd)
