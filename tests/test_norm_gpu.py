@@ -125,6 +125,16 @@ def test_strides_and_offsets(N, pitch, offset, out_pitch, out_offset, xd):
     check(19, N, xd, pitch=pitch, offset=offset, out_pitch=out_pitch, out_offset=out_offset)
 
 
+@pytest.mark.parametrize("xd,pd", [("f32", "f32"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("N", [1, 2, 3, 5, 7, 9, 17, 31, 33, 61, 100, 127, 251, 257, 511, 513, 517, 1001, 2047, 4093,
+                               4099, 8185, 8191])
+def test_aligned_rows_with_a_part_of_a_vector_at_the_end(N, xd, pd):
+    # rows on 16-byte boundaries, NaN between them; few rows, several rows a lane, and a single one
+    pitch = (N + 7) // 8 * 8
+    for M in (1, 37, 1500):
+        check(M, N, xd, pd, pitch=pitch + 8, out_pitch=pitch)
+
+
 def test_parameters_of_two_dtypes_and_none():
     x, dy, gamma, beta = inputs(33, 200, "bf16")
     g16, b16 = gamma.to(torch.bfloat16), beta.to(torch.float16)
@@ -196,6 +206,10 @@ def test_empty_shapes():
     assert torch.equal(dgamma, torch.zeros_like(g)) and torch.equal(dbeta, torch.zeros_like(g))
     y, _, _ = dyt().layer_norm_forward(torch.empty(3, 0, device="cuda"))
     assert y.shape == (3, 0)
+
+
+def test_a_part_of_a_vector_over_several_runs():
+    check(148 * 128 * 129 + 5, 61, "bf16", pitch=64, out_pitch=64)
 
 
 def test_rows_without_elements_have_no_statistics():
