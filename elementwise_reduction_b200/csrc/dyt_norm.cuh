@@ -652,53 +652,83 @@ template <typename T>
 __host__ __device__ constexpr int bwd_stages() {
   return sizeof(T) == 4 ? 2 : 3;
 }
-// Dynamic shared memory: the ring, then 16 bytes' worth of column sums of every thread.
+// Dynamic shared memory: the ring, then room for the column sums of a run, V
+// elements of every lane. (The sums of all elements at the end take the ring's place.)
 template <typename T>
 __host__ __device__ constexpr size_t bwd_ring(int block, int L, bool ragged) {
   return (size_t)bwd_stages<T>() * 2 * row_slots<T, kBwdElems>(block, L, ragged) * 16;
 }
+// An element's sums of all lanes lie L + kSumPad apart, so that neighbouring columns lie in different banks.
+constexpr int kSumPad = 4;
+// Bytes for `per` elements of every lane: a copy per group, or per warp of smaller rows.
+__host__ __device__ constexpr size_t sums_smem(int block, int L, int per) {
+  return (size_t)(block / (L < 32 ? 32 : L)) * 2 * per * (L + kSumPad) * sizeof(float);
+}
 template <typename T>
 __host__ __device__ constexpr size_t bwd_smem(int block, int L, bool ragged) {
-  return bwd_ring<T>(block, L, ragged) + (size_t)block * (16 / sizeof(T)) * 2 * sizeof(float);
+  return bwd_ring<T>(block, L, ragged) + sums_smem(block, L, 16 / (int)sizeof(T));
 }
+// A thread's share of the ring is at least 192 bytes, and of the sums 128 (1 + kSumPad / L) for
+// L >= 32, less for smaller rows: 144 at most.
+static_assert(bwd_ring<__half>(32, 32, false) >= sums_smem(32, 32, kBwdElems) &&
+                  bwd_ring<float>(32, 32, false) >= sums_smem(32, 32, kBwdElems),
+              "the last column sums take the ring's place");
 
 // The column sums of one run of rows, added over the CTA's rows in a fixed
 // order and moved to its partial sums in binary64 (added to them after the
 // first run). Rows side by side in a warp are added by a butterfly first; `sh`
-// then holds a copy per warp (rows within a warp) or per group, V elements of
+// then holds a copy per warp (rows within a warp) or per group, PER elements of
 // every lane at a time.
-template <int V, int E, bool RAGGED, int MODE>
+template <int V, int E, int PER, bool RAGGED, int MODE>
 __device__ __forceinline__ void flush_columns(const NormGradArgs &a, float2 (&dg)[E / 2], float2 (&db)[E / 2],
                                               const Place<MODE> &p, bool first, float *sh) {
   double *pg = a.parts + (int64_t)blockIdx.x * 2 * a.w.N;
   const int N = (int)a.w.N;
   const int copies = MODE != kGroup ? (int)blockDim.x / 32 : a.w.rows;
   const int copy = MODE != kGroup ? (int)threadIdx.x >> 5 : p.mine;
-  const int width = p.L * V;
+  const int stride = p.L + kSumPad, plane = 2 * PER * stride;
+  // element e of lane `lane`, column c: which = 0 dgamma, 1 dbeta
+  auto add = [&](int which, int e, int lane, int c) {
+    if (c >= N) return;
+    const float *q = sh + (which * PER + e) * stride + lane;
+    double t[2] = {0.0, 0.0};
+    for (int w = 0; w + 1 < copies; w += 2) {
+      t[0] += (double)q[w * plane];
+      t[1] += (double)q[(w + 1) * plane];
+    }
+    if (copies & 1) t[0] += (double)q[(copies - 1) * plane];
+    double *o = pg + (int64_t)which * a.w.N + c;
+    *o = first ? t[0] + t[1] : *o + (t[0] + t[1]);
+  };
 #pragma unroll
-  for (int k = 0; k < E / V; ++k) {
+  for (int k = 0; k < E; k += PER) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int i = (k * V + e) / 2;
+    for (int e = 0; e < PER; ++e) {
+      const int i = (k + e) / 2;
       float u = e & 1 ? dg[i].y : dg[i].x, w = e & 1 ? db[i].y : db[i].x;
       for (int o = p.seg(); o < 32; o <<= 1) {
         u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
         w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
       }
       if (MODE != kPart || ((int)threadIdx.x & 31) < p.L) {
-        sh[(copy * 2) * width + e * p.L + p.lane] = u;
-        sh[(copy * 2 + 1) * width + e * p.L + p.lane] = w;
+        sh[copy * plane + e * stride + p.lane] = u;
+        sh[copy * plane + (PER + e) * stride + p.lane] = w;
       }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * width; i += blockDim.x) {
-      const int which = i >= width, j = i - which * width, e = j / p.L;
-      const int c = column<V, E, RAGGED, MODE>(p.L, j - e * p.L, 0) + (RAGGED ? (k * V + e) * p.seg() : k * width + e);
-      if (c < N) {
-        double t = 0.0;
-        for (int w = 0; w < copies; ++w) t += (double)sh[(w * 2 + which) * width + j];
-        double *o = pg + (int64_t)which * a.w.N + c;
-        *o = first ? t : *o + t;
+    // neighbouring threads take neighbouring columns
+    if constexpr (RAGGED) {
+      for (int q = p.mine; q < 2 * PER; q += a.w.rows) {
+        const int which = q >= PER, e = q - which * PER;
+        add(which, e, p.lane, column<V, E, true, MODE>(p.L, p.lane, k + e));
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < PER; v += V) {
+        for (int j = threadIdx.x; j < 2 * V * p.L; j += blockDim.x) {
+          const int which = j >= V * p.L, r = j - which * V * p.L;
+          add(which, v + r % V, r / V, (k + v) * p.L + r);
+        }
       }
     }
     __syncthreads();
@@ -724,9 +754,10 @@ __device__ __forceinline__ void swap_halves(float v, float &u, float &w) {
 }
 
 // A row's two sums meet at one barrier (a group) or in a butterfly that gives
-// each half of the warp one of them. Measured: 32768 x 8192 bf16 300 us with the
-// sum of the partials (5.4 TB/s), 16384 x 4096 80 us, 16384 x 2048 fp32 70 us,
-// 100003 x 255 fp32 64 us. Bound by the arithmetic's latency: 16 warps hold all
+// each half of the warp one of them. Measured: 32768 x 8192 bf16 296 us with the
+// sum of the partials (5.4 TB/s), 16384 x 4096 77 us, 16384 x 2048 fp32 68 us,
+// 100003 x 255 fp32 64 us, 8191 x 1001 fp16 20.5 us (about 4 of them the launch
+// and the column sums, 4 the second kernel). Bound by the arithmetic's latency: 16 warps hold all
 // registers, and issue half of the time (300 instructions a warp and row). Not
 // kept: two rows at a barrier (290 us at full clock, 307 instead of 305 under
 // the power cap), 32 elements a lane in 8 warps (329 us), 8 in 32 (more
@@ -818,16 +849,17 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
     }
     row += a.w.step;
     out += a.w.inc[2];
-    if (++run == kRunRows) {
-      flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
+    if (++run == kRunRows && it + 1 < steps) {
+      flush_columns<V, E, V, RAGGED>(a, dg, db, p, first, sh);
       first = false;
       run = 0;
     }
   }
-  // Every warp of the CTA flushes equally often: one that left at the last step
-  // joins the flush that the others make in it or here.
-  if (steps % kRunRows != 0 || (MODE != kPart && left < steps)) flush_columns<V, E, RAGGED>(a, dg, db, p, first, sh);
+  // The last run, all elements at once where the ring was: every warp of the
+  // CTA is here, also one that left at the last step.
   cp_async_wait<0>();
+  __syncthreads();
+  flush_columns<V, E, E, RAGGED>(a, dg, db, p, first, reinterpret_cast<float *>(dyn));
 }
 
 // ---- backward: rows too long for registers ------------------------------------------
@@ -923,8 +955,8 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(NormGradArgs a, c
 constexpr int kSumCols = 32, kSumLanes = 16, kSumBatch = 10;
 
 // The CTAs' column sums added in binary64 in a fixed order (lane l takes
-// partials l, l + 16, ..., ten loads under way at a time; the lanes are added
-// in order) and rounded once. blockIdx.y: 0 = dgamma, 1 = dbeta.
+// partials l, l + 16, ..., ten loads under way at a time) and rounded once. The
+// sums go by halves: one binary64 addition after the other cost 1.4 us more. blockIdx.y: 0 = dgamma, 1 = dbeta.
 __global__ void __launch_bounds__(kSumCols *kSumLanes)
     norm_finalize_kernel(const double *__restrict__ parts, int nparts, int64_t N, void *dgamma, int gamma_dt,
                          void *dbeta, int beta_dt) {
@@ -945,16 +977,19 @@ __global__ void __launch_bounds__(kSumCols *kSumLanes)
         v[b] = j < nparts ? p[(int64_t)j * 2 * N] : 0.0;
       }
 #pragma unroll
-      for (int b = 0; b < kSumBatch; ++b) t += v[b];
+      for (int s = 1; s < kSumBatch; s <<= 1)  // by halves: few additions wait for one another
+#pragma unroll
+        for (int b = 0; b + s < kSumBatch; b += 2 * s) v[b] += v[b + s];
+      t += v[0];
     }
   }
   sh[lane][c] = t;
   __syncthreads();
   if (lane == 0 && col < N) {
-    double s = 0.0;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-    for (int l = 0; l < kSumLanes; ++l) s += sh[l][c];
-    store_param(out, blockIdx.y ? beta_dt : gamma_dt, col, s);
+    for (int l = 0; l < kSumLanes; ++l) s[l & 3] += sh[l][c];
+    store_param(out, blockIdx.y ? beta_dt : gamma_dt, col, (s[0] + s[1]) + (s[2] + s[3]));
   }
 }
 
