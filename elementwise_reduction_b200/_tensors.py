@@ -63,16 +63,25 @@ def _current(index: int) -> int:
 
 
 def _pitch(t: torch.Tensor, what: str) -> int:
-    """The row pitch of a CUDA tensor; contiguous ones need no look at their strides."""
+    """The row pitch of a CUDA tensor; contiguous ones need no look at their strides, and
+    ordinary matrices one."""
     if t.is_contiguous() and t.dim():
         return t.shape[-1]
+    if t.dim() == 2 and t.is_cuda:
+        ld, inner = t.stride()
+        if inner == 1 and ld >= t.shape[1]:
+            return ld
     return _rows(t, what)
 
 
 def _fresh(t: torch.Tensor) -> torch.Tensor:
     """An uninitialised contiguous tensor of t's shape, dtype and device. (empty_like of a
-    contiguous tensor takes 1.3 us, torch.empty of its shape 3.3.)"""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    contiguous tensor takes 1.3 us, empty_strided 1.4, torch.empty of its shape 3.3.)"""
+    if t.is_contiguous():
+        return torch.empty_like(t)
+    if t.dim() == 2:
+        return torch.empty_strided(t.shape, (t.shape[1], 1), dtype=t.dtype, device=t.device)
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _fresh_rows(rows: torch.Size, device: torch.device) -> torch.Tensor:
