@@ -53,7 +53,8 @@ LossPlan plan_forward(int64_t M, int64_t N, size_t es, int sms) {
   LossPlan p = {};
   const int64_t bytes = N * (int64_t)es, warps = (int64_t)sms * (kRowsPerSm / 32);
   const int64_t batches = std::max<int64_t>(1, ceil_div(bytes, 16) / (dyt::loss::kBatch * 32));
-  p.S = dyt::loss::choose_parts((float)M, (float)warps, (int)std::min<int64_t>(batches, kMostParts));
+  p.S = dyt::loss::choose_parts((float)M, (float)warps, (int)std::min<int64_t>(batches, kMostParts),
+                                (int)std::min<int64_t>(batches, INT32_MAX));
   p.most = (int)std::max<int64_t>(p.S, std::min<int64_t>(batches, dyt::loss::kListedParts));
   const int64_t items = M * p.S;
   // few items: small CTAs, one warp's work after the other over all SMs

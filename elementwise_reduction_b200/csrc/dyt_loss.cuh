@@ -132,19 +132,29 @@ constexpr int kBatch = 8, kStages = 3;  // a lane's 16-byte vectors in a batch, 
 
 __host__ __device__ constexpr size_t rows_smem(int block) { return (size_t)block * kBatch * kStages * 16; }
 
-// The parts of a row, at most `most`: two items for every warp if there can be
-// so many (the next item's copies then run under the current one's end), and a
-// few more where that makes the warps' rounds more nearly whole. Measured, us:
-// 4096 rows of 32000 bf16 over 2368 warps, 1.73 rounds whole, 63.6, 6.92 in
-// four parts, 51.2; 2368 rows of 56000, one round 56.8, two in halves 51.9.
+// The parts of a row of `batches` batches, at most `most`: two items for every
+// warp if that leaves a part of a long row three batches (the next item's copies then run under
+// the current one's end), and a few more where that makes the warps' rounds more
+// nearly whole; else one round of items, as many as there are warps. Measured,
+// us, bf16 over 2368 warps: 4096 rows of 32000 (16 batches), 1.73 rounds whole,
+// 58.4, 6.92 in four parts, 48.9, 13.8 in eight 51.5; 3072 rows, three parts 40.5,
+// ten 46.5; 400 rows of 50000 in five parts, one round, 14.9, in eight 17.4, in twelve 17.8.
 constexpr int kListedParts = 16;  // at most, where the kernel chooses
-__host__ __device__ inline int choose_parts(float rows, float warps, int most) {
+constexpr int kPartBatches = 3;   // at least, in more than one round
+__host__ __device__ inline int choose_parts(float rows, float warps, int most, int batches) {
   const float least = ceilf(2.0f * warps / fmaxf(rows, 1.0f));
-  int S = least < (float)most ? (int)least : most;
+  // (short rows: down to a batch)
+  int cap = batches < 2 * kPartBatches ? batches : (batches + kPartBatches - 1) / kPartBatches;
+  if (cap > most) cap = most;
+  if (least > (float)cap) {
+    const float one = floorf(warps / fmaxf(rows, 1.0f));
+    return one < 1.0f ? 1 : one < (float)most ? (int)one : most;
+  }
+  int S = (int)least;
   if (S < 1) S = 1;
   float best = 0.0f;
   int chosen = S;
-  for (int last = S + 8 < most ? S + 8 : most; S <= last; ++S) {
+  for (int last = S + 8 < cap ? S + 8 : cap; S <= last; ++S) {
     const float rounds = rows * (float)S / warps, even = rounds / ceilf(rounds);
     if (even > best + 0.02f) {
       best = even;
@@ -252,7 +262,7 @@ __global__ void __launch_bounds__(kRowsBlock, 2) loss_rows_kernel(LossArgs a) {
   int parts = a.S;
   if (a.listed) {
     rows = list.fill(a);
-    parts = choose_parts((float)rows, (float)warps, min(a.most, kListedParts));
+    parts = choose_parts((float)rows, (float)warps, min(a.most, kListedParts), a.batches);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.done[0] = 0u;
