@@ -137,8 +137,8 @@ __host__ __device__ constexpr size_t rows_smem(int block) { return (size_t)block
 // the current one's end), and a few more where that makes the warps' rounds more
 // nearly whole; else one round of items, as many as there are warps. Measured,
 // us, bf16 over 2368 warps: 4096 rows of 32000 (16 batches), 1.73 rounds whole,
-// 58.4, 6.92 in four parts, 48.9, 13.8 in eight 51.5; 3072 rows, three parts 40.5,
-// ten 46.5; 400 rows of 50000 in five parts, one round, 14.9, in eight 17.4, in twelve 17.8.
+// 58.4, 6.92 in four parts, 48.9, 13.8 in eight 51.5; 2000 rows of 131072 in five 87.7,
+// ten 91.6; 400 rows of 50000 in five parts, one round, 14.9, in eight 17.4, in twelve 17.8.
 constexpr int kListedParts = 16;  // at most, where the kernel chooses
 constexpr int kPartBatches = 3;   // at least, in more than one round
 __host__ __device__ inline int choose_parts(float rows, float warps, int most, int batches) {
