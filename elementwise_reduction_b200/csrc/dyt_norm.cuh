@@ -795,6 +795,7 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
   const float inv_n = a.w.inv_n;
   const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31, w0 = GROUP ? p.mine * warps : 0;
   char *out = reinterpret_cast<char *>(static_cast<T *>(a.dx) + row * a.lddx);
+  const bool full = N == p.L * E;  // no lane holds anything past the row's end
   bool first = true;
   int run = 0;
 #pragma unroll 1
@@ -811,16 +812,28 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
     if (it + 1 < left) stat += a.w.step;
     nmean = a.mean[stat];
     nrstd = a.rstd[stat];
-    // Past the row's end d and gamma are 0, so nothing there enters a sum that is used.
+    // Past the row's end d and gamma are 0, so that nothing there enters a sum that is used, as long as what
+    // they are multiplied with is finite. h = -mean rstd may not be (a row far from 0 with a small variance).
+    // Ragged rows therefore sum the products of gamma dy rstd and x - mean, which costs nothing there; aligned
+    // ones sum once more without the lanes' parts past the end if it is infinite. (16384 x 512 fp16 15.7 us, the
+    // ragged rows' way 16.3; 8191 x 1001 fp16 20.5 us, the aligned rows' way 22.3.)
     float2 s1[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)}, s2[2] = {s1[0], s1[0]};
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      h[i] = mul2(add2(h[i], f2(-mean)), f2(rstd));
+      const float2 c = add2(h[i], f2(-mean));
+      h[i] = mul2(c, f2(rstd));
       dg[i] = fma2(d[i], h[i], dg[i]);
       db[i] = add2(db[i], d[i]);
       d[i] = mul2(gam[i], d[i]);
+      if constexpr (RAGGED) d[i] = mul2(d[i], f2(rstd));
       s1[i & 1] = add2(s1[i & 1], d[i]);
-      s2[i & 1] = fma2(d[i], h[i], s2[i & 1]);
+      s2[i & 1] = fma2(d[i], RAGGED ? c : h[i], s2[i & 1]);
+    }
+    if (!RAGGED && !full && fabsf(mean * rstd) == __int_as_float(0x7F800000)) {
+      s2[0] = s2[1] = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (p.lane + 2 * i / V * p.L < a.w.NV) s2[i & 1] = fma2(d[i], h[i], s2[i & 1]);
     }
     s1[0] = add2(s1[0], s1[1]);
     s2[0] = add2(s2[0], s2[1]);
@@ -843,8 +856,14 @@ __global__ void __launch_bounds__(kBlock, 1) norm_bwd_kernel(NormGradArgs a) {
     if (MODE != kPart || in) {
       c1 *= inv_n;
       c2 *= inv_n;
+      if constexpr (RAGGED) {  // c1 has the factor rstd already, and c2 lacks it here
+        c2 *= rstd;
 #pragma unroll
-      for (int i = 0; i < P; ++i) d[i] = mul2(f2(rstd), add2(d[i], fma2(h[i], f2(-c2), f2(-c1))));
+        for (int i = 0; i < P; ++i) d[i] = fma2(h[i], f2(-c2), add2(d[i], f2(-c1)));
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) d[i] = mul2(f2(rstd), add2(d[i], fma2(h[i], f2(-c2), f2(-c1))));
+      }
       store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), d, p, feed, a.w.NV, N);
     }
     row += a.w.step;
