@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libdyt.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("dyt_api.cu", "dyt_inst_f32.cu", "dyt_inst_bf16.cu", "dyt_inst_f16.cu",
                                               "dyt_norm.cu", "dyt_loss.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("dyt_kernels.cuh", "dyt_math.cuh", "dyt_async.cuh", "dyt_finalize.cuh",
-                                                  "dyt_select.cuh", "dyt_select_impl.cuh", "dyt_host.h",
+                                                  "dyt_select.cuh", "dyt_select_impl.cuh", "dyt_host.h", "dyt_optin.h",
                                                   "dyt_norm.cuh", "dyt_loss.cuh")] + [
     os.path.join(INCLUDE, "dyt.h")]
 

@@ -15,6 +15,7 @@
 #include "dyt.h"
 #include "dyt_finalize.cuh"
 #include "dyt_host.h"
+#include "dyt_optin.h"
 #include "dyt_select.cuh"
 
 namespace dyt {
@@ -39,7 +40,7 @@ namespace {
 std::mutex g_mu;
 std::unordered_map<int, int> g_sms;                   // device -> SM count
 std::unordered_map<uint64_t, int> g_occ;              // (device, kernel, block) -> CTAs per SM
-std::unordered_map<uint64_t, int> g_smem_ready;       // (device, kernel) -> dynamic shared memory opted in
+SmemOptIn g_smem;                                     // (device, kernel) -> dynamic shared memory opted in
 
 uint64_t kernel_key(int dev, const void *kernel) {
   return ((uint64_t)(uint32_t)dev << 48) ^ (uint64_t)(uintptr_t)kernel;
@@ -92,19 +93,12 @@ dyt_status occupancy(int dev, const void *kernel, int block, int *ctas) {
   return DYT_OK;
 }
 
-// Opt a kernel in to `bytes` of dynamic shared memory, once per device.
+// Opt a kernel in to `bytes` of dynamic shared memory, once per device and size.
 dyt_status prepare_smem(int dev, const void *kernel, int bytes) {
-  const uint64_t key = kernel_key(dev, kernel);
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    auto it = g_smem_ready.find(key);
-    if (it != g_smem_ready.end() && it->second >= bytes) return DYT_OK;
-  }
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return cuda_fail(e);
-  std::lock_guard<std::mutex> lk(g_mu);
-  g_smem_ready[key] = bytes;
-  return DYT_OK;
+  const int e = g_smem.raise(kernel_key(dev, kernel), bytes, [&](int b) {
+    return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, b);
+  });
+  return e == (int)cudaSuccess ? DYT_OK : cuda_fail((cudaError_t)e);
 }
 
 dyt_status check_shape(int64_t M, int64_t N, int xd) {

@@ -23,7 +23,7 @@ void record_info(const dyt_launch_info &i);
 dyt_status current_sms(int *dev_out, int *sms_out);
 // CTAs of `block` threads of a kernel without dynamic shared memory that fit on an SM (cached).
 dyt_status occupancy(int dev, const void *kernel, int block, int *ctas);
-// Opt a kernel in to `bytes` of dynamic shared memory, once per device.
+// Opt a kernel in to at least `bytes` of dynamic shared memory, once per device and size; safe from any thread.
 dyt_status prepare_smem(int dev, const void *kernel, int bytes);
 
 dyt_status check_shape(int64_t M, int64_t N, int xd);
