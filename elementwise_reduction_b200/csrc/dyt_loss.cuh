@@ -139,7 +139,7 @@ __host__ __device__ constexpr size_t rows_smem(int block) { return (size_t)block
 // us, bf16 over 2368 warps: 4096 rows of 32000 (16 batches), 1.73 rounds whole,
 // 58.4, 6.92 in four parts, 48.9, 13.8 in eight 51.5; 2000 rows of 131072 in five 87.7,
 // ten 91.6; 400 rows of 50000 in five parts, one round, 14.9, in eight 17.4, in twelve 17.8.
-constexpr int kListedParts = 16;  // at most, where the kernel chooses
+constexpr int kListedParts = 16;  // room for at least so many (or all of a row's batches), where the kernel chooses
 constexpr int kPartBatches = 3;   // at least, in more than one round
 __host__ __device__ inline int choose_parts(float rows, float warps, int most, int batches) {
   const float least = ceilf(2.0f * warps / fmaxf(rows, 1.0f));
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kRowsBlock, 2) loss_rows_kernel(LossArgs a) {
   int parts = a.S;
   if (a.listed) {
     rows = list.fill(a);
-    parts = choose_parts((float)rows, (float)warps, min(a.most, kListedParts), a.batches);
+    parts = choose_parts((float)rows, (float)warps, a.most, a.batches);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.done[0] = 0u;

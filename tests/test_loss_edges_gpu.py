@@ -1,0 +1,47 @@
+"""The policy loss's kernels where its other tests do not reach: parts of few weighted
+rows, vocabularies beyond 70000, in place on ragged rows, sliced batches."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests import row_helpers as R
+from tests.test_loss_gpu import Case, dyt
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+
+
+def parts_written(c, parts):
+    """How many partial sums a call writes. They lie at the workspace's start, with room for at least 16
+    a row (of rows of 16 batches or more)."""
+    ws = dyt().policy_loss_workspace(c.z.t)
+    ws.fill_(255)
+    c.forward(ws=ws)
+    M = c.z.t.shape[0]
+    return int((ws[:M * max(parts, 16) * 8].view(torch.int32).view(-1, 2) != -1).any(-1).sum())
+
+
+@pytest.mark.parametrize("M,N,dtype", [(64, 131072, "bf16"), (32, 152064, "bf16"), (37, 131072, "f16"),
+                                       (40, 100000, "f32"), (300, 40000, "bf16")])
+def test_weights_leave_few_long_rows_their_parts(M, N, dtype):
+    # the same rows with and without weights: as many parts, whichever way the kernel finds the rows
+    c = Case(M, N, dtype)
+    c.forward()
+    parts = dyt().dyt_last_launch_info()["col_chunks"]
+    assert parts > 4
+    assert parts_written(c, parts) == M * parts
+    c.weight = torch.full((M,), 1.0 / M, device="cuda")
+    got, info = c.check_forward()
+    assert info["col_chunks"] == parts and parts_written(c, parts) == M * parts
+    c.check_backward(got, grad=100.0)
+    c.weight[1::2] = 0  # half of them
+    c.tokens[1::2] = -100
+    got, _ = c.check_forward()
+    assert parts_written(c, parts) >= M // 2 * parts // 2
+    c.check_backward(got, grad=100.0)
