@@ -30,15 +30,21 @@ def row_pitch(t: torch.Tensor) -> int | None:
         return None
     if t.dim() == 1:
         return t.shape[0] if t.shape[0] <= 1 or t.stride(0) == 1 else None
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    N, ld = shape[-1], stride[-2]
+    if N > 1 and stride[-1] != 1:
         return None
-    ld = t.stride(-2)
-    for i in range(t.dim() - 2):  # dimension i must step over whole blocks of dimension i + 1
-        if t.shape[i] > 1 and t.stride(i) != t.shape[i + 1] * t.stride(i + 1):
-            return None
-    if t.numel() > t.shape[-1] and ld < t.shape[-1]:
+    n, step = shape[-2], ld  # of the last dimension with more than one step (others have no stride that matters)
+    for i in range(len(shape) - 3, -1, -1):
+        if shape[i] > 1:
+            if n <= 1:
+                ld = stride[i]
+            elif stride[i] != n * step:  # dimension i must step over whole blocks of the next
+                return None
+            n, step = shape[i], stride[i]
+    if ld < N and t.numel() > N:
         return None
-    return max(ld, t.shape[-1])
+    return ld if ld > N else N
 
 
 def _rows(t: torch.Tensor, what: str) -> int:

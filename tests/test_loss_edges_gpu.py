@@ -45,3 +45,24 @@ def test_weights_leave_few_long_rows_their_parts(M, N, dtype):
     got, _ = c.check_forward()
     assert parts_written(c, parts) >= M // 2 * parts // 2
     c.check_backward(got, grad=100.0)
+
+
+def test_the_last_position_of_every_sequence():
+    # [:, -1:] and [:, k]: rows a whole sequence apart, read where they lie
+    B, S, N = 5, 7, 1003
+    z = torch.randn(B, S, N, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).to(torch.bfloat16)
+    tokens = torch.arange(B, device="cuda") * 100
+    adv = torch.linspace(-1, 1, B, device="cuda")
+    flat = z[:, -1].contiguous()
+    old = torch.full((B,), -7.0, device="cuda")
+    want = dyt().policy_loss_forward(flat, tokens, old, adv)
+    dwant = dyt().policy_loss_backward(flat, tokens, want[2], want[3])
+    for v, shape in ((z[:, -1:], (B, 1)), (z[:, -1], (B,))):
+        t, o, a = tokens.view(shape), old.view(shape), adv.view(shape)
+        got = dyt().policy_loss_forward(v, t, o, a)
+        assert got[1].shape == shape and got[2].shape == (*shape, 2)
+        assert all(torch.equal(p.flatten(), q.flatten()) for p, q in zip(got, want))
+        d = dyt().policy_loss_backward(v, t, got[2], got[3])
+        assert d.shape == v.shape and torch.equal(d.reshape(B, N), dwant)
+    x = z[:, 2:3]
+    assert torch.equal(dyt().layer_norm_forward(x)[0], dyt().layer_norm_forward(x.contiguous())[0])

@@ -43,3 +43,14 @@ def test_rows_far_from_zero_have_finite_gradients(N, xd):
     R.assert_close(dx, want[0], tol[0] + R.half_step(dx.dtype, want[0]), "dx")
     assert torch.equal(dgamma, torch.zeros_like(dgamma))
     R.assert_close(dbeta, want[2], tol[2] + R.half_step(dbeta.dtype, want[2]), "dbeta")
+
+
+def test_rows_cut_across_a_dimension_of_one_step():
+    # [:, :, :2] of (3, 1, 5, N) has no single pitch: refused, and copied by the modules
+    x = torch.randn(3, 1, 5, 40, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    v = x[:, :, :2]
+    with pytest.raises(ValueError):
+        dyt().layer_norm_forward(v)
+    assert torch.equal(dyt().LayerNorm(40, affine=False)(v), dyt().layer_norm_forward(v.contiguous())[0])
+    layer = dyt().DyT(40, device="cuda")
+    assert torch.equal(layer(v), layer(v.contiguous()))
