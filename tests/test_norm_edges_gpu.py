@@ -54,3 +54,33 @@ def test_rows_cut_across_a_dimension_of_one_step():
     assert torch.equal(dyt().LayerNorm(40, affine=False)(v), dyt().layer_norm_forward(v.contiguous())[0])
     layer = dyt().DyT(40, device="cuda")
     assert torch.equal(layer(v), layer(v.contiguous()))
+
+
+@pytest.mark.parametrize("N", [64, 1000, 4100, 9001])
+def test_parameters_that_the_kernel_before_has_written(N):
+    # gamma, beta and the upstream gradient straight from the calls before, with no other kernel between them
+    g = torch.Generator("cuda").manual_seed(N)
+    x = torch.randn(300, N, device="cuda", generator=g)
+    a = torch.randn(1, N, device="cuda", generator=g)
+    outs = []
+    for wait in (True, False):
+        got = []
+        rest = lambda: torch.cuda.synchronize() if wait else None  # noqa: E731
+        gamma = torch.zeros(1, N, device="cuda")
+        y, dgamma = torch.zeros_like(x), torch.zeros(N, device="cuda")
+        stats = [torch.zeros(300, device="cuda") for _ in range(2)]
+        ws = dyt().layer_norm_workspace(x)
+        rest()
+        for step in range(4):
+            dyt().layer_norm_forward(a * (step + 1.0) if step == 0 else y[:1], out=gamma)
+            rest()
+            dyt().layer_norm_forward(x, gamma.view(N), gamma.view(N), out=y, mean=stats[0], rstd=stats[1])
+            rest()
+            dyt().layer_norm_backward(x, y, stats[0], stats[1], gamma.view(N), dx=y, dgamma=dgamma, ws=ws)
+            rest()
+            dyt().layer_norm_forward(y, dgamma, gamma.view(N), out=y)
+            rest()
+            got += [y.clone(), dgamma.clone()]
+            rest()
+        outs.append(got)
+    assert all(torch.equal(p, q) for p, q in zip(*outs))
