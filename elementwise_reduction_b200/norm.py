@@ -78,15 +78,16 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
                         gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
                         dx: torch.Tensor | None = None, dgamma: torch.Tensor | None = None,
                         dbeta: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-                        stream: torch.cuda.Stream | None = None):
+                        stream: torch.cuda.Stream | None = None, frozen: bool = False):
     """(dx, dgamma, dbeta) from the forward's statistics: dx in x's dtype and each
     parameter's gradient in its parameter's dtype (None for a parameter that is not
     given; beta's values are not read). x, dy and dx may be row-strided views; dx may
-    be x or dy."""
+    be x or dy. frozen: gamma's gradient is not wanted (None; dx alone then takes one
+    kernel launch less)."""
     index = x.get_device()
     if _elsewhere(index, stream):
         with _there(x, stream):
-            return layer_norm_backward(x, dy, mean, rstd, gamma, beta, dx, dgamma, dbeta, ws)
+            return layer_norm_backward(x, dy, mean, rstd, gamma, beta, dx, dgamma, dbeta, ws, frozen=frozen)
     M, N = _shape(x)
     ldx, code, dev = _pitch(x, "x"), _code(x, "x"), x.device
     lddy = _like(dy, "dy", x)
@@ -97,13 +98,15 @@ def layer_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, r
     gp = None if gamma is None else _vector(gamma, "gamma", N, index, _PARAM)
     if beta is not None:
         _vector(beta, "beta", N, index, _PARAM)
-    if (gamma is None and dgamma is not None) or (beta is None and dbeta is not None):
-        raise ValueError("dgamma and dbeta need their parameters")
+    if ((gamma is None or frozen) and dgamma is not None) or (beta is None and dbeta is not None):
+        raise ValueError("dgamma and dbeta need their parameters, and dgamma one that is not frozen")
     gd = bd = code
     gg = bg = None
     if gamma is not None:
         gd = DTYPE_CODE[gamma.dtype]
-        if dgamma is None:
+        if frozen:
+            pass
+        elif dgamma is None:
             dgamma = torch.empty_like(gamma)
             gg = dgamma.data_ptr()
         else:
@@ -147,7 +150,9 @@ class LayerNormFunction(torch.autograd.Function):
     def backward(ctx, dy):
         x, mean, rstd, gamma, beta = ctx.saved_tensors
         dy = dy if row_pitch(dy) is not None else dy.contiguous()
-        dx, dgamma, dbeta = layer_norm_backward(x, dy, mean, rstd, gamma, beta)
+        _, want_gamma, want_beta, _ = ctx.needs_input_grad
+        dx, dgamma, dbeta = layer_norm_backward(x, dy, mean, rstd, gamma, beta if want_beta else None,
+                                                frozen=not want_gamma)
         return dx, dgamma, dbeta, None
 
 

@@ -84,3 +84,45 @@ def test_parameters_that_the_kernel_before_has_written(N):
             rest()
         outs.append(got)
     assert all(torch.equal(p, q) for p, q in zip(*outs))
+
+
+@pytest.mark.parametrize("N", [96, 1001, 9000])
+@pytest.mark.parametrize("want_gamma", [True, False])
+@pytest.mark.parametrize("want_beta", [True, False])
+def test_frozen_parameters(N, want_gamma, want_beta):
+    # no gradient, and no kernel for the gradients where none is wanted
+    g = torch.Generator("cuda").manual_seed(N)
+    x, up = (torch.randn(33, N, device="cuda", generator=g) for _ in range(2))
+    full, part = (dyt().LayerNorm(N, device="cuda") for _ in range(2))
+    part.gamma.requires_grad_(want_gamma)
+    part.beta.requires_grad_(want_beta)
+    grads = []
+    for layer in (full, part):
+        with torch.no_grad():
+            layer.gamma.copy_(torch.linspace(0.5, 1.5, N, device="cuda"))
+        a = x.clone().requires_grad_()
+        layer(a).backward(up)
+        grads.append((a.grad, layer.gamma.grad, layer.beta.grad))
+    assert torch.equal(grads[1][0], grads[0][0])
+    for want, i in ((want_gamma, 1), (want_beta, 2)):
+        assert torch.equal(grads[1][i], grads[0][i]) if want else grads[1][i] is None
+
+
+@pytest.mark.parametrize("N", [96, 9000])
+def test_a_frozen_gamma_and_its_refusals(N):
+    g = torch.Generator("cuda").manual_seed(N)
+    x, dy = (torch.randn(20, N, device="cuda", generator=g) for _ in range(2))
+    gamma = torch.rand(N, device="cuda", generator=g)
+    _, mean, rstd = dyt().layer_norm_forward(x, gamma, gamma, EPS)
+    want = dyt().layer_norm_backward(x, dy, mean, rstd, gamma, gamma)
+    kernels = dyt().dyt_last_launch_info()["kernels"]
+    got = dyt().layer_norm_backward(x, dy, mean, rstd, gamma, frozen=True)
+    assert torch.equal(got[0], want[0]) and got[1] is None and got[2] is None
+    assert dyt().dyt_last_launch_info()["kernels"] == kernels - 1
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = dyt().layer_norm_backward(x, dy, mean, rstd, gamma, gamma, stream=s, frozen=True)
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and got[1] is None and torch.equal(got[2], want[2])
+    with pytest.raises(ValueError):
+        dyt().layer_norm_backward(x, dy, mean, rstd, gamma, dgamma=gamma.clone(), frozen=True)
