@@ -16,6 +16,11 @@
 //
 // Exponentials are 2^((z - m) C) with C = log2(e) / T in binary32: the maximum is
 // taken out before anything is rounded to its size, and its own term is exactly 1.
+// C's rounding (up to 2^-24, the same way in every term) puts a row's log sum off by
+// that share of the mean of |z - m| / T under the row's probabilities. Measured over 512
+// rows at T = 0.7, where it is near its largest: log probabilities 3.3e-7 off on average
+// (131072 bf16; half of that is their own rounding, and the plain binary32 form's
+// 4.2e-7), with the constant in two parts 3.1e-7, for 3 to 4% more time.
 #pragma once
 
 #include "dyt_async.cuh"
