@@ -23,8 +23,13 @@ constexpr int kMostParts = 256;  // parts of a row, at most
 constexpr int kFinishCtasPerSm = 2;
 
 constexpr int kGradBlock = 256;
-constexpr int kGradCtasPerSm = 8;     // 2048 resident threads
-constexpr int64_t kWarpRow = 8192;    // rows of at most this many bytes take a warp
+// CTAs that an SM holds (the kernel's launch bounds). Few rows are split into as many parts as there is room
+// for at once: 64 x 131072 bf16 6.2 us, in 1.6 times as many parts 7.7; 300 x 50001 11.7 and 13.2.
+constexpr int kGradCtasPerSm = dyt::loss::kGradCtas;
+// Rows of at most kWarpRow bytes take a warp, unless there are fewer of them than kCtaRowsPerSm an SM
+// (1000 x 2000 bf16, a CTA each, 4.0 us, a warp each 4.3).
+constexpr int64_t kWarpRow = 8192;
+constexpr int kCtaRowsPerSm = 8;
 constexpr int64_t kGradPart = 65536;  // the largest part of a row, bytes
 constexpr int64_t kGradPartMin = 4096;  // and the smallest
 
@@ -74,7 +79,7 @@ LossPlan plan_backward(int64_t M, int64_t N, size_t es, int sms) {
   LossPlan p = {};
   const int64_t bytes = N * (int64_t)es;
   const int64_t slots = (int64_t)sms * kGradCtasPerSm;
-  p.cta = bytes > kWarpRow || M < slots;
+  p.cta = bytes > kWarpRow || M < (int64_t)sms * kCtaRowsPerSm;
   p.S = 1;
   p.block = kGradBlock;
   if (p.cta)

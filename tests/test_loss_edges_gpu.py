@@ -66,3 +66,15 @@ def test_the_last_position_of_every_sequence():
         assert d.shape == v.shape and torch.equal(d.reshape(B, N), dwant)
     x = z[:, 2:3]
     assert torch.equal(dyt().layer_norm_forward(x)[0], dyt().layer_norm_forward(x.contiguous())[0])
+
+
+@pytest.mark.parametrize("M,N,dtype,pad", [(1, 131072, "bf16", 0), (64, 131072, "bf16", 0), (300, 50001, "f16", 3),
+                                           (148, 32000, "bf16", 0), (9, 5003, "f32", 1)])
+def test_the_gradients_of_few_rows_take_no_more_parts_than_fit(M, N, dtype, pad):
+    # five CTAs an SM: a part of a row for each, in one go
+    c = Case(M, N, dtype, pitch=N + pad)
+    got, _ = c.check_forward()
+    info = c.check_backward(got, grad=100.0)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert info["path"] == 2 and info["grid"] == M * info["col_chunks"] <= 5 * sms
+    assert info["col_chunks"] > 1
