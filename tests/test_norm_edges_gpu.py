@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from tests import row_helpers as R
+from tests.test_norm_gpu import check
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +127,27 @@ def test_a_frozen_gamma_and_its_refusals(N):
     assert torch.equal(got[0], want[0]) and got[1] is None and torch.equal(got[2], want[2])
     with pytest.raises(ValueError):
         dyt().layer_norm_backward(x, dy, mean, rstd, gamma, dgamma=gamma.clone(), frozen=True)
+
+
+# rows side by side in a CTA: part of a warp, a warp and several warps per row, whole vectors and ragged
+@pytest.mark.parametrize("N,xd,rows", [(96, "bf16", 64), (30, "f32", 128), (512, "f16", 16), (509, "bf16", 16),
+                                       (1024, "bf16", 8), (1021, "f16", 8), (8192, "f32", 1), (7001, "bf16", 1)])
+@pytest.mark.parametrize("runs,more", [(2, 3), (1, 1)])
+def test_column_sums_over_several_runs(N, xd, rows, runs, more):
+    # runs of 128 rows a lane, then `more` rows, of which most rows of the grid do not make the last one
+    step = torch.cuda.get_device_properties(0).multi_processor_count * rows
+    M = step * (runs * 128 + more - 1) + (rows * 5 + 3 if rows > 1 else 5)
+    _, bwd = check(M, N, xd)
+    assert bwd["rows_per_step"] == rows and bwd["grid"] * rows == step
+    assert -(-M // step) == runs * 128 + more and M % step
+
+
+@pytest.mark.parametrize("N,xd", [(9000, "bf16"), (9001, "bf16"), (20000, "f32")])
+def test_column_sums_of_long_rows_over_several_runs(N, xd):
+    # the second pass's row groups take every row_groups-th row
+    _, bwd = check(1, N, xd)
+    groups = (torch.cuda.get_device_properties(0).multi_processor_count * 4
+              // -(-(N // (16 // R.DT[xd].itemsize) if N % 8 == 0 else N) // 256))
+    M = groups * (2 * 128 + 3) + 1
+    _, bwd = check(M, N, xd)
+    assert bwd["row_groups"] == groups and M > 256 * groups
