@@ -587,7 +587,8 @@ __global__ void __launch_bounds__(256, kGradCtas) loss_grad_kernel(LossGradArgs 
     };
     auto one = [&](int64_t j) {
       const float p = power(f2(to_f32<T>(z[j]))).x;
-      dz[j] = from_f32<T>(j == tok ? fmaf(B, p, A) : B * p);
+      // two roundings at the token, as in the vectors: the same bits at every offset
+      dz[j] = from_f32<T>(j == tok ? __fadd_rn(__fmul_rn(B, p), A) : B * p);
     };
     if (part == 0)
       for (int64_t j = t; j < head; j += G) one(j);

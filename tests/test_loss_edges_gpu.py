@@ -78,3 +78,66 @@ def test_the_gradients_of_few_rows_take_no_more_parts_than_fit(M, N, dtype, pad)
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     assert info["path"] == 2 and info["grid"] == M * info["col_chunks"] <= 5 * sms
     assert info["col_chunks"] > 1
+
+
+@pytest.mark.parametrize("M,N,dtype,pitch,offset", [(3, 151936, "bf16", None, 0), (300, 151936, "bf16", None, 0),
+                                                    (5, 256000, "f16", None, 0), (40, 256000, "bf16", 256003, 1),
+                                                    (2, 500001, "f32", None, 3), (1, 2000003, "bf16", None, 1)])
+def test_large_vocabularies(M, N, dtype, pitch, offset):
+    c = Case(M, N, dtype, pitch=pitch, offset=offset, T=0.9, masked=0.3 if M > 3 else 0.0)
+    got, _ = c.check_forward()
+    c.check_backward(got, grad=1000.0)
+    c.check_backward(got, grad=1000.0, out_pitch=N + 5, out_offset=2)  # the output at other offsets
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,N,pitch,offset", [(9, 5003, 5003, 3), (2000, 77, 77, 1), (1300, 1001, 1008, 0),
+                                              (5, 70001, 70003, 5), (700, 9, 9, 2)])
+def test_gradients_in_place_on_ragged_rows(M, N, pitch, offset, dtype):
+    c = Case(M, N, dtype, pitch=pitch, offset=offset, masked=0.2)
+    got, _ = c.check_forward()
+    dz = dyt().policy_loss_backward(c.z.t, c.tokens, got[2], got[3])
+    assert dyt().policy_loss_backward(c.z.t, c.tokens, got[2], got[3], dlogits=c.z.t) is c.z.t
+    want = R.Guarded(M, N, c.z.t.dtype, pitch, offset)
+    dyt().policy_loss_backward(Case(M, N, dtype, pitch=pitch, offset=offset, masked=0.2).z.t, c.tokens, got[2], got[3],
+                               dlogits=want.t)
+    assert torch.equal(c.z.t, dz) and torch.equal(c.z.t, want.t)
+    c.z.assert_surroundings_untouched("dlogits")
+
+
+def test_a_batch_cut_by_one_position():
+    # a causal model's logits predict the next token: logits[:, :-1] has no single pitch, is refused by the
+    # function and copied by the module; with weight 0 at the last position the whole logits are taken as they
+    # lie, those rows unread, for the same loss and gradient
+    B, S, N = 4, 30, 1003
+    g = torch.Generator("cuda").manual_seed(5)
+    z = torch.randn(B, S, N, device="cuda", generator=g).to(torch.bfloat16)
+    ids = torch.randint(0, N, (B, S), device="cuda", generator=g)
+    adv = torch.randn(B, 1, device="cuda", generator=g).expand(B, S - 1)
+    old = torch.full((B, S - 1), -7.0, device="cuda")
+    weight = torch.full((B, S - 1), 1.0 / (B * (S - 1)), device="cuda")
+    with pytest.raises(ValueError):
+        dyt().policy_loss_forward(z[:, :-1], ids[:, 1:].contiguous(), old, adv.contiguous())
+    loss = dyt().PolicyLoss()
+    a = z.clone().requires_grad_()
+    cut = loss(a[:, :-1], ids[:, 1:], old, adv, weight=weight)
+    cut.backward()
+    b = z.clone()
+    b[:, -1] = float("nan")
+    b.requires_grad_()
+    last = lambda t, v: torch.cat([t, torch.full_like(t[:, :1], v)], 1)  # noqa: E731
+    whole = loss(b, ids.roll(-1, 1), last(old, 0.0), last(adv, 0.0), weight=last(weight, 0.0))
+    whole.backward()
+    # the row sums are those of other parts and lanes: each loss is within its own bound of the formula
+    flat = z[:, :-1].reshape(-1, N)
+    want, tol = R.loss_forward(flat, ids[:, 1:].reshape(-1), old.reshape(-1), adv.reshape(-1),
+                               weight=weight.reshape(-1))
+    for v in (cut, whole):
+        R.assert_close(v.detach(), want[0], tol[0], "loss")
+    wdz, tdz = R.loss_backward(flat, ids[:, 1:].reshape(-1), want[2], want[3])
+    # (the rows' own statistics and coefficients are rounded: their bounds, by the gradient's derivatives)
+    extra = wdz.abs() * (tol[2][:, 1:] + 2 * R.U) + tol[3][:, None]
+    for v in (a, b):
+        got = v.grad[:, :-1].reshape(-1, N)
+        R.assert_close(got, wdz, tdz + extra + R.half_step(got.dtype, wdz), "dlogits")
+        assert torch.equal(v.grad[:, -1], torch.zeros_like(v.grad[:, -1]))
