@@ -419,7 +419,8 @@ __device__ __forceinline__ void cta_sum(float (&v)[C], float *red) {
   for (int c = 0; c < C; ++c) v[c] = warp_sum(lane < warps ? red[c * kMaxWarps + lane] : 0.0f);
 }
 
-// s / n for n = N: the product with 1 / n, corrected once (exact for a row of equal values).
+// s / n for n = N: the product with 1 / n, corrected once. A quotient that binary32 holds comes out exactly (a
+// row of equal values whose sum does not round); the sum's rounding stays.
 __device__ __forceinline__ float div_n(float s, float n, float inv_n) {
   const float q = s * inv_n;
   return fabsf(q) < __int_as_float(0x7F800000) ? fmaf(fmaf(-q, n, s), inv_n, q) : q;
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(NormArgs a) {
       for (int e = 0; e < V; ++e) s[0] += v[e];
     }
     cta_sum(s, red[0]);
-    const float mean = s[0] / (float)a.w.N;  // exact for a constant row
+    const float mean = s[0] / (float)a.w.N;  // a division: a row of equal values whose sum does not round is exact
     float q[1] = {0.0f};
 #pragma unroll 4
     for (int64_t cv = threadIdx.x; cv < a.w.NV; cv += B) {

@@ -151,3 +151,63 @@ def test_column_sums_of_long_rows_over_several_runs(N, xd):
     M = groups * (2 * 128 + 3) + 1
     _, bwd = check(M, N, xd)
     assert bwd["row_groups"] == groups and M > 256 * groups
+
+
+@pytest.mark.parametrize("xd", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N", [3, 61, 300, 513, 1001, 4099, 8192, 9001, 20000])
+def test_constant_rows_whose_sum_rounds(N, xd):
+    # The mean of N times c is off by the sum's rounding alone: D u |c| (D additions, see row_helpers.chain),
+    # two halves of a step more. eps bounds what is left: |y| <= |mean error| / sqrt(eps).
+    value = torch.tensor([0.1, -0.3, 1 / 3, 1e-3, 7.7, 0.0], device="cuda").to(R.DT[xd])
+    x = value[:, None].expand(6, N).contiguous()
+    gamma = torch.ones(N, device="cuda")
+    y, mean, rstd = dyt().layer_norm_forward(x, gamma, None, EPS)
+    v = value.double()
+    off = (R.chain(N) + 2) * R.U * v.abs()
+    R.assert_close(mean, v, off, "mean")
+    # the variance that is computed is at most the square of the mean's error
+    want = torch.full_like(v, EPS ** -0.5)
+    R.assert_close(rstd, want, want * (off.square() / EPS / 2 + 4 * R.U), "rstd")
+    t = (off * want)[:, None] * (1 + 4 * R.U)
+    R.assert_close(y, torch.zeros_like(y, dtype=torch.float64), t + R.half_step(y.dtype, t), "y")
+    assert torch.equal(y[5], torch.zeros_like(y[5]))
+    # the gradient with those statistics, against the formula with the same
+    dy = torch.randn(6, N, device="cuda", generator=torch.Generator("cuda").manual_seed(N)).to(R.DT[xd])
+    dx, dgamma, dbeta = dyt().layer_norm_backward(x, dy, mean, rstd, gamma, gamma)
+    want, tol = R.norm_backward(x, dy, mean, rstd, gamma)
+    for got, w, b, name in ((dx, want[0], tol[0], "dx"), (dgamma, want[1], tol[1], "dgamma"),
+                            (dbeta, want[2], tol[2], "dbeta")):
+        R.assert_close(got, w, b + R.half_step(got.dtype, w), name)
+
+
+@pytest.mark.parametrize("xd", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,N,pitch,offset", [(1500, 9, 9, 1), (1500, 61, 64, 3), (700, 255, 255, 1), (700, 509, 512, 0),
+                                              (400, 1001, 1001, 5), (400, 1001, 1008, 0), (50, 8191, 8191, 1),
+                                              (20, 9001, 9003, 1), (20, 20001, 20001, 3)])
+def test_in_place_on_ragged_rows(M, N, pitch, offset, xd):
+    # rows at any offset, one after the other or NaN between them; the output over x, and over dy
+    g = torch.Generator("cuda").manual_seed(N)
+    v = [torch.randn(M, N, device="cuda", generator=g) for _ in range(2)]
+    gamma, beta = (torch.randn(N, device="cuda", generator=g) for _ in range(2))
+    make = lambda t: R.Guarded(M, N, R.DT[xd], pitch, offset)  # noqa: E731
+    x, dy = make(0), make(0)
+    x.set(v[0])
+    dy.set(v[1])
+    y = make(0)
+    _, mean, rstd = dyt().layer_norm_forward(x.t, gamma, beta, EPS, out=y.t)
+    dx = make(0)
+    want = dyt().layer_norm_backward(x.t, dy.t, mean, rstd, gamma, beta, dx=dx.t)
+    for _ in range(3):
+        a = make(0)
+        a.set(v[0])
+        got = dyt().layer_norm_forward(a.t, gamma, beta, EPS, out=a.t)
+        assert torch.equal(a.t, y.t) and torch.equal(got[1], mean) and torch.equal(got[2], rstd)
+        a.assert_surroundings_untouched("y")
+        for which in (0, 1):
+            a, b = make(0), make(0)
+            a.set(v[0])
+            b.set(v[1])
+            out = (a, b)[which]
+            got = dyt().layer_norm_backward(a.t, b.t, mean, rstd, gamma, beta, dx=out.t)
+            assert torch.equal(out.t, dx.t) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+            out.assert_surroundings_untouched("dx")
