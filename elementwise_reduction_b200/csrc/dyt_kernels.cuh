@@ -260,7 +260,11 @@ __device__ __forceinline__ uint32_t dynamic_smem_bytes() {
 // predecessor), then let the next grid get scheduled. The kernels read and
 // write no global memory before this (the 16-byte kernels only issue L2
 // prefetch hints, which change no memory state), so programmatic launch keeps
-// stream order.
+// stream order. One exception: the policy loss's second kernel reads the first
+// one's inputs before it. That rests on this order, here and in every kernel
+// that is launched before such a one: wait first, then release the next grid.
+// A grid is released only when all CTAs of the one before have waited, so
+// whatever came before that one has ended.
 __device__ __forceinline__ void pdl_prologue() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -171,7 +171,10 @@ __host__ __device__ inline int choose_parts(float rows, float warps, int most, i
 
 // Which of the first kMaxListed rows count: a bit each, and how many do before
 // each word of bits. Every CTA makes the list itself, so that warps take equal
-// numbers of rows that count however the weights lie.
+// numbers of rows that count however the weights lie. A warp looks up at most 32
+// items, so the rows times the parts that there is room for must not pass that
+// many a warp: on 148 SMs 8192 rows of less than 10 batches, 4736 of 16 and more
+// (vocabularies of 32768 in 16 bits). Beyond it weights are looked up item by item.
 constexpr int kMaxListed = 8192;
 struct RowList {
   uint32_t bits[kMaxListed / 32];
@@ -433,6 +436,8 @@ constexpr int kThreadParts = 16;  // rows of at most this many parts take a thre
 // Before the wait for the first kernel a CTA reads its first rows' inputs: that
 // kernel lets this one start only after its own wait for what came before, and
 // writes none of them. (Those loads pass by L1, which may be older than that.)
+// This kernel is therefore launched directly after loss_rows_kernel, with nothing
+// between them, and that one releases its successor nowhere but in pdl_prologue.
 template <typename T>
 __global__ void __launch_bounds__(kFinishBlock) loss_finish_kernel(LossArgs a) {
   __shared__ double sh[kFinishBlock / 32];

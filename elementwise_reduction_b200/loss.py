@@ -6,7 +6,10 @@
 
 logits: [..., N], the other inputs one value per row; rows of weight 0 (padding,
 prompts) do not count and are not read. No tensor of the logits' size besides
-the gradient is made.
+the gradient is made, for logits whose rows are dense and evenly spaced. A batch
+cut by one position, logits[:, :-1], is not: the module copies it and the
+functions refuse it. Take the whole logits instead, with weight 0 at the last
+position: those rows are not read either.
 """
 from __future__ import annotations
 
@@ -106,7 +109,8 @@ def policy_loss_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: torc
 
 
 class PolicyLossFunction(torch.autograd.Function):
-    """Autograd wrapper: the logits and three numbers a row are saved; the gradient goes to the logits alone."""
+    """Autograd wrapper: the logits and three numbers a row are saved (a copy of logits that have no row
+    pitch); the gradient goes to the logits alone."""
 
     @staticmethod
     def forward(ctx, logits, tokens, old_logp, advantage, ref_logp, weight, clip_low, clip_high, kl_coef,

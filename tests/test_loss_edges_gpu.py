@@ -141,3 +141,17 @@ def test_a_batch_cut_by_one_position():
         got = v.grad[:, :-1].reshape(-1, N)
         R.assert_close(got, wdz, tdz + extra + R.half_step(got.dtype, wdz), "dlogits")
         assert torch.equal(v.grad[:, -1], torch.zeros_like(v.grad[:, -1]))
+
+
+@pytest.mark.parametrize("M,N,masked", [(4736, 33000, 0.6), (4737, 33000, 0.6), (6000, 32768, 0.3), (8192, 20000, 0.9),
+                                        (8192, 17000, 0.9)])
+def test_rows_listed_or_looked_up_one_by_one(M, N, masked):
+    # both sides of what a warp can look up in the list: 32 items, rows times the room for parts
+    c = Case(M, N, "bf16", masked=masked)
+    got, _ = c.check_forward()
+    c.check_backward(got, grad=1000.0)
+    M1 = M // 8
+    c.weight = torch.zeros_like(c.weight)
+    c.weight[:M1] = 1.0 / M1  # all of them side by side
+    c.tokens = torch.randint(0, N, (M,), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    c.check_forward()
