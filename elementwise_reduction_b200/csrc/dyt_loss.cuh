@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(256, kGradCtas) loss_grad_kernel(LossGradArgs 
       for (int64_t i = b0 + t; i < b1; i += G) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
       continue;
     }
-    // p = 2^((z - m) C) e^-s: the maximum leaves first, as in the forward
+    // p = 2^((z - m) C) e^-s: the maximum leaves first, as in the forward. (A power below 2^-126 is 0.)
     const float B = -A * expf(-st.y);
     auto power = [&](float2 z2) {
       const float2 e = mul2(add2(z2, f2(-st.x)), f2(a.C));

@@ -211,3 +211,16 @@ def test_in_place_on_ragged_rows(M, N, pitch, offset, xd):
             got = dyt().layer_norm_backward(a.t, b.t, mean, rstd, gamma, beta, dx=out.t)
             assert torch.equal(out.t, dx.t) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
             out.assert_surroundings_untouched("dx")
+
+
+def test_dyt_on_the_last_position_of_every_sequence():
+    g = torch.Generator("cuda").manual_seed(9)
+    x, dy = (torch.randn(6, 5, 72, device="cuda", generator=g)[:, -1:] for _ in range(2))
+    alpha, gamma, beta = torch.tensor([0.7], device="cuda"), torch.rand(72, device="cuda"), torch.rand(72, device="cuda")
+    y = dyt().forward(x, alpha, gamma, beta)
+    assert y.shape == x.shape and torch.equal(y, dyt().forward(x.contiguous(), alpha, gamma, beta))
+    got = dyt().backward(x, dy, alpha, gamma, beta)
+    want = dyt().backward(x.contiguous(), dy.contiguous(), alpha, gamma, beta)
+    assert torch.equal(got[0], want[0])
+    for a, b in zip(got[1:], want[1:]):  # sums of six rows in binary64, rounded once; another plan may add in another order
+        assert torch.allclose(a, b, rtol=4 * R.U, atol=0)
