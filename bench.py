@@ -4,10 +4,11 @@ One step = one forward and one backward (dx, dgamma, dbeta, dalpha) of the
 workload over one batch of synthetic input. Prints ONE JSON line on rank 0.
 The headline workload is the largest configuration (32768 x 8192 bf16); the
 line's `shapes` block times every other workload and layout variant the same
-way, each with its roofline entry, replay percentiles, clocks and the oracle's
-CPU time next to it.
+way, with the oracle's CPU rate next to it. The line keeps a few rounded figures
+of each; --details FILE writes all of them (roofline entries, replay percentiles,
+clocks, launch geometry), which come to tens of kilobytes.
 
-    python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME] [--impl ours|reference]
+    python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME] [--impl ours|reference] [--details FILE]
 
 Multi-GPU (torchrun, one process per GPU): each rank runs the whole workload
 on its own batch of rows (weak scaling); the parameter gradients are summed
@@ -62,6 +63,8 @@ def parse():
     p.add_argument("--no-shapes", action="store_true", help="skip the per-shape table of the other workloads")
     p.add_argument("--no-latency", action="store_true", help="skip the per-call cold-L2 latency percentiles")
     p.add_argument("--no-sustained", action="store_true", help="skip the 1 s back-to-back replay of the step")
+    p.add_argument("--details", metavar="FILE", default=None,
+                   help="write the per-shape and latency tables in full to FILE (JSON)")
     p.add_argument("--record-traffic", metavar="NCU_CSV", default=None,
                    help="store DRAM bytes per launch from an ncu --csv capture of dram__bytes_read.sum and "
                         "dram__bytes_write.sum into profiles/dram_traffic.json for --workload, then exit")
@@ -733,14 +736,42 @@ def run_ours(args, w):
                              "note": "the step graph replayed back to back for 1 s; second half"}
     if world > 1:
         dist.destroy_process_group()
+    details = {}
     if world == 1 and not args.no_shapes:
-        line["shapes"] = shape_table(args, dev, local, cpu=not args.no_cpu_baseline)
+        details["shapes"] = shape_table(args, dev, local, cpu=not args.no_cpu_baseline)
     if world == 1 and not args.no_latency:
-        line["latency_us"] = call_latency(args, dev)
+        details["latency_us"] = call_latency(args, dev)
+    if args.details:
+        with open(args.details, "w") as f:
+            json.dump(details, f, indent=1)
+    line.update(short_tables(details))
     if world == 1 and not args.no_cpu_baseline:  # the oracle's baseline belongs to the 1-GPU line
         line["cpu_baseline"] = cpu_baseline(w)
         line["cpu_baseline_threads"] = cpu_baseline_threads(w)
     print(json.dumps(line), flush=True)
+
+
+def short_tables(details):
+    """The tables of --details as the line carries them, a few figures of four digits
+    each. (A line of tens of kilobytes does not survive whoever keeps the end of a log.)"""
+    four = lambda v: None if v is None else float(f"{v:.4g}")  # noqa: E731
+    out = {}
+    if "shapes" in details:
+        out["shapes"] = {name: {} for name in details["shapes"]}
+        for name, res in details["shapes"].items():
+            for op in ("fwd", "bwd"):
+                t, r = res[op], res[op]["roofline"]
+                out["shapes"][name][op] = {
+                    "us": four(t["burst_us"]), "sustained_us": four(t["sustained_us"]), "GB_s": four(r["achieved"]),
+                    "frac": four(r["frac"]), "rows_per_s": four(t["rows_per_s"]), "traffic": four(r["traffic"])}
+            out["shapes"][name]["floor_us"] = [four(res[op]["burst_us"]) for op in ("copy_floor", "add3_floor")]
+            if "cpu_baseline" in res:
+                out["shapes"][name]["cpu_GB_s"] = [four(res[k]["value"])
+                                                   for k in ("cpu_baseline", "cpu_baseline_threads")]
+    if "latency_us" in details:
+        out["latency_us"] = {name: {op: q["p50"] for op, q in res.items()}
+                             for name, res in details["latency_us"].items()}
+    return out
 
 
 def call_latency(args, dev, calls=30):

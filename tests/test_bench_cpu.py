@@ -80,3 +80,32 @@ def test_threaded_oracle_baseline_uses_the_host_cores():
     d = bench.cpu_baseline_threads(workloads.WORKLOADS["c1_f32_1024x64"], seconds_budget=0.5)
     assert d["unit"] == "GB/s" and d["value"] > 0 and d["kind"].startswith("oracle")
     assert 1 <= d["cores"] <= len(os.sched_getaffinity(0))
+
+
+def test_the_line_stays_short_enough_for_a_log_tail():
+    # thirteen workloads with all that the full tables hold: a few kilobytes in the line
+    sys.path.insert(0, ROOT)
+    import bench
+    from synth import workloads
+
+    third = 1e9 / 3
+    clocks = {"sm_mhz": third, "sm_min_mhz": third, "sm_max_mhz": third, "power_w": third, "reasons": [], "samples": 60}
+    entry = {"us_p10": third, "us_p50": third, "us_p90": third, "replays": 2000, "burst_us": third,
+             "sustained_us": third, "clocks": clocks, "clocks_burst": clocks, "clocks_sustained": clocks,
+             "roofline": {"bound": "hbm", "achieved": third, "peak": third, "unit": "GB/s", "frac": 1 / 3,
+                          "peak_kind": "measured", "traffic": third, "algorithmic_bytes_per_launch": 10 ** 9},
+             "rows_per_s": third}
+    names = list({**workloads.WORKLOADS, **workloads.VARIANTS})
+    cpu = {"value": 1 / 3, "unit": "GB/s"}
+    details = {"shapes": {n: {**{op: entry for op in ("fwd", "bwd", "copy_floor", "add3_floor")},
+                              "cpu_baseline": cpu, "cpu_baseline_threads": cpu} for n in names},
+               "latency_us": {n: {op: {"p10": 1.23, "p50": 4.56, "p90": 7.89} for op in ("fwd", "bwd")}
+                              for n in names}}
+    short = bench.short_tables(details)
+    assert len(json.dumps(short)) < 6500 < len(json.dumps(details))
+    t = short["shapes"][names[0]]
+    assert t["fwd"] == {"us": 333300000.0, "sustained_us": 333300000.0, "GB_s": 333300000.0, "frac": 0.3333,
+                        "rows_per_s": 333300000.0, "traffic": 333300000.0}
+    assert t["cpu_GB_s"] == [0.3333, 0.3333] and len(t["floor_us"]) == 2
+    assert short["latency_us"][names[0]] == {"fwd": 4.56, "bwd": 4.56}
+    assert bench.short_tables({}) == {}
