@@ -118,6 +118,17 @@ lib.dyt_layer_norm_backward_workspace_bytes.restype = _sz
 lib.dyt_layer_norm_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i32,
                                         _i32, _i32, _vp, _sz, _vp]
 lib.dyt_layer_norm_backward.restype = _i32
+lib.dyt_rms_norm_forward.argtypes = [_vp, _i64, _vp, _i64, _vp, _f32, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32,
+                                     _i32, _vp]
+lib.dyt_rms_norm_forward.restype = _i32
+lib.dyt_rms_norm_quantize.argtypes = [_vp, _i64, _vp, _i64, _vp, _f32, _i32, _vp, _i64, _vp, _vp, _i64, _i64, _i64,
+                                      _i32, _i32, _vp]
+lib.dyt_rms_norm_quantize.restype = _i32
+lib.dyt_rms_norm_backward_workspace_bytes.argtypes = [_i64, _i64, _i32]
+lib.dyt_rms_norm_backward_workspace_bytes.restype = _sz
+lib.dyt_rms_norm_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32,
+                                      _i32, _vp, _sz, _vp]
+lib.dyt_rms_norm_backward.restype = _i32
 lib.dyt_policy_loss_workspace_bytes.argtypes = [_i64, _i64, _i32]
 lib.dyt_policy_loss_workspace_bytes.restype = _sz
 lib.dyt_policy_loss_forward.argtypes = [_vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _f64, _f64, _f64, _f64, _vp, _vp,
@@ -240,6 +251,31 @@ def dyt_layer_norm_backward(x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, dgamm
     """Raw C-ABI call: pointers as ints (gamma, dgamma and dbeta may be None). Returns the status code."""
     return lib.dyt_layer_norm_backward(x, ldx, dy, lddy, gamma, mean, rstd, dx, lddx, dgamma, dbeta, M, N, x_dtype,
                                        gamma_dtype, beta_dtype, workspace, workspace_bytes, stream)
+
+
+def dyt_rms_norm_forward(x, ldx, residual, ldr, gamma, eps, y, ldy, h, ldh, rstd, M, N, x_dtype, gamma_dtype,
+                         stream) -> int:
+    """Raw C-ABI call: pointers as ints (residual with h, gamma and rstd may be None). Returns the status code."""
+    return lib.dyt_rms_norm_forward(x, ldx, residual, ldr, gamma, eps, y, ldy, h, ldh, rstd, M, N, x_dtype,
+                                    gamma_dtype, stream)
+
+
+def dyt_rms_norm_quantize(x, ldx, residual, ldr, gamma, eps, group, q, ldq, scale, h, ldh, M, N, x_dtype, gamma_dtype,
+                          stream) -> int:
+    """Raw C-ABI call: pointers as ints (residual with h, and gamma may be None). Returns the status code."""
+    return lib.dyt_rms_norm_quantize(x, ldx, residual, ldr, gamma, eps, group, q, ldq, scale, h, ldh, M, N, x_dtype,
+                                     gamma_dtype, stream)
+
+
+def dyt_rms_norm_backward_workspace_bytes(M, N, x_dtype) -> int:
+    return int(lib.dyt_rms_norm_backward_workspace_bytes(M, N, x_dtype))
+
+
+def dyt_rms_norm_backward(h, ldh, dy, lddy, rstd, gamma, dh, lddh, dx, lddx, dgamma, M, N, x_dtype, gamma_dtype,
+                          workspace, workspace_bytes, stream) -> int:
+    """Raw C-ABI call: pointers as ints (gamma, dh and dgamma may be None). Returns the status code."""
+    return lib.dyt_rms_norm_backward(h, ldh, dy, lddy, rstd, gamma, dh, lddh, dx, lddx, dgamma, M, N, x_dtype,
+                                     gamma_dtype, workspace, workspace_bytes, stream)
 
 
 def dyt_policy_loss_workspace_bytes(M, N, dtype) -> int:

@@ -30,7 +30,7 @@ struct Walk {
   int L;         // lanes of a row
   int rows;      // rows side by side in a CTA
   int step;      // grid x rows
-  int64_t inc[3];  // bytes from a row to the one a step later: the inputs, the output
+  int64_t inc[4];  // bytes from a row to the one a step later: the inputs, the output
   int64_t fast;  // ragged rows: [fast, M - fast) are copied in whole 16-byte chunks
   int plane;     // bytes of the slots that a warp has for one tensor's rows (read for ragged rows of part of a warp)
   float n, inv_n;
@@ -1001,7 +1001,8 @@ constexpr int kSumCols = 32, kSumLanes = 16, kSumBatch = 10;
 
 // The CTAs' column sums added in binary64 in a fixed order (lane l takes
 // partials l, l + 16, ..., ten loads under way at a time) and rounded once. The
-// sums go by halves: one binary64 addition after the other cost 1.4 us more. blockIdx.y: 0 = dgamma, 1 = dbeta.
+// sums go by halves: one binary64 addition after the other cost 1.4 us more. blockIdx.y < SETS: 0 = dgamma, 1 = dbeta.
+template <int SETS>
 __global__ void __launch_bounds__(kSumCols *kSumLanes)
     norm_finalize_kernel(const double *parts, int nparts, int64_t N, void *dgamma, int gamma_dt,
                          void *dbeta, int beta_dt) {
@@ -1019,7 +1020,7 @@ __global__ void __launch_bounds__(kSumCols *kSumLanes)
 #pragma unroll
       for (int b = 0; b < kSumBatch; ++b) {
         const int j = i + b * kSumLanes;
-        v[b] = j < nparts ? p[(int64_t)j * 2 * N] : 0.0;
+        v[b] = j < nparts ? p[(int64_t)j * SETS * N] : 0.0;
       }
 #pragma unroll
       for (int s = 1; s < kSumBatch; s <<= 1)  // by halves: few additions wait for one another

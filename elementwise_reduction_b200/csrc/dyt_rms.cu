@@ -1,0 +1,264 @@
+// Root-mean-square norm entry points (declared in include/dyt.h): argument
+// checks, launch plans and dispatch of the kernels in dyt_rms.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "dyt.h"
+#include "dyt_host.h"
+#include "dyt_rms_select.cuh"
+#include "dyt_rows.h"
+
+namespace {
+
+using namespace dyt::host;
+using namespace dyt::norm::host;
+using dyt::norm::RmsArgs;
+using dyt::norm::RmsGradArgs;
+
+constexpr int kOpRmsForward = 9, kOpRmsQuantize = 10, kOpRmsBackward = 11;  // dyt_launch_info::op
+constexpr int kColumnsBlock = 256;  // vector-columns of a CTA in the long rows' second pass
+
+// A plan for few rows spreads them over the SMs: no more rows side by side than every SM gets.
+RowPlan plan_rms(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
+  RowPlan p = plan_rows(M, N, vec, aligned, E, sms);
+  if (!p.group || p.rowlong) return p;
+  p.rows = (int)std::max<int64_t>(1, std::min<int64_t>(p.rows, ceil_div(M, sms)));
+  p.block = p.rows * p.L;
+  return p;
+}
+
+struct BwdPlan {
+  RowPlan r;
+  int64_t grid = 0;   // CTAs (the row pass's for long rows)
+  int64_t parts = 0;  // partial sets
+  int col_ctas = 0;   // long rows: CTAs across the columns
+  size_t off_c = 0, bytes = 0;
+};
+
+BwdPlan plan_bwd(int64_t M, int64_t N, int vec, bool aligned, int sms) {
+  BwdPlan b;
+  b.r = plan_rms(M, N, vec, aligned, dyt::norm::kBwdElems, sms);
+  if (b.r.rowlong) {
+    b.grid = std::min<int64_t>(M, (int64_t)sms * 2);
+    b.col_ctas = (int)ceil_div(b.r.NV, kColumnsBlock);
+    b.parts = std::max<int64_t>(1, std::min<int64_t>(M, (int64_t)sms * 4 / b.col_ctas));
+  } else {
+    b.grid = std::min<int64_t>(ceil_div(M, b.r.rows), (int64_t)sms);
+    b.parts = b.grid;
+  }
+  b.off_c = ((size_t)b.parts * (size_t)N * sizeof(double) + 15) & ~(size_t)15;
+  b.bytes = b.off_c + (b.r.rowlong ? (size_t)M * sizeof(float) : 0);
+  b.bytes = (b.bytes + 15) & ~(size_t)15;
+  return b;
+}
+
+void record(int op, const RowPlan *p, int64_t grid, int kernels, int64_t groups, size_t ws) {
+  dyt_launch_info i = {};
+  i.op = op;
+  i.kernels = kernels;
+  i.workspace_bytes = (int64_t)ws;
+  if (p) {
+    i.path = p->group || p->rowlong ? 2 : 1;
+    i.vec = p->V;
+    i.block = p->block;
+    i.grid = (int)grid;
+    i.row_lanes = p->rows;
+    i.rows_per_step = p->rows;
+    i.col_chunks = 1;
+    i.row_groups = (int)groups;
+    i.pack_rows = 1;
+    i.shifted = p->ragged && !p->rowlong;
+  }
+  record_info(i);
+}
+
+// Both forward calls. q8: y is e4m3 bytes with scales, one a row (group 0) or one for each kScaleCols columns.
+dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t ldr, const void *gamma, float eps,
+                   int group, void *y, int64_t ldy, float *scale, void *h, int64_t ldh, float *rstd, int64_t M,
+                   int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype, dyt_stream_t stream) {
+  dyt_status st = check_shape(M, N, x_dtype);
+  if (st != DYT_OK) return st;
+  if (!valid_dtype(gamma_dtype)) return DYT_ERR_UNSUPPORTED_DTYPE;
+  if (!(eps >= 0.0f) || std::isinf(eps) || (group != 0 && group != dyt::norm::kScaleCols)) return DYT_ERR_INVALID_VALUE;
+  if (check_pitch(M, N, ldx) != DYT_OK || check_pitch(M, N, ldy) != DYT_OK) return DYT_ERR_INVALID_VALUE;
+  if (res && (check_pitch(M, N, ldr) != DYT_OK || check_pitch(M, N, ldh) != DYT_OK)) return DYT_ERR_INVALID_VALUE;
+  if (M == 1) ldx = ldr = ldy = ldh = N;  // one row has no pitch
+  const int op = q8 ? kOpRmsQuantize : kOpRmsForward;
+  if (M == 0 || N == 0) {
+    record(op, nullptr, 0, 0, 0, 0);
+    return DYT_OK;
+  }
+  const size_t es = dsize(x_dtype);
+  if (!x || !y || (q8 && !scale) || (res && !h) || !elem_aligned(x, es) || !elem_aligned(res, es) ||
+      (!q8 && !elem_aligned(y, es)) || (res && !elem_aligned(h, es)) || !param_ok(gamma, gamma_dtype) ||
+      !param_ok(rstd, DYT_F32) || !param_ok(scale, DYT_F32))
+    return DYT_ERR_INVALID_VALUE;
+  int dev = 0, sms = 0;
+  st = current_sms(&dev, &sms);
+  if (st != DYT_OK) return st;
+  return with_type(x_dtype, [&](auto t) -> dyt_status {
+    using T = decltype(t);
+    constexpr int VE = vec_elems<T>();
+    // an 8-bit row is whole vectors of VE bytes
+    const bool out = q8 ? elem_aligned(y, VE) && (ldy & (VE - 1)) == 0 : aligned16(y) && vec_pitch(ldy, es);
+    const bool vec = N % VE == 0 && out && aligned16(x) && vec_pitch(ldx, es) &&
+                     (!res || (aligned16(res) && aligned16(h) && vec_pitch(ldr, es) && vec_pitch(ldh, es)));
+    const RowPlan p = plan_rms(M, N, VE, vec, dyt::norm::fwd_elems<T>(), sms);
+    const dyt::norm::RmsFwdKernel k = dyt::norm::rms_fwd_kernel_of<T>(p, res != nullptr, q8);
+    const size_t smem = p.rowlong ? 0 : dyt::norm::rms_fwd_smem<T>(p.block, p.L, p.ragged, res != nullptr);
+    const dyt_status s = prepare_smem(dev, (const void *)k, (int)smem);
+    if (s != DYT_OK) return s;
+    const int64_t grid = std::min<int64_t>(ceil_div(M, p.rows), (int64_t)sms);
+    const int64_t lds[3] = {ldx, res ? ldr : ldx, ldx};  // the inputs (walk_of takes the last for an output)
+    RmsArgs a = {};
+    a.x = x;
+    a.ldx = ldx;
+    a.res = res;
+    a.ldr = ldr;
+    a.gamma = gamma;
+    a.y = y;
+    a.ldy = ldy;
+    a.h = res ? h : nullptr;
+    a.ldh = ldh;
+    a.rstd = rstd;
+    a.scale = scale;
+    a.gamma_dt = (int)gamma_dtype;
+    a.eps = eps;
+    a.grouped = group != 0;
+    a.groups = group ? (int)ceil_div(N, group) : 1;
+    a.w = walk_of(p, M, N, grid, lds, 3, es, p.rowlong ? 0 : dyt::norm::fwd_plane<T>(32, p.L, p.ragged));
+    a.inc_y = (int64_t)a.w.step * ldy * (int64_t)(q8 ? 1 : es);
+    a.inc_h = res ? (int64_t)a.w.step * ldh * (int64_t)es : 0;
+    PdlConfig lc((unsigned)grid, p.block, smem, (cudaStream_t)stream);
+    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
+    if (e != cudaSuccess) return cuda_fail(e);
+    record(op, &p, grid, 1, 0, 0);
+    return DYT_OK;
+  });
+}
+
+}  // namespace
+
+extern "C" {
+
+dyt_status dyt_rms_norm_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *gamma,
+                                float eps, void *y, int64_t ldy, void *h, int64_t ldh, float *rstd, int64_t M,
+                                int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype, dyt_stream_t stream) try {
+  return forward(false, x, ldx, residual, ldr, gamma, eps, 0, y, ldy, nullptr, h, ldh, rstd, M, N, x_dtype,
+                 gamma_dtype, stream);
+} catch (...) {
+  return cuda_fail(cudaErrorMemoryAllocation);  // the host ran out of memory for the per-device facts
+}
+
+dyt_status dyt_rms_norm_quantize(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *gamma,
+                                 float eps, int group, void *q, int64_t ldq, float *scale, void *h, int64_t ldh,
+                                 int64_t M, int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype,
+                                 dyt_stream_t stream) try {
+  return forward(true, x, ldx, residual, ldr, gamma, eps, group, q, ldq, scale, h, ldh, nullptr, M, N, x_dtype,
+                 gamma_dtype, stream);
+} catch (...) {
+  return cuda_fail(cudaErrorMemoryAllocation);
+}
+
+size_t dyt_rms_norm_backward_workspace_bytes(int64_t M, int64_t N, dyt_dtype x_dtype) try {
+  if (check_shape(M, N, x_dtype) != DYT_OK || M == 0 || N == 0) return 0;
+  int dev = 0, sms = 0;
+  if (current_sms(&dev, &sms) != DYT_OK) return 0;
+  const int v = 16 / (int)dsize(x_dtype);
+  return std::max(plan_bwd(M, N, v, false, sms).bytes, plan_bwd(M, N, v, true, sms).bytes);
+} catch (...) {
+  return 0;
+}
+
+dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int64_t lddy, const float *rstd,
+                                 const void *gamma, const void *dh, int64_t lddh, void *dx, int64_t lddx,
+                                 void *dgamma, int64_t M, int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype,
+                                 void *workspace, size_t workspace_bytes, dyt_stream_t stream) try {
+  dyt_status st = check_shape(M, N, x_dtype);
+  if (st != DYT_OK) return st;
+  if (!valid_dtype(gamma_dtype)) return DYT_ERR_UNSUPPORTED_DTYPE;
+  if (check_pitch(M, N, ldh) != DYT_OK || check_pitch(M, N, lddy) != DYT_OK || check_pitch(M, N, lddx) != DYT_OK ||
+      (dh && check_pitch(M, N, lddh) != DYT_OK) || !param_ok(dgamma, gamma_dtype))
+    return DYT_ERR_INVALID_VALUE;
+  if (M == 1) ldh = lddy = lddh = lddx = N;  // one row has no pitch
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (M == 0 || N == 0) {
+    if (N > 0 && dgamma) {  // empty sums
+      const cudaError_t e = cudaMemsetAsync(dgamma, 0, (size_t)N * dsize(gamma_dtype), s);
+      if (e != cudaSuccess) return cuda_fail(e);
+    }
+    record(kOpRmsBackward, nullptr, 0, 0, 0, 0);
+    return DYT_OK;
+  }
+  const size_t es = dsize(x_dtype);
+  if (!h || !dy || !dx || !rstd || !workspace || !aligned16(workspace) || !elem_aligned(h, es) ||
+      !elem_aligned(dy, es) || !elem_aligned(dh, es) || !elem_aligned(dx, es) || !param_ok(gamma, gamma_dtype) ||
+      !param_ok(rstd, DYT_F32))
+    return DYT_ERR_INVALID_VALUE;
+  int dev = 0, sms = 0;
+  st = current_sms(&dev, &sms);
+  if (st != DYT_OK) return st;
+  return with_type(x_dtype, [&](auto t) -> dyt_status {
+    using T = decltype(t);
+    constexpr int VE = vec_elems<T>();
+    const bool res = dh != nullptr;
+    const bool vec = N % VE == 0 && aligned16(h) && aligned16(dy) && aligned16(dh) && aligned16(dx) &&
+                     vec_pitch(ldh, es) && vec_pitch(lddy, es) && vec_pitch(lddx, es) && (!res || vec_pitch(lddh, es));
+    const BwdPlan b = plan_bwd(M, N, VE, vec, sms);
+    if (workspace_bytes < b.bytes) return DYT_ERR_WORKSPACE_TOO_SMALL;
+    double *parts = (double *)workspace;
+    const int64_t lds[4] = {ldh, lddy, res ? lddh : lddy, lddx};
+    RmsGradArgs a = {};
+    a.h = h;
+    a.ldh = ldh;
+    a.dy = dy;
+    a.lddy = lddy;
+    a.dres = dh;
+    a.lddr = lddh;
+    a.gamma = gamma;
+    a.rstd = rstd;
+    a.dx = dx;
+    a.lddx = lddx;
+    a.parts = parts;
+    a.gamma_dt = (int)gamma_dtype;
+    a.w = walk_of(b.r, M, N, b.grid, lds, 4, es,
+                  b.r.rowlong ? 0 : dyt::norm::row_slots<T, dyt::norm::kBwdElems>(32, b.r.L, b.r.ragged));
+    a.inc_dx = a.w.inc[3];
+    int kernels = 1;
+    cudaError_t e;
+    if (b.r.rowlong) {
+      float *c = (float *)((char *)workspace + b.off_c);
+      PdlConfig lr((unsigned)b.grid, 1024, 0, s);
+      e = cudaLaunchKernelEx(&lr.cfg, dyt::norm::rms_bwd_rows_kernel_of<T>(b.r), a, c);
+      if (e != cudaSuccess) return cuda_fail(e);
+      PdlConfig lc((unsigned)b.col_ctas, kColumnsBlock, 0, s);
+      lc.cfg.gridDim.y = (unsigned)b.parts;
+      e = cudaLaunchKernelEx(&lc.cfg, dyt::norm::rms_bwd_columns_kernel_of<T>(b.r, res), a, (const float *)c);
+      kernels = 2;
+    } else {
+      const dyt::norm::RmsBwdKernel k = dyt::norm::rms_bwd_kernel_of<T>(b.r, res);
+      const size_t smem = dyt::norm::rms_bwd_smem<T>(b.r.block, b.r.L, b.r.ragged, res);
+      const dyt_status ready = prepare_smem(dev, (const void *)k, (int)smem);
+      if (ready != DYT_OK) return ready;
+      PdlConfig lc((unsigned)b.grid, b.r.block, smem, s);
+      e = cudaLaunchKernelEx(&lc.cfg, k, a);
+    }
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dgamma) {
+      PdlConfig lf((unsigned)ceil_div(N, dyt::norm::kSumCols), dyt::norm::kSumCols * dyt::norm::kSumLanes, 0, s);
+      e = cudaLaunchKernelEx(&lf.cfg, dyt::norm::norm_finalize_kernel<1>, (const double *)parts, (int)b.parts, N,
+                             dgamma, (int)gamma_dtype, (void *)nullptr, (int)gamma_dtype);
+      if (e != cudaSuccess) return cuda_fail(e);
+      ++kernels;
+    }
+    record(kOpRmsBackward, &b.r, b.grid, kernels, b.parts, b.bytes);
+    return DYT_OK;
+  });
+} catch (...) {
+  return cuda_fail(cudaErrorMemoryAllocation);
+}
+
+}  // extern "C"

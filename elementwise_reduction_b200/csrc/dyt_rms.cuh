@@ -1,0 +1,655 @@
+// Root-mean-square norm with the residual's addition, forward (also with an 8-bit
+// output and its scales) and backward, for sm_100a over the rows of an M x N matrix.
+//
+//   h_j  = x_j + residual_j   (binary32; stored rounded; x_j without a residual)
+//   rstd = (sum_j h_j^2 / N + eps)^-1/2,   y_j = gamma_j h_j rstd
+//   scale = max(max_j |y_j|, 2^-100) / 448 over the row, or over 128 columns;  q_j = e4m3(y_j / scale)
+//   n_j  = h_j rstd,  g_j = gamma_j dy_j,  c = sum_j g_j n_j / N
+//   dx_j = rstd (g_j - n_j c) + dh_j,   dgamma_j = sum_i dy_ij n_ij
+//
+// Bound by memory, as layer norm is, and laid out as it: a row is read once into
+// the ring of RowFeed and kept in registers between its sum and its outputs, the
+// same columns of every row in the same lane. The norm is of the sum before it is
+// rounded to the stored residual stream, so y has one rounding. The largest |y|
+// of a row is rstd times the largest |gamma h|, which meets the sum of squares in
+// the one exchange a row takes.
+#pragma once
+
+#include "dyt_norm.cuh"
+
+namespace dyt {
+namespace norm {
+
+struct RmsArgs {
+  const void *x;
+  int64_t ldx;
+  const void *res;    // with a residual
+  int64_t ldr;
+  const void *gamma;  // NULL: 1
+  void *y;            // T, or e4m3
+  int64_t ldy;
+  void *h;            // with a residual
+  int64_t ldh;
+  float *rstd;        // NULL: not written
+  float *scale;       // [M] or [M][groups]
+  int gamma_dt;
+  float eps;
+  int groups;         // scales a row: 1, or one for each kScaleCols columns (grouped)
+  int grouped;
+  int64_t inc_y, inc_h;  // bytes from a row to the one a step later
+  Walk w;                // inc[0], inc[1]: of x and the residual
+};
+
+struct RmsGradArgs {
+  const void *h;
+  int64_t ldh;
+  const void *dy;
+  int64_t lddy;
+  const void *dres;   // the gradient of the stored sum (with one)
+  int64_t lddr;
+  const void *gamma;  // NULL: 1
+  const float *rstd;
+  void *dx;
+  int64_t lddx;
+  double *parts;      // [CTA][N] column sums
+  int gamma_dt;
+  int64_t inc_dx;
+  Walk w;             // inc[0 .. 2]: of h, dy and dres
+};
+
+constexpr int kScaleCols = 128;
+constexpr float kQMax = 448.0f;      // the largest e4m3 value
+constexpr float kLeastTop = 0x1p-100f;  // a row of zeros has a scale all the same: nothing is divided by 0
+
+// The larger value; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float lanes_max(float v, int width) {
+  for (int o = width >> 1; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+// Two values rounded to e4m3 (nearest even, at most 448; NaN stays): a in the low byte.
+__device__ __forceinline__ uint32_t e4m3_pair(float2 v) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+
+// A predicated store of a lane's V bytes (8, or 4 of binary32 rows).
+template <int V>
+__device__ __forceinline__ void st_bytes_if(bool p, void *dst, const float2 (&f)[V / 2]) {
+  const uint32_t lo = e4m3_pair(f[0]) | e4m3_pair(f[1]) << 16;
+  if constexpr (V == 8) {
+    const uint32_t hi = e4m3_pair(f[2]) | e4m3_pair(f[3]) << 16;
+    asm volatile("{.reg .pred p; setp.ne.b32 p, %3, 0; @p st.global.v2.u32 [%0], {%1,%2};}" ::"l"(dst), "r"(lo),
+                 "r"(hi), "r"((int)p)
+                 : "memory");
+  } else {
+    asm volatile("{.reg .pred p; setp.ne.b32 p, %2, 0; @p st.global.u32 [%0], %1;}" ::"l"(dst), "r"(lo), "r"((int)p)
+                 : "memory");
+  }
+}
+
+// A lane's outputs as e4m3 bytes.
+template <typename T, int E, bool RAGGED, int MODE, typename Feed>
+__device__ __forceinline__ void store_bytes(unsigned char *out, const float2 (&f)[E / 2], const Place<MODE> &p,
+                                            const Feed &feed, int NV, int N) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if constexpr (!RAGGED) {
+#pragma unroll
+    for (int k = 0; k < E / V; ++k)
+      st_bytes_if<V>(p.lane + k * p.L < NV, out + (p.lane + k * p.L) * V,
+                     *reinterpret_cast<const float2(*)[V / 2]>(f + k * (V / 2)));
+  } else {
+    const int c0 = column<V, E, true, MODE>(p.L, p.lane, 0), left = N - c0;
+    unsigned char *o = out + c0;
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const uint32_t b = e4m3_pair(f[i / 2]);
+      if (feed.whole(p, i & ~7) || i * p.seg() < left) o[i * p.seg()] = (unsigned char)b;
+      if (feed.whole(p, i & ~7) || (i + 1) * p.seg() < left) o[(i + 1) * p.seg()] = (unsigned char)(b >> 8);
+    }
+  }
+}
+
+// Scales of kScaleCols columns each. A lane's elements fall into slabs that lie in one group: its
+// vectors (aligned rows), or four elements (ragged ones, seg <= 32 apart). The slab's lanes are
+// reduced by a butterfly; rows in less than a warp may have several slabs of one group.
+template <typename T, int E, bool RAGGED, int MODE>
+struct Slabs {
+  static constexpr int V = 16 / (int)sizeof(T);
+  static constexpr int W = RAGGED ? 4 : V;  // elements of a slab
+  static constexpr int n = E / W;
+  static __device__ __forceinline__ int lanes(const Place<MODE> &p) {
+    return RAGGED || p.seg() < kScaleCols / V ? p.seg() : kScaleCols / V;
+  }
+  // The group of slab s.
+  static __device__ __forceinline__ int group(const Place<MODE> &p, int s) {
+    return column<V, E, RAGGED, MODE>(p.L, p.lane, s * W) / kScaleCols;
+  }
+  // top[s]: the largest of the lane's slab s; becomes that of the slab's group.
+  static __device__ __forceinline__ void join(float (&top)[n], const Place<MODE> &p) {
+    const int width = lanes(p);
+#pragma unroll
+    for (int s = 0; s < n; ++s) top[s] = lanes_max(top[s], width);
+    if constexpr (MODE == kPart) {  // (columns of the row's first lane: a slab's group is the same for all its lanes)
+      float all[n];
+#pragma unroll
+      for (int s = 0; s < n; ++s) {
+        all[s] = top[s];
+#pragma unroll
+        for (int o = 0; o < n; ++o)
+          if (o != s && group(p, o) == group(p, s)) all[s] = max_nan(all[s], top[o]);
+      }
+#pragma unroll
+      for (int s = 0; s < n; ++s) top[s] = all[s];
+    }
+  }
+};
+
+// ---- forward: a row in registers -------------------------------------------------
+
+constexpr int kRmsFwdStages = 3;
+template <typename T>
+__host__ __device__ constexpr size_t rms_fwd_smem(int block, int L, bool ragged, bool res) {
+  return (size_t)kRmsFwdStages * (res ? 2 : 1) * row_slots<T, fwd_elems<T>()>(block, L, ragged) * 16;
+}
+
+// RES: with a residual. Q: 8-bit output with scales.
+template <typename T, int MODE, bool RAGGED, bool RES, bool Q>
+__global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(RmsArgs a) {
+  constexpr bool GROUP = MODE == kGroup;
+  constexpr int V = 16 / (int)sizeof(T);
+  constexpr int E = fwd_elems<T>(), P = E / 2;
+  constexpr int S = kRmsFwdStages, TN = RES ? 2 : 1;
+  using Slab = Slabs<T, E, RAGGED, MODE>;
+  __shared__ float2 red[2][kBlock / 32];
+  extern __shared__ __align__(16) unsigned char dyn[];
+  pdl_prologue();
+  const Place<MODE> p(a.w.L);
+  if (dynamic_smem_bytes() < rms_fwd_smem<T>((int)blockDim.x, p.L, RAGGED, RES)) return;
+  const int N = (int)a.w.N;
+  const T *src[TN];
+  int64_t ld[TN];
+  src[0] = static_cast<const T *>(a.x);
+  ld[0] = a.ldx;
+  if constexpr (RES) {
+    src[1] = static_cast<const T *>(a.res);
+    ld[1] = a.ldr;
+  }
+  const int64_t r0 = (int64_t)blockIdx.x * a.w.rows;
+  int64_t row = r0 + p.mine;
+  const int steps = row_count(a.w.M, r0, a.w.step), left = row_count(a.w.M, row, a.w.step);  // the CTA's, this row's
+  RowFeed<T, E, TN, S, RAGGED, MODE> feed(dyn, src, ld, p, a.w, row);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.w, i < left, row + (int64_t)i * a.w.step);
+  float2 gam[P];
+  load_pairs<V, E, RAGGED, MODE>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
+  const float inv_n = a.w.inv_n;
+  const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31, w0 = GROUP ? p.mine * warps : 0;
+  char *y = static_cast<char *>(a.y) + row * a.ldy * (int64_t)(Q ? 1 : sizeof(T));
+  char *h = nullptr;
+  if constexpr (RES) h = static_cast<char *>(a.h) + row * a.ldh * (int64_t)sizeof(T);
+#pragma unroll 1
+  for (int it = 0; it < steps; ++it) {
+    if (MODE != kPart && it >= left) break;  // whole warps without a row: only at the CTA's last step
+    feed.wait();
+    float2 v[P];
+    feed.read(0, src[0], ld[0], row, p, a.w, v);
+    if constexpr (RES) {
+      float2 r[P];
+      feed.read(1, src[1], ld[1], row, p, a.w, r);
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = add2(v[i], r[i]);
+    }
+    feed.advance(a.w);
+    feed.issue(p, a.w, it + S - 1 < left, row + (int64_t)(S - 1) * a.w.step);
+    float2 t[2] = {f2(0.0f), f2(0.0f)};  // what lies past the row's end is zero
+#pragma unroll
+    for (int i = 0; i < P; ++i) t[i & 1] = fma2(v[i], v[i], t[i & 1]);
+    t[0] = add2(t[0], t[1]);
+    float q = t[0].x + t[0].y, top = 0.0f;
+    if (RES && it < left) store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(h), v, p, feed, a.w.NV, N);
+    if constexpr (Q) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = mul2(v[i], gam[i]);
+      if (!a.grouped) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) top = max_nan(top, max_nan(fabsf(v[i].x), fabsf(v[i].y)));
+      }
+    }
+    q = GROUP ? warp_sum(q) : lanes_sum(q, p.L);
+    if (Q && !a.grouped) top = lanes_max(top, p.seg());
+    if constexpr (GROUP) {
+      const int par = it & 1;
+      if (wl == 0) red[par][w0 + p.lane / 32] = make_float2(q, top);
+      group_barrier(p.mine, p.L);
+      // up to 16 warps, one a lane of each half
+      const float2 o = (wl & 15) < warps ? red[par][w0 + (wl & 15)] : make_float2(0.0f, 0.0f);
+      q = lanes_sum(o.x, 16);
+      if (Q && !a.grouped) top = lanes_max(o.y, 16);
+    }
+    const float rstd = rsqrtf(fmaf(q, inv_n, a.eps));
+    if (a.rstd && p.lane == 0 && it < left) a.rstd[row] = rstd;
+    if constexpr (Q) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = mul2(v[i], f2(rstd));
+      if (a.grouped) {
+        float tops[Slab::n];
+#pragma unroll
+        for (int s = 0; s < Slab::n; ++s) {
+          tops[s] = 0.0f;
+#pragma unroll
+          for (int i = s * Slab::W / 2; i < (s + 1) * Slab::W / 2; ++i)
+            tops[s] = max_nan(tops[s], max_nan(fabsf(v[i].x), fabsf(v[i].y)));
+        }
+        Slab::join(tops, p);
+#pragma unroll
+        for (int s = 0; s < Slab::n; ++s) {
+          tops[s] = max_nan(tops[s], kLeastTop);
+          const int g = Slab::group(p, s);
+          // (rows in less than a warp: several slabs may write the same value)
+          if (it < left && g < a.groups && (p.lane & (Slab::lanes(p) - 1)) == 0)
+            a.scale[row * a.groups + g] = tops[s] * (1.0f / kQMax);
+          const float inv = kQMax / tops[s];
+#pragma unroll
+          for (int i = s * Slab::W / 2; i < (s + 1) * Slab::W / 2; ++i) v[i] = mul2(v[i], f2(inv));
+        }
+      } else {
+        top = max_nan(top * rstd, kLeastTop);  // the largest |v|: rounding keeps the order
+        if (p.lane == 0 && it < left) a.scale[row] = top * (1.0f / kQMax);
+        const float inv = kQMax / top;
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = mul2(v[i], f2(inv));
+      }
+      if (it < left)
+        store_bytes<T, E, RAGGED>(reinterpret_cast<unsigned char *>(y), v, p, feed, a.w.NV, N);
+    } else if (it < left) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) v[i] = mul2(mul2(v[i], f2(rstd)), gam[i]);
+      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(y), v, p, feed, a.w.NV, N);
+    }
+    row += a.w.step;
+    y += a.inc_y;
+    if constexpr (RES) h += a.inc_h;
+  }
+  cp_async_wait<0>();
+}
+
+// ---- forward: rows too long for registers ----------------------------------------
+
+// The largest over a CTA (see cta_sum).
+__device__ __forceinline__ float cta_max(float v, float *red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  v = lanes_max(v, 32);
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  return lanes_max(lane < warps ? red[lane] : 0.0f, 32);
+}
+
+// One CTA reads each row twice (the second time mostly from L2): its sum of
+// squares, its outputs. A warp takes 32 x C consecutive columns at a time, C = 4
+// single elements or a vector a lane, which are whole groups of kScaleCols.
+template <typename T, int V, bool RES, bool Q>
+__global__ void __launch_bounds__(1024) rms_fwd_long_kernel(RmsArgs a) {
+  constexpr int C = V == 1 ? 4 : V;       // a lane's columns of a step
+  constexpr int B = V == 1 ? 4 : 1;       // loads for them
+  constexpr int GL = kScaleCols / C;      // lanes of a scale's columns
+  using IO = VecIO<T, V>;
+  __shared__ float red[2][kMaxWarps];
+  pdl_prologue();
+  const int64_t N = a.w.N;
+  const int lane = threadIdx.x & 31;
+  const int64_t c0 = (int64_t)(threadIdx.x >> 5) * (32 * C) + lane * V, step = (int64_t)blockDim.x * C;
+  for (int64_t row = blockIdx.x; row < a.w.M; row += gridDim.x) {
+    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+    const T *r = static_cast<const T *>(a.res) + (RES ? row * a.ldr : 0);
+    // the sum at columns c + b 32 V + e, 0 past the end
+    auto sum_at = [&](int64_t c, float (&v)[C]) {
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        float f[V], g[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = 0.0f;
+        if (c + b * 32 < N) {
+          IO::unpack(load_row<T, V>(x + c + b * 32), f);
+          if constexpr (RES) {
+            IO::unpack(load_row<T, V>(r + c + b * 32), g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[e] += g[e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[b * V + e] = f[e];
+      }
+    };
+    auto gamma_at = [&](int64_t c, float (&g)[C]) {
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        float f[V];
+        load_columns<V>(a.gamma, a.gamma_dt, c + b * 32 < N ? c + b * 32 : 0, 1.0f, f);
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[b * V + e] = f[e];
+      }
+    };
+    float s[1] = {0.0f}, top = 0.0f;
+#pragma unroll 2
+    for (int64_t c = c0; c < N; c += step) {
+      float v[C];
+      sum_at(c, v);
+#pragma unroll
+      for (int e = 0; e < C; ++e) s[0] = fmaf(v[e], v[e], s[0]);
+      if (Q && !a.grouped) {
+        float g[C];
+        gamma_at(c, g);
+#pragma unroll
+        for (int e = 0; e < C; ++e) top = max_nan(top, fabsf(v[e] * g[e]));
+      }
+    }
+    cta_sum(s, red[0]);
+    const float rstd = rsqrtf(fmaf(s[0], a.w.inv_n, a.eps));
+    if (Q && !a.grouped) top = max_nan(cta_max(top, red[1]) * rstd, kLeastTop);
+    if (threadIdx.x == 0) {
+      if (a.rstd) a.rstd[row] = rstd;
+      if (Q && !a.grouped) a.scale[row] = top * (1.0f / kQMax);
+    }
+    // whole warps stay together: a warp's first column decides
+    for (int64_t c = c0; c - lane * V < N; c += step) {
+      float v[C], g[C];
+      sum_at(c, v);
+      gamma_at(c, g);
+      if constexpr (RES) {
+        T *h = static_cast<T *>(a.h) + row * a.ldh + c;
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+          if (c + b * 32 < N) store_row<T, V>(h + b * 32, *reinterpret_cast<const float(*)[V]>(v + b * V));
+      }
+      if constexpr (!Q) {
+        T *y = static_cast<T *>(a.y) + row * a.ldy + c;
+#pragma unroll
+        for (int e = 0; e < C; ++e) v[e] = v[e] * rstd * g[e];
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+          if (c + b * 32 < N) store_row<T, V>(y + b * 32, *reinterpret_cast<const float(*)[V]>(v + b * V));
+      } else {
+        unsigned char *y = static_cast<unsigned char *>(a.y) + row * a.ldy + c;
+#pragma unroll
+        for (int e = 0; e < C; ++e) v[e] = v[e] * g[e] * rstd;
+        float t = top;
+        if (a.grouped) {
+          t = 0.0f;
+#pragma unroll
+          for (int e = 0; e < C; ++e) t = max_nan(t, fabsf(v[e]));
+          t = max_nan(lanes_max(t, GL), kLeastTop);
+          const int64_t grp = c / kScaleCols;
+          if ((lane & (GL - 1)) == 0 && grp < a.groups) a.scale[row * a.groups + grp] = t * (1.0f / kQMax);
+        }
+        const float inv = kQMax / t;
+        if constexpr (V == 1) {
+#pragma unroll
+          for (int b = 0; b < B; ++b)
+            if (c + b * 32 < N) y[b * 32] = (unsigned char)e4m3_pair(make_float2(v[b] * inv, 0.0f));
+        } else {
+          float2 f[V / 2];
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) f[e] = make_float2(v[2 * e] * inv, v[2 * e + 1] * inv);
+          st_bytes_if<V>(c < N, y, f);
+        }
+      }
+    }
+    __syncthreads();  // (the second exchange of this row is read before the first of the next is written)
+  }
+}
+
+// ---- backward: a row in registers ------------------------------------------------
+
+template <typename T>
+__host__ __device__ constexpr int rms_bwd_stages() {
+  return sizeof(T) == 4 ? 2 : 3;
+}
+template <typename T>
+__host__ __device__ constexpr size_t rms_bwd_ring(int block, int L, bool ragged, bool res) {
+  return (size_t)rms_bwd_stages<T>() * (res ? 3 : 2) * row_slots<T, kBwdElems>(block, L, ragged) * 16;
+}
+// Room for `per` elements' column sums of every lane: a copy per group, or per warp of smaller rows.
+__host__ __device__ constexpr size_t rms_sums_smem(int block, int L, int per) {
+  return (size_t)(block / (L < 32 ? 32 : L)) * per * (L + kSumPad) * sizeof(float);
+}
+template <typename T>
+__host__ __device__ constexpr size_t rms_bwd_smem(int block, int L, bool ragged, bool res) {
+  return rms_bwd_ring<T>(block, L, ragged, res) + rms_sums_smem(block, L, 16 / (int)sizeof(T));
+}
+static_assert(rms_bwd_ring<__half>(32, 32, false, false) >= rms_sums_smem(32, 32, kBwdElems) &&
+                  rms_bwd_ring<float>(32, 32, false, false) >= rms_sums_smem(32, 32, kBwdElems),
+              "the last column sums take the ring's place");
+
+// flush_columns for one sum a column: a run's sums of the CTA's rows, added in a fixed order and moved to
+// its partial sums in binary64.
+template <int V, int E, int PER, bool RAGGED, int MODE>
+__device__ __forceinline__ void rms_flush(const RmsGradArgs &a, float2 (&dg)[E / 2], const Place<MODE> &p, bool first,
+                                          float *sh) {
+  double *pg = a.parts + (int64_t)blockIdx.x * a.w.N;
+  const int N = (int)a.w.N;
+  const int copies = MODE != kGroup ? (int)blockDim.x / 32 : a.w.rows;
+  const int copy = MODE != kGroup ? (int)threadIdx.x >> 5 : p.mine;
+  const int stride = p.L + kSumPad, plane = PER * stride;
+  auto add = [&](int e, int lane, int c) {
+    if (c >= N) return;
+    const float *q = sh + e * stride + lane;
+    double t[2] = {0.0, 0.0};
+    for (int w = 0; w + 1 < copies; w += 2) {
+      t[0] += (double)q[w * plane];
+      t[1] += (double)q[(w + 1) * plane];
+    }
+    if (copies & 1) t[0] += (double)q[(copies - 1) * plane];
+    pg[c] = first ? t[0] + t[1] : pg[c] + (t[0] + t[1]);
+  };
+#pragma unroll
+  for (int k = 0; k < E; k += PER) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      float u = e & 1 ? dg[(k + e) / 2].y : dg[(k + e) / 2].x;
+      for (int o = p.seg(); o < 32; o <<= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+      if (MODE != kPart || ((int)threadIdx.x & 31) < p.L) sh[copy * plane + e * stride + p.lane] = u;
+    }
+    __syncthreads();
+    // neighbouring threads take neighbouring columns
+    if constexpr (RAGGED) {
+      for (int e = p.mine; e < PER; e += a.w.rows) add(e, p.lane, column<V, E, true, MODE>(p.L, p.lane, k + e));
+    } else {
+#pragma unroll
+      for (int v = 0; v < PER; v += V)
+        for (int j = threadIdx.x; j < V * p.L; j += blockDim.x) add(v + j % V, j / V, (k + v) * p.L + j);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) dg[i] = f2(0.0f);
+}
+
+// RES: the stored sum has a gradient of its own, read after the row's sum.
+template <typename T, int MODE, bool RAGGED, bool RES>
+__global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
+  constexpr bool GROUP = MODE == kGroup;
+  constexpr int V = 16 / (int)sizeof(T);
+  constexpr int E = kBwdElems, P = E / 2;
+  constexpr int S = rms_bwd_stages<T>(), TN = RES ? 3 : 2;
+  __shared__ float red[2][kBlock / 32];
+  extern __shared__ __align__(16) unsigned char dyn[];
+  pdl_prologue();
+  const Place<MODE> p(a.w.L);
+  if (dynamic_smem_bytes() < rms_bwd_smem<T>((int)blockDim.x, p.L, RAGGED, RES)) return;
+  float *sh = reinterpret_cast<float *>(dyn + rms_bwd_ring<T>((int)blockDim.x, p.L, RAGGED, RES));
+  const int N = (int)a.w.N;
+  const T *src[TN];
+  int64_t ld[TN];
+  src[0] = static_cast<const T *>(a.h);
+  ld[0] = a.ldh;
+  src[1] = static_cast<const T *>(a.dy);
+  ld[1] = a.lddy;
+  if constexpr (RES) {
+    src[2] = static_cast<const T *>(a.dres);
+    ld[2] = a.lddr;
+  }
+  const int64_t r0 = (int64_t)blockIdx.x * a.w.rows;
+  int64_t row = r0 + p.mine;
+  const int steps = row_count(a.w.M, r0, a.w.step), left = row_count(a.w.M, row, a.w.step);  // the CTA's, this row's
+  RowFeed<T, E, TN, S, RAGGED, MODE> feed(dyn, src, ld, p, a.w, row);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.w, i < left, row + (int64_t)i * a.w.step);
+  // The next row's factor, loaded one row ahead; past its last row a lane stays at that row (at M - 1 if it has none).
+  int64_t stat = left > 0 ? row : a.w.M - 1;
+  float next = a.rstd[stat];
+  float2 gam[P], dg[P];
+  load_pairs<V, E, RAGGED, MODE>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
+#pragma unroll
+  for (int i = 0; i < P; ++i) dg[i] = f2(0.0f);
+  const float inv_n = a.w.inv_n;
+  const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31, w0 = GROUP ? p.mine * warps : 0;
+  char *out = reinterpret_cast<char *>(static_cast<T *>(a.dx) + row * a.lddx);
+  bool first = true;
+  int run = 0;
+#pragma unroll 1
+  for (int it = 0; it < steps; ++it) {
+    const bool in = it < left;
+    const float rstd = in ? next : 0.0f;
+    if (MODE != kPart && !in) break;  // whole warps without a row: only at the CTA's last step
+    feed.wait();
+    float2 n[P], d[P];
+    feed.read(0, src[0], ld[0], row, p, a.w, n);
+    feed.read(1, src[1], ld[1], row, p, a.w, d);
+    feed.issue(p, a.w, it + S - 1 < left, row + (int64_t)(S - 1) * a.w.step);
+    if (it + 1 < left) stat += a.w.step;
+    next = a.rstd[stat];
+    // Past the row's end n, d and gamma are 0: nothing there enters a sum that is used.
+    float2 s[2] = {f2(0.0f), f2(0.0f)};
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      n[i] = mul2(n[i], f2(rstd));
+      dg[i] = fma2(d[i], n[i], dg[i]);
+      d[i] = mul2(gam[i], d[i]);
+      s[i & 1] = fma2(d[i], n[i], s[i & 1]);
+    }
+    s[0] = add2(s[0], s[1]);
+    float c = s[0].x + s[0].y;
+    c = GROUP ? warp_sum(c) : lanes_sum(c, p.L);
+    if constexpr (GROUP) {
+      const int par = it & 1;
+      if (wl == 0) red[par][w0 + p.lane / 32] = c;
+      group_barrier(p.mine, p.L);
+      c = lanes_sum((wl & 15) < warps ? red[par][w0 + (wl & 15)] : 0.0f, 16);
+    }
+    if (MODE != kPart || in) {
+      c *= inv_n;
+      if constexpr (RES) {
+        float2 r[P];
+        feed.read(2, src[2], ld[2], row, p, a.w, r);
+#pragma unroll
+        for (int i = 0; i < P; ++i) d[i] = fma2(f2(rstd), fma2(n[i], f2(-c), d[i]), r[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) d[i] = mul2(f2(rstd), fma2(n[i], f2(-c), d[i]));
+      }
+      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), d, p, feed, a.w.NV, N);
+    }
+    feed.advance(a.w);
+    row += a.w.step;
+    out += a.inc_dx;
+    if (++run == kRunRows && it + 1 < steps) {
+      rms_flush<V, E, V, RAGGED>(a, dg, p, first, sh);
+      first = false;
+      run = 0;
+    }
+  }
+  // The last run, all elements at once where the ring was: every warp of the
+  // CTA is here, also one that left at the last step.
+  cp_async_wait<0>();
+  __syncthreads();
+  rms_flush<V, E, E, RAGGED>(a, dg, p, first, reinterpret_cast<float *>(dyn));
+}
+
+// ---- backward: rows too long for registers ---------------------------------------
+
+// c of each row, one CTA per row. (The rows are then read once more.)
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) rms_bwd_rows_kernel(RmsGradArgs a, float *cs) {
+  using IO = VecIO<T, V>;
+  __shared__ float red[2][kMaxWarps];
+  pdl_prologue();
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < a.w.M; row += gridDim.x, par ^= 1) {
+    const T *h = static_cast<const T *>(a.h) + row * a.ldh;
+    const T *dy = static_cast<const T *>(a.dy) + row * a.lddy;
+    const float rstd = a.rstd[row];
+    float c[1] = {0.0f};
+#pragma unroll 2
+    for (int64_t cv = threadIdx.x; cv < a.w.NV; cv += blockDim.x) {
+      float v[V], d[V], g[V];
+      IO::unpack(load_row<T, V>(h + cv * V), v);
+      IO::unpack(load_row<T, V>(dy + cv * V), d);
+      load_columns<V>(a.gamma, a.gamma_dt, cv * V, 1.0f, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) c[0] = fmaf(g[e] * d[e], v[e] * rstd, c[0]);
+    }
+    cta_sum(c, red[par]);
+    if (threadIdx.x == 0) cs[row] = c[0] * a.w.inv_n;
+  }
+}
+
+// dx and the column sums: a CTA takes blockDim.x vector-columns (blockIdx.x)
+// of every gridDim.y-th row.
+template <typename T, int V, bool RES>
+__global__ void __launch_bounds__(256) rms_bwd_columns_kernel(RmsGradArgs a, const float *cs) {
+  using IO = VecIO<T, V>;
+  pdl_prologue();
+  const int64_t cv = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (cv >= a.w.NV) return;
+  const T *h = static_cast<const T *>(a.h) + cv * V;
+  const T *dy = static_cast<const T *>(a.dy) + cv * V;
+  const T *dr = static_cast<const T *>(a.dres) + (RES ? cv * V : 0);
+  T *dx = static_cast<T *>(a.dx) + cv * V;
+  float g[V], dg[V];
+  load_columns<V>(a.gamma, a.gamma_dt, cv * V, 1.0f, g);
+  double sg[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    sg[e] = 0.0;
+    dg[e] = 0.0f;
+  }
+  int run = 0;
+#pragma unroll 2
+  for (int64_t row = blockIdx.y; row < a.w.M; row += gridDim.y) {
+    float v[V], d[V], r[V], o[V];
+    IO::unpack(load_row<T, V>(h + row * a.ldh), v);
+    IO::unpack(load_row<T, V>(dy + row * a.lddy), d);
+    if constexpr (RES) IO::unpack(load_row<T, V>(dr + row * a.lddr), r);
+    const float rstd = a.rstd[row], c = cs[row];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float n = v[e] * rstd;
+      dg[e] = fmaf(d[e], n, dg[e]);
+      const float t = fmaf(n, -c, g[e] * d[e]);
+      o[e] = RES ? fmaf(rstd, t, r[e]) : rstd * t;
+    }
+    store_row<T, V>(dx + row * a.lddx, o);
+    if (++run == kRunRows) {
+      run = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        sg[e] += (double)dg[e];
+        dg[e] = 0.0f;
+      }
+    }
+  }
+  double *pg = a.parts + (int64_t)blockIdx.y * a.w.N + cv * V;
+#pragma unroll
+  for (int e = 0; e < V; ++e) pg[e] = sg[e] + (double)dg[e];
+}
+
+}  // namespace norm
+}  // namespace dyt

@@ -1,0 +1,50 @@
+// Definitions of the selectors in dyt_rms_select.cuh.
+#pragma once
+
+#include "dyt_rms_select.cuh"
+
+namespace dyt {
+namespace norm {
+
+template <typename T, bool RES, bool Q>
+RmsFwdKernel rms_fwd_of(const host::RowPlan &p) {
+  if (p.rowlong) return p.V == 1 ? rms_fwd_long_kernel<T, 1, RES, Q> : rms_fwd_long_kernel<T, 16 / (int)sizeof(T), RES, Q>;
+  if (p.group) return p.ragged ? rms_fwd_kernel<T, kGroup, true, RES, Q> : rms_fwd_kernel<T, kGroup, false, RES, Q>;
+  if (p.L == 32) return p.ragged ? rms_fwd_kernel<T, kWarp, true, RES, Q> : rms_fwd_kernel<T, kWarp, false, RES, Q>;
+  return p.ragged ? rms_fwd_kernel<T, kPart, true, RES, Q> : rms_fwd_kernel<T, kPart, false, RES, Q>;
+}
+template <typename T>
+RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool res, bool q8) {
+  if (q8) return res ? rms_fwd_of<T, true, true>(p) : rms_fwd_of<T, false, true>(p);
+  return res ? rms_fwd_of<T, true, false>(p) : rms_fwd_of<T, false, false>(p);
+}
+
+template <typename T, bool RES>
+RmsBwdKernel rms_bwd_of(const host::RowPlan &p) {
+  if (p.group) return p.ragged ? rms_bwd_kernel<T, kGroup, true, RES> : rms_bwd_kernel<T, kGroup, false, RES>;
+  if (p.L == 32) return p.ragged ? rms_bwd_kernel<T, kWarp, true, RES> : rms_bwd_kernel<T, kWarp, false, RES>;
+  return p.ragged ? rms_bwd_kernel<T, kPart, true, RES> : rms_bwd_kernel<T, kPart, false, RES>;
+}
+template <typename T>
+RmsBwdKernel rms_bwd_kernel_of(const host::RowPlan &p, bool res) {
+  return res ? rms_bwd_of<T, true>(p) : rms_bwd_of<T, false>(p);
+}
+template <typename T>
+RmsBwdLongKernel rms_bwd_rows_kernel_of(const host::RowPlan &p) {
+  return p.V == 1 ? rms_bwd_rows_kernel<T, 1> : rms_bwd_rows_kernel<T, 16 / (int)sizeof(T)>;
+}
+template <typename T>
+RmsBwdColumnsKernel rms_bwd_columns_kernel_of(const host::RowPlan &p, bool res) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (p.V == 1) return res ? rms_bwd_columns_kernel<T, 1, true> : rms_bwd_columns_kernel<T, 1, false>;
+  return res ? rms_bwd_columns_kernel<T, V, true> : rms_bwd_columns_kernel<T, V, false>;
+}
+
+#define DYT_INSTANTIATE_RMS(T)                                                            \
+  template RmsFwdKernel rms_fwd_kernel_of<T>(const host::RowPlan &, bool, bool);           \
+  template RmsBwdKernel rms_bwd_kernel_of<T>(const host::RowPlan &, bool);                 \
+  template RmsBwdLongKernel rms_bwd_rows_kernel_of<T>(const host::RowPlan &);              \
+  template RmsBwdColumnsKernel rms_bwd_columns_kernel_of<T>(const host::RowPlan &, bool);
+
+}  // namespace norm
+}  // namespace dyt

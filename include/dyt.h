@@ -289,7 +289,7 @@ int dyt_last_cuda_error(void);
 
 /*
  * Launch geometry of the calling thread's last successful call, so tests can
- * check which path ran. (Layer norm: path 1 = a row in a warp, 2 = in several
+ * check which path ran. (The norms: path 1 = a row in a warp, 2 = in several
  * warps; row_groups = partial sums per column; shifted = 1 for ragged rows.
  * Policy loss: path 1 = a warp per row or part of one, 2 = a CTA; col_chunks =
  * parts of a row. The other fields that do not apply are 0.)
@@ -297,7 +297,8 @@ int dyt_last_cuda_error(void);
 typedef struct dyt_launch_info {
   int op;            /* 1 = forward, 2 = backward, 3 = backward stage 1 (dyt_backward_partials),
                         4 = finalize (dyt_finalize_partials), 5 / 6 = layer norm forward /
-                        backward, 7 / 8 = policy loss forward / backward, 0 = none yet */
+                        backward, 7 / 8 = policy loss forward / backward, 9 / 10 / 11 =
+                        root-mean-square norm forward / quantize / backward, 0 = none yet */
   int path;          /* 0 = nothing launched, 1 = row-tiled (several rows per CTA step),
                         2 = row-per-CTA (one row per CTA step, columns across threads) */
   int vec;           /* elements per vector access (1 = the one-element kernels) */
@@ -493,6 +494,73 @@ dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *
                                     const float *stats, const float *coef, const float *grad, double temperature,
                                     void *dlogits, int64_t lddl, int64_t M, int64_t N, dyt_dtype dtype,
                                     dyt_stream_t stream);
+
+/*
+ * Root-mean-square norm over the rows of x, with the addition of a residual
+ * stream that stands before it:
+ *
+ *   h[i,j]  = x[i,j] + residual[i,j]     (without a residual h is x)
+ *   rstd[i] = (sum_j h[i,j]^2 / N + eps)^(-1/2)
+ *   y[i,j]  = gamma[j] * h[i,j] * rstd[i]
+ *
+ * One kernel launch; the conventions of dyt_layer_norm_forward hold. The sum and
+ * the row's sum of squares are binary32; y is computed from the sum before it is
+ * rounded, h and y are rounded once each.
+ *   residual  x_dtype, row pitch ldr; NULL: none, and h and ldh are not used
+ *   gamma     [N] gamma_dtype; NULL: 1
+ *   h         [M*N] x_dtype, row pitch ldh, written: the new residual stream. May
+ *             alias x or residual with an equal pitch, as y may, but not y.
+ *   rstd      [M] binary32, written for the backward; may be NULL
+ * A row is read once and kept on the SM when N is at most 16384 (16-bit) or 8192
+ * (binary32); longer rows are read twice. Ragged rows are read as there. A row
+ * whose sum of squares passes binary32's range has rstd 0. M * N == 0 launches
+ * nothing and writes nothing.
+ */
+dyt_status dyt_rms_norm_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *gamma,
+                                float eps, void *y, int64_t ldy, void *h, int64_t ldh, float *rstd, int64_t M,
+                                int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype, dyt_stream_t stream);
+
+/*
+ * The same norm with an output in 8 bits (e4m3: 4 bits of exponent, 3 behind the
+ * point, largest value 448) and the scales it is to be multiplied with:
+ *
+ *   a     = max_j |y[i,j]| over the row (group 0), or over each 128 columns (group
+ *           128; the last group of a row is shorter when N is no multiple)
+ *   scale = max(a, 2^-100) / 448        q[i,j] = e4m3(y[i,j] / scale)
+ *
+ * y is not rounded before. A group that holds a NaN has scale NaN and every q of
+ * it NaN; one whose largest value is infinite has scale infinite, and no finite
+ * product stands for it.
+ *   group     0 or 128, else DYT_ERR_INVALID_VALUE
+ *   q         [M*N] bytes, row pitch ldq, any alignment; may alias nothing
+ *   scale     [M] (group 0) or [M][ceil(N / 128)] binary32, written
+ * The other arguments as above. One kernel launch.
+ */
+dyt_status dyt_rms_norm_quantize(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *gamma,
+                                 float eps, int group, void *q, int64_t ldq, float *scale, void *h, int64_t ldh,
+                                 int64_t M, int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype,
+                                 dyt_stream_t stream);
+
+/*
+ * The norm's gradients, from the stored sum h (x, without a residual) and rstd:
+ *
+ *   n[i,j]    = h[i,j] * rstd[i]        g[i,j] = gamma[j] * dy[i,j]
+ *   dx[i,j]   = rstd[i] * (g[i,j] - n[i,j] * sum_k g[i,k] n[i,k] / N) + dh[i,j]
+ *   dgamma[j] = sum_i dy[i,j] * n[i,j]
+ *
+ * dx is the gradient of x and of the residual. Launches, sums and workspace as for
+ * dyt_layer_norm_backward (the second launch only for dgamma).
+ *   dh        x_dtype, row pitch lddh: the gradient that h received from elsewhere;
+ *             NULL: none
+ *   dgamma    [N] gamma_dtype, written; NULL: not wanted
+ *   dx        may alias h, dy or dh with an equal pitch
+ * M * N == 0: dgamma (when N > 0) is set to zero, and no workspace is used.
+ */
+size_t dyt_rms_norm_backward_workspace_bytes(int64_t M, int64_t N, dyt_dtype x_dtype);
+dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int64_t lddy, const float *rstd,
+                                 const void *gamma, const void *dh, int64_t lddh, void *dx, int64_t lddx,
+                                 void *dgamma, int64_t M, int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype,
+                                 void *workspace, size_t workspace_bytes, dyt_stream_t stream);
 
 #ifdef __cplusplus
 }
