@@ -1,6 +1,6 @@
 """Fused Dynamic Tanh (DyT) forward/backward for NVIDIA B200 (sm_100a), with the
-layer norm it takes the place of (``norm``), the root-mean-square norm (``rms``) and a
-policy loss on the logits (``loss``).
+layer norm it takes the place of (``norm``), the root-mean-square norm (``rms``), and on
+the logits a policy loss (``loss``) and log probabilities with entropy (``logp``).
 
 The computation lives in hand-written CUDA kernels behind a C ABI
 (``include/dyt.h``, built into ``libdyt.so``). This package is a thin layer
@@ -15,15 +15,17 @@ from __future__ import annotations
 import torch
 
 from . import _abi
-from ._abi import (DYT_BF16, DYT_F16, DYT_F32, MAX_RANKS, DytError, dyt_backward, dyt_backward_ex,
+from ._abi import (DYT_BF16, DYT_F16, DYT_F32, MAX_RANKS, MAX_TOP, DytError, dyt_backward, dyt_backward_ex,
                    dyt_backward_noalloc, dyt_backward_partials, dyt_backward_strided, dyt_backward_workspace_bytes,
                    dyt_finalize_partials, dyt_forward, dyt_forward_ex, dyt_forward_strided, dyt_ipc_close,
                    dyt_ipc_export, dyt_ipc_import, dyt_last_launch_info, dyt_layer_norm_backward,
-                   dyt_layer_norm_backward_workspace_bytes, dyt_layer_norm_forward, dyt_partials_layout_query,
-                   dyt_plan_query, dyt_policy_loss_backward, dyt_policy_loss_forward,
-                   dyt_policy_loss_workspace_bytes, dyt_rms_norm_backward, dyt_rms_norm_backward_workspace_bytes,
-                   dyt_rms_norm_forward, dyt_rms_norm_quantize, dyt_status_string)
+                   dyt_layer_norm_backward_workspace_bytes, dyt_layer_norm_forward, dyt_log_probs_backward,
+                   dyt_log_probs_forward, dyt_log_probs_workspace_bytes, dyt_partials_layout_query, dyt_plan_query,
+                   dyt_policy_loss_backward, dyt_policy_loss_forward, dyt_policy_loss_workspace_bytes,
+                   dyt_rms_norm_backward, dyt_rms_norm_backward_workspace_bytes, dyt_rms_norm_forward,
+                   dyt_rms_norm_quantize, dyt_status_string)
 from ._tensors import DTYPE_CODE, _code, _cuda_contig, _rows, _stream, row_pitch
+from .logp import LogProbs, LogProbsFunction, log_probs_backward, log_probs_forward, log_probs_workspace
 from .loss import (PolicyLoss, PolicyLossFunction, policy_loss_backward, policy_loss_forward,
                    policy_loss_workspace)
 from .norm import LayerNorm, LayerNormFunction, layer_norm_backward, layer_norm_forward, layer_norm_workspace
@@ -36,13 +38,15 @@ __all__ = ["forward", "backward", "workspace", "backward_partials", "partials_la
            "dyt_partials_layout_query", "dyt_finalize_partials", "dyt_ipc_export", "dyt_ipc_import",
            "dyt_ipc_close", "row_pitch", "dyt_backward_workspace_bytes", "dyt_status_string",
            "dyt_last_launch_info", "dyt_plan_query", "DytError", "DTYPE_CODE", "DYT_F32", "DYT_BF16", "DYT_F16",
-           "MAX_RANKS", "layer_norm_forward", "layer_norm_backward", "layer_norm_workspace", "LayerNorm",
+           "MAX_RANKS", "MAX_TOP", "layer_norm_forward", "layer_norm_backward", "layer_norm_workspace", "LayerNorm",
            "LayerNormFunction", "policy_loss_forward", "policy_loss_backward", "policy_loss_workspace", "PolicyLoss",
            "PolicyLossFunction", "dyt_layer_norm_forward", "dyt_layer_norm_backward",
            "dyt_layer_norm_backward_workspace_bytes", "dyt_policy_loss_forward", "dyt_policy_loss_backward",
            "dyt_policy_loss_workspace_bytes", "rms_norm_forward", "rms_norm_quantize", "rms_norm_backward",
            "rms_norm_workspace", "RMSNorm", "RMSNormFunction", "dyt_rms_norm_forward", "dyt_rms_norm_quantize",
-           "dyt_rms_norm_backward", "dyt_rms_norm_backward_workspace_bytes"]
+           "dyt_rms_norm_backward", "dyt_rms_norm_backward_workspace_bytes", "log_probs_forward", "log_probs_backward",
+           "log_probs_workspace", "LogProbs", "LogProbsFunction", "dyt_log_probs_forward", "dyt_log_probs_backward",
+           "dyt_log_probs_workspace_bytes"]
 
 
 def _shape(x: torch.Tensor, gamma: torch.Tensor):

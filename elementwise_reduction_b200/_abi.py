@@ -136,6 +136,15 @@ lib.dyt_policy_loss_forward.argtypes = [_vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp
 lib.dyt_policy_loss_forward.restype = _i32
 lib.dyt_policy_loss_backward.argtypes = [_vp, _i64, _vp, _i32, _vp, _vp, _vp, _f64, _vp, _i64, _i64, _i64, _i32, _vp]
 lib.dyt_policy_loss_backward.restype = _i32
+lib.dyt_log_probs_workspace_bytes.argtypes = [_i64, _i64, _i32, _i32]
+lib.dyt_log_probs_workspace_bytes.restype = _sz
+lib.dyt_log_probs_forward.argtypes = [_vp, _i64, _vp, _i32, _i64, _i32, _f64, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                                      _i32, _vp, _sz, _vp]
+lib.dyt_log_probs_forward.restype = _i32
+lib.dyt_log_probs_backward.argtypes = [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _f64, _vp, _i64, _i64, _i64,
+                                       _i32, _vp]
+lib.dyt_log_probs_backward.restype = _i32
+MAX_TOP = 32  # DYT_MAX_TOP in include/dyt.h
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # DYT_NOALLOC_SCRATCH_BYTES in include/dyt.h
 
 
@@ -296,6 +305,26 @@ def dyt_policy_loss_backward(logits, ld, tokens, token_bytes, stats, coef, grad,
     """Raw C-ABI call: pointers as ints (grad may be None). Returns the status code."""
     return lib.dyt_policy_loss_backward(logits, ld, tokens, token_bytes, stats, coef, grad, temperature, dlogits,
                                         lddl, M, N, dtype, stream)
+
+
+def dyt_log_probs_workspace_bytes(M, N, top, dtype) -> int:
+    return int(lib.dyt_log_probs_workspace_bytes(M, N, top, dtype))
+
+
+def dyt_log_probs_forward(logits, ld, tokens, token_bytes, ignore_index, top, temperature, logp, entropy, top_logp,
+                          top_tokens, stats, M, N, dtype, workspace, workspace_bytes, stream) -> int:
+    """Raw C-ABI call: pointers as ints (tokens with logp, top_logp and top_tokens may be None). Returns the
+    status code."""
+    return lib.dyt_log_probs_forward(logits, ld, tokens, token_bytes, ignore_index, top, temperature, logp, entropy,
+                                     top_logp, top_tokens, stats, M, N, dtype, workspace, workspace_bytes, stream)
+
+
+def dyt_log_probs_backward(logits, ld, tokens, token_bytes, ignore_index, stats, entropy, grad_logp, grad_entropy,
+                           temperature, dlogits, lddl, M, N, dtype, stream) -> int:
+    """Raw C-ABI call: pointers as ints (tokens, entropy and the two gradients may be None). Returns the status
+    code."""
+    return lib.dyt_log_probs_backward(logits, ld, tokens, token_bytes, ignore_index, stats, entropy, grad_logp,
+                                      grad_entropy, temperature, dlogits, lddl, M, N, dtype, stream)
 
 
 def dyt_ipc_export(ptr: int) -> bytes:

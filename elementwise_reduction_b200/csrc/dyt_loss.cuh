@@ -180,16 +180,17 @@ struct RowList {
   uint32_t bits[kMaxListed / 32];
   int before[kMaxListed / 32 + 1];
 
-  // All kRowsBlock threads of the CTA; returns how many rows count.
-  __device__ __forceinline__ int fill(const LossArgs &a) {
-    const int M = (int)a.M, words = (M + 31) / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // All kRowsBlock threads of the CTA; returns how many rows count: those whose weight(row) is not 0.
+  template <typename F>
+  __device__ __forceinline__ int fill(int M, F &&weight) {
+    const int words = (M + 31) / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kWarps = kRowsBlock / 32, kAtOnce = 16;  // the weights of so many words are under way together
     for (int w0 = warp; w0 < words; w0 += kAtOnce * kWarps) {
       float v[kAtOnce];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const int row = (w0 + i * kWarps) * 32 + lane;
-        v[i] = row < M ? a.weight[row] : 0.0f;
+        v[i] = row < M ? weight(row) : 0.0f;
       }
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kRowsBlock, 2) loss_rows_kernel(LossArgs a) {
   int64_t rows = a.M;
   int parts = a.S;
   if (a.listed) {
-    rows = list.fill(a);
+    rows = list.fill((int)a.M, [&](int row) { return a.weight[row]; });
     parts = choose_parts((float)rows, (float)warps, a.most, a.batches);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -524,6 +525,32 @@ __device__ __forceinline__ uint4 cut16(const uint4 &lo, const uint4 &hi, uint32_
                     __funnelshift_r(w[3], w[4], b));
 }
 
+// The loss's gradient in a row: A [j = tok] + B 2^((z - m) C), B = -A e^-s.
+struct LossGradRow {
+  using Args = LossGradArgs;
+  struct Call {  // what all rows share
+    double gt;
+    __device__ __forceinline__ Call(const Args &a) : gt((a.grad ? (double)*a.grad : 1.0) * a.inv_t) {}
+  };
+  int64_t tok;
+  float A, B, m, C;
+  __device__ __forceinline__ LossGradRow(const Args &a, const Call &c, int64_t row) : C(a.C) {
+    // (all of the row's numbers are asked for at once, whichever are used)
+    const float coef = a.coef[row];
+    tok = token_at(a.tokens, a.wide_tokens, row);
+    const float2 st = a.stats[row];
+    A = (float)(c.gt * (double)coef);
+    m = st.x;
+    B = -A * expf(-st.y);
+  }
+  __device__ __forceinline__ bool zero() const { return A == 0.0f; }  // no weight, or the clipped side
+  // p = 2^((z - m) C) e^-s: the maximum leaves first, as in the forward. (A power below 2^-126 is 0.)
+  __device__ __forceinline__ float2 pair(float2 z) const {
+    const float2 e = mul2(add2(z, f2(-m)), f2(C));
+    return mul2(f2(B), make_float2(ex2_approx(e.x), ex2_approx(e.y)));
+  }
+};
+
 constexpr int kGradCtas = 5;  // an SM's
 
 // Measured: 8192 x 131072 bf16 629 us (6.8 TB/s), 4096 x 32003 fp16 with a
@@ -537,8 +564,9 @@ constexpr int kGradCtas = 5;  // an SM's
 // the output row; SHIFT: the input row lies at another offset past a 16-byte
 // boundary, and each of its vectors is cut out of two aligned ones inside the
 // row. The elements before and after those vectors are taken one by one.
-template <typename T, bool CTA, bool SHIFT>
-__global__ void __launch_bounds__(256, kGradCtas) loss_grad_kernel(LossGradArgs a) {
+// Row: a row's numbers and what becomes of a logit (LossGradRow).
+template <typename T, bool CTA, bool SHIFT, typename Row>
+__global__ void __launch_bounds__(256, kGradCtas) loss_grad_kernel(typename Row::Args a) {
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int U = SHIFT ? 1 : 4;  // vectors under way (SHIFT, 1, 2 and 4: 98, 111 and 106 us for the case above)
   using IO = VecIO<T, V>;
@@ -548,17 +576,14 @@ __global__ void __launch_bounds__(256, kGradCtas) loss_grad_kernel(LossGradArgs 
   const int64_t items = a.M * a.S;
   const int64_t step = CTA ? gridDim.x : (int64_t)gridDim.x * (blockDim.x >> 5);
   int64_t item = CTA ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const double gt = (a.grad ? (double)*a.grad : 1.0) * a.inv_t;
+  const typename Row::Call call(a);
   for (; item < items; item += step) {
     const int64_t row = a.S == 1 ? item : item / a.S;
     const int part = (int)(item - row * a.S);
     const T *z = static_cast<const T *>(a.z) + row * a.ld;
     T *dz = static_cast<T *>(a.dz) + row * a.lddz;
-    // (all of the row's numbers are asked for at once, whichever are used)
-    const float coef = a.coef[row];
-    const int64_t tok = token_at(a.tokens, a.wide_tokens, row);
-    const float2 st = a.stats[row];
-    const float A = (float)(gt * (double)coef);
+    const Row r(a, call, row);
+    const int64_t tok = r.tok;
     // whole output vectors [head, head + nb V): with SHIFT, those whose two
     // input vectors lie inside the row
     int64_t head = head_elems(dz, a.N);
@@ -576,7 +601,7 @@ __global__ void __launch_bounds__(256, kGradCtas) loss_grad_kernel(LossGradArgs 
     const int64_t rest = a.N - head - nb * V;  // elements after the vectors
     const int64_t b0 = nb * part / a.S, b1 = nb * (part + 1) / a.S;
     uint4 *out = reinterpret_cast<uint4 *>(dz + head);
-    if (A == 0.0f) {  // no weight, or the clipped side: no gradient whatever the logits are
+    if (r.zero()) {  // no gradient whatever the logits are
       if (part == 0)
         for (int64_t j = t; j < head; j += G) dz[j] = from_f32<T>(0.0f);
       if (part == a.S - 1)
@@ -584,16 +609,10 @@ __global__ void __launch_bounds__(256, kGradCtas) loss_grad_kernel(LossGradArgs 
       for (int64_t i = b0 + t; i < b1; i += G) __stcs(out + i, make_uint4(0u, 0u, 0u, 0u));
       continue;
     }
-    // p = 2^((z - m) C) e^-s: the maximum leaves first, as in the forward. (A power below 2^-126 is 0.)
-    const float B = -A * expf(-st.y);
-    auto power = [&](float2 z2) {
-      const float2 e = mul2(add2(z2, f2(-st.x)), f2(a.C));
-      return make_float2(ex2_approx(e.x), ex2_approx(e.y));
-    };
     auto one = [&](int64_t j) {
-      const float p = power(f2(to_f32<T>(z[j]))).x;
+      const float v = r.pair(f2(to_f32<T>(z[j]))).x;
       // two roundings at the token, as in the vectors: the same bits at every offset
-      dz[j] = from_f32<T>(j == tok ? __fadd_rn(__fmul_rn(B, p), A) : B * p);
+      dz[j] = from_f32<T>(j == tok ? __fadd_rn(v, r.A) : v);
     };
     if (part == 0)
       for (int64_t j = t; j < head; j += G) one(j);
@@ -605,12 +624,12 @@ __global__ void __launch_bounds__(256, kGradCtas) loss_grad_kernel(LossGradArgs 
       IO::unpack2(raw, f);
       const int64_t j0 = head + i * V;
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) f[e] = mul2(f2(B), power(f[e]));
+      for (int e = 0; e < V / 2; ++e) f[e] = r.pair(f[e]);
       if (tok >= j0 && tok < j0 + V) {
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {
-          f[e].x += j0 + 2 * e == tok ? A : 0.0f;
-          f[e].y += j0 + 2 * e + 1 == tok ? A : 0.0f;
+          f[e].x += j0 + 2 * e == tok ? r.A : 0.0f;
+          f[e].y += j0 + 2 * e + 1 == tok ? r.A : 0.0f;
         }
       }
       __stcs(out + i, IO::pack2(f));
@@ -636,6 +655,12 @@ __global__ void __launch_bounds__(256, kGradCtas) loss_grad_kernel(LossGradArgs 
       vec(i, raw);
     }
   }
+}
+
+template <typename T, typename Row>
+auto grad_kernel(bool cta, bool shift) {
+  return cta ? (shift ? loss_grad_kernel<T, true, true, Row> : loss_grad_kernel<T, true, false, Row>)
+             : (shift ? loss_grad_kernel<T, false, true, Row> : loss_grad_kernel<T, false, false, Row>);
 }
 
 }  // namespace loss

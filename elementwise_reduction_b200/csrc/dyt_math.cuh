@@ -32,6 +32,13 @@ __device__ __forceinline__ float rcp_approx(float v) {
   return r;
 }
 
+// The larger value; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // ---- tanh(z) and 1 - tanh(z)^2 in binary32 --------------------------------
 //
 // a = |z|.

@@ -61,13 +61,6 @@ constexpr int kScaleCols = 128;
 constexpr float kQMax = 448.0f;      // the largest e4m3 value
 constexpr float kLeastTop = 0x1p-100f;  // a row of zeros has a scale all the same: nothing is divided by 0
 
-// The larger value; NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 __device__ __forceinline__ float lanes_max(float v, int width) {
   for (int o = width >> 1; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;

@@ -291,14 +291,15 @@ int dyt_last_cuda_error(void);
  * Launch geometry of the calling thread's last successful call, so tests can
  * check which path ran. (The norms: path 1 = a row in a warp, 2 = in several
  * warps; row_groups = partial sums per column; shifted = 1 for ragged rows.
- * Policy loss: path 1 = a warp per row or part of one, 2 = a CTA; col_chunks =
+ * Policy loss, log probabilities: path 1 = a warp per row or part of one, 2 = a CTA; col_chunks =
  * parts of a row. The other fields that do not apply are 0.)
  */
 typedef struct dyt_launch_info {
   int op;            /* 1 = forward, 2 = backward, 3 = backward stage 1 (dyt_backward_partials),
                         4 = finalize (dyt_finalize_partials), 5 / 6 = layer norm forward /
                         backward, 7 / 8 = policy loss forward / backward, 9 / 10 / 11 =
-                        root-mean-square norm forward / quantize / backward, 0 = none yet */
+                        root-mean-square norm forward / quantize / backward, 12 / 13 =
+                        log probabilities forward / backward, 0 = none yet */
   int path;          /* 0 = nothing launched, 1 = row-tiled (several rows per CTA step),
                         2 = row-per-CTA (one row per CTA step, columns across threads) */
   int vec;           /* elements per vector access (1 = the one-element kernels) */
@@ -561,6 +562,68 @@ dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int
                                  const void *gamma, const void *dh, int64_t lddh, void *dx, int64_t lddx,
                                  void *dgamma, int64_t M, int64_t N, dyt_dtype x_dtype, dyt_dtype gamma_dtype,
                                  void *workspace, size_t workspace_bytes, dyt_stream_t stream);
+
+/*
+ * Log probabilities of given tokens, with the entropy and the best alternatives of
+ * each of M rows of logits z over a vocabulary of N, T the temperature (the
+ * policy loss's old_logp and ref_logp):
+ *
+ *   m = max_j z[i,j],  s = log sum_j exp((z[i,j] - m) / T),  lp[i,j] = (z[i,j] - m) / T - s
+ *   logp[i]    = lp[i,tokens[i]]
+ *   entropy[i] = -sum_j exp(lp[i,j]) lp[i,j]
+ *   top_tokens[i][k], top_logp[i][k]: column and lp of the k-th largest logit of
+ *              the row (k < top); of equal logits the lower column comes first
+ *
+ * Two kernel launches. The logits are read once, and with alternatives a few
+ * pieces of a row (128 bytes each) a second time. Row sums are binary32, the
+ * rows' scalar arithmetic binary64, each output rounded once.
+ *   logits    [M*N] dtype, row pitch ld, any element alignment
+ *   tokens    [M] int64 (token_bytes 8) or int32 (token_bytes 4), or NULL: no
+ *             token is given, logp is not written, and every row counts. A row
+ *             whose token is ignore_index does not count: its logits are not
+ *             read, its logp, entropy, stats and top_logp are 0, its top_tokens
+ *             -1. Any other token outside [0, N) makes the row's logp NaN;
+ *             nothing outside the row is read.
+ *   top       0 <= top <= DYT_MAX_TOP and (M > 0) top <= N
+ *   logp, entropy [M], top_logp [M][top], stats [M][2] = (m, s): binary32, written;
+ *   top_tokens [M][top] int64, written (both may be NULL with top 0)
+ *   workspace 16-byte aligned scratch of at least dyt_log_probs_workspace_bytes(M,
+ *             N, top, dtype) bytes (about 1/64 of the logits with alternatives);
+ *             two calls in flight at once need two.
+ * temperature must be > 0 and finite. M == 0 writes nothing; N == 0 with M > 0
+ * gives DYT_ERR_INVALID_VALUE. A row whose logits are all -inf, or hold +inf or
+ * NaN, has NaN for logp, entropy and top_logp; NaN is no alternative: a row with
+ * fewer than `top` others has -1 (and NaN) in the places that are left.
+ */
+#define DYT_MAX_TOP 32
+
+size_t dyt_log_probs_workspace_bytes(int64_t M, int64_t N, int top, dyt_dtype dtype);
+dyt_status dyt_log_probs_forward(const void *logits, int64_t ld, const void *tokens, int token_bytes,
+                                 int64_t ignore_index, int top, double temperature, float *logp, float *entropy,
+                                 float *top_logp, int64_t *top_tokens, float *stats, int64_t M, int64_t N,
+                                 dyt_dtype dtype, void *workspace, size_t workspace_bytes, dyt_stream_t stream);
+
+/*
+ * The gradient by the logits of logp and entropy, from what the forward wrote:
+ *
+ *   p = exp(lp[i,j])
+ *   dlogits[i,j] = (grad_logp[i] * ((j == tokens[i]) - p) - grad_entropy[i] * p * (lp[i,j] + entropy[i])) / T
+ *
+ * One kernel launch, no workspace. Rows that do not count, and rows whose two
+ * gradients are 0, get zeros and are not read. A row whose token is outside the
+ * vocabulary gets NaN, unless its grad_logp is 0.
+ *   tokens, ignore_index, temperature  as in the forward
+ *   stats, entropy  [M][2], [M] binary32, read (entropy: only with grad_entropy)
+ *   grad_logp, grad_entropy  [M] binary32; NULL: 0. grad_logp needs tokens.
+ *   dlogits      [M*N] dtype, row pitch lddl, written; may alias logits with an
+ *                equal pitch
+ * M * N == 0 launches nothing.
+ */
+dyt_status dyt_log_probs_backward(const void *logits, int64_t ld, const void *tokens, int token_bytes,
+                                  int64_t ignore_index, const float *stats, const float *entropy,
+                                  const float *grad_logp, const float *grad_entropy, double temperature,
+                                  void *dlogits, int64_t lddl, int64_t M, int64_t N, dyt_dtype dtype,
+                                  dyt_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,4 +1,4 @@
-"""The root-mean-square norm without a GPU: the plain formulas the GPU tests compare with against autograd, and
+"""The root-mean-square norm and the log probabilities without a GPU: the plain formulas the GPU tests compare with against autograd, and
 the entry points' refusals, which come before any CUDA call."""
 from __future__ import annotations
 
@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import elementwise_reduction_b200 as dyt
+from tests import logp_helpers as L
 from tests import rms_helpers as S
 
 A = 1 << 20  # a 16-byte aligned stand-in for a device address
@@ -87,5 +88,73 @@ def test_tensors_must_be_on_a_gpu():
     x = torch.randn(3, 8)
     for call in (lambda: dyt.rms_norm_forward(x), lambda: dyt.rms_norm_quantize(x),
                  lambda: dyt.rms_norm_backward(x, x, x[:, 0])):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.parametrize("T", [1.0, 0.7])
+def test_log_probability_formulas_agree_with_autograd(T):
+    torch.manual_seed(2)
+    M, N = 30, 17
+    z = torch.randn(M, N, dtype=torch.float64, requires_grad=True)
+    tokens = torch.randint(0, N, (M,))
+    tokens[::4] = -100
+    on = tokens != -100
+    a, b = torch.randn(M, dtype=torch.float64), torch.randn(M, dtype=torch.float64)
+    lp = (z / T).log_softmax(-1)
+    entropy = -(lp.exp() * lp).sum(-1)
+    hit = lp.gather(1, tokens.clamp(min=0)[:, None])[:, 0]
+    ((hit * a)[on].sum() + (entropy * b)[on].sum()).backward()
+    (logp, ent, best, ids, stats), _ = L.forward(z.detach(), tokens, 3, T)
+    keep = on.double()
+    assert torch.allclose(logp, hit.detach() * keep, rtol=1e-12) and torch.allclose(ent, entropy.detach() * keep)
+    assert torch.equal(ids[on], z.detach().topk(3).indices[on]) and (ids[~on] == -1).all()
+    assert torch.allclose(best[on], lp.detach().topk(3).values[on]) and (stats[~on] == 0).all()
+    dz, _ = L.backward(z.detach(), tokens, stats, ent, a, b, T)
+    assert torch.allclose(dz, z.grad, rtol=1e-10, atol=1e-13)
+    v, t = torch.randn(M, N, dtype=torch.float64), 1e-6
+    f = lambda y: float((L.forward(y, tokens, 0, T)[0][0] * a + L.forward(y, tokens, 0, T)[0][1] * b).sum())  # noqa: E731
+    slope = (f(z.detach() + t * v) - f(z.detach() - t * v)) / (2 * t)
+    assert abs(slope - float((dz * v).sum())) < 1e-6
+
+
+def test_alternatives_go_by_column_and_leave_nan_out():
+    inf, nan = float("inf"), float("nan")
+    z = torch.tensor([[1.0, 2.0, 2.0, 0.0], [nan, -inf, nan, -inf], [0.0, -0.0, nan, inf], [nan] * 4])
+    assert L.alternatives(z, 3).tolist() == [[1, 2, 0], [1, 3, -1], [3, 0, 1], [-1, -1, -1]]
+
+
+def logp_fwd(z=A, ld=8, tok=A, tb=8, ignore=-100, top=3, T=1.0, logp=A, ent=A, best=A, ids=A, stats=A, M=4, N=8, dt=0,
+             ws=A, n=1 << 20):
+    return dyt.dyt_log_probs_forward(z, ld, tok, tb, ignore, top, T, logp, ent, best, ids, stats, M, N, dt, ws, n,
+                                     None)
+
+
+def logp_bwd(z=A, ld=8, tok=A, tb=8, ignore=-100, stats=A, ent=A, da=A, db=A, T=1.0, dz=A, lddz=8, M=4, N=8, dt=0):
+    return dyt.dyt_log_probs_backward(z, ld, tok, tb, ignore, stats, ent, da, db, T, dz, lddz, M, N, dt, None)
+
+
+def test_log_probability_refusals():
+    nan, inf = float("nan"), float("inf")
+    for kw in ({"M": -1}, {"N": -1}, {"N": 0, "ld": 0}, {"ld": 7}, {"tb": 2}, {"tb": 0}, {"z": 0}, {"logp": 0},
+               {"ent": 0}, {"stats": 0}, {"best": 0}, {"ids": 0}, {"ws": 0}, {"ws": A + 8}, {"z": A + 2},
+               {"tok": A + 4}, {"tok": A + 2, "tb": 4}, {"logp": A + 2}, {"ent": A + 1}, {"best": A + 2},
+               {"ids": A + 4}, {"stats": A + 4}, {"top": -1}, {"top": 9}, {"top": 33, "N": 64, "ld": 64}, {"T": 0.0},
+               {"T": -1.0}, {"T": nan}, {"T": inf}, {"T": 1e-60}, {"T": 1e300}):
+        assert logp_fwd(**kw) == 1, kw
+    assert logp_fwd(dt=3) == 2 and logp_bwd(dt=-1) == 2
+    for kw in ({"M": -1}, {"N": -1}, {"ld": 7}, {"lddz": 7}, {"tb": 3}, {"z": 0}, {"stats": 0}, {"dz": 0},
+               {"z": A + 2}, {"dz": A + 1}, {"stats": A + 4}, {"ent": 0}, {"tok": 0}, {"ent": A + 2}, {"da": A + 2},
+               {"db": A + 1}, {"T": 0.0}, {"T": inf}):
+        assert logp_bwd(**kw) == 1, kw
+    assert logp_fwd(z=0, M=0) == 0 and logp_bwd(z=0, M=0) == 0 and logp_bwd(z=0, N=0, ld=0, lddz=0) == 0
+    for M, N, top, d in ((-1, 4, 0, 0), (0, 4, 0, 0), (4, 0, 0, 0), (4, 4, 0, 7), (4, 4, 5, 0), (4, 64, 33, 0)):
+        assert dyt.dyt_log_probs_workspace_bytes(M, N, top, d) == 0
+
+
+def test_logits_must_be_on_a_gpu():
+    x = torch.randn(3, 8)
+    for call in (lambda: dyt.log_probs_forward(x), lambda: dyt.log_probs_workspace(x),
+                 lambda: dyt.log_probs_backward(x, None, x[:, :2])):
         with pytest.raises(ValueError):
             call()
