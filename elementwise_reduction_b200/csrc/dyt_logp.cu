@@ -22,14 +22,20 @@ constexpr int kOpLogpForward = 12, kOpLogpBackward = 13;  // dyt_launch_info::op
 
 struct LogpPlan {
   LossPlan p;
+  int together;  // rows that a warp of logp_top_kernel takes at a time
   size_t off_tops, off_taken, bytes;
 };
 
 LogpPlan plan_logp(int64_t M, int64_t N, int top, size_t es, int sms) {
   LogpPlan q = {};
   q.p = plan_forward(M, N, es, sms);
-  if (top > 0)
-    q.p.finish = (int)std::min<int64_t>(ceil_div(M, dyt::loss::kFinishBlock / 32), (int64_t)sms * dyt::loss::kTopCtasPerSm);
+  if (top > 0) {
+    // as many rows at a time as let the warps take them in one round
+    const int64_t warps = (int64_t)sms * dyt::loss::kTopCtas * (dyt::loss::kTopBlock / 32);
+    q.together = (int)std::max<int64_t>(1, std::min<int64_t>(32, ceil_div(M, warps)));
+    q.p.finish = (int)std::min<int64_t>(ceil_div(M, (int64_t)q.together * (dyt::loss::kTopBlock / 32)),
+                                        (int64_t)sms * dyt::loss::kTopCtas);
+  }
   const size_t batches = (size_t)ceil_div(ceil_div(N * (int64_t)es, 16), dyt::loss::kBatch * 32);
   q.off_tops = ((size_t)M * (size_t)q.p.most * sizeof(float4) + 15) & ~(size_t)15;
   q.off_taken = q.off_tops + (top > 0 ? ((size_t)M * batches * 32 * es + 15) & ~(size_t)15 : 0);
@@ -100,20 +106,21 @@ dyt_status dyt_log_probs_forward(const void *logits, int64_t ld, const void *tok
   a.aligned = N % (16 / (int64_t)es) == 0 && aligned16(logits) && vec_pitch(ld, es);
   a.wide_tokens = token_bytes == 8;
   a.K = top;
+  a.together = q.together;
   a.C = C;
   a.inv_t = 1.0 / temperature;
   const cudaStream_t s = (cudaStream_t)stream;
   return with_type(dtype, [&](auto t) -> dyt_status {
     using T = decltype(t);
     const auto rows = top > 0 ? dyt::loss::logp_rows_kernel<T, true> : dyt::loss::logp_rows_kernel<T, false>;
-    const auto finish = top > 0 ? dyt::loss::logp_finish_kernel<T, true> : dyt::loss::logp_finish_kernel<T, false>;
+    const auto finish = top > 0 ? dyt::loss::logp_top_kernel<T> : dyt::loss::logp_finish_kernel<T>;
     const size_t smem = dyt::loss::rows_smem(p.block);
     const dyt_status ready = prepare_smem(dev, (const void *)rows, (int)smem);
     if (ready != DYT_OK) return ready;
     PdlConfig lc((unsigned)p.grid, p.block, smem, s);
     cudaError_t e = cudaLaunchKernelEx(&lc.cfg, rows, a);
     if (e != cudaSuccess) return cuda_fail(e);
-    PdlConfig lf((unsigned)p.finish, dyt::loss::kFinishBlock, 0, s);
+    PdlConfig lf((unsigned)p.finish, top > 0 ? dyt::loss::kTopBlock : dyt::loss::kFinishBlock, 0, s);
     e = cudaLaunchKernelEx(&lf.cfg, finish, a);
     if (e != cudaSuccess) return cuda_fail(e);
     record(kOpLogpForward, &p, (int)(16 / sizeof(T)), 2, q.bytes);

@@ -18,6 +18,8 @@
 // here, and 0 times an exponent of -inf would be NaN.
 #pragma once
 
+#include <type_traits>
+
 #include "dyt_loss.cuh"
 
 namespace dyt {
@@ -45,6 +47,7 @@ struct LogpArgs {
   int aligned;         // every row is whole aligned 16-byte vectors
   int wide_tokens;
   int K;
+  int together;        // K > 0: rows that a warp of the second kernel takes at a time
   float C;             // log2(e) / T
   double inv_t;
 };
@@ -96,9 +99,10 @@ __device__ __forceinline__ Moments join(Moments a, Moments b, float C) {
   return a;
 }
 
-// 2 n values more; returns the largest. NaN passes over the maximum and reaches the sums.
-template <int n>
-__device__ __forceinline__ float add_values(Moments &r, const float2 (&v)[n], float C) {
+// 2 n values more; returns the largest. NaN passes over the maximum and reaches the sums. FAR: exponents
+// are kept from -inf; else a second sum that such a one has made NaN is left out, and false returned for it.
+template <bool FAR, int n>
+__device__ __forceinline__ float add_values(Moments &r, const float2 (&v)[n], float C, bool *done = nullptr) {
   float x[2] = {fmaxf(v[0].x, v[0].y), kNegInf};
 #pragma unroll
   for (int i = 1; i < n; ++i) x[i & 1] = max3(x[i & 1], v[i].x, v[i].y);
@@ -109,15 +113,20 @@ __device__ __forceinline__ float add_values(Moments &r, const float2 (&v)[n], fl
 #pragma unroll
   for (int i = 0; i < n; ++i) {
     float2 e = mul2(add2(v[i], f2(-m)), f2(C));
-    e = make_float2(max_nan(e.x, kFar), max_nan(e.y, kFar));
+    if constexpr (FAR) e = make_float2(max_nan(e.x, kFar), max_nan(e.y, kFar));
     const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
     s[i & 1] = add2(s[i & 1], p);
     t[i & 1] = fma2(p, e, t[i & 1]);
   }
   s[0] = add2(s[0], s[1]);
   t[0] = add2(t[0], t[1]);
+  const float more = t[0].x + t[0].y;
+  if constexpr (!FAR) {
+    *done = more == more;
+    if (!*done) return top;
+  }
   r.s += s[0].x + s[0].y;
-  r.t += t[0].x + t[0].y;
+  r.t += more;
   return top;
 }
 
@@ -213,23 +222,29 @@ __global__ void __launch_bounds__(kRowsBlock, 2) logp_rows_kernel(LogpArgs a) {
         uint4 raw[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) raw[u] = ring[rd + u * 32];
+        const int here = rd;
         rd = rd == (kStages - 1) * kBatch * 32 ? 0 : rd + kBatch * 32;
         issue();
         float2 v[kBatch * P];
         float top;
+        bool done = false;
         if (n >= kBatch * 32) {
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) IO::unpack2(raw[u], *reinterpret_cast<float2(*)[P]>(v + u * P));
-          top = add_values(r, v, C);
-        } else {
+          top = add_values<false>(r, v, C, &done);
+        }
+        // Batches with infinite exponents (masked logits) are taken once more, and those that end a row at once,
+        // with a look at every exponent: one instruction more an element. Their slots are not filled again before
+        // the next batch.
+        if (!done) {
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) {
-            IO::unpack2(raw[u], *reinterpret_cast<float2(*)[P]>(v + u * P));
+            IO::unpack2(ring[here + u * 32], *reinterpret_cast<float2(*)[P]>(v + u * P));
             if (u * 32 + lane >= n)
 #pragma unroll
               for (int i = 0; i < P; ++i) v[u * P + i] = f2(kNegInf);
           }
-          top = add_values(r, v, C);
+          top = add_values<true>(r, v, C);
         }
         if constexpr (TOP) {
           if (n > 0) *tops = from_f32<T>(top);  // (a part of no vectors has no chunks)
@@ -239,7 +254,7 @@ __global__ void __launch_bounds__(kRowsBlock, 2) logp_rows_kernel(LogpArgs a) {
       } while (n > 0);
       if (!a.aligned) {
         const float2 p[1] = {make_float2(first, last)};
-        add_values(r, p, C);
+        add_values<true>(r, p, C);
       }
       float m = r.m;
 #pragma unroll
@@ -261,13 +276,12 @@ __global__ void __launch_bounds__(kRowsBlock, 2) logp_rows_kernel(LogpArgs a) {
 
 // ---- the largest logits ------------------------------------------------------------
 
-// A logit's rank as a whole number: falling logits, rising columns. 0: none.
+// A logit's rank as a whole number: falling logits, rising columns.
 using Key = unsigned long long;
-__device__ __forceinline__ uint32_t value_key(float v) {
+__device__ __forceinline__ Key logit_key(float v, uint32_t col) {
   const uint32_t u = __float_as_uint(v + 0.0f);  // -0 is 0
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  return (Key)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32 | (0xFFFFFFFFu - col);
 }
-__device__ __forceinline__ Key logit_key(float v, uint32_t col) { return (Key)value_key(v) << 32 | (0xFFFFFFFFu - col); }
 __device__ __forceinline__ float key_value(Key k) {
   const uint32_t o = (uint32_t)(k >> 32);
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
@@ -276,209 +290,390 @@ __device__ __forceinline__ uint32_t key_col(Key k) { return 0xFFFFFFFFu - (uint3
 
 constexpr int kMaxTop = DYT_MAX_TOP;  // alternatives, at most: a lane each
 static_assert(kMaxTop <= 32, "a lane each");
-constexpr int kChunks = 256;  // chunks listed before they are read
-constexpr int kKeys = 256;    // candidates kept before all but K of them are dropped
+constexpr int kChunks = 512;  // chunks listed before they are read
+constexpr int kKeys = 512;    // candidates kept before all but K of them are dropped
 
-// A warp's candidates: every logit not below `least`, which rises to the K-th largest seen.
-struct Best {
+// A warp's lists.
+struct __align__(16) Best {
   Key keys[kKeys];
+  Key first[kMaxTop];
   int chunks[kChunks];
 };
-struct BestState {
-  Key least;
-  int n;  // candidates
+
+template <typename T>
+using Pair = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+template <typename T>
+__device__ __forceinline__ Pair<T> half_pair(const uint4 &r, int w) {
+  const uint32_t word = word_of(r, w);
+  return *reinterpret_cast<const Pair<T> *>(&word);
+}
+// The largest of 16 bytes of logits, the even and the odd elements apart (x, y); a NaN passes over.
+template <typename T>
+__device__ __forceinline__ float2 largest(const uint4 &r) {
+  if constexpr (sizeof(T) == 4) {
+    return make_float2(fmaxf(__uint_as_float(r.x), __uint_as_float(r.z)), fmaxf(__uint_as_float(r.y), __uint_as_float(r.w)));
+  } else {
+    const Pair<T> m = __hmax2(__hmax2(half_pair<T>(r, 0), half_pair<T>(r, 1)),
+                              __hmax2(half_pair<T>(r, 2), half_pair<T>(r, 3)));
+    return make_float2(to_f32<T>(m.x), to_f32<T>(m.y));
+  }
+}
+// A bit for each of 16 bytes of logits that is not below v, a value of T (NaN is).
+template <typename T>
+__device__ __forceinline__ uint32_t not_below(const uint4 &r, float v) {
+  uint32_t m = 0;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m |= (__uint_as_float(word_of(r, e)) >= v ? 1u : 0u) << e;
+  } else {  // pairs: all 16 bits of a half tell
+    Pair<T> l;
+    l.x = l.y = from_f32<T>(v);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m |= __hge2_mask(half_pair<T>(r, w), l) & (0x00020001u << (2 * w));
+    m = (m | m >> 16) & 0xFFu;
+  }
+  return m;
+}
+
+// How many elements the lanes before this one have, and all of them.
+__device__ __forceinline__ int lanes_before(int count, int lane, int &total) {
+  int sum = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+    if (lane >= o) sum += t;
+  }
+  total = __shfl_sync(0xFFFFFFFFu, sum, 31);
+  return sum - count;
+}
+
+// The K largest of n keys, in order. (There is room for one more behind them, or n is even.)
+__device__ __forceinline__ void rank(Key *keys, int n, Key *out, int K, int lane) {
+  if (lane == 0 && (n & 1)) keys[n] = 0;  // they are looked at in pairs; no key is 0
+  __syncwarp();
+  auto pass = [&](int j, auto pair) {  // a key or two a lane
+    constexpr bool two = decltype(pair)::value;
+    const Key k0 = j < n ? keys[j] : 0, k1 = two && j + 32 < n ? keys[j + 32] : 0;
+    int r0 = 0, r1 = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; i += 2) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(keys + i);
+      r0 += (o.x > k0) + (o.y > k0);
+      if (two) r1 += (o.x > k1) + (o.y > k1);
+    }
+    if (j < n && r0 < K) out[r0] = k0;
+    if (two && j + 32 < n && r1 < K) out[r1] = k1;
+  };
+  int j = lane;
+  for (; j - lane + 32 < n; j += 64) pass(j, std::true_type());
+  if (j - lane < n) pass(j, std::false_type());
+  __syncwarp();
+}
+
+// The lanes' values in falling order: lane l gets the l-th largest.
+__device__ __forceinline__ float sort_lanes(float v, int lane, int from) {
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      if (k < from) continue;
+      const float o = __shfl_xor_sync(0xFFFFFFFFu, v, j);
+      v = ((lane & j) == 0) == ((lane & k) == 0) ? fmaxf(v, o) : fminf(v, o);
+    }
+  return v;
+}
+
+// A row's vectors and the largest logits of its chunks.
+template <typename T>
+struct RowTops {
+  static constexpr int V = 16 / (int)sizeof(T);
+  const T *z, *tops;
+  int head, nb, batches;
+  int vecs;  // 16-byte vectors of tops; 0: too few for the warp (less than V batches), taken one by one
+  __device__ __forceinline__ RowTops(const LogpArgs &a, int64_t row) {
+    z = static_cast<const T *>(a.z) + row * a.ld;
+    head = a.aligned ? 0 : head_elems(z, a.N);
+    nb = (int)((a.N - head) / V);
+    batches = (nb + kBatch * 32 - 1) / (kBatch * 32);
+    tops = static_cast<const T *>(a.tops) + row * a.batches * 32;
+    vecs = batches * 32 / V;
+    if (vecs < 32) vecs = 0;
+  }
+  // The K-th largest of 64 groups' largest logits, two groups a lane: at least K logits are not below it.
+  __device__ __forceinline__ float bound(int K, int lane) const {
+    float2 m = f2(kNegInf);
+    if (vecs) {
+#pragma unroll 8
+      for (int i = lane; i < vecs; i += 32) {
+        const float2 o = largest<T>(reinterpret_cast<const uint4 *>(tops)[i]);
+        m = make_float2(fmaxf(m.x, o.x), fmaxf(m.y, o.y));
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < V; u += 2) {
+        if (u < batches) m.x = fmaxf(m.x, to_f32<T>(tops[u * 32 + lane]));
+        if (u + 1 < batches) m.y = fmaxf(m.y, to_f32<T>(tops[u * 32 + 32 + lane]));
+      }
+    }
+    const float x = sort_lanes(m.x, lane, 0), y = sort_lanes(m.y, lane, 0);
+    // the 32 largest of both, in order
+    const float v = sort_lanes(fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, y, 31)), lane, 32);
+    return __shfl_sync(0xFFFFFFFFu, v, K - 1);
+  }
+  // Chunk c's first vector.
+  __device__ __forceinline__ int first_vec(int c) const { return (c >> 5) * (kBatch * 32) + (c & 31); }
+  // The chunk of bit k of a lane's look at 8 vectors of tops from i0 (or at all of few tops, one by one).
+  __device__ __forceinline__ int chunk(int i0, int k, int lane) const {
+    return vecs ? (i0 + k / V * 32 + lane) * V + k % V : k * 32 + lane;
+  }
 };
 
-// All but the K largest candidates go; those stand in order.
-__device__ __forceinline__ void prune(Best &b, BestState &st, int K, int lane) {
-  __syncwarp();
-  Key mine[kKeys / 32];
-  int rank[kKeys / 32];
-#pragma unroll
-  for (int j = 0; j < kKeys / 32; ++j) {
-    mine[j] = j * 32 + lane < st.n ? b.keys[j * 32 + lane] : 0;
-    rank[j] = 0;
-  }
-  for (int i = 0; i < st.n; ++i) {
-    const Key k = b.keys[i];
-#pragma unroll
-    for (int j = 0; j < kKeys / 32; ++j)
-      if (j * 32 < st.n) rank[j] += k > mine[j];
-  }
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < kKeys / 32; ++j)
-    if (j * 32 + lane < st.n && rank[j] < K) b.keys[rank[j]] = mine[j];
-  st.n = min(st.n, K);
-  __syncwarp();
-  if (st.n == K) st.least = b.keys[K - 1];
-}
+// A bit for each of a lane's 8 vectors of V.
+template <int V>
+struct Bits {
+  using type = typename std::conditional<V == 8, unsigned long long, uint32_t>::type;
+  static __device__ __forceinline__ int count(type m) { return V == 8 ? __popcll(m) : __popc((uint32_t)m); }
+  static __device__ __forceinline__ int lowest(type m) { return (V == 8 ? __ffsll((long long)m) : __ffs((int)m)) - 1; }
+};
 
-__device__ __forceinline__ void push(Best &b, BestState &st, bool in, float v, uint32_t col, int K, int lane) {
-  const Key k = logit_key(v, col);
-  in = in && v == v && k >= st.least;  // NaN is no alternative
-  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
-  if (mask == 0) return;
-  if (in) b.keys[st.n + __popc(mask & ((1u << lane) - 1u))] = k;
-  st.n += __popc(mask);
-  if (st.n > kKeys - 32) prune(b, st, K, lane);
-}
-
-// The K largest logits of a row into b.keys[0 .. st.n).
+// Candidates among the elements off the vectors (less than 32): those not below v.
 template <typename T>
-__device__ __forceinline__ void find_best(const LogpArgs &a, int64_t row, Best &b, BestState &st, int lane) {
-  constexpr int V = 16 / (int)sizeof(T);
+__device__ __forceinline__ int off_vectors(const LogpArgs &a, const RowTops<T> &t, float v, Key *keys, int lane) {
+  const int tail = (int)((a.N - t.head) % RowTops<T>::V);
+  const bool off = lane < t.head + tail;
+  const uint32_t col = lane < t.head ? (uint32_t)lane : (uint32_t)(a.N - tail + lane - t.head);
+  const float x = off ? to_f32<T>(t.z[col]) : 0.0f;
+  const bool in = off && x >= v;
+  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
+  if (in) keys[__popc(mask & ((1u << lane) - 1u))] = logit_key(x, col);
+  return __popc(mask);
+}
+
+// The K largest logits of a row into b.first, in order; returns how many there are (K, but for NaN). -1: there
+// are more candidates than room, as where many logits are equal.
+template <typename T>
+__device__ __forceinline__ int find_best(const LogpArgs &a, const RowTops<T> &t, Best &b, int lane) {
+  constexpr int V = RowTops<T>::V;
+  using B = Bits<V>;
   const int K = a.K;
-  const T *z = static_cast<const T *>(a.z) + row * a.ld;
-  const int head = a.aligned ? 0 : head_elems(z, a.N);
-  const int nb = (int)((a.N - head) / V), tail = (int)((a.N - head) % V);
-  const int batches = (nb + kBatch * 32 - 1) / (kBatch * 32);
-  const T *tops = static_cast<const T *>(a.tops) + row * a.batches * 32 + lane;
-  // The K-th largest of the lanes' largest chunks: at least K logits are not below it.
-  float mine = kNegInf;
-#pragma unroll 8
-  for (int i = 0; i < batches; ++i) mine = fmaxf(mine, to_f32<T>(tops[i * 32]));
-  const uint32_t o = value_key(mine);
-  int above = 0;
+  const float v = t.bound(K, lane);
+  int n = off_vectors(a, t, v, b.keys, lane), listed = 0;  // candidates, chunks: the same in every lane
+  for (int i0 = 0; i0 == 0 || i0 < t.vecs; i0 += 8 * 32) {
+    typename B::type mask = 0;
 #pragma unroll
-  for (int l = 0; l < 32; ++l) {
-    const uint32_t other = __shfl_sync(0xFFFFFFFFu, o, l);
-    above += other > o || (other == o && l < lane);
-  }
-  const uint32_t kth = __ballot_sync(0xFFFFFFFFu, above == K - 1);
-  st.least = (Key)__shfl_sync(0xFFFFFFFFu, o, __ffs((int)kth) - 1) << 32;
-  st.n = 0;
-  if (head > 0) push(b, st, lane < head, lane < head ? to_f32<T>(z[lane]) : 0.0f, (uint32_t)lane, K, lane);
-  if (tail > 0)
-    push(b, st, lane < tail, lane < tail ? to_f32<T>(z[a.N - tail + lane]) : 0.0f, (uint32_t)(a.N - tail + lane), K,
-         lane);
-  int listed = 0;
-  // A chunk is kBatch vectors: a lane takes four bytes of one, several chunks under way at once.
-  auto read_chunks = [&]() {
-    __syncwarp();
-    constexpr int U = 4, W = 4 / (int)sizeof(T);
-    for (int i = 0; i < listed; i += U) {
-      uint32_t raw[U], col[U];
-      bool in[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = i + u < listed ? b.chunks[i + u] : 0;
-        const int vec = (c >> 5) * (kBatch * 32) + (lane >> 2) * 32 + (c & 31);
-        in[u] = i + u < listed && vec < nb;
-        col[u] = (uint32_t)(head + vec * V + (lane & 3) * W);
-        raw[u] = in[u] ? *reinterpret_cast<const uint32_t *>(z + col[u]) : 0u;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if constexpr (sizeof(T) == 4) {
-          push(b, st, in[u], __uint_as_float(raw[u]), col[u], K, lane);
-        } else {
-          const T *h = reinterpret_cast<const T *>(&raw[u]);
-          push(b, st, in[u], to_f32<T>(h[0]), col[u], K, lane);
-          push(b, st, in[u], to_f32<T>(h[1]), col[u] + 1, K, lane);
-        }
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * 32 + lane;
+      if (t.vecs) {
+        if (i < t.vecs)
+          mask |= (typename B::type)not_below<T>(reinterpret_cast<const uint4 *>(t.tops)[i], v) << (u * V);
+      } else if (u < V && u < t.batches) {
+        mask |= (typename B::type)(to_f32<T>(t.tops[u * 32 + lane]) >= v) << u;
       }
     }
-    listed = 0;
+    int total, at = lanes_before(B::count(mask), lane, total);
+    if (listed + total > kChunks) return -1;
+    for (at += listed; mask; mask &= mask - 1) b.chunks[at++] = t.chunk(i0, B::lowest(mask), lane);
+    listed += total;
+  }
+  __syncwarp();
+  const uint4 *zv = reinterpret_cast<const uint4 *>(t.z + t.head);
+  for (int i = lane; i - lane < listed; i += 32) {  // a chunk a lane
+    const int first = i < listed ? t.first_vec(b.chunks[i]) : t.nb;
+    uint4 raw[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (first + u * 32 < t.nb) raw[u] = zv[first + u * 32];
+    typename B::type mask = 0;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (first + u * 32 < t.nb) mask |= (typename B::type)not_below<T>(raw[u], v) << (u * V);
+    int total, at = lanes_before(B::count(mask), lane, total);
+    if (n + total > kKeys) return -1;
+    for (at += n; mask; mask &= mask - 1) {
+      const int k = B::lowest(mask), e = (first + k / V * 32) * V + k % V;
+      b.keys[at++] = logit_key(to_f32<T>(t.z[t.head + e]), (uint32_t)(t.head + e));
+    }
+    n += total;
+  }
+  rank(b.keys, n, b.first, K, lane);
+  return min(n, K);
+}
+
+// The same where candidates are many: a chunk at a time, all but the K largest dropped whenever there is no room.
+template <typename T>
+__device__ __noinline__ int find_best_of_many(const LogpArgs &a, int64_t row, Best &b, int lane) {
+  constexpr int V = RowTops<T>::V;
+  const RowTops<T> t(a, row);
+  const int K = a.K;
+  Key least = logit_key(t.bound(K, lane), 0xFFFFFFFFu);  // of that value at any column
+  __syncwarp();
+  int n = off_vectors(a, t, key_value(least), b.keys, lane);
+  auto prune = [&]() {
+    rank(b.keys, n, b.first, K, lane);
+    if (n >= K) least = b.first[K - 1];
+    n = min(n, K);
+    if (lane < n) b.keys[lane] = b.first[lane];
     __syncwarp();
   };
-  constexpr int B = 4;  // batches looked at together
-  for (int i0 = 0; i0 < batches; i0 += B) {
-    float top[B];
-#pragma unroll
-    for (int u = 0; u < B; ++u) top[u] = i0 + u < batches ? to_f32<T>(tops[(i0 + u) * 32]) : kNegInf;
-#pragma unroll
-    for (int u = 0; u < B; ++u) {
-      const int vec = (i0 + u) * (kBatch * 32) + lane;
-      // the chunk's best key, if its largest logit stood first
-      const bool in = vec < nb && logit_key(top[u], (uint32_t)(head + vec * V)) >= st.least;
-      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
-      if (in) b.chunks[listed + __popc(mask & ((1u << lane) - 1u))] = (i0 + u) * 32 + lane;
-      listed += __popc(mask);
+  for (int c0 = 0; c0 < t.batches * 32; c0 += 32) {
+    // a chunk's logits stand behind its first one
+    const int first = t.first_vec(c0 + lane);
+    const bool could = logit_key(to_f32<T>(t.tops[c0 + lane]), (uint32_t)(t.head + first * V)) >= least;
+    uint32_t todo = __ballot_sync(0xFFFFFFFFu, could);
+    while (todo) {
+      const int c = c0 + __ffs((int)todo) - 1;
+      todo &= todo - 1;
+      for (int o = lane; o - lane < kBatch * V; o += 32) {  // its logits, 32 at a time
+        const int vec = t.first_vec(c) + o / V * 32, e = vec * V + o % V;
+        const bool in = vec < t.nb;
+        const float x = in ? to_f32<T>(t.z[t.head + e]) : 0.0f;
+        const Key k = logit_key(x, (uint32_t)(t.head + e));
+        const bool take = in && x == x && k >= least;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, take);
+        if (take) b.keys[n + __popc(mask & ((1u << lane) - 1u))] = k;
+        n += __popc(mask);
+        if (n > kKeys / 4) prune();
+      }
     }
-    if (listed > kChunks - 32 * B) read_chunks();
   }
-  read_chunks();
-  prune(b, st, K, lane);
+  prune();
+  return n;
 }
 
 // ---- second kernel -----------------------------------------------------------------
 
-constexpr int kTopCtasPerSm = 8;
+// What is read of a row before the first kernel is waited for (see loss_finish_kernel: this one too is launched
+// directly after its first kernel, and that one releases it nowhere but in pdl_prologue).
+struct LogpInput {
+  bool counts = false;
+  double hit = 0.0;
+};
+template <typename T>
+__device__ __forceinline__ LogpInput logp_input(const LogpArgs &a, int64_t row) {
+  LogpInput in;
+  in.counts = true;
+  if (a.tokens) {
+    const int64_t tok = token_at(a.tokens, a.wide_tokens, row);
+    in.counts = tok != a.ignore;
+    // a token outside the vocabulary has no probability
+    in.hit = (double)__int_as_float(0x7FC00000);
+    if (in.counts && tok >= 0 && tok < a.N)
+      in.hit = (double)to_f32<T>(__ldcg(static_cast<const T *>(a.z) + row * a.ld + tok));
+  }
+  return in;
+}
 
-// Joins the rows' parts and finishes the rows. A row takes a thread, or a warp (with alternatives, or of
-// many parts). As in loss_finish_kernel, a CTA reads its first rows' tokens and their logits before the wait.
-template <typename T, bool TOP>
+// Parts first, first + step, ... of a row.
+__device__ __forceinline__ Moments some_parts(const LogpArgs &a, int64_t row, int parts, int first, int step) {
+  Moments r;
+  for (int i = first; i < parts; i += step) {
+    const float4 p = a.parts[row * a.most + i];
+    Moments o;
+    o.m = p.x;
+    o.s = p.y;
+    o.t = p.z;
+    r = join(r, o, a.C);
+  }
+  return r;
+}
+// The lanes' parts together.
+__device__ __forceinline__ Moments join_lanes(Moments r, float C) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Moments other;
+    other.m = __shfl_xor_sync(0xFFFFFFFFu, r.m, o);
+    other.s = __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
+    other.t = __shfl_xor_sync(0xFFFFFFFFu, r.t, o);
+    // the lower lane's part first, on both sides: the same bits
+    r = (threadIdx.x & o) ? join(other, r, C) : join(r, other, C);
+  }
+  return r;
+}
+// Writes a row's outputs; returns the log of its sum.
+__device__ __forceinline__ double finish_row(const LogpArgs &a, int64_t row, const Moments &r, const LogpInput &in) {
+  if (!in.counts) {
+    if (a.logp) a.logp[row] = 0.0f;
+    a.entropy[row] = 0.0f;
+    a.stats[row] = make_float2(0.0f, 0.0f);
+    return 0.0;
+  }
+  const double s = log((double)r.s);
+  if (a.logp) a.logp[row] = (float)((in.hit - (double)r.m) * a.inv_t - s);
+  a.entropy[row] = (float)(s - kLn2D * ((double)r.t / (double)r.s));
+  a.stats[row] = make_float2(r.m, (float)s);
+  return s;
+}
+
+// Joins the rows' parts and finishes the rows: a thread each, or a warp where there are many parts.
+template <typename T>
 __global__ void __launch_bounds__(kFinishBlock) logp_finish_kernel(LogpArgs a) {
-  __shared__ Best best[TOP ? kFinishBlock / 32 : 1];
   const int tid = threadIdx.x, lane = tid & 31;
-  const bool wide = TOP || a.most > kThreadParts;
+  const bool wide = a.most > kThreadParts;
   const int64_t per = wide ? kFinishBlock / 32 : kFinishBlock;  // rows of a CTA step
-  struct Input {
-    bool counts;
-    double hit;
-  };
-  auto input = [&](int64_t row) {
-    Input in = {true, 0.0};
-    if (a.tokens) {
-      const int64_t tok = token_at(a.tokens, a.wide_tokens, row);
-      in.counts = tok != a.ignore;
-      // a token outside the vocabulary has no probability
-      in.hit = (double)__int_as_float(0x7FC00000);
-      if (in.counts && tok >= 0 && tok < a.N)
-        in.hit = (double)to_f32<T>(__ldcg(static_cast<const T *>(a.z) + row * a.ld + tok));
-    }
-    return in;
-  };
   int64_t row = blockIdx.x * per + (wide ? tid >> 5 : tid);
-  Input in = {};
-  if (row < a.M) in = input(row);
+  LogpInput in;
+  if (row < a.M) in = logp_input<T>(a, row);
   pdl_prologue();
   const int parts = *a.taken;
   while (row < a.M) {
     Moments r;
-    if (in.counts) {
-      for (int i = wide ? lane : 0; i < parts; i += wide ? 32 : 1) {
-        const float4 p = a.parts[row * a.most + i];
-        Moments o;
-        o.m = p.x;
-        o.s = p.y;
-        o.t = p.z;
-        r = join(r, o, a.C);
+    if (in.counts) r = some_parts(a, row, parts, wide ? lane : 0, wide ? 32 : 1);
+    if (wide) r = join_lanes(r, a.C);
+    if (!wide || lane == 0) finish_row(a, row, r, in);
+    row += per * gridDim.x;
+    if (row < a.M) in = logp_input<T>(a, row);
+  }
+}
+
+constexpr int kTopBlock = 128, kTopCtas = 4;  // CTAs that an SM holds
+// The same with alternatives. A warp takes `a.together` rows at a time: a lane each for their parts and their
+// scalars, all lanes for each row's alternatives. (One row: all lanes for its parts too.)
+template <typename T>
+__global__ void __launch_bounds__(kTopBlock, kTopCtas) logp_top_kernel(const __grid_constant__ LogpArgs a) {
+  __shared__ Best best[kTopBlock / 32];
+  const int lane = threadIdx.x & 31;
+  Best &b = best[threadIdx.x >> 5];
+  const int R = a.together;
+  const int64_t step = (int64_t)gridDim.x * (kTopBlock / 32) * R;
+  int64_t base = ((int64_t)blockIdx.x * (kTopBlock / 32) + (threadIdx.x >> 5)) * R;
+  LogpInput in;
+  if (lane < R && base + lane < a.M) in = logp_input<T>(a, base + lane);
+  pdl_prologue();
+  const int parts = *a.taken;
+  while (base < a.M) {
+    const int rows = (int)min((int64_t)R, a.M - base);
+    Moments mine;
+    double s = 0.0;
+    if (R == 1) {
+      in.counts = __shfl_sync(0xFFFFFFFFu, in.counts, 0);
+      if (in.counts) mine = some_parts(a, base, parts, lane, 32);
+      mine = join_lanes(mine, a.C);
+    } else if (in.counts) {
+      mine = some_parts(a, base + lane, parts, 0, 1);
+    }
+    if (lane < rows) s = finish_row(a, base + lane, mine, in);
+    const uint32_t counting = __ballot_sync(0xFFFFFFFFu, in.counts && lane < rows);
+    for (int k = 0; k < rows; ++k) {
+      const bool counts = counting >> k & 1u;
+      const double m_k = (double)__shfl_sync(0xFFFFFFFFu, mine.m, k), s_k = __shfl_sync(0xFFFFFFFFu, s, k);
+      int n = 0;
+      if (counts) {
+        n = find_best<T>(a, RowTops<T>(a, base + k), b, lane);
+        if (n < 0) n = find_best_of_many<T>(a, base + k, b, lane);
       }
-    }
-    if (wide) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        Moments other;
-        other.m = __shfl_xor_sync(0xFFFFFFFFu, r.m, o);
-        other.s = __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
-        other.t = __shfl_xor_sync(0xFFFFFFFFu, r.t, o);
-        // the lower lane's part first, on both sides: the same bits
-        r = (tid & o) ? join(other, r, a.C) : join(r, other, a.C);
-      }
-    }
-    const double s = in.counts ? log((double)r.s) : 0.0;
-    if (!wide || lane == 0) {
-      if (a.logp) a.logp[row] = in.counts ? (float)((in.hit - (double)r.m) * a.inv_t - s) : 0.0f;
-      a.entropy[row] = in.counts ? (float)(s - kLn2D * ((double)r.t / (double)r.s)) : 0.0f;
-      a.stats[row] = in.counts ? make_float2(r.m, (float)s) : make_float2(0.0f, 0.0f);
-    }
-    if constexpr (TOP) {
-      Best &b = best[tid >> 5];
-      BestState st = {0, 0};
-      if (in.counts) find_best<T>(a, row, b, st, lane);
       if (lane < a.K) {
-        const bool found = lane < st.n;
-        const Key k = found ? b.keys[lane] : 0;
-        const float none = in.counts ? __int_as_float(0x7FC00000) : 0.0f;
-        a.best[row * a.K + lane] = found ? (float)(((double)key_value(k) - (double)r.m) * a.inv_t - s) : none;
-        a.ids[row * a.K + lane] = found ? (long long)key_col(k) : -1;
+        const bool found = lane < n;
+        const Key key = found ? b.first[lane] : 0;
+        const float none = counts ? __int_as_float(0x7FC00000) : 0.0f;
+        const int64_t at = (base + k) * a.K + lane;
+        a.best[at] = found ? (float)(((double)key_value(key) - m_k) * a.inv_t - s_k) : none;
+        a.ids[at] = found ? (long long)key_col(key) : -1;
       }
       __syncwarp();  // (the next row's candidates take their place)
     }
-    row += per * gridDim.x;
-    if (row < a.M) in = input(row);
+    base += step;
+    in = LogpInput();
+    if (lane < R && base + lane < a.M) in = logp_input<T>(a, base + lane);
   }
 }
 
