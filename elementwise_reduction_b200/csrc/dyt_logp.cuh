@@ -130,6 +130,13 @@ __device__ __forceinline__ float add_values(Moments &r, const float2 (&v)[n], fl
   return top;
 }
 
+// The largest of the warp's values; a NaN passes over.
+__device__ __forceinline__ float warp_largest(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // Whether a row counts.
 __device__ __forceinline__ bool row_counts(const LogpArgs &a, int64_t row) {
   return a.tokens == nullptr || token_at(a.tokens, a.wide_tokens, row) != a.ignore;
@@ -256,15 +263,14 @@ __global__ void __launch_bounds__(kRowsBlock, 2) logp_rows_kernel(LogpArgs a) {
         const float2 p[1] = {make_float2(first, last)};
         add_values<true>(r, p, C);
       }
-      float m = r.m;
+      // one instruction for the largest, and the two sums by halves of the warp: a lane of each half has one
+      raise(r, warp_largest(r.m), C);
+      const bool up = (lane & 16) != 0;
+      float sum = (up ? r.t : r.s) + __shfl_xor_sync(0xFFFFFFFFu, up ? r.s : r.t, 16);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      raise(r, m, C);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
-        r.t += __shfl_xor_sync(0xFFFFFFFFu, r.t, o);
-      }
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      r.t = __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+      r.s = sum;
       if (lane == 0) a.parts[row * a.most + part] = make_float4(r.m, r.s, r.t, 0.0f);
     }
     // The batches of nothing at the end: the ring starts the next items where it stands.
@@ -290,11 +296,12 @@ __device__ __forceinline__ uint32_t key_col(Key k) { return 0xFFFFFFFFu - (uint3
 
 constexpr int kMaxTop = DYT_MAX_TOP;  // alternatives, at most: a lane each
 static_assert(kMaxTop <= 32, "a lane each");
-constexpr int kChunks = 512;  // chunks listed before they are read
-constexpr int kKeys = 512;    // candidates kept before all but K of them are dropped
+constexpr int kChunks = 256;  // room for chunks
+constexpr int kKeys = 256;    // and for candidates
 
-// A warp's lists.
+// A warp's lists, and 8 vectors a lane on their way to it (asynchronous copies: no registers wait for them).
 struct __align__(16) Best {
+  uint4 stage[8][32];
   Key keys[kKeys];
   Key first[kMaxTop];
   int chunks[kChunks];
@@ -399,14 +406,27 @@ struct RowTops {
     vecs = batches * 32 / V;
     if (vecs < 32) vecs = 0;
   }
+  // The lane's vectors i0 + lane, i0 + lane + 32, ... of tops, 8 of them, into its slots.
+  __device__ __forceinline__ void fetch(Best &b, int i0, int lane) const {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u * 32 + lane < vecs) cp_async16(&b.stage[u][lane], reinterpret_cast<const uint4 *>(tops) + i0 + u * 32 + lane);
+    cp_async_commit();
+    cp_async_wait<0>();
+  }
   // The K-th largest of 64 groups' largest logits, two groups a lane: at least K logits are not below it.
-  __device__ __forceinline__ float bound(int K, int lane) const {
+  // Leaves the last 8 vectors of tops in the stage.
+  __device__ __forceinline__ float bound(Best &b, int K, int lane) const {
     float2 m = f2(kNegInf);
     if (vecs) {
-#pragma unroll 8
-      for (int i = lane; i < vecs; i += 32) {
-        const float2 o = largest<T>(reinterpret_cast<const uint4 *>(tops)[i]);
-        m = make_float2(fmaxf(m.x, o.x), fmaxf(m.y, o.y));
+      for (int i0 = 0; i0 < vecs; i0 += 8 * 32) {
+        fetch(b, i0, lane);
+#pragma unroll 2
+        for (int u = 0; u < 8; ++u) {
+          if (i0 + u * 32 + lane >= vecs) break;
+          const float2 o = largest<T>(b.stage[u][lane]);
+          m = make_float2(fmaxf(m.x, o.x), fmaxf(m.y, o.y));
+        }
       }
     } else {
 #pragma unroll
@@ -456,19 +476,21 @@ __device__ __forceinline__ int find_best(const LogpArgs &a, const RowTops<T> &t,
   constexpr int V = RowTops<T>::V;
   using B = Bits<V>;
   const int K = a.K;
-  const float v = t.bound(K, lane);
+  const float v = t.bound(b, K, lane);
   int n = off_vectors(a, t, v, b.keys, lane), listed = 0;  // candidates, chunks: the same in every lane
   for (int i0 = 0; i0 == 0 || i0 < t.vecs; i0 += 8 * 32) {
     typename B::type mask = 0;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u * 32 + lane;
-      if (t.vecs) {
-        if (i < t.vecs)
-          mask |= (typename B::type)not_below<T>(reinterpret_cast<const uint4 *>(t.tops)[i], v) << (u * V);
-      } else if (u < V && u < t.batches) {
-        mask |= (typename B::type)(to_f32<T>(t.tops[u * 32 + lane]) >= v) << u;
+    if (t.vecs > 8 * 32) t.fetch(b, i0, lane);
+    if (t.vecs) {
+#pragma unroll 2
+      for (int u = 0; u < 8; ++u) {
+        if (i0 + u * 32 + lane >= t.vecs) break;
+        mask |= (typename B::type)not_below<T>(b.stage[u][lane], v) << (u * V);
       }
+    } else {
+#pragma unroll
+      for (int u = 0; u < V; ++u)
+        if (u < t.batches) mask |= (typename B::type)(to_f32<T>(t.tops[u * 32 + lane]) >= v) << u;
     }
     int total, at = lanes_before(B::count(mask), lane, total);
     if (listed + total > kChunks) return -1;
@@ -479,19 +501,21 @@ __device__ __forceinline__ int find_best(const LogpArgs &a, const RowTops<T> &t,
   const uint4 *zv = reinterpret_cast<const uint4 *>(t.z + t.head);
   for (int i = lane; i - lane < listed; i += 32) {  // a chunk a lane
     const int first = i < listed ? t.first_vec(b.chunks[i]) : t.nb;
-    uint4 raw[kBatch];
+    const int vecs = min(kBatch, (t.nb - first + 31) / 32);  // of the chunk
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-      if (first + u * 32 < t.nb) raw[u] = zv[first + u * 32];
+      if (u < vecs) cp_async16(&b.stage[u][lane], zv + first + u * 32);
+    cp_async_commit();
+    cp_async_wait<0>();
     typename B::type mask = 0;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (first + u * 32 < t.nb) mask |= (typename B::type)not_below<T>(raw[u], v) << (u * V);
+#pragma unroll 2
+    for (int u = 0; u < vecs; ++u) mask |= (typename B::type)not_below<T>(b.stage[u][lane], v) << (u * V);
     int total, at = lanes_before(B::count(mask), lane, total);
     if (n + total > kKeys) return -1;
     for (at += n; mask; mask &= mask - 1) {
-      const int k = B::lowest(mask), e = (first + k / V * 32) * V + k % V;
-      b.keys[at++] = logit_key(to_f32<T>(t.z[t.head + e]), (uint32_t)(t.head + e));
+      const int k = B::lowest(mask);
+      b.keys[at++] = logit_key(to_f32<T>(reinterpret_cast<const T *>(&b.stage[k / V][lane])[k % V]),
+                               (uint32_t)(t.head + (first + k / V * 32) * V + k % V));
     }
     n += total;
   }
@@ -505,7 +529,7 @@ __device__ __noinline__ int find_best_of_many(const LogpArgs &a, int64_t row, Be
   constexpr int V = RowTops<T>::V;
   const RowTops<T> t(a, row);
   const int K = a.K;
-  Key least = logit_key(t.bound(K, lane), 0xFFFFFFFFu);  // of that value at any column
+  Key least = logit_key(t.bound(b, K, lane), 0xFFFFFFFFu);  // of that value at any column
   __syncwarp();
   int n = off_vectors(a, t, key_value(least), b.keys, lane);
   auto prune = [&]() {
@@ -532,7 +556,7 @@ __device__ __noinline__ int find_best_of_many(const LogpArgs &a, int64_t row, Be
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, take);
         if (take) b.keys[n + __popc(mask & ((1u << lane) - 1u))] = k;
         n += __popc(mask);
-        if (n > kKeys / 4) prune();
+        if (n > kKeys / 2) prune();
       }
     }
   }
@@ -625,7 +649,7 @@ __global__ void __launch_bounds__(kFinishBlock) logp_finish_kernel(LogpArgs a) {
   }
 }
 
-constexpr int kTopBlock = 128, kTopCtas = 4;  // CTAs that an SM holds
+constexpr int kTopBlock = 128, kTopCtas = 6;  // CTAs that an SM holds
 // The same with alternatives. A warp takes `a.together` rows at a time: a lane each for their parts and their
 // scalars, all lanes for each row's alternatives. (One row: all lanes for its parts too.)
 template <typename T>
