@@ -97,6 +97,14 @@ def _fresh_rows(rows: torch.Size, device: torch.device) -> torch.Tensor:
     return torch.empty(rows, dtype=torch.float32, device=device)
 
 
+def _fresh_matrix(rows: torch.Size, n: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """An uninitialised contiguous tensor of n values per row. (empty_strided takes 1.5 us, torch.empty of a
+    shape 2.3 to 3.)"""
+    if len(rows) == 1:
+        return torch.empty_strided((rows[0], n), (n, 1), dtype=dtype, device=device)
+    return torch.empty((*rows, n), dtype=dtype, device=device)
+
+
 def _scratch(n: int, device: torch.device) -> torch.Tensor:
     """An uninitialised workspace of at least n bytes."""
     return torch.empty_strided((n if n > 16 else 16,), (1,), dtype=torch.uint8, device=device)

@@ -302,6 +302,14 @@ struct RowFeed {
     for (int t = 0; t < TENSORS; ++t) at[t] += w.inc[t];
   }
 
+  // The next row to copy is this one (for rows that do not follow at equal steps: with w.inc 0).
+  __device__ __forceinline__ void seek(const T *const (&base)[TENSORS], const int64_t (&ld)[TENSORS],
+                                       const Place<MODE> &p, int64_t row) {
+    const int c0 = RAGGED ? column<V, E, true, MODE>(p.L, p.lane - p.at, 0) : p.lane * V;
+#pragma unroll
+    for (int i = 0; i < TENSORS; ++i) at[i] = reinterpret_cast<const char *>(base[i] + row * ld[i] + c0);
+  }
+
   // RAGGED: elements g .. g + 7 of every lane of the warp lie inside the row.
   __device__ __forceinline__ bool whole(const Place<MODE> &p, int g) const {
     return (g + 8) * p.seg() * (int)sizeof(T) <= need;

@@ -21,6 +21,42 @@ using dyt::norm::RmsGradArgs;
 constexpr int kOpRmsForward = 9, kOpRmsQuantize = 10, kOpRmsBackward = 11;  // dyt_launch_info::op
 constexpr int kColumnsBlock = 256;  // vector-columns of a CTA in the long rows' second pass
 
+struct FwdPlan {
+  RowPlan r;
+  bool shortrow;  // rms_short_kernel
+  int slots;      // its vectors of a lane
+  bool steal;     // rows in several warps: more of them than CTAs at a time
+  int64_t grid;
+};
+
+FwdPlan plan_fwd(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
+  FwdPlan p = {};
+  p.shortrow = aligned && N / vec <= dyt::norm::kShortVectors;
+  if (p.shortrow) {
+    const int64_t vectors = N / vec;
+    p.slots = dyt::norm::kShortSlots;
+    if (M * vectors <= (int64_t)sms * 1024) p.slots = 1;  // few rows: all lanes of all rows at once
+    p.r.V = vec;
+    p.r.NV = (int)vectors;
+    const int64_t lanes = ceil_div(vectors, p.slots);
+    p.r.group = lanes > 32;
+    p.r.L = p.r.group ? (int)ceil_div(lanes, 32) * 32 : pow2_at_least(lanes);
+    p.r.rows = p.r.group ? 1 : 32 * dyt::norm::kShortWarps / p.r.L;
+    p.r.block = p.r.rows * p.r.L;
+    p.grid = std::min<int64_t>(ceil_div(M, p.r.rows), (int64_t)1 << 30);
+    return p;
+  }
+  p.r = plan_rows(M, N, vec, aligned, E, sms);
+  p.grid = std::min<int64_t>(ceil_div(M, p.r.rows), (int64_t)sms);
+  if (p.r.group && !p.r.rowlong) {  // a CTA a row (there is no room in memory for 2^31 rows of more than 512 elements)
+    p.r.rows = 1;
+    p.r.block = p.r.L;
+    p.grid = M;
+    p.steal = M > (int64_t)sms * (dyt::norm::kBlock / p.r.L);
+  }
+  return p;
+}
+
 // A plan for few rows spreads them over the SMs: no more rows side by side than every SM gets.
 RowPlan plan_rms(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
   RowPlan p = plan_rows(M, N, vec, aligned, E, sms);
@@ -106,12 +142,13 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
     const bool out = q8 ? elem_aligned(y, VE) && (ldy & (VE - 1)) == 0 : aligned16(y) && vec_pitch(ldy, es);
     const bool vec = N % VE == 0 && out && aligned16(x) && vec_pitch(ldx, es) &&
                      (!res || (aligned16(res) && aligned16(h) && vec_pitch(ldr, es) && vec_pitch(ldh, es)));
-    const RowPlan p = plan_rms(M, N, VE, vec, dyt::norm::fwd_elems<T>(), sms);
-    const dyt::norm::RmsFwdKernel k = dyt::norm::rms_fwd_kernel_of<T>(p, res != nullptr, q8);
-    const size_t smem = p.rowlong ? 0 : dyt::norm::rms_fwd_smem<T>(p.block, p.L, p.ragged, res != nullptr);
+    const FwdPlan p = plan_fwd(M, N, VE, vec, dyt::norm::fwd_elems<T>(), sms);
+    const RowPlan &r = p.r;
+    const bool ring = !p.shortrow && !r.rowlong;
+    const dyt::norm::RmsFwdKernel k = dyt::norm::rms_fwd_kernel_of<T>(r, p.shortrow, res != nullptr, q8);
+    const size_t smem = ring ? dyt::norm::rms_fwd_smem<T>(r.block, r.L, r.ragged, res != nullptr) : 0;
     const dyt_status s = prepare_smem(dev, (const void *)k, (int)smem);
     if (s != DYT_OK) return s;
-    const int64_t grid = std::min<int64_t>(ceil_div(M, p.rows), (int64_t)sms);
     const int64_t lds[3] = {ldx, res ? ldr : ldx, ldx};  // the inputs (walk_of takes the last for an output)
     RmsArgs a = {};
     a.x = x;
@@ -129,13 +166,17 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
     a.eps = eps;
     a.grouped = group != 0;
     a.groups = group ? (int)ceil_div(N, group) : 1;
-    a.w = walk_of(p, M, N, grid, lds, 3, es, p.rowlong ? 0 : dyt::norm::fwd_plane<T>(32, p.L, p.ragged));
+    a.slots = p.slots;
+    a.steal = p.steal;
+    a.w = walk_of(r, M, N, ring && !r.group ? p.grid : 0, lds, 3, es,
+                  ring ? dyt::norm::fwd_plane<T>(32, r.L, r.ragged) : 0);
+    a.step = p.grid * r.rows;
     a.inc_y = (int64_t)a.w.step * ldy * (int64_t)(q8 ? 1 : es);
     a.inc_h = res ? (int64_t)a.w.step * ldh * (int64_t)es : 0;
-    PdlConfig lc((unsigned)grid, p.block, smem, (cudaStream_t)stream);
+    PdlConfig lc((unsigned)p.grid, r.block, smem, (cudaStream_t)stream);
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
     if (e != cudaSuccess) return cuda_fail(e);
-    record(op, &p, grid, 1, 0, 0);
+    record(op, &r, p.grid, 1, 0, 0);
     return DYT_OK;
   });
 }

@@ -7,16 +7,17 @@ namespace dyt {
 namespace norm {
 
 template <typename T, bool RES, bool Q>
-RmsFwdKernel rms_fwd_of(const host::RowPlan &p) {
-  if (p.rowlong) return p.V == 1 ? rms_fwd_long_kernel<T, 1, RES, Q> : rms_fwd_long_kernel<T, 16 / (int)sizeof(T), RES, Q>;
+RmsFwdKernel rms_fwd_of(const host::RowPlan &p, bool shortrow) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (shortrow) return rms_short_kernel<T, RES, Q>;
+  if (p.rowlong) return p.V == 1 ? rms_fwd_long_kernel<T, 1, RES, Q> : rms_fwd_long_kernel<T, V, RES, Q>;
   if (p.group) return p.ragged ? rms_fwd_kernel<T, kGroup, true, RES, Q> : rms_fwd_kernel<T, kGroup, false, RES, Q>;
-  if (p.L == 32) return p.ragged ? rms_fwd_kernel<T, kWarp, true, RES, Q> : rms_fwd_kernel<T, kWarp, false, RES, Q>;
-  return p.ragged ? rms_fwd_kernel<T, kPart, true, RES, Q> : rms_fwd_kernel<T, kPart, false, RES, Q>;
+  return p.L == 32 ? rms_fwd_kernel<T, kWarp, true, RES, Q> : rms_fwd_kernel<T, kPart, true, RES, Q>;
 }
 template <typename T>
-RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool res, bool q8) {
-  if (q8) return res ? rms_fwd_of<T, true, true>(p) : rms_fwd_of<T, false, true>(p);
-  return res ? rms_fwd_of<T, true, false>(p) : rms_fwd_of<T, false, false>(p);
+RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool shortrow, bool res, bool q8) {
+  if (q8) return res ? rms_fwd_of<T, true, true>(p, shortrow) : rms_fwd_of<T, false, true>(p, shortrow);
+  return res ? rms_fwd_of<T, true, false>(p, shortrow) : rms_fwd_of<T, false, false>(p, shortrow);
 }
 
 template <typename T, bool RES>
@@ -41,7 +42,7 @@ RmsBwdColumnsKernel rms_bwd_columns_kernel_of(const host::RowPlan &p, bool res) 
 }
 
 #define DYT_INSTANTIATE_RMS(T)                                                            \
-  template RmsFwdKernel rms_fwd_kernel_of<T>(const host::RowPlan &, bool, bool);           \
+  template RmsFwdKernel rms_fwd_kernel_of<T>(const host::RowPlan &, bool, bool, bool);     \
   template RmsBwdKernel rms_bwd_kernel_of<T>(const host::RowPlan &, bool);                 \
   template RmsBwdLongKernel rms_bwd_rows_kernel_of<T>(const host::RowPlan &);              \
   template RmsBwdColumnsKernel rms_bwd_columns_kernel_of<T>(const host::RowPlan &, bool);

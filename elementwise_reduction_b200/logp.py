@@ -16,8 +16,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._tensors import (_code, _current, _elsewhere, _fresh, _fresh_rows, _like, _pitch, _scratch, _there, _vector,
-                       _workspace, row_pitch)
+from ._tensors import (_code, _current, _elsewhere, _fresh, _fresh_matrix, _fresh_rows, _like, _pitch, _scratch,
+                       _there, _vector, _workspace, row_pitch)
 from .loss import _shape
 
 _F32 = (torch.float32,)
@@ -68,12 +68,10 @@ def log_probs_forward(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
         tp, token_bytes = _vector(tokens, "tokens", M, index, _TOKEN), tokens.element_size()
         logp = _fresh_rows(rows, dev)
     entropy = _fresh_rows(rows, dev)
-    stats = (torch.empty_strided((M, 2), (2, 1), dtype=torch.float32, device=dev) if len(rows) == 1 else
-             torch.empty((*rows, 2), dtype=torch.float32, device=dev))
+    stats = _fresh_matrix(rows, 2, torch.float32, dev)
     best = ids = None
     if top:
-        best = torch.empty((*rows, top), dtype=torch.float32, device=dev)
-        ids = torch.empty((*rows, top), dtype=torch.int64, device=dev)
+        best, ids = _fresh_matrix(rows, top, torch.float32, dev), _fresh_matrix(rows, top, torch.int64, dev)
     st = _abi.lib.dyt_log_probs_forward(
         logits.data_ptr(), ld, tp, token_bytes, ignore_index, top, temperature,
         None if logp is None else logp.data_ptr(), entropy.data_ptr(), None if best is None else best.data_ptr(),

@@ -13,8 +13,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._tensors import (DTYPE_CODE, _code, _current, _elsewhere, _fresh, _fresh_rows, _like, _pitch, _scratch, _there,
-                       _vector, _workspace, row_pitch)
+from ._tensors import (DTYPE_CODE, _code, _current, _elsewhere, _fresh, _fresh_matrix, _fresh_rows, _like, _pitch,
+                       _scratch, _there, _vector, _workspace, row_pitch)
 from .norm import _shape
 
 _F32 = (torch.float32,)
@@ -87,11 +87,11 @@ def rms_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, residu
     M, N = _shape(x)
     if group not in (0, SCALE_COLUMNS):
         raise ValueError(f"group must be 0 (a scale per row) or {SCALE_COLUMNS}, not {group}")
-    ldx, code, dev = _pitch(x, "x"), _code(x, "x"), x.device
+    ldx, code, dev, rows = _pitch(x, "x"), _code(x, "x"), x.device, x.shape[:-1]
     gp = None if gamma is None else _vector(gamma, "gamma", N, index, _PARAM)
     rp, ldr, hp, ldh, h = _residual(x, residual, residual_out, N)
     if out is None:
-        q, ldq = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev), N
+        q, ldq = _fresh_matrix(rows, N, torch.float8_e4m3fn, dev), N
     else:
         q = out
         if q.shape != x.shape or q.dtype != torch.float8_e4m3fn or q.get_device() != index:
@@ -99,10 +99,9 @@ def rms_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, residu
         ldq = _pitch(q, "out")
     groups = -(-N // group) if group else 1
     if scale is None:
-        rows = x.shape[:-1]
-        scale = torch.empty((*rows, groups), dtype=torch.float32, device=dev) if group else _fresh_rows(rows, dev)
+        scale = _fresh_matrix(rows, groups, torch.float32, dev) if group else _fresh_rows(rows, dev)
     else:
-        _vector(scale, "scale", x.shape[:-1].numel() * groups, index, _F32)
+        _vector(scale, "scale", rows.numel() * groups, index, _F32)
     st = _abi.lib.dyt_rms_norm_quantize(
         x.data_ptr(), ldx, rp, ldr, gp, eps, group, q.data_ptr(), ldq, scale.data_ptr(), hp, ldh, M, N, code,
         code if gamma is None else DTYPE_CODE[gamma.dtype], _current(index))
