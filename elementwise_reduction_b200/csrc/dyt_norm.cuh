@@ -78,14 +78,16 @@ constexpr int kRunRows = 128;
 constexpr int kMaxWarps = 32;
 
 // How many lanes share a row: less than a warp (a power of two), a warp, or a group of warps.
-enum RowMode { kPart = 0, kWarp = 1, kGroup = 2 };
+// (kHalf is kPart with 16 lanes, known to the compiler: the offsets of a lane's elements are constants.)
+enum RowMode { kPart = 0, kWarp = 1, kGroup = 2, kHalf = 3 };
+__host__ __device__ constexpr bool shares_warp(int mode) { return mode == kPart || mode == kHalf; }
 
 // Where a thread stands: lane `lane` of the L that share row `mine` of the
 // CTA's rows; seg() of those lanes are in this warp, this is number `at` of them.
 template <int MODE>
 struct Place {
   int L, lane, mine, at;
-  __device__ __forceinline__ Place(int L_) : L(MODE == kWarp ? 32 : L_) {
+  __device__ __forceinline__ Place(int L_) : L(MODE == kWarp ? 32 : MODE == kHalf ? 16 : L_) {
     const int t = (int)threadIdx.x;
     if constexpr (MODE == kGroup) {
       mine = t / L;
@@ -93,10 +95,10 @@ struct Place {
       at = t & 31;
     } else {
       lane = at = t & (L - 1);
-      mine = MODE == kWarp ? t >> 5 : t / L;
+      mine = MODE == kWarp ? t >> 5 : MODE == kHalf ? t >> 4 : t / L;
     }
   }
-  __device__ __forceinline__ int seg() const { return MODE == kPart ? L : 32; }
+  __device__ __forceinline__ int seg() const { return MODE == kPart ? L : MODE == kHalf ? 16 : 32; }
 };
 
 // The column of a lane's element i of E. Aligned rows: vectors lane, lane + L,
@@ -106,7 +108,7 @@ template <int V, int E, bool RAGGED, int MODE>
 __device__ __forceinline__ int column(int L, int lane, int i) {
   if constexpr (!RAGGED) return (lane + i / V * L) * V + i % V;
   else if constexpr (MODE == kGroup) return (lane >> 5) * (32 * E) + (lane & 31) + i * 32;
-  else return lane + i * (MODE == kWarp ? 32 : L);
+  else return lane + i * (MODE == kWarp ? 32 : MODE == kHalf ? 16 : L);
 }
 
 // ---- parameters ------------------------------------------------------------------
@@ -247,6 +249,7 @@ struct RowFeed {
   // Bytes of a warp's slots for one tensor's rows; its ring is S x TENSORS of them.
   static __device__ __forceinline__ int plane(const Walk &w) {
     if constexpr (!RAGGED) return K * 512;
+    else if constexpr (MODE == kHalf) return (32 * K + 2) * 16;
     else if constexpr (MODE != kPart) return (32 * K + 1) * 16;
     else return w.plane;
   }
@@ -291,7 +294,7 @@ struct RowFeed {
           cp_async16_if(p.at == 0 && o < end, s + o, q + o);
         }
       }
-    } else if (!RAGGED && MODE == kPart) {  // lanes without a row take part in the warp's sums: with zeros
+    } else if (!RAGGED && shares_warp(MODE)) {  // lanes without a row take part in the warp's sums: with zeros
 #pragma unroll
       for (int i = 0; i < TENSORS * K; ++i)
         *reinterpret_cast<uint4 *>(mine + wr + i / K * plane(w) + i % K * 512) = make_uint4(0u, 0u, 0u, 0u);

@@ -24,6 +24,7 @@ constexpr int kColumnsBlock = 256;  // vector-columns of a CTA in the long rows'
 struct FwdPlan {
   RowPlan r;
   bool shortrow;  // rms_short_kernel
+  bool narrow;    // ragged rows of kRaggedElems elements a lane
   int slots;      // its vectors of a lane
   bool steal;     // rows in several warps: more of them than CTAs at a time
   int64_t grid;
@@ -46,7 +47,8 @@ FwdPlan plan_fwd(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
     p.grid = std::min<int64_t>(ceil_div(M, p.r.rows), (int64_t)1 << 30);
     return p;
   }
-  p.r = plan_rows(M, N, vec, aligned, E, sms);
+  p.narrow = !aligned && N <= 32 * dyt::norm::kRaggedElems;
+  p.r = plan_rows(M, N, vec, aligned, p.narrow ? dyt::norm::kRaggedElems : E, sms);
   p.grid = std::min<int64_t>(ceil_div(M, p.r.rows), (int64_t)sms);
   if (p.r.group && !p.r.rowlong) {  // a CTA a row (there is no room in memory for 2^31 rows of more than 512 elements)
     p.r.rows = 1;
@@ -146,7 +148,9 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
     const RowPlan &r = p.r;
     const bool ring = !p.shortrow && !r.rowlong;
     const dyt::norm::RmsFwdKernel k = dyt::norm::rms_fwd_kernel_of<T>(r, p.shortrow, res != nullptr, q8);
-    const size_t smem = ring ? dyt::norm::rms_fwd_smem<T>(r.block, r.L, r.ragged, res != nullptr) : 0;
+    constexpr int E = dyt::norm::fwd_elems<T>(), ER = dyt::norm::kRaggedElems;
+    const size_t smem = !ring ? 0 : p.narrow ? dyt::norm::rms_fwd_smem<T, ER>(r.block, r.L, true, res != nullptr)
+                                             : dyt::norm::rms_fwd_smem<T, E>(r.block, r.L, r.ragged, res != nullptr);
     const dyt_status s = prepare_smem(dev, (const void *)k, (int)smem);
     if (s != DYT_OK) return s;
     const int64_t lds[3] = {ldx, res ? ldr : ldx, ldx};  // the inputs (walk_of takes the last for an output)
@@ -169,7 +173,7 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
     a.slots = p.slots;
     a.steal = p.steal;
     a.w = walk_of(r, M, N, ring && !r.group ? p.grid : 0, lds, 3, es,
-                  ring ? dyt::norm::fwd_plane<T>(32, r.L, r.ragged) : 0);
+                  !ring ? 0 : p.narrow ? dyt::norm::row_slots<T, ER>(32, r.L, true) : dyt::norm::row_slots<T, E>(32, r.L, r.ragged));
     a.step = p.grid * r.rows;
     a.inc_y = (int64_t)a.w.step * ldy * (int64_t)(q8 ? 1 : es);
     a.inc_h = res ? (int64_t)a.w.step * ldh * (int64_t)es : 0;

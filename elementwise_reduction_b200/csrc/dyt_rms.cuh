@@ -140,7 +140,7 @@ struct Slabs {
     const int width = lanes(p);
 #pragma unroll
     for (int s = 0; s < n; ++s) top[s] = lanes_max(top[s], width);
-    if constexpr (MODE == kPart) {  // (columns of the row's first lane: a slab's group is the same for all its lanes)
+    if constexpr (shares_warp(MODE)) {  // (columns of the row's first lane: a slab's group is the same for all its lanes)
       float all[n];
 #pragma unroll
       for (int s = 0; s < n; ++s) {
@@ -158,9 +158,12 @@ struct Slabs {
 // ---- forward: a row in registers -------------------------------------------------
 
 constexpr int kRmsFwdStages = 3;
-template <typename T>
+// Elements of a row a lane holds in ragged rows of at most 32 times as many: with 32 of them and the lanes' number
+// unknown the 16-bit rows spill (100003 x 255 bf16 with a residual 92 us, with 16 49).
+constexpr int kRaggedElems = 16;
+template <typename T, int E>
 __host__ __device__ constexpr size_t rms_fwd_smem(int block, int L, bool ragged, bool res) {
-  return (size_t)kRmsFwdStages * (res ? 2 : 1) * row_slots<T, fwd_elems<T>()>(block, L, ragged) * 16;
+  return (size_t)kRmsFwdStages * (res ? 2 : 1) * row_slots<T, E>(block, L, ragged) * 16;
 }
 
 // What a CTA leaves whose wait for an answer ran out of its limit, which the hardware does not let happen: the row
@@ -176,11 +179,11 @@ __device__ __noinline__ void give_up(const RmsArgs &a, int64_t row) {
 // RES: with a residual. Q: 8-bit output with scales. Rows that take several warps: a CTA a row, several CTAs an
 // SM, and the CTAs that run take the rows of those that were not launched yet (dyt_steal.cuh): an SM gets as many rows as it has
 // time for. Ragged rows in a warp or less: a fixed share of them for every CTA.
-template <typename T, int MODE, bool RAGGED, bool RES, bool Q>
+template <typename T, int E, int MODE, bool RAGGED, bool RES, bool Q>
 __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constant__ RmsArgs a) {
   constexpr bool GROUP = MODE == kGroup;
   constexpr int V = 16 / (int)sizeof(T);
-  constexpr int E = fwd_elems<T>(), P = E / 2;
+  constexpr int P = E / 2;
   constexpr int S = kRmsFwdStages, TN = RES ? 2 : 1;
   using Slab = Slabs<T, E, RAGGED, MODE>;
   __shared__ float2 red[2][kBlock / 32];
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
   extern __shared__ __align__(16) unsigned char dyn[];
   pdl_prologue();
   const Place<MODE> p(a.w.L);
-  if (dynamic_smem_bytes() < rms_fwd_smem<T>((int)blockDim.x, p.L, RAGGED, RES)) return;
+  if (dynamic_smem_bytes() < rms_fwd_smem<T, E>((int)blockDim.x, p.L, RAGGED, RES)) return;
   const int N = (int)a.w.N;
   const T *src[TN];
   int64_t ld[TN];
@@ -681,7 +684,7 @@ __device__ __forceinline__ void rms_flush(const RmsGradArgs &a, float2 (&dg)[E /
     for (int e = 0; e < PER; ++e) {
       float u = e & 1 ? dg[(k + e) / 2].y : dg[(k + e) / 2].x;
       for (int o = p.seg(); o < 32; o <<= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-      if (MODE != kPart || ((int)threadIdx.x & 31) < p.L) sh[copy * plane + e * stride + p.lane] = u;
+      if (!shares_warp(MODE) || ((int)threadIdx.x & 31) < p.L) sh[copy * plane + e * stride + p.lane] = u;
     }
     __syncthreads();
     // neighbouring threads take neighbouring columns
@@ -744,7 +747,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
   for (int it = 0; it < steps; ++it) {
     const bool in = it < left;
     const float rstd = in ? next : 0.0f;
-    if (MODE != kPart && !in) break;  // whole warps without a row: only at the CTA's last step
+    if (!shares_warp(MODE) && !in) break;  // whole warps without a row: only at the CTA's last step
     feed.wait();
     float2 n[P], d[P];
     feed.read(0, src[0], ld[0], row, p, a.w, n);
@@ -770,7 +773,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
       group_barrier(p.mine, p.L);
       c = lanes_sum((wl & 15) < warps ? red[par][w0 + (wl & 15)] : 0.0f, 16);
     }
-    if (MODE != kPart || in) {
+    if (!shares_warp(MODE) || in) {
       c *= inv_n;
       if constexpr (RES) {
         float2 r[P];

@@ -11,8 +11,11 @@ RmsFwdKernel rms_fwd_of(const host::RowPlan &p, bool shortrow) {
   constexpr int V = 16 / (int)sizeof(T);
   if (shortrow) return rms_short_kernel<T, RES, Q>;
   if (p.rowlong) return p.V == 1 ? rms_fwd_long_kernel<T, 1, RES, Q> : rms_fwd_long_kernel<T, V, RES, Q>;
-  if (p.group) return p.ragged ? rms_fwd_kernel<T, kGroup, true, RES, Q> : rms_fwd_kernel<T, kGroup, false, RES, Q>;
-  return p.L == 32 ? rms_fwd_kernel<T, kWarp, true, RES, Q> : rms_fwd_kernel<T, kPart, true, RES, Q>;
+  constexpr int E = fwd_elems<T>(), ER = kRaggedElems;
+  if (p.group)
+    return p.ragged ? rms_fwd_kernel<T, E, kGroup, true, RES, Q> : rms_fwd_kernel<T, E, kGroup, false, RES, Q>;
+  if (p.L == 32) return p.NV > 32 * ER ? rms_fwd_kernel<T, E, kWarp, true, RES, Q> : rms_fwd_kernel<T, ER, kWarp, true, RES, Q>;
+  return p.L == 16 ? rms_fwd_kernel<T, ER, kHalf, true, RES, Q> : rms_fwd_kernel<T, ER, kPart, true, RES, Q>;
 }
 template <typename T>
 RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool shortrow, bool res, bool q8) {
@@ -24,6 +27,7 @@ template <typename T, bool RES>
 RmsBwdKernel rms_bwd_of(const host::RowPlan &p) {
   if (p.group) return p.ragged ? rms_bwd_kernel<T, kGroup, true, RES> : rms_bwd_kernel<T, kGroup, false, RES>;
   if (p.L == 32) return p.ragged ? rms_bwd_kernel<T, kWarp, true, RES> : rms_bwd_kernel<T, kWarp, false, RES>;
+  if (p.L == 16) return p.ragged ? rms_bwd_kernel<T, kHalf, true, RES> : rms_bwd_kernel<T, kHalf, false, RES>;
   return p.ragged ? rms_bwd_kernel<T, kPart, true, RES> : rms_bwd_kernel<T, kPart, false, RES>;
 }
 template <typename T>
