@@ -48,7 +48,8 @@ LogpPlan plan_logp(int64_t M, int64_t N, int top, size_t es, int sms) {
 extern "C" {
 
 size_t dyt_log_probs_workspace_bytes(int64_t M, int64_t N, int top, dyt_dtype dtype) try {
-  if (check_shape(M, N, dtype) != DYT_OK || M == 0 || N == 0 || top < 0 || top > dyt::loss::kMaxTop || top > N) return 0;
+  if (check_shape(M, N, dtype) != DYT_OK || M == 0 || N == 0) return 0;
+  if (top < 0 || top > dyt::loss::kMaxTop || top > N) return 0;
   int dev = 0, sms = 0;
   if (current_sms(&dev, &sms) != DYT_OK) return 0;
   return plan_logp(M, N, top, dsize(dtype), sms).bytes;
@@ -179,7 +180,8 @@ dyt_status dyt_log_probs_backward(const void *logits, int64_t ld, const void *to
   return with_type(dtype, [&](auto t) -> dyt_status {
     using T = decltype(t);
     PdlConfig lc((unsigned)p.grid, p.block, 0, (cudaStream_t)stream);
-    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, dyt::loss::grad_kernel<T, dyt::loss::LogpGradRow>(p.cta, shift), a);
+    const auto k = dyt::loss::grad_kernel<T, dyt::loss::LogpGradRow>(p.cta, shift);
+    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
     if (e != cudaSuccess) return cuda_fail(e);
     record(kOpLogpBackward, &p, (int)(16 / sizeof(T)), 1, 0);
     return DYT_OK;

@@ -318,7 +318,8 @@ __device__ __forceinline__ Pair<T> half_pair(const uint4 &r, int w) {
 template <typename T>
 __device__ __forceinline__ float2 largest(const uint4 &r) {
   if constexpr (sizeof(T) == 4) {
-    return make_float2(fmaxf(__uint_as_float(r.x), __uint_as_float(r.z)), fmaxf(__uint_as_float(r.y), __uint_as_float(r.w)));
+    return make_float2(fmaxf(__uint_as_float(r.x), __uint_as_float(r.z)),
+                       fmaxf(__uint_as_float(r.y), __uint_as_float(r.w)));
   } else {
     const Pair<T> m = __hmax2(__hmax2(half_pair<T>(r, 0), half_pair<T>(r, 1)),
                               __hmax2(half_pair<T>(r, 2), half_pair<T>(r, 3)));
@@ -410,7 +411,8 @@ struct RowTops {
   __device__ __forceinline__ void fetch(Best &b, int i0, int lane) const {
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (i0 + u * 32 + lane < vecs) cp_async16(&b.stage[u][lane], reinterpret_cast<const uint4 *>(tops) + i0 + u * 32 + lane);
+      if (i0 + u * 32 + lane < vecs)
+        cp_async16(&b.stage[u][lane], reinterpret_cast<const uint4 *>(tops) + i0 + u * 32 + lane);
     cp_async_commit();
     cp_async_wait<0>();
   }

@@ -130,7 +130,7 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
     return DYT_OK;
   }
   const size_t es = dsize(x_dtype);
-  if (!x || !y || (q8 && !scale) || (res && !h) || !elem_aligned(x, es) || !elem_aligned(res, es) ||
+  if (!x || !y || (q8 && !scale) || (res && (!h || h == y)) || !elem_aligned(x, es) || !elem_aligned(res, es) ||
       (!q8 && !elem_aligned(y, es)) || (res && !elem_aligned(h, es)) || !param_ok(gamma, gamma_dtype) ||
       !param_ok(rstd, DYT_F32) || !param_ok(scale, DYT_F32))
     return DYT_ERR_INVALID_VALUE;
@@ -173,7 +173,9 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
     a.slots = p.slots;
     a.steal = p.steal;
     a.w = walk_of(r, M, N, ring && !r.group ? p.grid : 0, lds, 3, es,
-                  !ring ? 0 : p.narrow ? dyt::norm::row_slots<T, ER>(32, r.L, true) : dyt::norm::row_slots<T, E>(32, r.L, r.ragged));
+                  !ring      ? 0
+                  : p.narrow ? dyt::norm::row_slots<T, ER>(32, r.L, true)
+                             : dyt::norm::row_slots<T, E>(32, r.L, r.ragged));
     a.step = p.grid * r.rows;
     a.inc_y = (int64_t)a.w.step * ldy * (int64_t)(q8 ? 1 : es);
     a.inc_h = res ? (int64_t)a.w.step * ldh * (int64_t)es : 0;

@@ -140,7 +140,7 @@ struct Slabs {
     const int width = lanes(p);
 #pragma unroll
     for (int s = 0; s < n; ++s) top[s] = lanes_max(top[s], width);
-    if constexpr (shares_warp(MODE)) {  // (columns of the row's first lane: a slab's group is the same for all its lanes)
+    if constexpr (shares_warp(MODE)) {  // (a slab's group is the same for all its lanes)
       float all[n];
 #pragma unroll
       for (int s = 0; s < n; ++s) {
@@ -177,8 +177,8 @@ __device__ __noinline__ void give_up(const RmsArgs &a, int64_t row) {
 }
 
 // RES: with a residual. Q: 8-bit output with scales. Rows that take several warps: a CTA a row, several CTAs an
-// SM, and the CTAs that run take the rows of those that were not launched yet (dyt_steal.cuh): an SM gets as many rows as it has
-// time for. Ragged rows in a warp or less: a fixed share of them for every CTA.
+// SM, and the CTAs that run take the rows of those that were not launched yet (dyt_steal.cuh): an SM gets as many
+// rows as it has time for. Ragged rows in a warp or less: a fixed share of them for every CTA.
 template <typename T, int E, int MODE, bool RAGGED, bool RES, bool Q>
 __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constant__ RmsArgs a) {
   constexpr bool GROUP = MODE == kGroup;

@@ -14,7 +14,8 @@ RmsFwdKernel rms_fwd_of(const host::RowPlan &p, bool shortrow) {
   constexpr int E = fwd_elems<T>(), ER = kRaggedElems;
   if (p.group)
     return p.ragged ? rms_fwd_kernel<T, E, kGroup, true, RES, Q> : rms_fwd_kernel<T, E, kGroup, false, RES, Q>;
-  if (p.L == 32) return p.NV > 32 * ER ? rms_fwd_kernel<T, E, kWarp, true, RES, Q> : rms_fwd_kernel<T, ER, kWarp, true, RES, Q>;
+  if (p.L == 32)
+    return p.NV > 32 * ER ? rms_fwd_kernel<T, E, kWarp, true, RES, Q> : rms_fwd_kernel<T, ER, kWarp, true, RES, Q>;
   return p.L == 16 ? rms_fwd_kernel<T, ER, kHalf, true, RES, Q> : rms_fwd_kernel<T, ER, kPart, true, RES, Q>;
 }
 template <typename T>

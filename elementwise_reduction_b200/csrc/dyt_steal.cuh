@@ -26,9 +26,10 @@ struct Steal {
     const uint32_t a = (uint32_t)__cvta_generic_to_shared(&answer);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], 16;" ::"r"(bar_at()) : "memory");
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(a),
-                 "r"(bar_at())
-                 : "memory");
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(a),
+        "r"(bar_at())
+        : "memory");
   }
   // The index of the CTA whose work is now this one's; -1: none is left (then nothing more may be asked).
   // phase: 0 for the first answer, then 1, 0, ...

@@ -16,12 +16,14 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._tensors import (_code, _current, _elsewhere, _fresh, _fresh_matrix, _fresh_rows, _like, _pitch, _scratch,
-                       _there, _vector, _workspace, row_pitch)
+from ._tensors import (_bytes, _code, _current, _elsewhere, _fresh, _fresh_matrix, _fresh_rows, _like, _pitch,
+                       _scratch, _there, _vector, _workspace, row_pitch)
 from .loss import _shape
 
 _F32 = (torch.float32,)
 _TOKEN = (torch.int64, torch.int32)
+_FORWARD, _BACKWARD = _abi.lib.dyt_log_probs_forward, _abi.lib.dyt_log_probs_backward
+_SIZE = "dyt_log_probs_workspace_bytes"
 
 
 def _top(top: int, N: int) -> None:
@@ -36,8 +38,7 @@ def log_probs_workspace(logits: torch.Tensor, top: int = 0) -> torch.Tensor:
             return log_probs_workspace(logits, top)
     M, N = _shape(logits)
     _top(top, N)
-    n = _abi.lib.dyt_log_probs_workspace_bytes(M, N, top, _code(logits, "logits"))
-    return _scratch(n, logits.device)
+    return _scratch(_bytes(_SIZE, logits.get_device(), M, N, top, _code(logits, "logits")), logits.device)
 
 
 def log_probs_forward(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0,
@@ -57,7 +58,7 @@ def log_probs_forward(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
     _top(top, N)
     ld, code, dev, rows = _pitch(logits, "logits"), _code(logits, "logits"), logits.device, logits.shape[:-1]
     if ws is None:
-        n = _abi.lib.dyt_log_probs_workspace_bytes(M, N, top, code)
+        n = _bytes(_SIZE, index, M, N, top, code)
         ws = _scratch(n, dev)
         wp = ws.data_ptr()
     else:
@@ -72,7 +73,7 @@ def log_probs_forward(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
     best = ids = None
     if top:
         best, ids = _fresh_matrix(rows, top, torch.float32, dev), _fresh_matrix(rows, top, torch.int64, dev)
-    st = _abi.lib.dyt_log_probs_forward(
+    st = _FORWARD(
         logits.data_ptr(), ld, tp, token_bytes, ignore_index, top, temperature,
         None if logp is None else logp.data_ptr(), entropy.data_ptr(), None if best is None else best.data_ptr(),
         None if ids is None else ids.data_ptr(), stats.data_ptr(), M, N, code, wp, n, _current(index))
@@ -104,7 +105,7 @@ def log_probs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, stats:
         dlogits, lddl = _fresh(logits), N
     else:
         lddl = _like(dlogits, "dlogits", logits)
-    st = _abi.lib.dyt_log_probs_backward(
+    st = _BACKWARD(
         logits.data_ptr(), ld, None if tokens is None else _vector(tokens, "tokens", M, index, _TOKEN),
         8 if tokens is None else tokens.element_size(), ignore_index, _vector(stats, "stats", 2 * M, index, _F32),
         None if entropy is None else _vector(entropy, "entropy", M, index, _F32),

@@ -13,27 +13,15 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from ._tensors import (DTYPE_CODE, _code, _current, _elsewhere, _fresh, _fresh_matrix, _fresh_rows, _like, _pitch,
-                       _scratch, _there, _vector, _workspace, row_pitch)
+from ._tensors import (DTYPE_CODE, _bytes, _code, _current, _elsewhere, _fresh, _fresh_matrix, _fresh_rows, _like,
+                       _pitch, _rows_of, _scratch, _there, _vector, _workspace, row_pitch)
 from .norm import _shape
 
 _F32 = (torch.float32,)
 _PARAM = DTYPE_CODE
+_FORWARD, _QUANTIZE = _abi.lib.dyt_rms_norm_forward, _abi.lib.dyt_rms_norm_quantize
+_BACKWARD, _SIZE = _abi.lib.dyt_rms_norm_backward, "dyt_rms_norm_backward_workspace_bytes"
 SCALE_COLUMNS = 128  # columns of a group of the 8-bit output
-
-
-def _residual(x, residual, residual_out, N):
-    """(address, pitch) of the residual and of h, and h."""
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs a residual")
-        return None, N, None, N, x
-    ldr = _like(residual, "residual", x)
-    if residual_out is None:
-        h, ldh = _fresh(x), N
-    else:
-        h, ldh = residual_out, _like(residual_out, "residual_out", x)
-    return residual.data_ptr(), ldr, h.data_ptr(), ldh, h
 
 
 def rms_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None,
@@ -48,22 +36,29 @@ def rms_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, residua
     if _elsewhere(index, stream):
         with _there(x, stream):
             return rms_norm_forward(x, gamma, residual, eps, out, residual_out, rstd)
-    M, N = _shape(x)
-    ldx, code, dev = _pitch(x, "x"), _code(x, "x"), x.device
-    gp = None if gamma is None else _vector(gamma, "gamma", N, index, _PARAM)
-    rp, ldr, hp, ldh, h = _residual(x, residual, residual_out, N)
+    M, N, ldx, code = _rows_of(x, "x")
+    gp, gd, rp, ldr, hp, ldh, h = None, code, None, N, None, N, x
+    if gamma is not None:
+        gp, gd = _vector(gamma, "gamma", N, index, _PARAM), DTYPE_CODE[gamma.dtype]
+    if residual is not None:
+        rp, ldr = residual.data_ptr(), _like(residual, "residual", x)
+        if residual_out is None:
+            h = _fresh(x)
+        else:
+            h, ldh = residual_out, _like(residual_out, "residual_out", x)
+        hp = h.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
     if out is None:
         y, ldy = _fresh(x), N
     else:
         y, ldy = out, _like(out, "out", x)
-    rows = x.shape[:-1]
     if rstd is None:
-        rstd = _fresh_rows(rows, dev)
+        rstd = _fresh_rows(x.shape[:-1], x.device)
     else:
-        _vector(rstd, "rstd", rows.numel(), index, _F32)
-    st = _abi.lib.dyt_rms_norm_forward(
-        x.data_ptr(), ldx, rp, ldr, gp, eps, y.data_ptr(), ldy, hp, ldh, rstd.data_ptr(), M, N, code,
-        code if gamma is None else DTYPE_CODE[gamma.dtype], _current(index))
+        _vector(rstd, "rstd", x.shape[:-1].numel(), index, _F32)
+    st = _FORWARD(x.data_ptr(), ldx, rp, ldr, gp, eps, y.data_ptr(), ldy, hp, ldh, rstd.data_ptr(), M, N, code, gd,
+                  _current(index))
     if st:
         _abi._check(st, "dyt_rms_norm_forward")
     if N == 0:  # no elements: no statistics, and no kernel that would write them
@@ -84,12 +79,22 @@ def rms_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, residu
     if _elsewhere(index, stream):
         with _there(x, stream):
             return rms_norm_quantize(x, gamma, residual, eps, group, out, scale, residual_out)
-    M, N = _shape(x)
     if group not in (0, SCALE_COLUMNS):
         raise ValueError(f"group must be 0 (a scale per row) or {SCALE_COLUMNS}, not {group}")
-    ldx, code, dev, rows = _pitch(x, "x"), _code(x, "x"), x.device, x.shape[:-1]
-    gp = None if gamma is None else _vector(gamma, "gamma", N, index, _PARAM)
-    rp, ldr, hp, ldh, h = _residual(x, residual, residual_out, N)
+    M, N, ldx, code = _rows_of(x, "x")
+    rows, dev = x.shape[:-1], x.device
+    gp, gd, rp, ldr, hp, ldh, h = None, code, None, N, None, N, x
+    if gamma is not None:
+        gp, gd = _vector(gamma, "gamma", N, index, _PARAM), DTYPE_CODE[gamma.dtype]
+    if residual is not None:
+        rp, ldr = residual.data_ptr(), _like(residual, "residual", x)
+        if residual_out is None:
+            h = _fresh(x)
+        else:
+            h, ldh = residual_out, _like(residual_out, "residual_out", x)
+        hp = h.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
     if out is None:
         q, ldq = _fresh_matrix(rows, N, torch.float8_e4m3fn, dev), N
     else:
@@ -102,9 +107,8 @@ def rms_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, residu
         scale = _fresh_matrix(rows, groups, torch.float32, dev) if group else _fresh_rows(rows, dev)
     else:
         _vector(scale, "scale", rows.numel() * groups, index, _F32)
-    st = _abi.lib.dyt_rms_norm_quantize(
-        x.data_ptr(), ldx, rp, ldr, gp, eps, group, q.data_ptr(), ldq, scale.data_ptr(), hp, ldh, M, N, code,
-        code if gamma is None else DTYPE_CODE[gamma.dtype], _current(index))
+    st = _QUANTIZE(x.data_ptr(), ldx, rp, ldr, gp, eps, group, q.data_ptr(), ldq, scale.data_ptr(), hp, ldh, M, N, code,
+                   gd, _current(index))
     if st:
         _abi._check(st, "dyt_rms_norm_quantize")
     if N == 0:
@@ -118,8 +122,7 @@ def rms_norm_workspace(x: torch.Tensor) -> torch.Tensor:
         with _there(x, None):
             return rms_norm_workspace(x)
     M, N = _shape(x)
-    n = _abi.lib.dyt_rms_norm_backward_workspace_bytes(M, N, _code(x, "x"))
-    return _scratch(n, x.device)
+    return _scratch(_bytes(_SIZE, x.get_device(), M, N, _code(x, "x")), x.device)
 
 
 def rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, rstd: torch.Tensor, gamma: torch.Tensor | None = None,
@@ -135,8 +138,7 @@ def rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, rstd: torch.Tensor, gam
     if _elsewhere(index, stream):
         with _there(h, stream):
             return rms_norm_backward(h, dy, rstd, gamma, dresidual, dx, dgamma, ws, frozen=frozen)
-    M, N = _shape(h)
-    ldh, code, dev = _pitch(h, "h"), _code(h, "h"), h.device
+    M, N, ldh, code = _rows_of(h, "h")
     lddy = _like(dy, "dy", h)
     rp, lddr = (None, N) if dresidual is None else (dresidual.data_ptr(), _like(dresidual, "dresidual", h))
     if dx is None:
@@ -157,12 +159,12 @@ def rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, rstd: torch.Tensor, gam
         else:
             gg = _vector(dgamma, "dgamma", N, index, (gamma.dtype,))
     if ws is None:
-        n = _abi.lib.dyt_rms_norm_backward_workspace_bytes(M, N, code)
-        ws = _scratch(n, dev)
+        n = _bytes(_SIZE, index, M, N, code)
+        ws = _scratch(n, h.device)
         wp = ws.data_ptr()
     else:
         wp, n = _workspace(ws, index), ws.numel()
-    st = _abi.lib.dyt_rms_norm_backward(
+    st = _BACKWARD(
         h.data_ptr(), ldh, dy.data_ptr(), lddy, _vector(rstd, "rstd", h.shape[:-1].numel(), index, _F32), gp, rp,
         lddr, dx.data_ptr(), lddx, gg, M, N, code, gd, wp, n, _current(index))
     if st:

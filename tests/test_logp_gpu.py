@@ -386,8 +386,8 @@ def test_module_gradients_agree_with_autograd():
     y = z.detach().double().requires_grad_()
     lp = (y / 0.8).log_softmax(-1)
     on = tokens != -100
-    want = (lp.gather(-1, tokens.clamp(min=0)[..., None])[..., 0] * ua)[on].sum() - ((lp.exp() * lp).sum(-1) * ub)[on].sum()
-    want.backward()
+    hit = lp.gather(-1, tokens.clamp(min=0)[..., None])[..., 0]
+    ((hit * ua)[on].sum() - ((lp.exp() * lp).sum(-1) * ub)[on].sum()).backward()
     assert torch.allclose(z.grad.double(), y.grad, rtol=1e-5, atol=1e-6)
     # sums: gradients of one value for all rows; one output alone; nothing used
     for use in (lambda o: o[0].sum(), lambda o: o[1].mean(), lambda o: o[0].sum() + o[1].sum()):

@@ -1,5 +1,6 @@
-"""The root-mean-square norm and the log probabilities without a GPU: the plain formulas the GPU tests compare with against autograd, and
-the entry points' refusals, which come before any CUDA call."""
+"""The root-mean-square norm and the log probabilities without a GPU: the plain formulas
+the GPU tests compare with against autograd, and the entry points' refusals, which come
+before any CUDA call."""
 from __future__ import annotations
 
 import pytest
@@ -46,11 +47,11 @@ def test_the_check_of_an_8_bit_output_finds_mistakes():
             ok(q, scale * factor)
 
 
-def rms_fwd(x=A, ldx=8, r=A, ldr=8, g=A, eps=1e-5, y=A, ldy=8, h=A, ldh=8, rstd=A, M=4, N=8, xd=0, gd=0):
+def rms_fwd(x=A, ldx=8, r=A, ldr=8, g=A, eps=1e-5, y=A, ldy=8, h=2 * A, ldh=8, rstd=A, M=4, N=8, xd=0, gd=0):
     return dyt.dyt_rms_norm_forward(x, ldx, r, ldr, g, eps, y, ldy, h, ldh, rstd, M, N, xd, gd, None)
 
 
-def rms_q8(x=A, ldx=8, r=A, ldr=8, g=A, eps=1e-5, group=0, q=A, ldq=8, s=A, h=A, ldh=8, M=4, N=8, xd=0, gd=0):
+def rms_q8(x=A, ldx=8, r=A, ldr=8, g=A, eps=1e-5, group=0, q=A, ldq=8, s=A, h=2 * A, ldh=8, M=4, N=8, xd=0, gd=0):
     return dyt.dyt_rms_norm_quantize(x, ldx, r, ldr, g, eps, group, q, ldq, s, h, ldh, M, N, xd, gd, None)
 
 
@@ -70,7 +71,7 @@ def test_norm_refusals():
             assert call(**kw) == 2, kw
         assert call(x=0, M=0) == 0 and call(x=0, N=0) == 0
         assert dyt.dyt_last_launch_info()["kernels"] == 0
-    for kw in ({"y": 0}, {"y": A + 1}, {"ldy": 7}, {"rstd": A + 2}):
+    for kw in ({"y": 0}, {"y": A + 1}, {"ldy": 7}, {"rstd": A + 2}, {"h": A}):
         assert rms_fwd(**kw) == 1, kw
     for kw in ({"q": 0}, {"ldq": 7}, {"s": 0}, {"s": A + 2}, {"group": 64}, {"group": -128}, {"group": 1}):
         assert rms_q8(**kw) == 1, kw
@@ -113,7 +114,9 @@ def test_log_probability_formulas_agree_with_autograd(T):
     dz, _ = L.backward(z.detach(), tokens, stats, ent, a, b, T)
     assert torch.allclose(dz, z.grad, rtol=1e-10, atol=1e-13)
     v, t = torch.randn(M, N, dtype=torch.float64), 1e-6
-    f = lambda y: float((L.forward(y, tokens, 0, T)[0][0] * a + L.forward(y, tokens, 0, T)[0][1] * b).sum())  # noqa: E731
+    def f(y):
+        out = L.forward(y, tokens, 0, T)[0]
+        return float((out[0] * a + out[1] * b).sum())
     slope = (f(z.detach() + t * v) - f(z.detach() - t * v)) / (2 * t)
     assert abs(slope - float((dz * v).sum())) < 1e-6
 
