@@ -55,7 +55,8 @@
  * - Every argument error is reported by a status code before anything is
  *   launched. No kernel waits on another CTA, grid or device; the only waits
  *   are hardware completion waits (a thread's own asynchronous copies, the
- *   preceding grid in the stream).
+ *   preceding grid in the stream, the hardware's answer to a CTA that asks for
+ *   more work).
  */
 #ifndef DYT_H_
 #define DYT_H_
@@ -512,8 +513,11 @@ dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *
  *   h         [M*N] x_dtype, row pitch ldh, written: the new residual stream. May
  *             alias x or residual with an equal pitch, as y may, but not y.
  *   rstd      [M] binary32, written for the backward; may be NULL
- * A row is read once and kept on the SM when N is at most 16384 (16-bit) or 8192
- * (binary32); longer rows are read twice. Ragged rows are read as there. A row
+ * The rows of several warps go to whichever CTA is free, in no fixed order; a
+ * row's bits do not depend on it. (Should the hardware leave a CTA's question for
+ * a row unanswered, the CTA's own row has NaN for y's first element, rstd or
+ * scale.) A row is read once and kept on the SM when N is at most 16384 (16-bit) or
+ * 8192 (binary32); longer rows are read twice. Ragged rows are read as there. A row
  * whose sum of squares passes binary32's range has rstd 0. M * N == 0 launches
  * nothing and writes nothing.
  */

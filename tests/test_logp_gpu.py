@@ -396,6 +396,18 @@ def test_module_gradients_agree_with_autograd():
         assert torch.isfinite(z.grad).all() and (z.grad[1, 4:] == 0).all() and (z.grad[0] != 0).any()
 
 
+def test_module_without_tokens():
+    # a sampler's view, before a token is drawn: the entropy has a gradient
+    z = torch.randn(5, 300, device="cuda", requires_grad=True)
+    logp, entropy, best, ids = dyt().LogProbs(top=2)(z)
+    assert logp is None and torch.equal(ids[:, 0], z.argmax(-1))
+    entropy.sum().backward()
+    lp = z.detach().double().requires_grad_()
+    p = lp.log_softmax(-1)
+    (-(p.exp() * p).sum()).backward()
+    assert torch.allclose(z.grad.double(), lp.grad, rtol=1e-5, atol=1e-7)
+
+
 def test_module_gradient_against_differences():
     g = torch.Generator("cuda").manual_seed(10)
     z, v = (torch.randn(8, 50, device="cuda", generator=g) for _ in range(2))

@@ -338,6 +338,57 @@ def test_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+@pytest.mark.parametrize("N,xd,pitch", [(4096, "bf16", 4096), (4100, "bf16", 4101), (1504, "f16", 1600),
+                                        (8192, "f32", 8192), (640, "f32", 640), (16384, "bf16", 16384)])
+def test_many_rows_go_to_free_ctas(N, xd, pitch):
+    # more rows than CTAs at a time, each done once: alone, beside another call, and from graphs
+    d = dyt()
+    M = 3001
+    cases = []
+    for seed in (0, 1):
+        x, r, dy, gamma = inputs(M, N, xd, seed=seed, pitch=pitch)
+        y, h, rstd = (torch.full_like(t, NAN) for t in (x.t, x.t, dy.t[:, 0].float()))
+        q = torch.full((M, N), NAN, device="cuda").to(torch.float8_e4m3fn)
+        scale = torch.full((M, -(-N // 128)), NAN, device="cuda")
+        cases.append((x, r, gamma, y, h, rstd, q, scale))
+    def step(c):
+        x, r, gamma, y, h, rstd, q, scale = c
+        d.rms_norm_forward(x.t, gamma, r.t, EPS, out=y, residual_out=h, rstd=rstd)
+        d.rms_norm_quantize(x.t, gamma, r.t, EPS, 128, out=q, scale=scale, residual_out=h)
+    def outputs(c):
+        return [t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t for t in c[3:]]
+    for c in cases:
+        step(c)
+        assert d.dyt_last_launch_info()["grid"] == M
+        want, tol = S.forward(c[0].t, c[1].t, c[2], EPS)
+        R.assert_close(c[5], want[2], tol[2], "rstd")
+        R.assert_close(c[3], want[0], tol[0] + R.half_step(c[3].dtype, want[0]), "y")
+        R.assert_close(c[4], want[1], tol[1] + R.half_step(c[3].dtype, want[1]), "h")
+        S.assert_quantized(c[6], c[7], c[0].t, c[1].t, c[2], EPS, 128)
+    want = [[t.clone() for t in outputs(c)] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    graphs = []
+    for s, c in zip(streams, cases):
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step(c)
+            step(c)
+        graphs.append(graph)
+    for c in cases:
+        for t in outputs(c):
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, c, graph in zip(streams, cases, graphs):
+            with torch.cuda.stream(s):
+                step(c)
+                graph.replay()
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert all(torch.equal(a, b) for a, b in zip(outputs(c), w))
+
+
 # ---- module ------------------------------------------------------------------------------------
 
 def test_module_gradients_agree_with_the_formula():
@@ -435,7 +486,8 @@ def test_refusals():
            lambda: d.rms_norm_forward(x, gamma, x.t()), lambda: d.rms_norm_forward(x.t()),
            lambda: d.rms_norm_forward(x, gamma, residual_out=x), lambda: d.rms_norm_forward(x, gamma, out=x[:5]),
            lambda: d.rms_norm_forward(x, eps=-1.0), lambda: d.rms_norm_forward(x, rstd=rstd[:5]),
-           lambda: d.rms_norm_forward(x, gamma, x.cpu()), lambda: d.rms_norm_quantize(x, group=64),
+           lambda: d.rms_norm_forward(x, gamma, x.cpu()),
+           lambda: d.rms_norm_forward(x, gamma, x, out=x, residual_out=x), lambda: d.rms_norm_quantize(x, group=64),
            lambda: d.rms_norm_quantize(x, out=torch.empty(6, 64, dtype=torch.uint8, device="cuda")),
            lambda: d.rms_norm_quantize(x, scale=rstd[:5]), lambda: d.rms_norm_quantize(x, group=-128),
            lambda: d.rms_norm_quantize(x, eps=NAN), lambda: d.rms_norm_backward(x, x, rstd[:5], gamma),
