@@ -23,39 +23,32 @@ constexpr int kColumnsBlock = 256;  // vector-columns of a CTA in the long rows'
 
 struct FwdPlan {
   RowPlan r;
-  bool shortrow;  // rms_short_kernel
-  bool narrow;    // ragged rows of kRaggedElems elements a lane
-  int slots;      // its vectors of a lane
-  bool steal;     // rows in several warps: more of them than CTAs at a time
+  bool narrow;    // kNarrowElems elements a lane
+  bool steal;
+  int64_t items;  // a CTA's rows of a step
   int64_t grid;
 };
 
+// Work is taken from CTAs that do not run yet where every CTA has more than kFewSteps items: the first answers cost
+// 0.3 us, fixed shares the difference between the SMs. Measured with a residual, fixed and taken: 1184 x 4096 bf16
+// (2 steps) 6.1 and 6.5 us, 2368 x 4096 14.0 and 14.1, 4736 x 4096 27.4 and 25.8, 9472 x 4096 56.1 and 48.2. Narrow
+// rows, more of a CTA's time at its ends, gain from the second step on: 9472 x 256 5.3 and 4.5, 18944 x 256 7.1 and 6.5.
+constexpr int kFewSteps = 4;
+constexpr int kNarrowCtas = 6;  // of an SM, as the registers of most of these kernels allow
+
 FwdPlan plan_fwd(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
   FwdPlan p = {};
-  p.shortrow = aligned && N / vec <= dyt::norm::kShortVectors;
-  if (p.shortrow) {
-    const int64_t vectors = N / vec;
-    p.slots = dyt::norm::kShortSlots;
-    if (M * vectors <= (int64_t)sms * 1024) p.slots = 1;  // few rows: all lanes of all rows at once
-    p.r.V = vec;
-    p.r.NV = (int)vectors;
-    const int64_t lanes = ceil_div(vectors, p.slots);
-    p.r.group = lanes > 32;
-    p.r.L = p.r.group ? (int)ceil_div(lanes, 32) * 32 : pow2_at_least(lanes);
-    p.r.rows = p.r.group ? 1 : 32 * dyt::norm::kShortWarps / p.r.L;
-    p.r.block = p.r.rows * p.r.L;
-    p.grid = std::min<int64_t>(ceil_div(M, p.r.rows), (int64_t)1 << 30);
-    return p;
-  }
-  p.narrow = !aligned && N <= 32 * dyt::norm::kRaggedElems;
-  p.r = plan_rows(M, N, vec, aligned, p.narrow ? dyt::norm::kRaggedElems : E, sms);
-  p.grid = std::min<int64_t>(ceil_div(M, p.r.rows), (int64_t)sms);
-  if (p.r.group && !p.r.rowlong) {  // a CTA a row (there is no room in memory for 2^31 rows of more than 512 elements)
-    p.r.rows = 1;
-    p.r.block = p.r.L;
-    p.grid = M;
-    p.steal = M > (int64_t)sms * (dyt::norm::kBlock / p.r.L);
-  }
+  p.narrow = N <= 32 * dyt::norm::kNarrowElems;
+  p.r = plan_rows(M, N, vec, aligned, p.narrow ? dyt::norm::kNarrowElems : E, sms);
+  p.items = M;
+  p.grid = std::min<int64_t>(M, (int64_t)sms * 2);
+  if (p.r.rowlong) return p;
+  p.r.rows = p.r.group ? 1 : dyt::norm::kNarrowBlock / p.r.L;
+  p.r.block = p.r.rows * p.r.L;
+  p.items = ceil_div(M, p.r.rows);
+  const int64_t at_once = (int64_t)sms * (p.narrow ? kNarrowCtas : dyt::norm::kBlock / p.r.block);
+  p.steal = p.items > (p.narrow ? 1 : kFewSteps) * at_once;
+  p.grid = p.steal ? p.items : std::min(p.items, at_once);
   return p;
 }
 
@@ -146,10 +139,11 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
                      (!res || (aligned16(res) && aligned16(h) && vec_pitch(ldr, es) && vec_pitch(ldh, es)));
     const FwdPlan p = plan_fwd(M, N, VE, vec, dyt::norm::fwd_elems<T>(), sms);
     const RowPlan &r = p.r;
-    const bool ring = !p.shortrow && !r.rowlong;
-    const dyt::norm::RmsFwdKernel k = dyt::norm::rms_fwd_kernel_of<T>(r, p.shortrow, res != nullptr, q8);
-    constexpr int E = dyt::norm::fwd_elems<T>(), ER = dyt::norm::kRaggedElems;
-    const size_t smem = !ring ? 0 : p.narrow ? dyt::norm::rms_fwd_smem<T, ER>(r.block, r.L, true, res != nullptr)
+    const bool ring = !r.rowlong;
+    const dyt::norm::RmsFwdKernel k = dyt::norm::rms_fwd_kernel_of<T>(r, res != nullptr, q8);
+    if (p.grid > INT32_MAX) return DYT_ERR_INVALID_VALUE;  // (more rows than any memory holds)
+    constexpr int E = dyt::norm::fwd_elems<T>(), EN = dyt::norm::kNarrowElems;
+    const size_t smem = !ring ? 0 : p.narrow ? dyt::norm::rms_fwd_smem<T, EN>(r.block, r.L, r.ragged, res != nullptr)
                                              : dyt::norm::rms_fwd_smem<T, E>(r.block, r.L, r.ragged, res != nullptr);
     const dyt_status s = prepare_smem(dev, (const void *)k, (int)smem);
     if (s != DYT_OK) return s;
@@ -170,15 +164,12 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
     a.eps = eps;
     a.grouped = group != 0;
     a.groups = group ? (int)ceil_div(N, group) : 1;
-    a.slots = p.slots;
     a.steal = p.steal;
-    a.w = walk_of(r, M, N, ring && !r.group ? p.grid : 0, lds, 3, es,
+    a.items = p.items;
+    a.w = walk_of(r, M, N, 0, lds, 3, es,
                   !ring      ? 0
-                  : p.narrow ? dyt::norm::row_slots<T, ER>(32, r.L, true)
+                  : p.narrow ? dyt::norm::row_slots<T, EN>(32, r.L, r.ragged)
                              : dyt::norm::row_slots<T, E>(32, r.L, r.ragged));
-    a.step = p.grid * r.rows;
-    a.inc_y = (int64_t)a.w.step * ldy * (int64_t)(q8 ? 1 : es);
-    a.inc_h = res ? (int64_t)a.w.step * ldh * (int64_t)es : 0;
     PdlConfig lc((unsigned)p.grid, r.block, smem, (cudaStream_t)stream);
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
     if (e != cudaSuccess) return cuda_fail(e);

@@ -7,10 +7,10 @@
 //   n_j  = h_j rstd,  g_j = gamma_j dy_j,  c = sum_j g_j n_j / N
 //   dx_j = rstd (g_j - n_j c) + dh_j,   dgamma_j = sum_i dy_ij n_ij
 //
-// Bound by memory, as layer norm is, and laid out as it: a row is read once into
-// the ring of RowFeed and kept in registers between its sum and its outputs, the
-// same columns of every row in the same lane. The norm is of the sum before it is
-// rounded to the stored residual stream, so y has one rounding. The largest |y|
+// Bound by memory, as layer norm is, and mostly laid out as it: a row is read once
+// into the ring of RowFeed and kept in registers between its sum and its outputs,
+// the same columns of every row in the same lane. The norm is of the sum before it
+// is rounded to the stored residual stream, so y has one rounding. The largest |y|
 // of a row is rstd times the largest |gamma h|, which meets the sum of squares in
 // the one exchange a row takes.
 #pragma once
@@ -39,11 +39,9 @@ struct RmsArgs {
   float eps;
   int groups;         // scales a row: 1, or one for each kScaleCols columns (grouped)
   int grouped;
-  int slots;             // short rows: vectors of a lane
-  int64_t step;          // and rows of the grid
-  int steal;             // rows in several warps: there are more of them than CTAs at a time
-  int64_t inc_y, inc_h;  // ragged rows in a warp or less: bytes from a row to the one a step later
-  Walk w;                // inc[0], inc[1]: of x and the residual there
+  int steal;          // a CTA an item, and work is taken from those that do not run yet; else a fixed share
+  int64_t items;      // a CTA's rows of a step each
+  Walk w;             // (a step is 0: rows come in no order)
 };
 
 struct RmsGradArgs {
@@ -112,10 +110,22 @@ __device__ __forceinline__ void store_bytes(unsigned char *out, const float2 (&f
     const int c0 = column<V, E, true, MODE>(p.L, p.lane, 0), left = N - c0;
     unsigned char *o = out + c0;
 #pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const uint32_t b = e4m3_pair(f[i / 2]);
-      if (feed.whole(p, i & ~7) || i * p.seg() < left) o[i * p.seg()] = (unsigned char)b;
-      if (feed.whole(p, i & ~7) || (i + 1) * p.seg() < left) o[(i + 1) * p.seg()] = (unsigned char)(b >> 8);
+    for (int g = 0; g < E; g += 8) {
+      if (feed.whole(p, g)) {
+#pragma unroll
+        for (int i = g; i < g + 8; i += 2) {
+          const uint32_t b = e4m3_pair(f[i / 2]);
+          o[i * p.seg()] = (unsigned char)b;
+          o[(i + 1) * p.seg()] = (unsigned char)(b >> 8);
+        }
+      } else {
+#pragma unroll
+        for (int i = g; i < g + 8; i += 2) {
+          const uint32_t b = e4m3_pair(f[i / 2]);
+          if (i * p.seg() < left) o[i * p.seg()] = (unsigned char)b;
+          if ((i + 1) * p.seg() < left) o[(i + 1) * p.seg()] = (unsigned char)(b >> 8);
+        }
+      }
     }
   }
 }
@@ -158,9 +168,10 @@ struct Slabs {
 // ---- forward: a row in registers -------------------------------------------------
 
 constexpr int kRmsFwdStages = 3;
-// Elements of a row a lane holds in ragged rows of at most 32 times as many: with 32 of them and the lanes' number
-// unknown the 16-bit rows spill (100003 x 255 bf16 with a residual 92 us, with 16 49).
-constexpr int kRaggedElems = 16;
+// Elements of a row a lane holds in rows of at most 32 times as many: with 32 of them and the lanes' number unknown
+// ragged 16-bit rows spill (100003 x 255 bf16 with a residual 92 us, with 16 49).
+constexpr int kNarrowElems = 16;
+constexpr int kNarrowBlock = 128;  // threads of a CTA of rows in a warp or less
 template <typename T, int E>
 __host__ __device__ constexpr size_t rms_fwd_smem(int block, int L, bool ragged, bool res) {
   return (size_t)kRmsFwdStages * (res ? 2 : 1) * row_slots<T, E>(block, L, ragged) * 16;
@@ -176,9 +187,9 @@ __device__ __noinline__ void give_up(const RmsArgs &a, int64_t row) {
   else static_cast<T *>(a.y)[row * a.ldy] = from_f32<T>(nan);
 }
 
-// RES: with a residual. Q: 8-bit output with scales. Rows that take several warps: a CTA a row, several CTAs an
-// SM, and the CTAs that run take the rows of those that were not launched yet (dyt_steal.cuh): an SM gets as many
-// rows as it has time for. Ragged rows in a warp or less: a fixed share of them for every CTA.
+// RES: with a residual. Q: 8-bit output with scales. A CTA has a row of several warps, or a few smaller ones side by
+// side; several CTAs share an SM, and those that run take the rows of those that were not launched yet
+// (dyt_steal.cuh): an SM gets as many rows as it has time for.
 template <typename T, int E, int MODE, bool RAGGED, bool RES, bool Q>
 __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constant__ RmsArgs a) {
   constexpr bool GROUP = MODE == kGroup;
@@ -201,52 +212,56 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
     src[1] = static_cast<const T *>(a.res);
     ld[1] = a.ldr;
   }
-  const int64_t r0 = (int64_t)blockIdx.x * (GROUP ? 1 : a.w.rows);
-  int64_t row = r0 + p.mine;
-  // fixed shares: the CTA's steps, this row's
-  const int steps = GROUP ? 1 : row_count(a.w.M, r0, a.w.step), left = GROUP ? 1 : row_count(a.w.M, row, a.w.step);
-  RowFeed<T, E, TN, S, RAGGED, MODE> feed(dyn, src, ld, p, a.w, row);
-  int64_t next = -1;  // groups: the row after this one, -1: none
-  uint32_t asked = 0; // and the answers taken
-  if constexpr (GROUP) {
-    static_assert(S == 3, "this row and the next one are on their way");
-    feed.issue(p, a.w, true, row);
-    if (a.steal) {
-      if (threadIdx.x == 0) queue.init();
-      __syncthreads();
-      if (threadIdx.x == 0) queue.ask();
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) feed.issue(p, a.w, i < left, row + (int64_t)i * a.w.step);
+  // Item i: rows i rows .. i rows + rows - 1. (M for the row of none.) With fixed shares the CTA's items lie a grid
+  // apart.
+  const int64_t M = a.w.M;
+  auto row_of = [&](int64_t item) {
+    const int64_t r = GROUP ? item : item * a.w.rows + p.mine;
+    return item >= 0 && r < M ? r : M;
+  };
+  int64_t item = blockIdx.x, next = -1;  // this one and the one after, -1: none
+  uint32_t asked = 0;                    // answers taken
+  RowFeed<T, E, TN, S, RAGGED, MODE> feed(dyn, src, ld, p, a.w, row_of(item));
+  static_assert(S == 3, "this row and the next one are on their way");
+  auto fetch = [&](int64_t i) {
+    const int64_t r = row_of(i);
+    feed.seek(src, ld, p, r);
+    feed.issue(p, a.w, r < M, r);
+  };
+  fetch(item);
+  if (a.steal) {
+    if (threadIdx.x == 0) queue.init();
+    __syncthreads();
+    if (threadIdx.x == 0) queue.ask();
   }
   float2 gam[P];
   load_pairs<V, E, RAGGED, MODE>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
   const float inv_n = a.w.inv_n;
   const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31;
-  char *y = static_cast<char *>(a.y) + row * a.ldy * (int64_t)(Q ? 1 : sizeof(T));
-  char *h = nullptr;
-  if constexpr (RES) h = static_cast<char *>(a.h) + row * a.ldh * (int64_t)sizeof(T);
-  // All have taken the answer, which was `got`: the next question.
+  bool lost = false;
+  auto take = [&](int64_t last) {
+    if (a.steal) return queue.take(asked++ & 1u);
+    return last + gridDim.x < a.items ? last + gridDim.x : (int64_t)-1;
+  };
+  // All have taken the answer, which was `got`: the next question. (Groups meet here in any case.)
   auto taken = [&](int64_t &got) {
+    if (!a.steal) {
+      if constexpr (GROUP) __syncthreads();
+      return;
+    }
     if (__syncthreads_or(got == Steal::kLost)) {  // (whichever thread it was: all stop asking)
-      if (threadIdx.x == 0) give_up<T, Q>(a, r0);
+      lost = true;
       got = -1;
     }
     if (got >= 0 && threadIdx.x == 0) queue.ask();
   };
-  if constexpr (GROUP) {
-    if (a.steal) {
-      next = queue.take(asked++ & 1u);
-      taken(next);
-    }
-    feed.seek(src, ld, p, next);
-    feed.issue(p, a.w, next >= 0, next);
-  }
+  next = take(item);
+  taken(next);
+  fetch(next);
 #pragma unroll 1
-  for (int it = 0; GROUP ? row >= 0 : it < steps; ++it) {
-    if (MODE == kWarp && it >= left) break;  // whole warps without a row: only at the CTA's last step
-    const bool in = GROUP || it < left;
+  for (int it = 0; item >= 0; ++it) {
+    const int64_t row = row_of(item);
+    const bool in = GROUP || row < M;  // (lanes without a row take all steps with the others)
     feed.wait();
     float2 v[P];
     feed.read(0, src[0], ld[0], row, p, a.w, v);
@@ -258,19 +273,14 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
     }
     feed.advance(a.w);
     int64_t after = -1;
-    if constexpr (GROUP) {
-      if (next >= 0) after = queue.take(asked++ & 1u);
-      feed.seek(src, ld, p, after);
-      feed.issue(p, a.w, after >= 0, after);
-    } else {
-      feed.issue(p, a.w, it + S - 1 < left, row + (int64_t)(S - 1) * a.w.step);
-    }
+    if (next >= 0) after = take(next);
+    fetch(after);
     float2 t[2] = {f2(0.0f), f2(0.0f)};  // what lies past the row's end is zero
 #pragma unroll
     for (int i = 0; i < P; ++i) t[i & 1] = fma2(v[i], v[i], t[i & 1]);
     t[0] = add2(t[0], t[1]);
     float q = t[0].x + t[0].y, top = 0.0f;
-    if (RES && in) store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(h), v, p, feed, a.w.NV, N);
+    if (RES && in) store_pairs<T, E, RAGGED>(static_cast<T *>(a.h) + row * a.ldh, v, p, feed, a.w.NV, N);
     if constexpr (Q) {
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = mul2(v[i], gam[i]);
@@ -289,6 +299,8 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
       const float2 o = (wl & 15) < warps ? red[par][wl & 15] : make_float2(0.0f, 0.0f);
       q = lanes_sum(o.x, 16);
       if (Q && !a.grouped) top = lanes_max(o.y, 16);
+    } else {
+      taken(after);
     }
     const float rstd = rsqrtf(fmaf(q, inv_n, a.eps));
     if (a.rstd && p.lane == 0 && in) a.rstd[row] = rstd;
@@ -324,194 +336,19 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
         for (int i = 0; i < P; ++i) v[i] = mul2(v[i], f2(inv));
       }
       if (in)
-        store_bytes<T, E, RAGGED>(reinterpret_cast<unsigned char *>(y), v, p, feed, a.w.NV, N);
+        store_bytes<T, E, RAGGED>(static_cast<unsigned char *>(a.y) + row * a.ldy, v, p, feed, a.w.NV, N);
     } else if (in) {
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = mul2(mul2(v[i], f2(rstd)), gam[i]);
-      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(y), v, p, feed, a.w.NV, N);
+      store_pairs<T, E, RAGGED>(static_cast<T *>(a.y) + row * a.ldy, v, p, feed, a.w.NV, N);
     }
-    if constexpr (GROUP) {
-      row = next;
-      next = after;
-      y = static_cast<char *>(a.y) + row * a.ldy * (int64_t)(Q ? 1 : sizeof(T));
-      if constexpr (RES) h = static_cast<char *>(a.h) + row * a.ldh * (int64_t)sizeof(T);
-    } else {
-      row += a.w.step;
-      y += a.inc_y;
-      if constexpr (RES) h += a.inc_h;
-    }
+    item = next;
+    next = after;
   }
   cp_async_wait<0>();
-}
-
-// ---- forward: short aligned rows ---------------------------------------------------
-
-// gamma at columns c .. c + V - 1 (1 without gamma). c is a multiple of V.
-template <int V>
-__device__ __forceinline__ void load_gamma(const void *p, int dt, int c, float (&g)[V]) {
-  if (p == nullptr) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) g[e] = 1.0f;
-  } else if (V >= 4 && ((uintptr_t)p & 15u) == 0) {
-    if (dt == DYT_F32) {
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        const float4 q = static_cast<const float4 *>(p)[c / 4 + i];
-        g[4 * i] = q.x;
-        g[4 * i + 1] = q.y;
-        g[4 * i + 2] = q.z;
-        g[4 * i + 3] = q.w;
-      }
-    } else {
-      uint2 q[V / 4 > 0 ? V / 4 : 1];
-#pragma unroll
-      for (int i = 0; i < V / 4; ++i) q[i] = static_cast<const uint2 *>(p)[c / 4 + i];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const uint32_t w = e & 2 ? q[e / 4].y : q[e / 4].x, u = e & 1 ? w >> 16 : w & 0xFFFFu;
-        g[e] = dt == DYT_BF16 ? __uint_as_float(u << 16) : __half2float(__ushort_as_half((unsigned short)u));
-      }
-    }
-  } else {
-    int64_t col[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) col[e] = c + e;
-    params_at<V>(p, dt, col, g);
-  }
-}
-
-// A row takes L lanes: a power of two of them up to a warp, several rows side by side in a CTA of kShortWarps
-// warps, or two or more warps and a CTA to itself. A lane holds up to a.slots vectors; 32 lanes (seg, with fewer) hold
-// consecutive vectors of the row's stretch of 32 V slots columns, so that the columns of a scale lie in one warp.
-constexpr int kShortWarps = 4;
-constexpr int kShortSlots = 2;
-constexpr int kShortVectors = 128;  // of a row, at most: 1024 elements of 16 bits, 512 of binary32
-constexpr int kShortBlock = kShortVectors;
-
-// RES: with a residual. Q: 8-bit output with scales. A row a CTA (or a few), one wave of CTAs after the other, and
-// nothing but registers: many rows are on an SM at once. Measured with a residual, in the ring of the kernel above
-// and here: 65536 x 1024 bf16 92.1 and 87.1 us, 65536 x 512 47.9 and 44.8, 131072 x 64 17.7 and 12.8; wider rows
-// lose, as fewer fit on an SM (16384 x 8192 to 8 bits 163 and 222), and so do rows taken by elements (100003 x 255
-// fp32 38.9 and 55.6).
-template <typename T, bool RES, bool Q>
-__global__ void __launch_bounds__(kShortBlock) rms_short_kernel(RmsArgs a) {
-  constexpr int V = 16 / (int)sizeof(T), P = V / 2, NS = kShortSlots;
-  using IO = VecIO<T, V>;
-  __shared__ float2 red[2][kShortBlock / 32];
-  pdl_prologue();
-  const int L = a.w.L, seg = L < 32 ? L : 32;
-  const int mine = L > 32 ? 0 : (int)threadIdx.x / L, lane = (int)threadIdx.x - mine * L;
-  const int c0 = ((lane / seg) * (seg * a.slots) + lane % seg) * V;  // the first slot's column; the next is seg V on
-  // vectors of this lane
-  const int n = c0 < (int)a.w.N ? min(a.slots, ((int)a.w.N - V - c0) / (seg * V) + 1) : 0;
-  float2 g[NS][P];
-#pragma unroll
-  for (int k = 0; k < NS; ++k) {
-    float f[V] = {};
-    if (k < n) load_gamma<V>(a.gamma, a.gamma_dt, c0 + k * seg * V, f);
-#pragma unroll
-    for (int i = 0; i < P; ++i) g[k][i] = make_float2(f[2 * i], f[2 * i + 1]);
-  }
-  int par = 0;
-  for (int64_t row = (int64_t)blockIdx.x * a.w.rows + mine; row - mine < a.w.M; row += a.step, par ^= 1) {
-    const bool in = row < a.w.M;  // (lanes without a row take part in the sums)
-    const int m = in ? n : 0;
-    float2 v[NS][P];
-    {
-      uint4 x[NS] = {}, r[RES ? NS : 1] = {};
-      const T *px = static_cast<const T *>(a.x) + row * a.ldx;
-      const T *pr = static_cast<const T *>(a.res) + (RES ? row * a.ldr : 0);
-#pragma unroll
-      for (int k = 0; k < NS; ++k) {
-        if (k < m) {
-          x[k] = load_row<T, V>(px + c0 + k * seg * V);
-          if constexpr (RES) r[k] = load_row<T, V>(pr + c0 + k * seg * V);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < NS; ++k) {
-        IO::unpack2(x[k], v[k]);
-        if constexpr (RES) {
-          float2 f[P];
-          IO::unpack2(r[k], f);
-#pragma unroll
-          for (int i = 0; i < P; ++i) v[k][i] = add2(v[k][i], f[i]);
-        }
-      }
-    }
-    float2 t = f2(0.0f);
-#pragma unroll
-    for (int k = 0; k < NS; ++k)
-#pragma unroll
-      for (int i = 0; i < P; ++i) t = fma2(v[k][i], v[k][i], t);
-    float q = t.x + t.y, tops[NS] = {};
-    if constexpr (RES) {
-      T *h = static_cast<T *>(a.h) + row * a.ldh;
-#pragma unroll
-      for (int k = 0; k < NS; ++k)
-        if (k < m) st16(h + c0 + k * seg * V, IO::pack2(v[k]));
-    }
-    const int width = V == 8 && seg > kScaleCols / 8 ? kScaleCols / 8 : seg;  // lanes of a scale's columns
-    float top = 0.0f;
-    if constexpr (Q) {  // the largest of gamma h in a row, or in a vector's group
-#pragma unroll
-      for (int k = 0; k < NS; ++k) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          v[k][i] = mul2(v[k][i], g[k][i]);
-          tops[k] = max_nan(tops[k], max_nan(fabsf(v[k][i].x), fabsf(v[k][i].y)));
-        }
-        if (a.grouped) tops[k] = lanes_max(tops[k], width);
-        top = max_nan(top, tops[k]);
-      }
-      if (!a.grouped) top = lanes_max(top, seg);
-    }
-    q = lanes_sum(q, seg);
-    if (L > 32) {
-      const int wl = (int)threadIdx.x & 31;
-      if (wl == 0) red[par][threadIdx.x >> 5] = make_float2(q, top);
-      __syncthreads();
-      const float2 o = wl < L / 32 ? red[par][wl] : make_float2(0.0f, 0.0f);
-      q = lanes_sum(o.x, kShortBlock / 32);
-      if (Q && !a.grouped) top = lanes_max(o.y, kShortBlock / 32);
-      q = __shfl_sync(0xFFFFFFFFu, q, 0);
-      top = __shfl_sync(0xFFFFFFFFu, top, 0);
-    }
-    const float rstd = rsqrtf(fmaf(q, a.w.inv_n, a.eps));
-    if (a.rstd && lane == 0 && in) a.rstd[row] = rstd;
-    if constexpr (!Q) {
-      T *y = static_cast<T *>(a.y) + row * a.ldy;
-#pragma unroll
-      for (int k = 0; k < NS; ++k) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[k][i] = mul2(mul2(v[k][i], f2(rstd)), g[k][i]);
-        if (k < m) st16(y + c0 + k * seg * V, IO::pack2(v[k]));
-      }
-    } else {
-      auto group = [&](int k) { return (c0 + k * seg * V) / kScaleCols; };
-      if (a.grouped && seg * V < kScaleCols) {  // several vectors of one group
-        static_assert(NS == 2, "one other");
-        if (group(0) == group(1)) tops[0] = tops[1] = max_nan(tops[0], tops[1]);
-      }
-      unsigned char *y = static_cast<unsigned char *>(a.y) + row * a.ldy;
-#pragma unroll
-      for (int k = 0; k < NS; ++k) {
-        // the largest |y|: rounding keeps the order
-        const float most = max_nan((a.grouped ? tops[k] : top) * rstd, kLeastTop);
-        // (several vectors of one group write the same value)
-        if (in && (a.grouped ? k < a.slots && group(k) < a.groups && (lane & (width - 1)) == 0 : k == 0 && lane == 0))
-          a.scale[row * a.groups + (a.grouped ? group(k) : 0)] = most * (1.0f / kQMax);
-        const float inv = kQMax / most;
-        float f[V];
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float2 o = mul2(mul2(v[k][i], f2(rstd)), f2(inv));
-          f[2 * i] = o.x;
-          f[2 * i + 1] = o.y;
-        }
-        if (k < m) store_e4m3<V>(y + c0 + k * seg * V, f);
-      }
-    }
+  if (lost) {
+    __syncthreads();  // behind what the CTA wrote of the row
+    if (threadIdx.x == 0) give_up<T, Q>(a, (int64_t)blockIdx.x * (GROUP ? 1 : a.w.rows));
   }
 }
 

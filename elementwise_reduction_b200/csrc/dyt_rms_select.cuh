@@ -15,9 +15,8 @@ using RmsBwdLongKernel = void (*)(RmsGradArgs, float *);
 using RmsBwdColumnsKernel = void (*)(RmsGradArgs, const float *);
 
 // res: with a residual (in the backward: the stored sum has a gradient). q8: an 8-bit output.
-// shortrow: aligned rows of at most kShortVectors vectors.
 template <typename T>
-RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool shortrow, bool res, bool q8);
+RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool res, bool q8);
 // Rows in registers.
 template <typename T>
 RmsBwdKernel rms_bwd_kernel_of(const host::RowPlan &p, bool res);

@@ -6,22 +6,24 @@
 namespace dyt {
 namespace norm {
 
-template <typename T, bool RES, bool Q>
-RmsFwdKernel rms_fwd_of(const host::RowPlan &p, bool shortrow) {
-  constexpr int V = 16 / (int)sizeof(T);
-  if (shortrow) return rms_short_kernel<T, RES, Q>;
-  if (p.rowlong) return p.V == 1 ? rms_fwd_long_kernel<T, 1, RES, Q> : rms_fwd_long_kernel<T, V, RES, Q>;
-  constexpr int E = fwd_elems<T>(), ER = kRaggedElems;
-  if (p.group)
-    return p.ragged ? rms_fwd_kernel<T, E, kGroup, true, RES, Q> : rms_fwd_kernel<T, E, kGroup, false, RES, Q>;
+template <typename T, bool RAGGED, bool RES, bool Q>
+RmsFwdKernel rms_fwd_ring_of(const host::RowPlan &p) {
+  constexpr int E = fwd_elems<T>(), EN = kNarrowElems;
+  if (p.group) return rms_fwd_kernel<T, E, kGroup, RAGGED, RES, Q>;
   if (p.L == 32)
-    return p.NV > 32 * ER ? rms_fwd_kernel<T, E, kWarp, true, RES, Q> : rms_fwd_kernel<T, ER, kWarp, true, RES, Q>;
-  return p.L == 16 ? rms_fwd_kernel<T, ER, kHalf, true, RES, Q> : rms_fwd_kernel<T, ER, kPart, true, RES, Q>;
+    return p.NV * p.V > 32 * EN ? rms_fwd_kernel<T, E, kWarp, RAGGED, RES, Q> : rms_fwd_kernel<T, EN, kWarp, RAGGED, RES, Q>;
+  return p.L == 16 ? rms_fwd_kernel<T, EN, kHalf, RAGGED, RES, Q> : rms_fwd_kernel<T, EN, kPart, RAGGED, RES, Q>;
+}
+template <typename T, bool RES, bool Q>
+RmsFwdKernel rms_fwd_of(const host::RowPlan &p) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (p.rowlong) return p.V == 1 ? rms_fwd_long_kernel<T, 1, RES, Q> : rms_fwd_long_kernel<T, V, RES, Q>;
+  return p.ragged ? rms_fwd_ring_of<T, true, RES, Q>(p) : rms_fwd_ring_of<T, false, RES, Q>(p);
 }
 template <typename T>
-RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool shortrow, bool res, bool q8) {
-  if (q8) return res ? rms_fwd_of<T, true, true>(p, shortrow) : rms_fwd_of<T, false, true>(p, shortrow);
-  return res ? rms_fwd_of<T, true, false>(p, shortrow) : rms_fwd_of<T, false, false>(p, shortrow);
+RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool res, bool q8) {
+  if (q8) return res ? rms_fwd_of<T, true, true>(p) : rms_fwd_of<T, false, true>(p);
+  return res ? rms_fwd_of<T, true, false>(p) : rms_fwd_of<T, false, false>(p);
 }
 
 template <typename T, bool RES>
@@ -47,7 +49,7 @@ RmsBwdColumnsKernel rms_bwd_columns_kernel_of(const host::RowPlan &p, bool res) 
 }
 
 #define DYT_INSTANTIATE_RMS(T)                                                            \
-  template RmsFwdKernel rms_fwd_kernel_of<T>(const host::RowPlan &, bool, bool, bool);     \
+  template RmsFwdKernel rms_fwd_kernel_of<T>(const host::RowPlan &, bool, bool);           \
   template RmsBwdKernel rms_bwd_kernel_of<T>(const host::RowPlan &, bool);                 \
   template RmsBwdLongKernel rms_bwd_rows_kernel_of<T>(const host::RowPlan &);              \
   template RmsBwdColumnsKernel rms_bwd_columns_kernel_of<T>(const host::RowPlan &, bool);

@@ -343,7 +343,7 @@ def test_streams_and_graphs():
 def test_many_rows_go_to_free_ctas(N, xd, pitch):
     # more rows than CTAs at a time, each done once: alone, beside another call, and from graphs
     d = dyt()
-    M = 3001
+    M = 5003 if N > 640 else 9001
     cases = []
     for seed in (0, 1):
         x, r, dy, gamma = inputs(M, N, xd, seed=seed, pitch=pitch)
