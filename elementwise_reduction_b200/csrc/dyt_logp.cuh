@@ -99,10 +99,88 @@ __device__ __forceinline__ Moments join(Moments a, Moments b, float C) {
   return a;
 }
 
-// 2 n values more; returns the largest. NaN passes over the maximum and reaches the sums. FAR: exponents
-// are kept from -inf; else a second sum that such a one has made NaN is left out, and false returned for it.
-template <bool FAR, int n>
-__device__ __forceinline__ float add_values(Moments &r, const float2 (&v)[n], float C, bool *done = nullptr) {
+template <typename T>
+using Pair = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+template <typename T>
+__device__ __forceinline__ Pair<T> half_pair(const uint4 &r, int w) {
+  const uint32_t word = word_of(r, w);
+  return *reinterpret_cast<const Pair<T> *>(&word);
+}
+// The largest of 16 bytes of logits, the even and the odd elements apart (x, y); a NaN passes over.
+template <typename T>
+__device__ __forceinline__ float2 largest(const uint4 &r) {
+  if constexpr (sizeof(T) == 4) {
+    return make_float2(fmaxf(__uint_as_float(r.x), __uint_as_float(r.z)),
+                       fmaxf(__uint_as_float(r.y), __uint_as_float(r.w)));
+  } else {
+    const Pair<T> m = __hmax2(__hmax2(half_pair<T>(r, 0), half_pair<T>(r, 1)),
+                              __hmax2(half_pair<T>(r, 2), half_pair<T>(r, 3)));
+    return make_float2(to_f32<T>(m.x), to_f32<T>(m.y));
+  }
+}
+// Pair i of 16 bytes of logits plus c, each rounded once to binary32. (16-bit logits are added as they are.)
+template <typename T>
+__device__ __forceinline__ float2 plus(const uint4 &r, int i, float c) {
+  if constexpr (sizeof(T) == 4) {
+    return add2(make_float2(__uint_as_float(word_of(r, 2 * i)), __uint_as_float(word_of(r, 2 * i + 1))), f2(c));
+  } else {
+    float2 d;
+    if constexpr (std::is_same<T, __half>::value)
+      asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; add.f32.f16 %0, l, %3; add.f32.f16 %1, h, %3;}"
+          : "=f"(d.x), "=f"(d.y)
+          : "r"(word_of(r, i)), "f"(c));
+    else
+      asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; add.f32.bf16 %0, l, %3; add.f32.bf16 %1, h, %3;}"
+          : "=f"(d.x), "=f"(d.y)
+          : "r"(word_of(r, i)), "f"(c));
+    return d;
+  }
+}
+
+// A whole batch; `top` is its largest logit. NaN passes over the maximum and reaches the sums. Exponents are not looked at:
+// the second sum is NaN where one of them was -inf. Nothing is added then, and false returned.
+template <typename T>
+__device__ __forceinline__ bool add_batch(Moments &r, const uint4 (&raw)[kBatch], float C, float &top) {
+  constexpr int P = 8 / (int)sizeof(T);  // pairs of 16 bytes
+  if constexpr (sizeof(T) == 4) {
+    float x[2] = {kNegInf, kNegInf};
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      x[0] = max3(x[0], __uint_as_float(raw[u].x), __uint_as_float(raw[u].y));
+      x[1] = max3(x[1], __uint_as_float(raw[u].z), __uint_as_float(raw[u].w));
+    }
+    top = fmaxf(x[0], x[1]);
+  } else {
+    Pair<T> x[2] = {half_pair<T>(raw[0], 0), half_pair<T>(raw[0], 1)};
+#pragma unroll
+    for (int i = 2; i < 4 * kBatch; ++i) x[i & 1] = __hmax2(x[i & 1], half_pair<T>(raw[i / 4], i % 4));
+    x[0] = __hmax2(x[0], x[1]);
+    top = max3(to_f32<T>(x[0].x), to_f32<T>(x[0].y), kNegInf);
+  }
+  if (top > r.m) raise(r, top, C);
+  const float m = r.m == kNegInf ? 0.0f : r.m;  // only -inf so far
+  float2 s[2] = {f2(0.0f), f2(0.0f)}, t[2] = {f2(0.0f), f2(0.0f)};
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float2 e = mul2(plus<T>(raw[u], i, -m), f2(C));
+      const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+      s[i & 1] = add2(s[i & 1], p);
+      t[i & 1] = fma2(p, e, t[i & 1]);
+    }
+  s[0] = add2(s[0], s[1]);
+  t[0] = add2(t[0], t[1]);
+  const float more = t[0].x + t[0].y;
+  if (more != more) return false;
+  r.s += s[0].x + s[0].y;
+  r.t += more;
+  return true;
+}
+
+// 2 n values more, every exponent kept from -inf; returns the largest.
+template <int n>
+__device__ __forceinline__ float add_values(Moments &r, const float2 (&v)[n], float C) {
   float x[2] = {fmaxf(v[0].x, v[0].y), kNegInf};
 #pragma unroll
   for (int i = 1; i < n; ++i) x[i & 1] = max3(x[i & 1], v[i].x, v[i].y);
@@ -113,20 +191,15 @@ __device__ __forceinline__ float add_values(Moments &r, const float2 (&v)[n], fl
 #pragma unroll
   for (int i = 0; i < n; ++i) {
     float2 e = mul2(add2(v[i], f2(-m)), f2(C));
-    if constexpr (FAR) e = make_float2(max_nan(e.x, kFar), max_nan(e.y, kFar));
+    e = make_float2(max_nan(e.x, kFar), max_nan(e.y, kFar));
     const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
     s[i & 1] = add2(s[i & 1], p);
     t[i & 1] = fma2(p, e, t[i & 1]);
   }
   s[0] = add2(s[0], s[1]);
   t[0] = add2(t[0], t[1]);
-  const float more = t[0].x + t[0].y;
-  if constexpr (!FAR) {
-    *done = more == more;
-    if (!*done) return top;
-  }
   r.s += s[0].x + s[0].y;
-  r.t += more;
+  r.t += t[0].x + t[0].y;
   return top;
 }
 
@@ -232,26 +305,22 @@ __global__ void __launch_bounds__(kRowsBlock, 2) logp_rows_kernel(LogpArgs a) {
         const int here = rd;
         rd = rd == (kStages - 1) * kBatch * 32 ? 0 : rd + kBatch * 32;
         issue();
-        float2 v[kBatch * P];
         float top;
         bool done = false;
-        if (n >= kBatch * 32) {
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) IO::unpack2(raw[u], *reinterpret_cast<float2(*)[P]>(v + u * P));
-          top = add_values<false>(r, v, C, &done);
-        }
+        if (n >= kBatch * 32) done = add_batch<T>(r, raw, C, top);
         // Batches with infinite exponents (masked logits) are taken once more, and those that end a row at once,
-        // with a look at every exponent: one instruction more an element. Their slots are not filled again before
-        // the next batch.
+        // a vector at a time with a look at every exponent. Their slots are not filled again before the next batch.
         if (!done) {
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            IO::unpack2(ring[here + u * 32], *reinterpret_cast<float2(*)[P]>(v + u * P));
+          top = kNegInf;
+#pragma unroll 1
+          for (int u = 0; u * 32 < n && u < kBatch; ++u) {
+            float2 v[P];
+            IO::unpack2(ring[here + u * 32], v);
             if (u * 32 + lane >= n)
 #pragma unroll
-              for (int i = 0; i < P; ++i) v[u * P + i] = f2(kNegInf);
+              for (int i = 0; i < P; ++i) v[i] = f2(kNegInf);
+            top = fmaxf(top, add_values(r, v, C));
           }
-          top = add_values<true>(r, v, C);
         }
         if constexpr (TOP) {
           if (n > 0) *tops = from_f32<T>(top);  // (a part of no vectors has no chunks)
@@ -261,7 +330,7 @@ __global__ void __launch_bounds__(kRowsBlock, 2) logp_rows_kernel(LogpArgs a) {
       } while (n > 0);
       if (!a.aligned) {
         const float2 p[1] = {make_float2(first, last)};
-        add_values<true>(r, p, C);
+        add_values(r, p, C);
       }
       // one instruction for the largest, and the two sums by halves of the warp: a lane of each half has one
       raise(r, warp_largest(r.m), C);
@@ -307,25 +376,6 @@ struct __align__(16) Best {
   int chunks[kChunks];
 };
 
-template <typename T>
-using Pair = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-template <typename T>
-__device__ __forceinline__ Pair<T> half_pair(const uint4 &r, int w) {
-  const uint32_t word = word_of(r, w);
-  return *reinterpret_cast<const Pair<T> *>(&word);
-}
-// The largest of 16 bytes of logits, the even and the odd elements apart (x, y); a NaN passes over.
-template <typename T>
-__device__ __forceinline__ float2 largest(const uint4 &r) {
-  if constexpr (sizeof(T) == 4) {
-    return make_float2(fmaxf(__uint_as_float(r.x), __uint_as_float(r.z)),
-                       fmaxf(__uint_as_float(r.y), __uint_as_float(r.w)));
-  } else {
-    const Pair<T> m = __hmax2(__hmax2(half_pair<T>(r, 0), half_pair<T>(r, 1)),
-                              __hmax2(half_pair<T>(r, 2), half_pair<T>(r, 3)));
-    return make_float2(to_f32<T>(m.x), to_f32<T>(m.y));
-  }
-}
 // A bit for each of 16 bytes of logits that is not below v, a value of T (NaN is).
 template <typename T>
 __device__ __forceinline__ uint32_t not_below(const uint4 &r, float v) {
