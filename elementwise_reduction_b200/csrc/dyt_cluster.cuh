@@ -1,0 +1,89 @@
+// A thread-block cluster whose CTAs share a row: each has a stretch of its columns, and what their warps found of
+// it meets in all CTAs' shared memory at the cluster's barrier.
+#pragma once
+
+#include <cstdint>
+
+namespace dyt {
+
+constexpr int kMaxCluster = 4;  // CTAs
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster; what each wrote before, anywhere in the cluster, is there for the others behind it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Where a row's sums of all the cluster's warps meet: each warp sends its own to every CTA (st.async) and waits for all
+// of them at its CTA's mbarrier. Rows take turns between two places; a warp is at most one row ahead of another, as it
+// has the other's sums of the row before. In shared memory, for V = float or float2.
+template <typename V>
+struct Meet {
+  static constexpr int kWarps = 16;        // of a CTA, at most
+  static constexpr int kPolls = 1 << 20;   // of a wait, each waits for a while itself
+  V of[2][kMaxCluster * kWarps];           // (0 where there is no warp)
+  unsigned long long bar[2];
+
+  // All threads of the cluster, once.
+  __device__ __forceinline__ void init() {
+    for (int i = threadIdx.x; i < 2 * kMaxCluster * kWarps; i += blockDim.x) of[0][i] = V{};
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 2; ++i) {
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_at(i)) : "memory");
+        expect(i);
+      }
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    cluster_sync();
+  }
+  // The warp's v (the same in all its lanes) of row `it`.
+  __device__ __forceinline__ void put(int it, V v) {
+    const uint32_t cta = threadIdx.x & 31;
+    if (cta >= cluster_ctas()) return;
+    const int par = it & 1;
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(&of[par][cluster_rank() * kWarps + threadIdx.x / 32]);
+    if constexpr (sizeof(V) == 8)
+      asm volatile(
+          "{.reg .u32 r, m; mapa.shared::cluster.u32 r, %0, %2; mapa.shared::cluster.u32 m, %1, %2;"
+          "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [r], {%3, %4}, [m];}" ::"r"(at),
+          "r"(bar_at(par)), "r"(cta), "f"(v.x), "f"(v.y)
+          : "memory");
+    else
+      asm volatile(
+          "{.reg .u32 r, m; mapa.shared::cluster.u32 r, %0, %2; mapa.shared::cluster.u32 m, %1, %2;"
+          "st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [r], %3, [m];}" ::"r"(at),
+          "r"(bar_at(par)), "r"(cta), "f"(v)
+          : "memory");
+  }
+  // All of row `it` is in of[it & 1]; false: not within the limit.
+  __device__ __forceinline__ bool wait(int it) {
+    const int par = it & 1;
+    uint32_t done = 0;
+    for (int i = 0; i < kPolls && !done; ++i)
+      asm volatile(
+          "{.reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
+          : "=r"(done)
+          : "r"(bar_at(par)), "r"((uint32_t)it >> 1 & 1u)
+          : "memory");
+    if (threadIdx.x == 0) expect(par);
+    return done != 0;
+  }
+
+ private:
+  __device__ __forceinline__ uint32_t bar_at(int i) const { return (uint32_t)__cvta_generic_to_shared(&bar[i]); }
+  __device__ __forceinline__ void expect(int i) const {
+    const uint32_t bytes = cluster_ctas() * (blockDim.x / 32) * (uint32_t)sizeof(V);
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar_at(i)), "r"(bytes) : "memory");
+  }
+};
+
+}  // namespace dyt

@@ -23,6 +23,9 @@ void record_info(const dyt_launch_info &i);
 dyt_status current_sms(int *dev_out, int *sms_out);
 // CTAs of `block` threads of a kernel without dynamic shared memory that fit on an SM (cached).
 dyt_status occupancy(int dev, const void *kernel, int block, int *ctas);
+// Clusters of the launch's kernel that run at once (cached by kernel, block and cluster; its shared memory follows
+// from them).
+dyt_status cluster_capacity(int dev, const void *kernel, const cudaLaunchConfig_t &cfg, int ctas, int *clusters);
 // Opt a kernel in to at least `bytes` of dynamic shared memory, once per device and size; safe from any thread.
 dyt_status prepare_smem(int dev, const void *kernel, int bytes);
 
@@ -46,7 +49,7 @@ inline bool vec_pitch(int64_t ld, size_t elem) { return ((uint64_t)ld * elem) % 
 // predecessor in the stream drains; its first instruction waits
 // (griddepcontrol.wait) for that predecessor, so stream order holds.
 struct PdlConfig {
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg;
   PdlConfig(unsigned grid, unsigned block, size_t smem, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -58,6 +61,13 @@ struct PdlConfig {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+  }
+  // CTAs of a cluster, along the grid.
+  void cluster(unsigned ctas) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   }
 };
 

@@ -78,8 +78,9 @@ constexpr int kRunRows = 128;
 constexpr int kMaxWarps = 32;
 
 // How many lanes share a row: less than a warp (a power of two), a warp, or a group of warps.
-// (kHalf is kPart with 16 lanes, known to the compiler: the offsets of a lane's elements are constants.)
-enum RowMode { kPart = 0, kWarp = 1, kGroup = 2, kHalf = 3 };
+// (kHalf is kPart with 16 lanes, known to the compiler: the offsets of a lane's elements are constants. kCluster: all
+// of a CTA's warps share its part of a row, whose other parts are the other CTAs' of its cluster; aligned rows only.)
+enum RowMode { kPart = 0, kWarp = 1, kGroup = 2, kHalf = 3, kCluster = 4 };
 __host__ __device__ constexpr bool shares_warp(int mode) { return mode == kPart || mode == kHalf; }
 
 // Where a thread stands: lane `lane` of the L that share row `mine` of the
@@ -89,7 +90,11 @@ struct Place {
   int L, lane, mine, at;
   __device__ __forceinline__ Place(int L_) : L(MODE == kWarp ? 32 : MODE == kHalf ? 16 : L_) {
     const int t = (int)threadIdx.x;
-    if constexpr (MODE == kGroup) {
+    if constexpr (MODE == kCluster) {
+      mine = 0;
+      lane = t;
+      at = t & 31;
+    } else if constexpr (MODE == kGroup) {
       mine = t / L;
       lane = t - mine * L;
       at = t & 31;

@@ -17,6 +17,7 @@ using namespace dyt::host;
 using namespace dyt::norm::host;
 using dyt::norm::RmsArgs;
 using dyt::norm::RmsGradArgs;
+using dyt::norm::Walk;
 
 constexpr int kOpRmsForward = 9, kOpRmsQuantize = 10, kOpRmsBackward = 11;  // dyt_launch_info::op
 constexpr int kColumnsBlock = 256;  // vector-columns of a CTA in the long rows' second pass
@@ -36,13 +37,28 @@ struct FwdPlan {
 constexpr int kFewSteps = 4;
 constexpr int kNarrowCtas = 6;  // of an SM, as the registers of most of these kernels allow
 
+// Aligned rows too long for one CTA's registers are shared by a cluster: 2 CTAs, or 4.
+void plan_cluster(RowPlan &p, int64_t N, int vec, int E) {
+  if (!p.rowlong || p.V == 1) return;
+  const int64_t per = (int64_t)dyt::norm::kBlock * E;
+  const int c = N <= 2 * per ? 2 : dyt::kMaxCluster;
+  if (N > c * per) return;
+  p.rowlong = false;
+  p.group = true;
+  p.cluster = c;
+  p.L = p.block = (int)ceil_div(ceil_div(N, c), 32 * E) * 32;
+  p.cols = (int)ceil_div(ceil_div(N, c), 32 * vec) * 32 * vec;
+  p.rows = 1;
+}
+
 FwdPlan plan_fwd(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
   FwdPlan p = {};
   p.narrow = N <= 32 * dyt::norm::kNarrowElems;
   p.r = plan_rows(M, N, vec, aligned, p.narrow ? dyt::norm::kNarrowElems : E, sms);
+  plan_cluster(p.r, N, vec, E);
   p.items = M;
-  p.grid = std::min<int64_t>(M, (int64_t)sms * 2);
-  if (p.r.rowlong) return p;
+  p.grid = std::min<int64_t>(M, (int64_t)sms * 2);  // (long rows)
+  if (p.r.rowlong || p.r.cluster) return p;
   p.r.rows = p.r.group ? 1 : dyt::norm::kNarrowBlock / p.r.L;
   p.r.block = p.r.rows * p.r.L;
   p.items = ceil_div(M, p.r.rows);
@@ -55,7 +71,8 @@ FwdPlan plan_fwd(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
 // A plan for few rows spreads them over the SMs: no more rows side by side than every SM gets.
 RowPlan plan_rms(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
   RowPlan p = plan_rows(M, N, vec, aligned, E, sms);
-  if (!p.group || p.rowlong) return p;
+  plan_cluster(p, N, vec, E);
+  if (!p.group || p.rowlong || p.cluster) return p;
   p.rows = (int)std::max<int64_t>(1, std::min<int64_t>(p.rows, ceil_div(M, sms)));
   p.block = p.rows * p.L;
   return p;
@@ -77,7 +94,8 @@ BwdPlan plan_bwd(int64_t M, int64_t N, int vec, bool aligned, int sms) {
     b.col_ctas = (int)ceil_div(b.r.NV, kColumnsBlock);
     b.parts = std::max<int64_t>(1, std::min<int64_t>(M, (int64_t)sms * 4 / b.col_ctas));
   } else {
-    b.grid = std::min<int64_t>(ceil_div(M, b.r.rows), (int64_t)sms);
+    // (of clusters at most as many: the launch knows how many fit)
+    b.grid = std::min<int64_t>(ceil_div(M, b.r.rows), (int64_t)(b.r.cluster ? sms / b.r.cluster : sms));
     b.parts = b.grid;
   }
   b.off_c = ((size_t)b.parts * (size_t)N * sizeof(double) + 15) & ~(size_t)15;
@@ -98,12 +116,25 @@ void record(int op, const RowPlan *p, int64_t grid, int kernels, int64_t groups,
     i.grid = (int)grid;
     i.row_lanes = p->rows;
     i.rows_per_step = p->rows;
-    i.col_chunks = 1;
+    i.col_chunks = p->cluster ? p->cluster : 1;
     i.row_groups = (int)groups;
     i.pack_rows = 1;
     i.shifted = p->ragged && !p->rowlong;
   }
   record_info(i);
+}
+
+// The launch of as many of a plan's clusters as there are rows, or as run at once.
+dyt_status fit_clusters(int dev, const void *kernel, const RowPlan &r, int64_t M, int sms, PdlConfig &lc,
+                        int64_t *clusters) {
+  int n = 0;
+  lc.cluster((unsigned)r.cluster);
+  lc.cfg.gridDim.x = (unsigned)r.cluster;  // (the question is of whole clusters)
+  const dyt_status st = cluster_capacity(dev, kernel, lc.cfg, r.cluster, &n);
+  if (st != DYT_OK) return st;
+  *clusters = std::min<int64_t>(M, std::min(n, sms / r.cluster));
+  lc.cfg.gridDim.x = (unsigned)(*clusters * r.cluster);
+  return DYT_OK;
 }
 
 // Both forward calls. q8: y is e4m3 bytes with scales, one a row (group 0) or one for each kScaleCols columns.
@@ -145,7 +176,7 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
     constexpr int E = dyt::norm::fwd_elems<T>(), EN = dyt::norm::kNarrowElems;
     const size_t smem = !ring ? 0 : p.narrow ? dyt::norm::rms_fwd_smem<T, EN>(r.block, r.L, r.ragged, res != nullptr)
                                              : dyt::norm::rms_fwd_smem<T, E>(r.block, r.L, r.ragged, res != nullptr);
-    const dyt_status s = prepare_smem(dev, (const void *)k, (int)smem);
+    dyt_status s = prepare_smem(dev, (const void *)k, (int)smem);
     if (s != DYT_OK) return s;
     const int64_t lds[3] = {ldx, res ? ldr : ldx, ldx};  // the inputs (walk_of takes the last for an output)
     RmsArgs a = {};
@@ -170,10 +201,16 @@ dyt_status forward(bool q8, const void *x, int64_t ldx, const void *res, int64_t
                   !ring      ? 0
                   : p.narrow ? dyt::norm::row_slots<T, EN>(32, r.L, r.ragged)
                              : dyt::norm::row_slots<T, E>(32, r.L, r.ragged));
+    a.cols = r.cols;
     PdlConfig lc((unsigned)p.grid, r.block, smem, (cudaStream_t)stream);
+    if (r.cluster) {
+      int64_t clusters = 0;
+      s = fit_clusters(dev, (const void *)k, r, M, sms, lc, &clusters);
+      if (s != DYT_OK) return s;
+    }
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, k, a);
     if (e != cudaSuccess) return cuda_fail(e);
-    record(op, &r, p.grid, 1, 0, 0);
+    record(op, &r, lc.cfg.gridDim.x, 1, 0, 0);
     return DYT_OK;
   });
 }
@@ -266,6 +303,7 @@ dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int
                   b.r.rowlong ? 0 : dyt::norm::row_slots<T, dyt::norm::kBwdElems>(32, b.r.L, b.r.ragged));
     a.inc_dx = a.w.inc[3];
     int kernels = 1;
+    int64_t parts_used = b.parts, ctas = b.grid;
     cudaError_t e;
     if (b.r.rowlong) {
       float *c = (float *)((char *)workspace + b.off_c);
@@ -282,17 +320,27 @@ dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int
       const dyt_status ready = prepare_smem(dev, (const void *)k, (int)smem);
       if (ready != DYT_OK) return ready;
       PdlConfig lc((unsigned)b.grid, b.r.block, smem, s);
+      a.cols = b.r.cols;
+      if (b.r.cluster) {
+        const dyt_status fit = fit_clusters(dev, (const void *)k, b.r, M, sms, lc, &parts_used);
+        if (fit != DYT_OK) return fit;
+        const Walk w = walk_of(b.r, M, N, parts_used, lds, 4, es, 0);
+        a.w.step = w.step;
+        for (int i = 0; i < 4; ++i) a.w.inc[i] = w.inc[i];
+        a.inc_dx = w.inc[3];
+      }
+      ctas = (int64_t)lc.cfg.gridDim.x;
       e = cudaLaunchKernelEx(&lc.cfg, k, a);
     }
     if (e != cudaSuccess) return cuda_fail(e);
     if (dgamma) {
       PdlConfig lf((unsigned)ceil_div(N, dyt::norm::kSumCols), dyt::norm::kSumCols * dyt::norm::kSumLanes, 0, s);
-      e = cudaLaunchKernelEx(&lf.cfg, dyt::norm::norm_finalize_kernel<1>, (const double *)parts, (int)b.parts, N,
+      e = cudaLaunchKernelEx(&lf.cfg, dyt::norm::norm_finalize_kernel<1>, (const double *)parts, (int)parts_used, N,
                              dgamma, (int)gamma_dtype, (void *)nullptr, (int)gamma_dtype);
       if (e != cudaSuccess) return cuda_fail(e);
       ++kernels;
     }
-    record(kOpRmsBackward, &b.r, b.grid, kernels, b.parts, b.bytes);
+    record(kOpRmsBackward, &b.r, ctas, kernels, parts_used, b.bytes);
     return DYT_OK;
   });
 } catch (...) {

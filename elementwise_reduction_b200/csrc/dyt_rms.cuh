@@ -17,6 +17,7 @@
 
 #include <type_traits>
 
+#include "dyt_cluster.cuh"
 #include "dyt_norm.cuh"
 #include "dyt_steal.cuh"
 
@@ -41,6 +42,7 @@ struct RmsArgs {
   int grouped;
   int steal;          // a CTA an item, and work is taken from those that do not run yet; else a fixed share
   int64_t items;      // a CTA's rows of a step each
+  int cols;           // kCluster: columns of a CTA, whole warps' vectors
   Walk w;             // (a step is 0: rows come in no order)
 };
 
@@ -58,6 +60,7 @@ struct RmsGradArgs {
   double *parts;      // [CTA][N] column sums
   int gamma_dt;
   int64_t inc_dx;
+  int cols;           // kCluster: columns of a CTA
   Walk w;             // inc[0 .. 2]: of h, dy and dres
 };
 
@@ -68,6 +71,28 @@ constexpr float kLeastTop = 0x1p-100f;  // a row of zeros has a scale all the sa
 __device__ __forceinline__ float lanes_max(float v, int width) {
   for (int o = width >> 1; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
+}
+
+// A CTA's place among those that share its rows (one, but for kCluster): its number of them and its stretch's first
+// column; `unit` counts the clusters, or the CTAs.
+template <int MODE>
+struct Share {
+  static __device__ __forceinline__ uint32_t rank() { return MODE == kCluster ? cluster_rank() : 0; }
+  static __device__ __forceinline__ uint32_t ctas() { return MODE == kCluster ? cluster_ctas() : 1; }
+  static __device__ __forceinline__ uint32_t unit() { return MODE == kCluster ? blockIdx.x / cluster_ctas() : blockIdx.x; }
+  static __device__ __forceinline__ uint32_t units() { return MODE == kCluster ? gridDim.x / cluster_ctas() : gridDim.x; }
+  static __device__ __forceinline__ int first(int cols) { return MODE == kCluster ? (int)cluster_rank() * cols : 0; }
+};
+// The walk over a CTA's stretch of the rows' columns.
+template <int MODE>
+using ShareWalk = std::conditional_t<MODE == kCluster, Walk, const Walk &>;
+__device__ __forceinline__ void cut(Walk &w, int first, int cols, int vec) {
+  const int left = (int)w.N - first;
+  w.N = left < cols ? left : cols;
+  w.NV = (int)w.N / vec;
+}
+__device__ __forceinline__ const void *param_from(const void *p, int dt, int first) {
+  return p ? static_cast<const char *>(p) + (int64_t)first * (dt == DYT_F32 ? 4 : 2) : p;
 }
 
 // Two values rounded to e4m3 (nearest even, at most 448; NaN stays): a in the low byte.
@@ -192,61 +217,70 @@ __device__ __noinline__ void give_up(const RmsArgs &a, int64_t row) {
 // (dyt_steal.cuh): an SM gets as many rows as it has time for.
 template <typename T, int E, int MODE, bool RAGGED, bool RES, bool Q>
 __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constant__ RmsArgs a) {
-  constexpr bool GROUP = MODE == kGroup;
+  constexpr bool CLUSTER = MODE == kCluster, GROUP = MODE == kGroup || CLUSTER;
+  using Mine = Share<MODE>;
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int P = E / 2;
   constexpr int S = kRmsFwdStages, TN = RES ? 2 : 1;
   using Slab = Slabs<T, E, RAGGED, MODE>;
-  __shared__ float2 red[2][kBlock / 32];
+  __shared__ std::conditional_t<CLUSTER, Meet<float2>, float2[2][kBlock / 32]> red;
   __shared__ Steal queue;
   extern __shared__ __align__(16) unsigned char dyn[];
   pdl_prologue();
   const Place<MODE> p(a.w.L);
   if (dynamic_smem_bytes() < rms_fwd_smem<T, E>((int)blockDim.x, p.L, RAGGED, RES)) return;
-  const int N = (int)a.w.N;
+  const int col0 = Mine::first(a.cols);
+  ShareWalk<MODE> w = a.w;
+  if constexpr (CLUSTER) {
+    cut(w, col0, a.cols, V);
+    red.init();
+  }
+  const bool steal = !CLUSTER && a.steal;
+  const int groups = CLUSTER ? ((int)w.N + kScaleCols - 1) / kScaleCols : a.groups;  // of the CTA's stretch
+  const int N = (int)w.N;
   const T *src[TN];
   int64_t ld[TN];
-  src[0] = static_cast<const T *>(a.x);
+  src[0] = static_cast<const T *>(a.x) + col0;
   ld[0] = a.ldx;
   if constexpr (RES) {
-    src[1] = static_cast<const T *>(a.res);
+    src[1] = static_cast<const T *>(a.res) + col0;
     ld[1] = a.ldr;
   }
   // Item i: rows i rows .. i rows + rows - 1. (M for the row of none.) With fixed shares the CTA's items lie a grid
   // apart.
-  const int64_t M = a.w.M;
+  const int64_t M = w.M;
   auto row_of = [&](int64_t item) {
-    const int64_t r = GROUP ? item : item * a.w.rows + p.mine;
+    const int64_t r = GROUP ? item : item * w.rows + p.mine;
     return item >= 0 && r < M ? r : M;
   };
-  int64_t item = blockIdx.x, next = -1;  // this one and the one after, -1: none
+  int64_t item = Mine::unit(), next = -1;  // this one and the one after, -1: none
   uint32_t asked = 0;                    // answers taken
-  RowFeed<T, E, TN, S, RAGGED, MODE> feed(dyn, src, ld, p, a.w, row_of(item));
+  RowFeed<T, E, TN, S, RAGGED, MODE> feed(dyn, src, ld, p, w, row_of(item));
   static_assert(S == 3, "this row and the next one are on their way");
   auto fetch = [&](int64_t i) {
     const int64_t r = row_of(i);
     feed.seek(src, ld, p, r);
-    feed.issue(p, a.w, r < M, r);
+    feed.issue(p, w, r < M, r);
   };
   fetch(item);
-  if (a.steal) {
+  if (steal) {
     if (threadIdx.x == 0) queue.init();
     __syncthreads();
     if (threadIdx.x == 0) queue.ask();
   }
   float2 gam[P];
-  load_pairs<V, E, RAGGED, MODE>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
-  const float inv_n = a.w.inv_n;
+  load_pairs<V, E, RAGGED, MODE>(param_from(a.gamma, a.gamma_dt, col0), a.gamma_dt, p, N, 1.0f, gam);
+  const float inv_n = w.inv_n;
   const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31;
   bool lost = false;
   auto take = [&](int64_t last) {
-    if (a.steal) return queue.take(asked++ & 1u);
-    return last + gridDim.x < a.items ? last + gridDim.x : (int64_t)-1;
+    if (steal) return queue.take(asked++ & 1u);
+    return last + Mine::units() < a.items ? last + Mine::units() : (int64_t)-1;
   };
   // All have taken the answer, which was `got`: the next question. (Groups meet here in any case.)
   auto taken = [&](int64_t &got) {
-    if (!a.steal) {
-      if constexpr (GROUP) __syncthreads();
+    if (!steal) {
+      if constexpr (MODE == kGroup) __syncthreads();
       return;
     }
     if (__syncthreads_or(got == Steal::kLost)) {  // (whichever thread it was: all stop asking)
@@ -264,14 +298,14 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
     const bool in = GROUP || row < M;  // (lanes without a row take all steps with the others)
     feed.wait();
     float2 v[P];
-    feed.read(0, src[0], ld[0], row, p, a.w, v);
+    feed.read(0, src[0], ld[0], row, p, w, v);
     if constexpr (RES) {
       float2 r[P];
-      feed.read(1, src[1], ld[1], row, p, a.w, r);
+      feed.read(1, src[1], ld[1], row, p, w, r);
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = add2(v[i], r[i]);
     }
-    feed.advance(a.w);
+    feed.advance(w);
     int64_t after = -1;
     if (next >= 0) after = take(next);
     fetch(after);
@@ -280,7 +314,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
     for (int i = 0; i < P; ++i) t[i & 1] = fma2(v[i], v[i], t[i & 1]);
     t[0] = add2(t[0], t[1]);
     float q = t[0].x + t[0].y, top = 0.0f;
-    if (RES && in) store_pairs<T, E, RAGGED>(static_cast<T *>(a.h) + row * a.ldh, v, p, feed, a.w.NV, N);
+    if (RES && in) store_pairs<T, E, RAGGED>(static_cast<T *>(a.h) + row * a.ldh + col0, v, p, feed, w.NV, N);
     if constexpr (Q) {
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = mul2(v[i], gam[i]);
@@ -293,17 +327,26 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
     if (Q && !a.grouped) top = lanes_max(top, p.seg());
     if constexpr (GROUP) {
       const int par = it & 1;
-      if (wl == 0) red[par][p.lane / 32] = make_float2(q, top);
-      taken(after);
-      // up to 16 warps, one a lane of each half
-      const float2 o = (wl & 15) < warps ? red[par][wl & 15] : make_float2(0.0f, 0.0f);
-      q = lanes_sum(o.x, 16);
-      if (Q && !a.grouped) top = lanes_max(o.y, 16);
+      if constexpr (CLUSTER) {
+        const float nan = __int_as_float(0x7FC00000);
+        red.put(it, make_float2(lost ? nan : q, top));
+        if (!lost) lost = !red.wait(it);
+        const float2 o = red.of[par][wl], u = red.of[par][wl + 32];
+        q = lost ? nan : warp_sum(o.x + u.x);
+        if (Q && !a.grouped) top = lanes_max(max_nan(o.y, u.y), 32);
+      } else {
+        if (wl == 0) red[par][p.lane / 32] = make_float2(q, top);
+        taken(after);
+        // up to 16 warps, one a lane of each half
+        const float2 o = (wl & 15) < warps ? red[par][wl & 15] : make_float2(0.0f, 0.0f);
+        q = lanes_sum(o.x, 16);
+        if (Q && !a.grouped) top = lanes_max(o.y, 16);
+      }
     } else {
       taken(after);
     }
     const float rstd = rsqrtf(fmaf(q, inv_n, a.eps));
-    if (a.rstd && p.lane == 0 && in) a.rstd[row] = rstd;
+    if (a.rstd && p.lane == 0 && in && Mine::rank() == 0) a.rstd[row] = rstd;
     if constexpr (Q) {
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = mul2(v[i], f2(rstd));
@@ -322,33 +365,35 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
           tops[s] = max_nan(tops[s], kLeastTop);
           const int g = Slab::group(p, s);
           // (rows in less than a warp: several slabs may write the same value)
-          if (in && g < a.groups && (p.lane & (Slab::lanes(p) - 1)) == 0)
-            a.scale[row * a.groups + g] = tops[s] * (1.0f / kQMax);
+          if (in && g < groups && (p.lane & (Slab::lanes(p) - 1)) == 0)
+            a.scale[row * a.groups + col0 / kScaleCols + g] = tops[s] * (1.0f / kQMax);
           const float inv = kQMax / tops[s];
 #pragma unroll
           for (int i = s * Slab::W / 2; i < (s + 1) * Slab::W / 2; ++i) v[i] = mul2(v[i], f2(inv));
         }
       } else {
         top = max_nan(top * rstd, kLeastTop);  // the largest |v|: rounding keeps the order
-        if (p.lane == 0 && in) a.scale[row] = top * (1.0f / kQMax);
+        if (p.lane == 0 && in && Mine::rank() == 0) a.scale[row] = top * (1.0f / kQMax);
         const float inv = kQMax / top;
 #pragma unroll
         for (int i = 0; i < P; ++i) v[i] = mul2(v[i], f2(inv));
       }
       if (in)
-        store_bytes<T, E, RAGGED>(static_cast<unsigned char *>(a.y) + row * a.ldy, v, p, feed, a.w.NV, N);
+        store_bytes<T, E, RAGGED>(static_cast<unsigned char *>(a.y) + row * a.ldy + col0, v, p, feed, w.NV, N);
     } else if (in) {
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = mul2(mul2(v[i], f2(rstd)), gam[i]);
-      store_pairs<T, E, RAGGED>(static_cast<T *>(a.y) + row * a.ldy, v, p, feed, a.w.NV, N);
+      store_pairs<T, E, RAGGED>(static_cast<T *>(a.y) + row * a.ldy + col0, v, p, feed, w.NV, N);
     }
     item = next;
     next = after;
   }
   cp_async_wait<0>();
-  if (lost) {
+  if constexpr (CLUSTER) {
+    cluster_sync();  // a CTA ends behind what the others send it
+  } else if (lost) {
     __syncthreads();  // behind what the CTA wrote of the row
-    if (threadIdx.x == 0) give_up<T, Q>(a, (int64_t)blockIdx.x * (GROUP ? 1 : a.w.rows));
+    if (threadIdx.x == 0) give_up<T, Q>(a, (int64_t)blockIdx.x * (GROUP ? 1 : w.rows));
   }
 }
 
@@ -495,14 +540,14 @@ static_assert(rms_bwd_ring<__half>(32, 32, false, false) >= rms_sums_smem(32, 32
               "the last column sums take the ring's place");
 
 // flush_columns for one sum a column: a run's sums of the CTA's rows, added in a fixed order and moved to
-// its partial sums in binary64.
+// the partial sums pg in binary64.
 template <int V, int E, int PER, bool RAGGED, int MODE>
-__device__ __forceinline__ void rms_flush(const RmsGradArgs &a, float2 (&dg)[E / 2], const Place<MODE> &p, bool first,
+__device__ __forceinline__ void rms_flush(double *pg, const Walk &w, float2 (&dg)[E / 2], const Place<MODE> &p, bool first,
                                           float *sh) {
-  double *pg = a.parts + (int64_t)blockIdx.x * a.w.N;
-  const int N = (int)a.w.N;
-  const int copies = MODE != kGroup ? (int)blockDim.x / 32 : a.w.rows;
-  const int copy = MODE != kGroup ? (int)threadIdx.x >> 5 : p.mine;
+  constexpr bool GROUP = MODE == kGroup || MODE == kCluster;
+  const int N = (int)w.N;
+  const int copies = !GROUP ? (int)blockDim.x / 32 : w.rows;
+  const int copy = !GROUP ? (int)threadIdx.x >> 5 : p.mine;
   const int stride = p.L + kSumPad, plane = PER * stride;
   auto add = [&](int e, int lane, int c) {
     if (c >= N) return;
@@ -526,7 +571,7 @@ __device__ __forceinline__ void rms_flush(const RmsGradArgs &a, float2 (&dg)[E /
     __syncthreads();
     // neighbouring threads take neighbouring columns
     if constexpr (RAGGED) {
-      for (int e = p.mine; e < PER; e += a.w.rows) add(e, p.lane, column<V, E, true, MODE>(p.L, p.lane, k + e));
+      for (int e = p.mine; e < PER; e += w.rows) add(e, p.lane, column<V, E, true, MODE>(p.L, p.lane, k + e));
     } else {
 #pragma unroll
       for (int v = 0; v < PER; v += V)
@@ -541,44 +586,52 @@ __device__ __forceinline__ void rms_flush(const RmsGradArgs &a, float2 (&dg)[E /
 // RES: the stored sum has a gradient of its own, read after the row's sum.
 template <typename T, int MODE, bool RAGGED, bool RES>
 __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
-  constexpr bool GROUP = MODE == kGroup;
+  constexpr bool CLUSTER = MODE == kCluster, GROUP = MODE == kGroup || CLUSTER;
+  using Mine = Share<MODE>;
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int E = kBwdElems, P = E / 2;
   constexpr int S = rms_bwd_stages<T>(), TN = RES ? 3 : 2;
-  __shared__ float red[2][kBlock / 32];
+  __shared__ std::conditional_t<CLUSTER, Meet<float>, float[2][kBlock / 32]> red;
   extern __shared__ __align__(16) unsigned char dyn[];
   pdl_prologue();
   const Place<MODE> p(a.w.L);
   if (dynamic_smem_bytes() < rms_bwd_smem<T>((int)blockDim.x, p.L, RAGGED, RES)) return;
   float *sh = reinterpret_cast<float *>(dyn + rms_bwd_ring<T>((int)blockDim.x, p.L, RAGGED, RES));
-  const int N = (int)a.w.N;
+  const int col0 = Mine::first(a.cols);
+  double *const parts = a.parts + Mine::unit() * a.w.N + col0;
+  ShareWalk<MODE> w = a.w;
+  if constexpr (CLUSTER) {
+    cut(w, col0, a.cols, V);
+    red.init();
+  }
+  const int N = (int)w.N;
   const T *src[TN];
   int64_t ld[TN];
-  src[0] = static_cast<const T *>(a.h);
+  src[0] = static_cast<const T *>(a.h) + col0;
   ld[0] = a.ldh;
-  src[1] = static_cast<const T *>(a.dy);
+  src[1] = static_cast<const T *>(a.dy) + col0;
   ld[1] = a.lddy;
   if constexpr (RES) {
-    src[2] = static_cast<const T *>(a.dres);
+    src[2] = static_cast<const T *>(a.dres) + col0;
     ld[2] = a.lddr;
   }
-  const int64_t r0 = (int64_t)blockIdx.x * a.w.rows;
+  const int64_t r0 = (int64_t)Mine::unit() * w.rows;
   int64_t row = r0 + p.mine;
-  const int steps = row_count(a.w.M, r0, a.w.step), left = row_count(a.w.M, row, a.w.step);  // the CTA's, this row's
-  RowFeed<T, E, TN, S, RAGGED, MODE> feed(dyn, src, ld, p, a.w, row);
+  const int steps = row_count(w.M, r0, w.step), left = row_count(w.M, row, w.step);  // the CTA's, this row's
+  RowFeed<T, E, TN, S, RAGGED, MODE> feed(dyn, src, ld, p, w, row);
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) feed.issue(p, a.w, i < left, row + (int64_t)i * a.w.step);
+  for (int i = 0; i < S - 1; ++i) feed.issue(p, w, i < left, row + (int64_t)i * w.step);
   // The next row's factor, loaded one row ahead; past its last row a lane stays at that row (at M - 1 if it has none).
-  int64_t stat = left > 0 ? row : a.w.M - 1;
+  int64_t stat = left > 0 ? row : w.M - 1;
   float next = a.rstd[stat];
   float2 gam[P], dg[P];
-  load_pairs<V, E, RAGGED, MODE>(a.gamma, a.gamma_dt, p, N, 1.0f, gam);
+  load_pairs<V, E, RAGGED, MODE>(param_from(a.gamma, a.gamma_dt, col0), a.gamma_dt, p, N, 1.0f, gam);
 #pragma unroll
   for (int i = 0; i < P; ++i) dg[i] = f2(0.0f);
-  const float inv_n = a.w.inv_n;
+  const float inv_n = w.inv_n;
   const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31, w0 = GROUP ? p.mine * warps : 0;
-  char *out = reinterpret_cast<char *>(static_cast<T *>(a.dx) + row * a.lddx);
-  bool first = true;
+  char *out = reinterpret_cast<char *>(static_cast<T *>(a.dx) + row * a.lddx + col0);
+  bool first = true, lost = false;  // (lost: the others' sums did not come, which the hardware does not let happen)
   int run = 0;
 #pragma unroll 1
   for (int it = 0; it < steps; ++it) {
@@ -587,10 +640,10 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
     if (!shares_warp(MODE) && !in) break;  // whole warps without a row: only at the CTA's last step
     feed.wait();
     float2 n[P], d[P];
-    feed.read(0, src[0], ld[0], row, p, a.w, n);
-    feed.read(1, src[1], ld[1], row, p, a.w, d);
-    feed.issue(p, a.w, it + S - 1 < left, row + (int64_t)(S - 1) * a.w.step);
-    if (it + 1 < left) stat += a.w.step;
+    feed.read(0, src[0], ld[0], row, p, w, n);
+    feed.read(1, src[1], ld[1], row, p, w, d);
+    feed.issue(p, w, it + S - 1 < left, row + (int64_t)(S - 1) * w.step);
+    if (it + 1 < left) stat += w.step;
     next = a.rstd[stat];
     // Past the row's end n, d and gamma are 0: nothing there enters a sum that is used.
     float2 s[2] = {f2(0.0f), f2(0.0f)};
@@ -606,28 +659,35 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
     c = GROUP ? warp_sum(c) : lanes_sum(c, p.L);
     if constexpr (GROUP) {
       const int par = it & 1;
-      if (wl == 0) red[par][w0 + p.lane / 32] = c;
-      group_barrier(p.mine, p.L);
-      c = lanes_sum((wl & 15) < warps ? red[par][w0 + (wl & 15)] : 0.0f, 16);
+      if constexpr (CLUSTER) {
+        const float nan = __int_as_float(0x7FC00000);
+        red.put(it, lost ? nan : c);
+        if (!lost) lost = !red.wait(it);
+        c = lost ? nan : warp_sum(red.of[par][wl] + red.of[par][wl + 32]);
+      } else {
+        if (wl == 0) red[par][w0 + p.lane / 32] = c;
+        group_barrier(p.mine, p.L);
+        c = lanes_sum((wl & 15) < warps ? red[par][w0 + (wl & 15)] : 0.0f, 16);
+      }
     }
     if (!shares_warp(MODE) || in) {
       c *= inv_n;
       if constexpr (RES) {
         float2 r[P];
-        feed.read(2, src[2], ld[2], row, p, a.w, r);
+        feed.read(2, src[2], ld[2], row, p, w, r);
 #pragma unroll
         for (int i = 0; i < P; ++i) d[i] = fma2(f2(rstd), fma2(n[i], f2(-c), d[i]), r[i]);
       } else {
 #pragma unroll
         for (int i = 0; i < P; ++i) d[i] = mul2(f2(rstd), fma2(n[i], f2(-c), d[i]));
       }
-      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), d, p, feed, a.w.NV, N);
+      store_pairs<T, E, RAGGED>(reinterpret_cast<T *>(out), d, p, feed, w.NV, N);
     }
-    feed.advance(a.w);
-    row += a.w.step;
+    feed.advance(w);
+    row += w.step;
     out += a.inc_dx;
     if (++run == kRunRows && it + 1 < steps) {
-      rms_flush<V, E, V, RAGGED>(a, dg, p, first, sh);
+      rms_flush<V, E, V, RAGGED>(parts, w, dg, p, first, sh);
       first = false;
       run = 0;
     }
@@ -636,7 +696,8 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
   // CTA is here, also one that left at the last step.
   cp_async_wait<0>();
   __syncthreads();
-  rms_flush<V, E, E, RAGGED>(a, dg, p, first, reinterpret_cast<float *>(dyn));
+  rms_flush<V, E, E, RAGGED>(parts, w, dg, p, first, reinterpret_cast<float *>(dyn));
+  if constexpr (CLUSTER) cluster_sync();  // a CTA ends behind what the others send it
 }
 
 // ---- backward: rows too long for registers ---------------------------------------

@@ -22,6 +22,8 @@ struct RowPlan {
   bool group = false;    // a row takes several warps
   bool ragged = false;   // rows off 16-byte boundaries, or of no whole vectors
   bool rowlong = false;  // too long for a CTA's registers
+  int cluster = 0;       // CTAs that share a row in their registers
+  int cols = 0;          // columns of each
 };
 
 inline int pow2_at_least(int64_t v) {
