@@ -28,29 +28,28 @@ __device__ __forceinline__ void cluster_sync() {
 // has the other's sums of the row before. In shared memory, for V = float or float2.
 template <typename V>
 struct Meet {
-  static constexpr int kWarps = 16;        // of a CTA, at most
-  static constexpr int kPolls = 1 << 20;   // of a wait, each waits for a while itself
-  V of[2][kMaxCluster * kWarps];           // (0 where there is no warp)
+  static constexpr int kWarps = 16 * kMaxCluster;  // of a row, at most
+  static constexpr int kPolls = 1 << 20;           // of a wait, each waits for a while itself
+  V of[2][kWarps];                         // (0 where there is no warp)
   unsigned long long bar[2];
 
-  // All threads of the cluster, once.
-  __device__ __forceinline__ void init() {
-    for (int i = threadIdx.x; i < 2 * kMaxCluster * kWarps; i += blockDim.x) of[0][i] = V{};
-    if (threadIdx.x == 0) {
+  // Lane `lane` of the CTA's L; before any put all threads of the cluster meet.
+  __device__ __forceinline__ void init(int lane, int L) {
+    for (int i = lane; i < 2 * kWarps; i += L) of[0][i] = V{};
+    if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_at(i)) : "memory");
-        expect(i);
+        expect(i, L);
       }
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    cluster_sync();
   }
-  // The warp's v (the same in all its lanes) of row `it`.
-  __device__ __forceinline__ void put(int it, V v) {
-    const uint32_t cta = threadIdx.x & 31;
+  // The warp's v (the same in all its lanes) of the CTA's row number `it`.
+  __device__ __forceinline__ void put(int it, V v, int lane, int L) {
+    const uint32_t cta = lane & 31;
     if (cta >= cluster_ctas()) return;
     const int par = it & 1;
-    const uint32_t at = (uint32_t)__cvta_generic_to_shared(&of[par][cluster_rank() * kWarps + threadIdx.x / 32]);
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(&of[par][((int)cluster_rank() * L + lane) / 32]);
     if constexpr (sizeof(V) == 8)
       asm volatile(
           "{.reg .u32 r, m; mapa.shared::cluster.u32 r, %0, %2; mapa.shared::cluster.u32 m, %1, %2;"
@@ -65,7 +64,7 @@ struct Meet {
           : "memory");
   }
   // All of row `it` is in of[it & 1]; false: not within the limit.
-  __device__ __forceinline__ bool wait(int it) {
+  __device__ __forceinline__ bool wait(int it, int lane, int L) {
     const int par = it & 1;
     uint32_t done = 0;
     for (int i = 0; i < kPolls && !done; ++i)
@@ -74,14 +73,14 @@ struct Meet {
           : "=r"(done)
           : "r"(bar_at(par)), "r"((uint32_t)it >> 1 & 1u)
           : "memory");
-    if (threadIdx.x == 0) expect(par);
+    if (lane == 0) expect(par, L);
     return done != 0;
   }
 
  private:
   __device__ __forceinline__ uint32_t bar_at(int i) const { return (uint32_t)__cvta_generic_to_shared(&bar[i]); }
-  __device__ __forceinline__ void expect(int i) const {
-    const uint32_t bytes = cluster_ctas() * (blockDim.x / 32) * (uint32_t)sizeof(V);
+  __device__ __forceinline__ void expect(int i, int L) const {
+    const uint32_t bytes = cluster_ctas() * ((uint32_t)L / 32) * (uint32_t)sizeof(V);
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar_at(i)), "r"(bytes) : "memory");
   }
 };

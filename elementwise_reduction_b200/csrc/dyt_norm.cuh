@@ -79,7 +79,7 @@ constexpr int kMaxWarps = 32;
 
 // How many lanes share a row: less than a warp (a power of two), a warp, or a group of warps.
 // (kHalf is kPart with 16 lanes, known to the compiler: the offsets of a lane's elements are constants. kCluster: all
-// of a CTA's warps share its part of a row, whose other parts are the other CTAs' of its cluster; aligned rows only.)
+// warps of a cluster's CTAs, which have a stretch of the row's columns each; aligned rows only.)
 enum RowMode { kPart = 0, kWarp = 1, kGroup = 2, kHalf = 3, kCluster = 4 };
 __host__ __device__ constexpr bool shares_warp(int mode) { return mode == kPart || mode == kHalf; }
 

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
   using Slab = Slabs<T, E, RAGGED, MODE>;
   __shared__ std::conditional_t<CLUSTER, Meet<float2>, float2[2][kBlock / 32]> red;
   __shared__ Steal queue;
-  extern __shared__ __align__(16) unsigned char dyn[];
+  extern __shared__ __align__(128) unsigned char dyn[];
   pdl_prologue();
   const Place<MODE> p(a.w.L);
   if (dynamic_smem_bytes() < rms_fwd_smem<T, E>((int)blockDim.x, p.L, RAGGED, RES)) return;
@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
   ShareWalk<MODE> w = a.w;
   if constexpr (CLUSTER) {
     cut(w, col0, a.cols, V);
-    red.init();
+    red.init(p.lane, p.L);
+    cluster_sync();
   }
   const bool steal = !CLUSTER && a.steal;
   const int groups = CLUSTER ? ((int)w.N + kScaleCols - 1) / kScaleCols : a.groups;  // of the CTA's stretch
@@ -329,8 +330,8 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
       const int par = it & 1;
       if constexpr (CLUSTER) {
         const float nan = __int_as_float(0x7FC00000);
-        red.put(it, make_float2(lost ? nan : q, top));
-        if (!lost) lost = !red.wait(it);
+        red.put(it, make_float2(lost ? nan : q, top), p.lane, p.L);
+        if (!lost) lost = !red.wait(it, p.lane, p.L);
         const float2 o = red.of[par][wl], u = red.of[par][wl + 32];
         q = lost ? nan : warp_sum(o.x + u.x);
         if (Q && !a.grouped) top = lanes_max(max_nan(o.y, u.y), 32);
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
   constexpr int E = kBwdElems, P = E / 2;
   constexpr int S = rms_bwd_stages<T>(), TN = RES ? 3 : 2;
   __shared__ std::conditional_t<CLUSTER, Meet<float>, float[2][kBlock / 32]> red;
-  extern __shared__ __align__(16) unsigned char dyn[];
+  extern __shared__ __align__(128) unsigned char dyn[];
   pdl_prologue();
   const Place<MODE> p(a.w.L);
   if (dynamic_smem_bytes() < rms_bwd_smem<T>((int)blockDim.x, p.L, RAGGED, RES)) return;
@@ -602,7 +603,8 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
   ShareWalk<MODE> w = a.w;
   if constexpr (CLUSTER) {
     cut(w, col0, a.cols, V);
-    red.init();
+    red.init(p.lane, p.L);
+    cluster_sync();
   }
   const int N = (int)w.N;
   const T *src[TN];
@@ -661,8 +663,8 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
       const int par = it & 1;
       if constexpr (CLUSTER) {
         const float nan = __int_as_float(0x7FC00000);
-        red.put(it, lost ? nan : c);
-        if (!lost) lost = !red.wait(it);
+        red.put(it, lost ? nan : c, p.lane, p.L);
+        if (!lost) lost = !red.wait(it, p.lane, p.L);
         c = lost ? nan : warp_sum(red.of[par][wl] + red.of[par][wl + 32]);
       } else {
         if (wl == 0) red[par][w0 + p.lane / 32] = c;
