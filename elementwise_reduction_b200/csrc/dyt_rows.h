@@ -48,7 +48,7 @@ inline RowPlan plan_rows(int64_t M, int64_t N, int vec, bool aligned, int E, int
   p.NV = (int)ceil_div(N, p.V);
   p.group = lanes > 32;
   p.L = p.group ? (int)ceil_div(lanes, 32) * 32 : pow2_at_least(lanes);
-  // Ragged rows keep one slot more per row and warp: half the threads where that is up to half a slot per lane.
+  // Ragged rows keep two slots more per row: half the threads where that is up to as many as its lanes fill.
   int block = p.ragged && p.L < 8 ? kBlock / 2 : kBlock;
   // Few short rows: smaller CTAs, so that more SMs take part.
   while (!p.group && block > 128 && ceil_div(M, block / p.L) < sms) block >>= 1;
