@@ -79,7 +79,7 @@ constexpr int kMaxWarps = 32;
 
 // How many lanes share a row: less than a warp (a power of two), a warp, or a group of warps.
 // (kHalf is kPart with 16 lanes, known to the compiler: the offsets of a lane's elements are constants. kCluster: all
-// warps of a cluster's CTAs, which have a stretch of the row's columns each; aligned rows only.)
+// warps of a cluster's CTAs, which have a stretch of the row's columns each.)
 enum RowMode { kPart = 0, kWarp = 1, kGroup = 2, kHalf = 3, kCluster = 4 };
 __host__ __device__ constexpr bool shares_warp(int mode) { return mode == kPart || mode == kHalf; }
 
@@ -112,7 +112,7 @@ struct Place {
 template <int V, int E, bool RAGGED, int MODE>
 __device__ __forceinline__ int column(int L, int lane, int i) {
   if constexpr (!RAGGED) return (lane + i / V * L) * V + i % V;
-  else if constexpr (MODE == kGroup) return (lane >> 5) * (32 * E) + (lane & 31) + i * 32;
+  else if constexpr (MODE == kGroup || MODE == kCluster) return (lane >> 5) * (32 * E) + (lane & 31) + i * 32;
   else return lane + i * (MODE == kWarp ? 32 : MODE == kHalf ? 16 : L);
 }
 

@@ -26,7 +26,7 @@ struct FwdPlan {
   RowPlan r;
   bool narrow;    // kNarrowElems elements a lane
   bool steal;
-  int64_t items;  // a CTA's rows of a step
+  int64_t items;  // a CTA's or a cluster's rows of a step
   int64_t grid;
 };
 
@@ -37,11 +37,11 @@ struct FwdPlan {
 constexpr int kFewSteps = 4;
 constexpr int kNarrowCtas = 6;  // of an SM, as the registers of most of these kernels allow
 
-// Aligned rows too long for one CTA's registers are shared by a cluster: of 2 CTAs, or of 4. (Of 4 no more than 33
+// Rows too long for one CTA's registers are shared by a cluster: of 2 CTAs, or of 4. (Of 4 no more than 33
 // run at once on 148 SMs; 3, 49 at once, are slower still: 8192 x 12288 bf16 backward 144 us with 2, 230 with 3, 244
 // with 4, whose rows take as long each.)
 void plan_cluster(RowPlan &p, int64_t N, int vec, int E) {
-  if (!p.rowlong || p.V == 1) return;
+  if (!p.rowlong) return;
   const int64_t per = (int64_t)dyt::norm::kBlock * E;
   const int c = N <= 2 * per ? 2 : dyt::kMaxCluster;
   if (N > c * per) return;
@@ -49,6 +49,7 @@ void plan_cluster(RowPlan &p, int64_t N, int vec, int E) {
   p.group = true;
   p.cluster = c;
   p.L = p.block = (int)ceil_div(ceil_div(N, c), 32 * E) * 32;
+  static_assert(dyt::norm::kScaleCols == 32 * 16 / sizeof(float));  // (a CTA's columns: see RmsArgs)
   p.cols = (int)ceil_div(ceil_div(N, c), 32 * vec) * 32 * vec;
   p.rows = 1;
 }

@@ -42,7 +42,7 @@ struct RmsArgs {
   int grouped;
   int steal;          // a CTA an item, and work is taken from those that do not run yet; else a fixed share
   int64_t items;      // a CTA's rows of a step each
-  int cols;           // kCluster: columns of a CTA, whole warps' vectors
+  int cols;           // kCluster: columns of a CTA, whole warps' vectors and scales' columns
   Walk w;             // (a step is 0: rows come in no order)
 };
 
@@ -79,17 +79,17 @@ template <int MODE>
 struct Share {
   static __device__ __forceinline__ uint32_t rank() { return MODE == kCluster ? cluster_rank() : 0; }
   static __device__ __forceinline__ uint32_t ctas() { return MODE == kCluster ? cluster_ctas() : 1; }
-  static __device__ __forceinline__ uint32_t unit() { return MODE == kCluster ? blockIdx.x / cluster_ctas() : blockIdx.x; }
-  static __device__ __forceinline__ uint32_t units() { return MODE == kCluster ? gridDim.x / cluster_ctas() : gridDim.x; }
+  static __device__ __forceinline__ uint32_t unit() { return blockIdx.x / ctas(); }
+  static __device__ __forceinline__ uint32_t units() { return gridDim.x / ctas(); }
   static __device__ __forceinline__ int first(int cols) { return MODE == kCluster ? (int)cluster_rank() * cols : 0; }
 };
 // The walk over a CTA's stretch of the rows' columns.
 template <int MODE>
 using ShareWalk = std::conditional_t<MODE == kCluster, Walk, const Walk &>;
-__device__ __forceinline__ void cut(Walk &w, int first, int cols, int vec) {
+__device__ __forceinline__ void cut(Walk &w, int first, int cols, int V) {  // V: elements of a vector
   const int left = (int)w.N - first;
   w.N = left < cols ? left : cols;
-  w.NV = (int)w.N / vec;
+  w.NV = (int)w.N / V;
 }
 __device__ __forceinline__ const void *param_from(const void *p, int dt, int first) {
   return p ? static_cast<const char *>(p) + (int64_t)first * (dt == DYT_F32 ? 4 : 2) : p;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
   const int col0 = Mine::first(a.cols);
   ShareWalk<MODE> w = a.w;
   if constexpr (CLUSTER) {
-    cut(w, col0, a.cols, V);
+    cut(w, col0, a.cols, RAGGED ? 1 : V);
     red.init(p.lane, p.L);
     cluster_sync();
   }
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
   double *const parts = a.parts + Mine::unit() * a.w.N + col0;
   ShareWalk<MODE> w = a.w;
   if constexpr (CLUSTER) {
-    cut(w, col0, a.cols, V);
+    cut(w, col0, a.cols, RAGGED ? 1 : V);
     red.init(p.lane, p.L);
     cluster_sync();
   }

@@ -9,6 +9,7 @@ namespace norm {
 template <typename T, bool RAGGED, bool RES, bool Q>
 RmsFwdKernel rms_fwd_ring_of(const host::RowPlan &p) {
   constexpr int E = fwd_elems<T>(), EN = kNarrowElems;
+  if (p.cluster) return rms_fwd_kernel<T, E, kCluster, RAGGED, RES, Q>;
   if (p.group) return rms_fwd_kernel<T, E, kGroup, RAGGED, RES, Q>;
   if (p.L == 32)
     return p.NV * p.V > 32 * EN ? rms_fwd_kernel<T, E, kWarp, RAGGED, RES, Q>
@@ -18,7 +19,6 @@ RmsFwdKernel rms_fwd_ring_of(const host::RowPlan &p) {
 template <typename T, bool RES, bool Q>
 RmsFwdKernel rms_fwd_of(const host::RowPlan &p) {
   constexpr int V = 16 / (int)sizeof(T);
-  if (p.cluster) return rms_fwd_kernel<T, fwd_elems<T>(), kCluster, false, RES, Q>;
   if (p.rowlong) return p.V == 1 ? rms_fwd_long_kernel<T, 1, RES, Q> : rms_fwd_long_kernel<T, V, RES, Q>;
   return p.ragged ? rms_fwd_ring_of<T, true, RES, Q>(p) : rms_fwd_ring_of<T, false, RES, Q>(p);
 }
@@ -30,7 +30,7 @@ RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool res, bool q8) {
 
 template <typename T, bool RES>
 RmsBwdKernel rms_bwd_of(const host::RowPlan &p) {
-  if (p.cluster) return rms_bwd_kernel<T, kCluster, false, RES>;
+  if (p.cluster) return p.ragged ? rms_bwd_kernel<T, kCluster, true, RES> : rms_bwd_kernel<T, kCluster, false, RES>;
   if (p.group) return p.ragged ? rms_bwd_kernel<T, kGroup, true, RES> : rms_bwd_kernel<T, kGroup, false, RES>;
   if (p.L == 32) return p.ragged ? rms_bwd_kernel<T, kWarp, true, RES> : rms_bwd_kernel<T, kWarp, false, RES>;
   if (p.L == 16) return p.ragged ? rms_bwd_kernel<T, kHalf, true, RES> : rms_bwd_kernel<T, kHalf, false, RES>;

@@ -136,7 +136,9 @@ def test_long_rows_more_than_ctas():
 SHARED = [(8192, "f32", 0, 0), (8200, "f32", 2, 2), (12288, "f32", 2, 2), (16384, "f32", 2, 2), (16388, "f32", 4, 4),
           (32768, "f32", 4, 4), (32772, "f32", 0, 0), (8200, "bf16", 0, 2), (12288, "bf16", 0, 2),
           (16384, "f16", 0, 2), (16392, "bf16", 2, 4), (20480, "bf16", 2, 4), (32768, "f16", 2, 4),
-          (32776, "bf16", 4, 0), (65536, "bf16", 4, 0), (65544, "bf16", 0, 0), (12290, "bf16", 0, 0)]
+          (32776, "bf16", 4, 0), (65536, "bf16", 4, 0), (65544, "bf16", 0, 0),
+          (8193, "f32", 2, 2), (12290, "bf16", 0, 2), (16385, "f16", 2, 4), (20481, "bf16", 2, 4), (30001, "f32", 4, 4),
+          (32767, "bf16", 2, 4), (32769, "f32", 0, 0), (65535, "f16", 4, 0)]
 
 
 @pytest.mark.parametrize("N,xd,fwd,bwd", SHARED)
@@ -147,7 +149,8 @@ def test_rows_that_a_cluster_shares(N, xd, fwd, bwd):
         assert infos[0]["grid"] <= (fwd or 2) * M and infos[1]["grid"] <= (bwd or 2) * M
 
 
-@pytest.mark.parametrize("N,xd,pitch", [(12288, "bf16", 12304), (16384, "f32", 16384), (20480, "f16", 20480)])
+@pytest.mark.parametrize("N,xd,pitch", [(12288, "bf16", 12304), (16384, "f32", 16384), (20480, "f16", 20480),
+                                       (12289, "bf16", 12289), (20480, "f16", 20481)])
 def test_many_rows_that_a_cluster_shares(N, xd, pitch):
     """More rows than run at once, beside a second call and from a graph: the same bits."""
     M = 20000 if xd != "f32" else 10000
@@ -240,7 +243,7 @@ def test_without_gamma(N):
         x, r, dy, _ = inputs(13, N, "bf16", res=res)
         got, _ = check_forward(x, r, None)
         check_quantize(x, r, None, 128)
-        assert check_backward(x, dy, got[2], None, r)["kernels"] == (2 if N == 9001 else 1)
+        assert check_backward(x, dy, got[2], None, r)["kernels"] == 1
 
 
 def test_offsets_beyond_32_bits():
