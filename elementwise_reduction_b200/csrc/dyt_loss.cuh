@@ -556,10 +556,9 @@ constexpr int kGradCtas = 5;  // an SM's
 // Measured: 8192 x 131072 bf16 629 us (6.8 TB/s), 4096 x 32003 fp16 with a
 // quarter of the rows without weight 79 us (5.8 TB/s); rows at different
 // offsets, 4096 x 32003 bf16, 98 us. Bound by memory. Five CTAs an SM, 48
-// registers, gain 4% over four on ragged rows (78.9 and 82.1 us). A warp per row
-// of 16-bit logits spills 11 registers at that; with four CTAs an SM 16384 x 4096 bf16
-// takes 44.5 instead of 45.8 us, but 16384 x 2000 27.4 instead of 26.5 and 16384 x 1000
-// fp16 18.5 instead of 17.8.
+// registers, gain 4% over four on ragged rows (78.9 and 82.1 us); a warp per row of 16-bit
+// logits with four CTAs an SM: 16384 x 4096 bf16 44.5 instead of 45.8 us, but 16384 x 2000
+// 27.4 instead of 26.5 and 16384 x 1000 fp16 18.5 instead of 17.8.
 // G threads (a warp, or the CTA) per part of a row. The vectors are those of
 // the output row; SHIFT: the input row lies at another offset past a 16-byte
 // boundary, and each of its vectors is cut out of two aligned ones inside the

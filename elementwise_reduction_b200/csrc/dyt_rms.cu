@@ -33,13 +33,14 @@ struct FwdPlan {
 // Work is taken from CTAs that do not run yet where every CTA has more than kFewSteps items: the first answers cost
 // 0.3 us, fixed shares the difference between the SMs. Measured with a residual, fixed and taken: 1184 x 4096 bf16
 // (2 steps) 6.1 and 6.5 us, 2368 x 4096 14.0 and 14.1, 4736 x 4096 27.4 and 25.8, 9472 x 4096 56.1 and 48.2. Narrow
-// rows, more of a CTA's time at its ends, gain from the second step on: 9472 x 256 5.3 and 4.5, 18944 x 256 7.1 and 6.5.
+// rows, more of a CTA's time at its ends, gain from the second step on: 9472 x 256 5.3 and 4.5, 18944 x 256 7.1 and
+// 6.5.
 constexpr int kFewSteps = 4;
 constexpr int kNarrowCtas = 6;  // of an SM, as the registers of most of these kernels allow
 
-// Rows too long for one CTA's registers are shared by a cluster: of 2 CTAs, or of 4. (Of 4 no more than 33
-// run at once on 148 SMs; 3, 49 at once, are slower still: 8192 x 12288 bf16 backward 144 us with 2, 230 with 3, 244
-// with 4, whose rows take as long each.)
+// Rows too long for one CTA's registers are shared by a cluster: of 2 CTAs, or of 4. A row takes a cluster as long
+// whatever its size (1 us), so larger clusters than it needs are slower: 8192 x 12288 bf16 backward with a residual
+// 144 us with 2 CTAs, 230 with 3, 244 with 4 (of which 33 run at once on 148 SMs).
 void plan_cluster(RowPlan &p, int64_t N, int vec, int E) {
   if (!p.rowlong) return;
   const int64_t per = (int64_t)dyt::norm::kBlock * E;

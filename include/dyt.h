@@ -53,10 +53,13 @@
  * - Results are deterministic: the same inputs on the same device give the
  *   same bits (static schedule, fixed reduction order, no atomics in sums).
  * - Every argument error is reported by a status code before anything is
- *   launched. No kernel waits on another CTA, grid or device; the only waits
- *   are hardware completion waits (a thread's own asynchronous copies, the
- *   preceding grid in the stream, the hardware's answer to a CTA that asks for
- *   more work).
+ *   launched. No kernel waits on another grid or device, nor on a CTA that may
+ *   not be running; the only waits are hardware completion waits (a thread's
+ *   own asynchronous copies, the preceding grid in the stream, the hardware's
+ *   answer to a CTA that asks for more work, and, for a root-mean-square norm's
+ *   long rows, what the other CTAs of the same thread-block cluster send, which
+ *   run together with it). The last two have a limit, after which the rows
+ *   concerned are NaN.
  */
 #ifndef DYT_H_
 #define DYT_H_
@@ -292,6 +295,7 @@ int dyt_last_cuda_error(void);
  * Launch geometry of the calling thread's last successful call, so tests can
  * check which path ran. (The norms: path 1 = a row in a warp, 2 = in several
  * warps; row_groups = partial sums per column; shifted = 1 for ragged rows.
+ * Root-mean-square norm: col_chunks = CTAs that share a row.
  * Policy loss, log probabilities: path 1 = a warp per row or part of one, 2 = a CTA; col_chunks =
  * parts of a row. The other fields that do not apply are 0.)
  */
@@ -517,9 +521,10 @@ dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *
  * row's bits do not depend on it. (Should the hardware leave a CTA's question for
  * a row unanswered, the CTA's own row has NaN for y's first element, rstd or
  * scale.) A row is read once and kept on the SM when N is at most 16384 (16-bit) or
- * 8192 (binary32); longer rows are read twice. Ragged rows are read as there. A row
- * whose sum of squares passes binary32's range has rstd 0. M * N == 0 launches
- * nothing and writes nothing.
+ * 8192 (binary32), and on the SMs of a cluster of 2 or 4 CTAs up to four times as
+ * many; longer rows are read twice. Ragged rows are read as there. A row whose sum
+ * of squares passes binary32's range has rstd 0. M * N == 0 launches nothing and
+ * writes nothing.
  */
 dyt_status dyt_rms_norm_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *gamma,
                                 float eps, void *y, int64_t ldy, void *h, int64_t ldh, float *rstd, int64_t M,
@@ -554,7 +559,8 @@ dyt_status dyt_rms_norm_quantize(const void *x, int64_t ldx, const void *residua
  *   dgamma[j] = sum_i dy[i,j] * n[i,j]
  *
  * dx is the gradient of x and of the residual. Launches, sums and workspace as for
- * dyt_layer_norm_backward (the second launch only for dgamma).
+ * dyt_layer_norm_backward (the second launch only for dgamma; the launch more is that
+ * of rows of more than 32768 elements, shorter ones are shared by a cluster as above).
  *   dh        x_dtype, row pitch lddh: the gradient that h received from elsewhere;
  *             NULL: none
  *   dgamma    [N] gamma_dtype, written; NULL: not wanted
