@@ -7,7 +7,7 @@
 
 namespace dyt {
 
-constexpr int kMaxCluster = 4;  // CTAs
+constexpr int kMaxCluster = 8;  // CTAs
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -26,15 +26,16 @@ __device__ __forceinline__ void cluster_sync() {
 
 // Where a row's sums of all the cluster's warps meet: each warp sends its own to every CTA (st.async) and waits for all
 // of them at its CTA's mbarrier. Rows take turns between two places; a warp is at most one row ahead of another, as it
-// has the other's sums of the row before. In shared memory, for V = float or float2.
+// has the other's sums of the row before. In shared memory, one for each of a CTA's rows side by
+// side, for V = float or float2.
 template <typename V>
 struct Meet {
-  static constexpr int kWarps = 16 * kMaxCluster;  // of a row, at most
+  static constexpr int kWarps = 64;               // of a row, at most
   static constexpr int kPolls = 1 << 20;           // of a wait, each waits for a while itself
   V of[2][kWarps];                         // (0 where there is no warp)
   unsigned long long bar[2];
 
-  // Lane `lane` of the CTA's L; before any put all threads of the cluster meet.
+  // Lane `lane` of the row's L in this CTA; before any put all threads of the cluster meet.
   __device__ __forceinline__ void init(int lane, int L) {
     for (int i = lane; i < 2 * kWarps; i += L) of[0][i] = V{};
     if (lane == 0) {
@@ -45,7 +46,7 @@ struct Meet {
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
   }
-  // The warp's v (the same in all its lanes) of the CTA's row number `it`.
+  // The warp's v (the same in all its lanes) of the row's step `it`.
   __device__ __forceinline__ void put(int it, V v, int lane, int L) {
     const uint32_t cta = lane & 31;
     if (cta >= cluster_ctas()) return;
@@ -64,7 +65,7 @@ struct Meet {
           "r"(bar_at(par)), "r"(cta), "f"(v)
           : "memory");
   }
-  // All of row `it` is in of[it & 1]; false: not within the limit.
+  // All of step `it` is in of[it & 1]; false: not within the limit.
   __device__ __forceinline__ bool wait(int it, int lane, int L) {
     const int par = it & 1;
     uint32_t done = 0;

@@ -79,9 +79,12 @@ constexpr int kMaxWarps = 32;
 
 // How many lanes share a row: less than a warp (a power of two), a warp, or a group of warps.
 // (kHalf is kPart with 16 lanes, known to the compiler: the offsets of a lane's elements are constants. kCluster: all
-// warps of a cluster's CTAs, which have a stretch of the row's columns each.)
-enum RowMode { kPart = 0, kWarp = 1, kGroup = 2, kHalf = 3, kCluster = 4 };
+// warps of a cluster's CTAs, which have a stretch of the row's columns each; kClusterRows: a group of warps in each of
+// them, and several rows side by side.)
+enum RowMode { kPart = 0, kWarp = 1, kGroup = 2, kHalf = 3, kCluster = 4, kClusterRows = 5 };
 __host__ __device__ constexpr bool shares_warp(int mode) { return mode == kPart || mode == kHalf; }
+__host__ __device__ constexpr bool in_cluster(int mode) { return mode == kCluster || mode == kClusterRows; }
+__host__ __device__ constexpr bool in_warps(int mode) { return mode == kGroup || in_cluster(mode); }
 
 // Where a thread stands: lane `lane` of the L that share row `mine` of the
 // CTA's rows; seg() of those lanes are in this warp, this is number `at` of them.
@@ -94,7 +97,7 @@ struct Place {
       mine = 0;
       lane = t;
       at = t & 31;
-    } else if constexpr (MODE == kGroup) {
+    } else if constexpr (MODE == kGroup || MODE == kClusterRows) {
       mine = t / L;
       lane = t - mine * L;
       at = t & 31;
@@ -112,7 +115,7 @@ struct Place {
 template <int V, int E, bool RAGGED, int MODE>
 __device__ __forceinline__ int column(int L, int lane, int i) {
   if constexpr (!RAGGED) return (lane + i / V * L) * V + i % V;
-  else if constexpr (MODE == kGroup || MODE == kCluster) return (lane >> 5) * (32 * E) + (lane & 31) + i * 32;
+  else if constexpr (in_warps(MODE)) return (lane >> 5) * (32 * E) + (lane & 31) + i * 32;
   else return lane + i * (MODE == kWarp ? 32 : MODE == kHalf ? 16 : L);
 }
 

@@ -38,28 +38,38 @@ struct FwdPlan {
 constexpr int kFewSteps = 4;
 constexpr int kNarrowCtas = 6;  // of an SM, as the registers of most of these kernels allow
 
-// Rows too long for one CTA's registers are shared by a cluster: of 2 CTAs, or of 4. A row takes a cluster as long
-// whatever its size (1 us), so larger clusters than it needs are slower: 8192 x 12288 bf16 backward with a residual
-// 144 us with 2 CTAs, 230 with 3, 244 with 4 (of which 33 run at once on 148 SMs).
-void plan_cluster(RowPlan &p, int64_t N, int vec, int E) {
-  if (!p.rowlong) return;
-  const int64_t per = (int64_t)dyt::norm::kBlock * E;
-  const int c = N <= 2 * per ? 2 : dyt::kMaxCluster;
-  if (N > c * per) return;
+// Rows too long for one CTA's registers, and not for four CTAs', are shared by a cluster of 2, 4 or 8 CTAs. A step
+// takes a cluster as long whatever its lanes (1.1 us), so as many threads of the device as can be have a row: `side`
+// (backward): rows side by side fill the CTAs of larger clusters. Measured, bf16 with a residual, 4096 rows, clusters
+// of 2, 4 and 8: 9216 columns 60, 54 and -, 12288 69, 75 and -, 20480 -, 137 and 121, 32768 -, 174 and 188. (Clusters
+// of 3, 5, 6 or 7 take between these times and twice as long: not all that should fit run at once.)
+void plan_cluster(RowPlan &p, int64_t M, int64_t N, int E, int sms, bool side) {
+  if (!p.rowlong || N > (int64_t)4 * dyt::norm::kBlock * E) return;
+  constexpr int kSizes[] = {2, 4, 8}, kReached[] = {74, 66, 60};  // parts of 74 of the SMs that run such clusters
+  int64_t most = 0;
+  for (int i = 0; i < (side ? 3 : 2); ++i) {
+    const int c = kSizes[i], L = (int)ceil_div(ceil_div(N, c), 32 * E) * 32;
+    if (L > dyt::norm::kBlock) continue;
+    const int64_t room = side ? std::min(dyt::norm::kBlock / L, dyt::norm::kClusterMost) : 1;
+    const int64_t rows = std::max<int64_t>(1, std::min(room, ceil_div(M, sms / c)));
+    if (rows * L * kReached[i] <= most) continue;
+    most = rows * L * kReached[i];
+    p.cluster = c;
+    p.L = L;
+    p.rows = (int)rows;
+    p.block = (int)rows * L;
+  }
   p.rowlong = false;
   p.group = true;
-  p.cluster = c;
-  p.L = p.block = (int)ceil_div(ceil_div(N, c), 32 * E) * 32;
-  static_assert(dyt::norm::kScaleCols == 32 * 16 / sizeof(float));  // (a CTA's columns: see RmsArgs)
-  p.cols = (int)ceil_div(ceil_div(N, c), 32 * vec) * 32 * vec;
-  p.rows = 1;
+  // (whole vectors and scales; the last CTA has some too, with more than 8 x 7 x kScaleCols columns)
+  p.cols = (int)ceil_div(ceil_div(N, p.cluster), dyt::norm::kScaleCols) * dyt::norm::kScaleCols;
 }
 
 FwdPlan plan_fwd(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
   FwdPlan p = {};
   p.narrow = N <= 32 * dyt::norm::kNarrowElems;
   p.r = plan_rows(M, N, vec, aligned, p.narrow ? dyt::norm::kNarrowElems : E, sms);
-  plan_cluster(p.r, N, vec, E);
+  plan_cluster(p.r, M, N, E, sms, false);
   p.items = M;
   p.grid = std::min<int64_t>(M, (int64_t)sms * 2);  // (long rows)
   if (p.r.rowlong || p.r.cluster) return p;
@@ -75,7 +85,7 @@ FwdPlan plan_fwd(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
 // A plan for few rows spreads them over the SMs: no more rows side by side than every SM gets.
 RowPlan plan_rms(int64_t M, int64_t N, int vec, bool aligned, int E, int sms) {
   RowPlan p = plan_rows(M, N, vec, aligned, E, sms);
-  plan_cluster(p, N, vec, E);
+  plan_cluster(p, M, N, E, sms, true);
   if (!p.group || p.rowlong || p.cluster) return p;
   p.rows = (int)std::max<int64_t>(1, std::min<int64_t>(p.rows, ceil_div(M, sms)));
   p.block = p.rows * p.L;
@@ -136,7 +146,7 @@ dyt_status fit_clusters(int dev, const void *kernel, const RowPlan &r, int64_t M
   lc.cfg.gridDim.x = (unsigned)r.cluster;  // (the question is of whole clusters)
   const dyt_status st = cluster_capacity(dev, kernel, lc.cfg, r.cluster, &n);
   if (st != DYT_OK) return st;
-  *clusters = std::min<int64_t>(M, std::min(n, sms / r.cluster));
+  *clusters = std::min<int64_t>(ceil_div(M, r.rows), std::min(n, sms / r.cluster));
   lc.cfg.gridDim.x = (unsigned)(*clusters * r.cluster);
   return DYT_OK;
 }

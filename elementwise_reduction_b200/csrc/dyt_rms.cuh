@@ -42,7 +42,7 @@ struct RmsArgs {
   int grouped;
   int steal;          // a CTA an item, and work is taken from those that do not run yet; else a fixed share
   int64_t items;      // a CTA's rows of a step each
-  int cols;           // kCluster: columns of a CTA, whole warps' vectors and scales' columns
+  int cols;           // clusters: columns of a CTA, a multiple of kScaleCols
   Walk w;             // (a step is 0: rows come in no order)
 };
 
@@ -60,11 +60,12 @@ struct RmsGradArgs {
   double *parts;      // [CTA][N] column sums
   int gamma_dt;
   int64_t inc_dx;
-  int cols;           // kCluster: columns of a CTA
+  int cols;           // clusters: columns of a CTA
   Walk w;             // inc[0 .. 2]: of h, dy and dres
 };
 
 constexpr int kScaleCols = 128;
+constexpr int kClusterMost = 4;  // rows of a cluster side by side, at most
 constexpr float kQMax = 448.0f;      // the largest e4m3 value
 constexpr float kLeastTop = 0x1p-100f;  // a row of zeros has a scale all the same: nothing is divided by 0
 
@@ -77,15 +78,15 @@ __device__ __forceinline__ float lanes_max(float v, int width) {
 // column; `unit` counts the clusters, or the CTAs.
 template <int MODE>
 struct Share {
-  static __device__ __forceinline__ uint32_t rank() { return MODE == kCluster ? cluster_rank() : 0; }
-  static __device__ __forceinline__ uint32_t ctas() { return MODE == kCluster ? cluster_ctas() : 1; }
+  static __device__ __forceinline__ uint32_t rank() { return in_cluster(MODE) ? cluster_rank() : 0; }
+  static __device__ __forceinline__ uint32_t ctas() { return in_cluster(MODE) ? cluster_ctas() : 1; }
   static __device__ __forceinline__ uint32_t unit() { return blockIdx.x / ctas(); }
   static __device__ __forceinline__ uint32_t units() { return gridDim.x / ctas(); }
-  static __device__ __forceinline__ int first(int cols) { return MODE == kCluster ? (int)cluster_rank() * cols : 0; }
+  static __device__ __forceinline__ int first(int cols) { return in_cluster(MODE) ? (int)cluster_rank() * cols : 0; }
 };
 // The walk over a CTA's stretch of the rows' columns.
 template <int MODE>
-using ShareWalk = std::conditional_t<MODE == kCluster, Walk, const Walk &>;
+using ShareWalk = std::conditional_t<in_cluster(MODE), Walk, const Walk &>;
 __device__ __forceinline__ void cut(Walk &w, int first, int cols, int V) {  // V: elements of a vector
   const int left = (int)w.N - first;
   w.N = left < cols ? left : cols;
@@ -222,7 +223,7 @@ __device__ __noinline__ void give_up(const RmsArgs &a, int64_t row) {
 // memory and a store of its own: 100003 x 255 bf16 43.4 (4.7), 8191 x 1001 fp16 to 8 bits 10.2 (2.4).
 template <typename T, int E, int MODE, bool RAGGED, bool RES, bool Q>
 __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constant__ RmsArgs a) {
-  constexpr bool CLUSTER = MODE == kCluster, GROUP = MODE == kGroup || CLUSTER;
+  constexpr bool CLUSTER = in_cluster(MODE), GROUP = in_warps(MODE);
   using Mine = Share<MODE>;
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int P = E / 2;
@@ -551,7 +552,7 @@ static_assert(rms_bwd_ring<__half>(32, 32, false, false) >= rms_sums_smem(32, 32
 template <int V, int E, int PER, bool RAGGED, int MODE>
 __device__ __forceinline__ void rms_flush(double *pg, const Walk &w, float2 (&dg)[E / 2], const Place<MODE> &p,
                                           bool first, float *sh) {
-  constexpr bool GROUP = MODE == kGroup || MODE == kCluster;
+  constexpr bool GROUP = in_warps(MODE);
   const int N = (int)w.N;
   const int copies = !GROUP ? (int)blockDim.x / 32 : w.rows;
   const int copy = !GROUP ? (int)threadIdx.x >> 5 : p.mine;
@@ -597,12 +598,12 @@ __device__ __forceinline__ void rms_flush(double *pg, const Walk &w, float2 (&dg
 // ring: binary32 2 (3: 100003 x 255 59 us instead of 57, 16384 x 2048 68 instead of 66), 16 bits 3 (4 and 5: 1% more).
 template <typename T, int MODE, bool RAGGED, bool RES>
 __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
-  constexpr bool CLUSTER = MODE == kCluster, GROUP = MODE == kGroup || CLUSTER;
+  constexpr bool CLUSTER = in_cluster(MODE), GROUP = in_warps(MODE);
   using Mine = Share<MODE>;
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int E = kBwdElems, P = E / 2;
   constexpr int S = rms_bwd_stages<T>(), TN = RES ? 3 : 2;
-  __shared__ std::conditional_t<CLUSTER, Meet<float>, float[2][kBlock / 32]> red;
+  __shared__ std::conditional_t<CLUSTER, Meet<float>[kClusterMost], float[2][kBlock / 32]> red;
   extern __shared__ __align__(128) unsigned char dyn[];
   pdl_prologue();
   const Place<MODE> p(a.w.L);
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
   ShareWalk<MODE> w = a.w;
   if constexpr (CLUSTER) {
     cut(w, col0, a.cols, RAGGED ? 1 : V);
-    red.init(p.lane, p.L);
+    red[p.mine].init(p.lane, p.L);
     cluster_sync();
   }
   const int N = (int)w.N;
@@ -673,9 +674,10 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
       const int par = it & 1;
       if constexpr (CLUSTER) {
         const float nan = __int_as_float(0x7FC00000);
-        red.put(it, lost ? nan : c, p.lane, p.L);
-        if (!lost) lost = !red.wait(it, p.lane, p.L);
-        c = lost ? nan : warp_sum(red.of[par][wl] + red.of[par][wl + 32]);
+        Meet<float> &meet = red[p.mine];
+        meet.put(it, lost ? nan : c, p.lane, p.L);
+        if (!lost) lost = !meet.wait(it, p.lane, p.L);
+        c = lost ? nan : warp_sum(meet.of[par][wl] + meet.of[par][wl + 32]);
       } else {
         if (wl == 0) red[par][w0 + p.lane / 32] = c;
         group_barrier(p.mine, p.L);

@@ -132,25 +132,26 @@ def test_long_rows_more_than_ctas():
     check(700, 9001, "f32")
 
 
-# columns, dtype, CTAs that share a row forward and backward (0: no cluster)
+# columns, dtype, CTAs that share a row forward, and at least in the backward (0: no cluster)
 SHARED = [(8192, "f32", 0, 0), (8200, "f32", 2, 2), (12288, "f32", 2, 2), (16384, "f32", 2, 2), (16388, "f32", 4, 4),
           (32768, "f32", 4, 4), (32772, "f32", 0, 0), (8200, "bf16", 0, 2), (12288, "bf16", 0, 2),
           (16384, "f16", 0, 2), (16392, "bf16", 2, 4), (20480, "bf16", 2, 4), (32768, "f16", 2, 4),
           (32776, "bf16", 4, 0), (65536, "bf16", 4, 0), (65544, "bf16", 0, 0),
           (8193, "f32", 2, 2), (12290, "bf16", 0, 2), (16385, "f16", 2, 4), (20481, "bf16", 2, 4), (30001, "f32", 4, 4),
-          (32767, "bf16", 2, 4), (32769, "f32", 0, 0), (65535, "f16", 4, 0)]
+          (32767, "bf16", 2, 4), (8193, "bf16", 0, 2), (9216, "bf16", 0, 2), (18432, "f16", 2, 4), (32769, "f32", 0, 0), (65535, "f16", 4, 0)]
 
 
 @pytest.mark.parametrize("N,xd,fwd,bwd", SHARED)
 def test_rows_that_a_cluster_shares(N, xd, fwd, bwd):
-    for M in (1, 5, 41):
+    for M in (1, 5, 41, 200):
         infos = check(M, N, xd)
-        assert [i["col_chunks"] for i in infos] == [max(1, fwd), max(1, bwd)]
-        assert infos[0]["grid"] <= (fwd or 2) * M and infos[1]["grid"] <= (bwd or 2) * M
+        assert infos[0]["col_chunks"] == max(1, fwd)
+        assert infos[1]["col_chunks"] in ((bwd, 8) if bwd == 4 else (bwd, 2 * bwd, 4 * bwd) if bwd else (1,))
+        assert all(i["grid"] % i["col_chunks"] == 0 for i in infos)
 
 
 @pytest.mark.parametrize("N,xd,pitch", [(12288, "bf16", 12304), (16384, "f32", 16384), (20480, "f16", 20480),
-                                       (12289, "bf16", 12289), (20480, "f16", 20481)])
+                                       (12289, "bf16", 12289), (20480, "f16", 20481), (9217, "bf16", 9217)])
 def test_many_rows_that_a_cluster_shares(N, xd, pitch):
     """More rows than run at once, beside a second call and from a graph: the same bits."""
     M = 20000 if xd != "f32" else 10000
