@@ -560,7 +560,8 @@ dyt_status dyt_rms_norm_quantize(const void *x, int64_t ldx, const void *residua
  *
  * dx is the gradient of x and of the residual. Launches, sums and workspace as for
  * dyt_layer_norm_backward (the second launch only for dgamma; the launch more is that
- * of rows of more than 32768 elements, shorter ones are shared by a cluster as above).
+ * of rows of more than 32768 elements; those of more than 8192 are shared by the CTAs
+ * of a cluster, 2, 4 or 8 of them).
  *   dh        x_dtype, row pitch lddh: the gradient that h received from elsewhere;
  *             NULL: none
  *   dgamma    [N] gamma_dtype, written; NULL: not wanted
