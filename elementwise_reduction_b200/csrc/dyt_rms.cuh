@@ -594,8 +594,9 @@ __device__ __forceinline__ void rms_flush(double *pg, const Walk &w, float2 (&dg
 // RES: the stored sum has a gradient of its own, read after the row's sum.
 // A CTA's share of the rows is fixed, so that the column sums are added in the same order every time. Measured: 32768
 // x 8192 bf16 with a residual 318 us (6.75 TB/s), 16384 x 4096 84 (6.4), 100003 x 255 binary32 53 (5.75), 4096 x 16384
-// bf16 by clusters of 2 88 (6.1), 4096 x 20480 by clusters of 8 120 (5.6). Bound by memory, and in short calls by the second kernel (2 to 4 us). Stages of the
-// ring: binary32 2 (3: 100003 x 255 59 us instead of 57, 16384 x 2048 68 instead of 66), 16 bits 3 (4 and 5: 1% more).
+// bf16 by clusters of 2 88 (6.1), 4096 x 20480 by clusters of 8 120 (5.6). Bound by memory, in clusters by a step's
+// latency, and in short calls by the second kernel (2 to 4 us). Stages of the ring: binary32 2 (3: 100003 x 255 59 us
+// instead of 57, 16384 x 2048 68 instead of 66), 16 bits 3 (4 and 5: 1% more).
 template <typename T, int MODE, bool RAGGED, bool RES>
 __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
   constexpr bool CLUSTER = in_cluster(MODE), GROUP = in_warps(MODE);

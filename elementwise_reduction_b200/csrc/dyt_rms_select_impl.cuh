@@ -30,7 +30,8 @@ RmsFwdKernel rms_fwd_kernel_of(const host::RowPlan &p, bool res, bool q8) {
 
 template <typename T, bool RES>
 RmsBwdKernel rms_bwd_of(const host::RowPlan &p) {
-  if (p.cluster) return p.ragged ? rms_bwd_kernel<T, kClusterRows, true, RES> : rms_bwd_kernel<T, kClusterRows, false, RES>;
+  if (p.cluster)
+    return p.ragged ? rms_bwd_kernel<T, kClusterRows, true, RES> : rms_bwd_kernel<T, kClusterRows, false, RES>;
   if (p.group) return p.ragged ? rms_bwd_kernel<T, kGroup, true, RES> : rms_bwd_kernel<T, kGroup, false, RES>;
   if (p.L == 32) return p.ragged ? rms_bwd_kernel<T, kWarp, true, RES> : rms_bwd_kernel<T, kWarp, false, RES>;
   if (p.L == 16) return p.ragged ? rms_bwd_kernel<T, kHalf, true, RES> : rms_bwd_kernel<T, kHalf, false, RES>;

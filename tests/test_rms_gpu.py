@@ -3,6 +3,8 @@ element, ragged and strided rows, with and without a residual, 8-bit output with
 a row and a scale for 128 columns, dtypes, extreme values, refusals."""
 from __future__ import annotations
 
+import threading
+
 import pytest
 import torch
 
@@ -138,7 +140,8 @@ SHARED = [(8192, "f32", 0, 0), (8200, "f32", 2, 2), (12288, "f32", 2, 2), (16384
           (16384, "f16", 0, 2), (16392, "bf16", 2, 4), (20480, "bf16", 2, 4), (32768, "f16", 2, 4),
           (32776, "bf16", 4, 0), (65536, "bf16", 4, 0), (65544, "bf16", 0, 0),
           (8193, "f32", 2, 2), (12290, "bf16", 0, 2), (16385, "f16", 2, 4), (20481, "bf16", 2, 4), (30001, "f32", 4, 4),
-          (32767, "bf16", 2, 4), (8193, "bf16", 0, 2), (9216, "bf16", 0, 2), (18432, "f16", 2, 4), (32769, "f32", 0, 0), (65535, "f16", 4, 0)]
+          (32767, "bf16", 2, 4),
+          (8193, "bf16", 0, 2), (9216, "bf16", 0, 2), (18432, "f16", 2, 4), (32769, "f32", 0, 0), (65535, "f16", 4, 0)]
 
 
 @pytest.mark.parametrize("N,xd,fwd,bwd", SHARED)
@@ -195,6 +198,53 @@ def test_many_rows_that_a_cluster_shares(N, xd, pitch):
     torch.cuda.synchronize()
     for got in ((*again, *back), (*other, *obwd)):
         assert all(torch.equal(u, v) for u, v in zip(got, (*want, *grads)))
+
+
+def test_first_calls_of_a_cluster_inside_a_capture():
+    """What the launch asks about the device is asked while a stream is captured."""
+    M, N = 300, 8968  # (no other test has CTAs of this size)
+    x, r, dy, gamma = inputs(M, N, "bf16")
+    x32, r32, _, _ = inputs(M, N, "f32")
+    rstd = torch.rand(M, device="cuda") + 0.5
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx, dgamma = dyt().rms_norm_backward(x.t, dy.t, rstd, gamma, r.t)
+        y, h, _ = dyt().rms_norm_forward(x32.t, gamma, r32.t, EPS)
+    graph.replay()
+    want, tol = S.backward(x.t, dy.t, rstd, gamma, r.t)
+    R.assert_close(dx, want[0], tol[0] + R.half_step(dx.dtype, want[0]), "dx")
+    R.assert_close(dgamma, want[1], tol[1] + R.half_step(gamma.dtype, want[1]), "dgamma")
+    want, tol = S.forward(x32.t, r32.t, gamma, EPS)
+    R.assert_close(y, want[0], tol[0] + R.half_step(y.dtype, want[0]), "y")
+    R.assert_close(h, want[1], tol[1] + R.half_step(h.dtype, want[1]), "h")
+
+
+def test_threads_that_call_at_once():
+    """Two threads on streams of their own, clusters and rows for free CTAs: the bits of one after the other."""
+    cases = [inputs(2000, N, xd, seed=i) for i, (N, xd) in enumerate([(4096, "bf16"), (9216, "bf16"), (1001, "f16")])]
+    run = lambda x, r, dy, g: (*(f := dyt().rms_norm_forward(x.t, g, r.t, EPS)),  # noqa: E731
+                               *dyt().rms_norm_backward(f[1], dy.t, f[2], g, r.t))
+    want = [run(*c) for c in cases]
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[k] = [run(*cases[(k + i) % 3]) for i in range(30)]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for k in range(2):
+        for i, o in enumerate(got[k]):
+            assert all(torch.equal(a, b) for a, b in zip(o, want[(k + i) % 3]))
 
 
 @pytest.mark.parametrize("M", [1, 2, 3, 7, 8, 9, 63, 147, 149, 297, 1000, 4097, 65537])
