@@ -122,36 +122,44 @@ __device__ __forceinline__ void store_e4m3(unsigned char *p, const float (&f)[V]
   }
 }
 
-// A lane's outputs as e4m3 bytes.
+// A lane's outputs as e4m3 bytes to the row at `out`, where the row is (`in`). RAGGED: they pass through `room`, the
+// slots that the row came from, where they lie as in their 16-byte chunks of memory. (Single bytes instead, 32 a store:
+// 8191 x 1001 fp16 10.2 us, so 9.9; with a residual 100003 x 700 bf16 133 and 125, 4096 x 20481 254 and 227; but
+// 100003 x 100 31.7 and 34.2.)
 template <typename T, int E, bool RAGGED, int MODE, typename Feed>
 __device__ __forceinline__ void store_bytes(unsigned char *out, const float2 (&f)[E / 2], const Place<MODE> &p,
-                                            const Feed &feed, int NV, int N) {
+                                            const Feed &feed, int NV, unsigned char *room, bool in) {
   constexpr int V = 16 / (int)sizeof(T);
   if constexpr (!RAGGED) {
+    if (!in) return;
 #pragma unroll
     for (int k = 0; k < E / V; ++k)
       if (p.lane + k * p.L < NV)
         store_e4m3<V>(out + (p.lane + k * p.L) * V, *reinterpret_cast<const float(*)[V]>(f + k * (V / 2)));
   } else {
-    const int c0 = column<V, E, true, MODE>(p.L, p.lane, 0), left = N - c0;
-    unsigned char *o = out + c0;
+    unsigned char *o = out + column<V, E, true, MODE>(p.L, p.lane - p.at, 0);  // the warp's stretch
+    const int len = in ? feed.need / (int)sizeof(T) : 0, d = (int)((uintptr_t)o & 15u), end = d + len;
+    unsigned char *s = room + d + p.at;
+    __syncwarp();  // all lanes have what they read there
 #pragma unroll
-    for (int g = 0; g < E; g += 8) {
-      if (feed.whole(p, g)) {
+    for (int i = 0; i < E; i += 2) {
+      const uint32_t b = e4m3_pair(f[i / 2]);
+      s[i * p.seg()] = (unsigned char)b;
+      s[(i + 1) * p.seg()] = (unsigned char)(b >> 8);
+    }
+    __syncwarp();
+    if (len > 0) {
 #pragma unroll
-        for (int i = g; i < g + 8; i += 2) {
-          const uint32_t b = e4m3_pair(f[i / 2]);
-          o[i * p.seg()] = (unsigned char)b;
-          o[(i + 1) * p.seg()] = (unsigned char)(b >> 8);
-        }
-      } else {
-#pragma unroll
-        for (int i = g; i < g + 8; i += 2) {
-          const uint32_t b = e4m3_pair(f[i / 2]);
-          if (i * p.seg() < left) o[i * p.seg()] = (unsigned char)b;
-          if ((i + 1) * p.seg() < left) o[(i + 1) * p.seg()] = (unsigned char)(b >> 8);
-        }
+      for (int k = 0; k <= E / 16; ++k) {
+        const int c = (p.at + k * p.seg()) * 16;
+        if (c >= d && c + 16 <= end) *reinterpret_cast<uint4 *>(o - d + c) = *reinterpret_cast<const uint4 *>(room + c);
       }
+      // the bytes of chunks that are not all the stretch's, at its two ends
+      const int tail = end & ~15;
+      if (d)
+        for (int c = d + p.at; c < 16 && c < end; c += p.seg()) o[c - d] = room[c];
+      if (tail >= d)
+        for (int c = tail + p.at; c < end; c += p.seg()) o[c - d] = room[c];
     }
   }
 }
@@ -220,7 +228,7 @@ __device__ __noinline__ void give_up(const RmsArgs &a, int64_t row) {
 // Measured with a residual, bf16: 16384 x 4096 80.7 us (6.65 TB/s), 65536 x 1024 80.3 (6.7), 4096 x 20480 by clusters
 // of 2 118 (5.7); without one, 100003 x 255 binary32 32.6 (6.3). 8-bit, with a residual and a scale for 128 columns:
 // 8192 x 8192 72.5 (6.5). Bound by memory; ragged 16-bit rows by instructions, as each element is a load from shared
-// memory and a store of its own: 100003 x 255 bf16 43.4 (4.7), 8191 x 1001 fp16 to 8 bits 10.2 (2.4).
+// memory and a store of its own: 100003 x 255 bf16 43.4 (4.7), 8191 x 1001 fp16 to 8 bits 9.9 (2.5).
 template <typename T, int E, int MODE, bool RAGGED, bool RES, bool Q>
 __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constant__ RmsArgs a) {
   constexpr bool CLUSTER = in_cluster(MODE), GROUP = in_warps(MODE);
@@ -312,6 +320,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = add2(v[i], r[i]);
     }
+    unsigned char *const room = feed.mine + feed.rd;  // the row's slots, free until the row after next is copied
     feed.advance(w);
     int64_t after = -1;
     if (next >= 0) after = take(next);
@@ -385,8 +394,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < P; ++i) v[i] = mul2(v[i], f2(inv));
       }
-      if (in)
-        store_bytes<T, E, RAGGED>(static_cast<unsigned char *>(a.y) + row * a.ldy + col0, v, p, feed, w.NV, N);
+      store_bytes<T, E, RAGGED>(static_cast<unsigned char *>(a.y) + row * a.ldy + col0, v, p, feed, w.NV, room, in);
     } else if (in) {
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = mul2(mul2(v[i], f2(rstd)), gam[i]);
