@@ -333,6 +333,13 @@ struct RowFeed {
     return (g + 8) * p.seg() * (int)sizeof(T) <= need;
   }
 
+  // RAGGED: none of them does. (Rows of one warp or less with 16 elements a lane fill more than half of them: never.
+  // Looked for, empty ones take 100003 x 700 bf16 104 -> 97 us, backward 121 -> 113.)
+  __device__ __forceinline__ bool empty(const Place<MODE> &p, int g) const {
+    if constexpr (E <= 16 && !in_warps(MODE)) return false;
+    else return g * p.seg() * (int)sizeof(T) >= need;
+  }
+
   // The oldest row has landed.
   __device__ __forceinline__ void wait() const {
     cp_async_wait<S - 2>();
@@ -361,6 +368,9 @@ struct RowFeed {
           if (whole(p, g)) {
 #pragma unroll
             for (int i = g; i < g + 8; ++i) v[i] = e[i * p.seg()];
+          } else if (empty(p, g)) {
+#pragma unroll
+            for (int i = g; i < g + 8; ++i) v[i] = from_f32<T>(0.0f);
           } else {
 #pragma unroll
             for (int i = g; i < g + 8; ++i) v[i] = i * p.seg() < left ? e[i * p.seg()] : from_f32<T>(0.0f);
@@ -398,7 +408,7 @@ __device__ __forceinline__ void store_pairs(T *out, const float2 (&f)[E / 2], co
       if (feed.whole(p, g)) {
 #pragma unroll
         for (int i = g; i < g + 8; ++i) o[i * p.seg()] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
-      } else {
+      } else if (!feed.empty(p, g)) {
 #pragma unroll
         for (int i = g; i < g + 8; ++i)
           if (i * p.seg() < left) o[i * p.seg()] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
