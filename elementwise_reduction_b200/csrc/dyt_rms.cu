@@ -52,7 +52,7 @@ void plan_cluster(RowPlan &p, int64_t M, int64_t N, int E, int sms, bool side) {
     const int c = kSizes[i], L = (int)ceil_div(ceil_div(N, c), 32 * E) * 32;
     if (L > dyt::norm::kBlock) continue;
     const int64_t room = side ? std::min(dyt::norm::kBlock / L, dyt::norm::kClusterMost) : 1;
-    const int64_t rows = std::max<int64_t>(1, std::min(room, ceil_div(M, sms / c)));
+    const int64_t rows = std::max<int64_t>(1, std::min(room, ceil_div(M, std::max(1, sms / c))));
     if (rows * L * kReached[i] <= most) continue;
     most = rows * L * kReached[i];
     p.cluster = c;
@@ -101,6 +101,13 @@ struct BwdPlan {
   size_t off_c = 0, bytes = 0;
 };
 
+// Few rows, one or two steps of a CTA, are one CTA's, whose column sums need no others: a launch less, and no
+// workspace. Measured, with a CTA for each row or few and in one CTA: the call, by the host, 16.6 and 12.0 us; the
+// kernels, bf16 with a residual, 1 x 4096 5.8 and 4.6, 4 x 4096 (two steps) 5.9 and 6.4, 40 x 255 binary32 (two) 4.9 and
+// 6.2; three steps, 6 x 4096 6.1 and 7.3, 300 x 64 binary32 5.9 and 9.0.
+constexpr int kOneCtaSteps = 2;
+int one_cta_rows(const RowPlan &p) { return (p.ragged && p.L < 8 ? dyt::norm::kBlock / 2 : dyt::norm::kBlock) / p.L; }
+
 BwdPlan plan_bwd(int64_t M, int64_t N, int vec, bool aligned, int sms) {
   BwdPlan b;
   b.r = plan_rms(M, N, vec, aligned, dyt::norm::kBwdElems, sms);
@@ -108,15 +115,27 @@ BwdPlan plan_bwd(int64_t M, int64_t N, int vec, bool aligned, int sms) {
     b.grid = std::min<int64_t>(M, (int64_t)sms * 2);
     b.col_ctas = (int)ceil_div(b.r.NV, kColumnsBlock);
     b.parts = std::max<int64_t>(1, std::min<int64_t>(M, (int64_t)sms * 4 / b.col_ctas));
+  } else if (!b.r.cluster && ceil_div(M, one_cta_rows(b.r)) <= kOneCtaSteps) {
+    const int side = b.r.L < 32 ? 32 / b.r.L : 1;  // rows of a warp
+    b.r.rows = (int)std::min<int64_t>(one_cta_rows(b.r), ceil_div(M, side) * side);
+    b.r.block = b.r.rows * b.r.L;
+    b.grid = 1;
+    return b;
   } else {
     // (of clusters at most as many: the launch knows how many fit)
-    b.grid = std::min<int64_t>(ceil_div(M, b.r.rows), (int64_t)(b.r.cluster ? sms / b.r.cluster : sms));
+    b.grid = std::min<int64_t>(ceil_div(M, b.r.rows), (int64_t)(b.r.cluster ? std::max(1, sms / b.r.cluster) : sms));
     b.parts = b.grid;
   }
   b.off_c = ((size_t)b.parts * (size_t)N * sizeof(double) + 15) & ~(size_t)15;
   b.bytes = b.off_c + (b.r.rowlong ? (size_t)M * sizeof(float) : 0);
   b.bytes = (b.bytes + 15) & ~(size_t)15;
   return b;
+}
+
+// The workspace, whatever the rows' alignment.
+size_t most_bytes(int64_t M, int64_t N, size_t es, int sms) {
+  const int v = 16 / (int)es;
+  return std::max(plan_bwd(M, N, v, false, sms).bytes, plan_bwd(M, N, v, true, sms).bytes);
 }
 
 void record(int op, const RowPlan *p, int64_t grid, int kernels, int64_t groups, size_t ws) {
@@ -147,7 +166,7 @@ dyt_status fit_clusters(int dev, const void *kernel, const RowPlan &r, int64_t M
   lc.cfg.gridDim.x = (unsigned)r.cluster;  // (the question is of whole clusters)
   const dyt_status st = cluster_capacity(dev, kernel, lc.cfg, r.cluster, &n);
   if (st != DYT_OK) return st;
-  *clusters = std::min<int64_t>(ceil_div(M, r.rows), std::min(n, sms / r.cluster));
+  *clusters = std::min<int64_t>(ceil_div(M, r.rows), std::min(n, std::max(1, sms / r.cluster)));
   lc.cfg.gridDim.x = (unsigned)(*clusters * r.cluster);
   return DYT_OK;
 }
@@ -257,8 +276,7 @@ size_t dyt_rms_norm_backward_workspace_bytes(int64_t M, int64_t N, dyt_dtype x_d
   if (check_shape(M, N, x_dtype) != DYT_OK || M == 0 || N == 0) return 0;
   int dev = 0, sms = 0;
   if (current_sms(&dev, &sms) != DYT_OK) return 0;
-  const int v = 16 / (int)dsize(x_dtype);
-  return std::max(plan_bwd(M, N, v, false, sms).bytes, plan_bwd(M, N, v, true, sms).bytes);
+  return std::max<size_t>(16, most_bytes(M, N, dsize(x_dtype), sms));
 } catch (...) {
   return 0;
 }
@@ -284,10 +302,11 @@ dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int
     return DYT_OK;
   }
   const size_t es = dsize(x_dtype);
-  if (!h || !dy || !dx || !rstd || !workspace || !aligned16(workspace) || !elem_aligned(h, es) ||
+  if (!h || !dy || !dx || !rstd || !aligned16(workspace) || !elem_aligned(h, es) ||
       !elem_aligned(dy, es) || !elem_aligned(dh, es) || !elem_aligned(dx, es) || !param_ok(gamma, gamma_dtype) ||
       !param_ok(rstd, DYT_F32))
     return DYT_ERR_INVALID_VALUE;
+  if (!workspace && most_bytes(M, N, es, 1)) return DYT_ERR_INVALID_VALUE;  // (whether there are any: on any device)
   int dev = 0, sms = 0;
   st = current_sms(&dev, &sms);
   if (st != DYT_OK) return st;
@@ -299,7 +318,7 @@ dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int
                      vec_pitch(ldh, es) && vec_pitch(lddy, es) && vec_pitch(lddx, es) && (!res || vec_pitch(lddh, es));
     const BwdPlan b = plan_bwd(M, N, VE, vec, sms);
     if (workspace_bytes < b.bytes) return DYT_ERR_WORKSPACE_TOO_SMALL;
-    double *parts = (double *)workspace;
+    double *parts = b.bytes ? (double *)workspace : nullptr;
     const int64_t lds[4] = {ldh, lddy, res ? lddh : lddy, lddx};
     RmsGradArgs a = {};
     a.h = h;
@@ -313,6 +332,7 @@ dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int
     a.dx = dx;
     a.lddx = lddx;
     a.parts = parts;
+    a.dgamma = dgamma;
     a.gamma_dt = (int)gamma_dtype;
     a.w = walk_of(b.r, M, N, b.grid, lds, 4, es,
                   b.r.rowlong ? 0 : dyt::norm::row_slots<T, dyt::norm::kBwdElems>(32, b.r.L, b.r.ragged));
@@ -348,7 +368,7 @@ dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int
       e = cudaLaunchKernelEx(&lc.cfg, k, a);
     }
     if (e != cudaSuccess) return cuda_fail(e);
-    if (dgamma) {
+    if (dgamma && parts) {
       PdlConfig lf((unsigned)ceil_div(N, dyt::norm::kSumCols), dyt::norm::kSumCols * dyt::norm::kSumLanes, 0, s);
       e = cudaLaunchKernelEx(&lf.cfg, dyt::norm::norm_finalize_kernel<1>, (const double *)parts, (int)parts_used, N,
                              dgamma, (int)gamma_dtype, (void *)nullptr, (int)gamma_dtype);

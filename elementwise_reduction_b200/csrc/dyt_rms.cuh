@@ -57,7 +57,8 @@ struct RmsGradArgs {
   const float *rstd;
   void *dx;
   int64_t lddx;
-  double *parts;      // [CTA][N] column sums
+  double *parts;      // [CTA][N] column sums; NULL: the one CTA's are dgamma
+  void *dgamma;       // then (NULL: not wanted)
   int gamma_dt;
   int64_t inc_dx;
   int cols;           // clusters: columns of a CTA
@@ -556,10 +557,11 @@ static_assert(rms_bwd_ring<__half>(32, 32, false, false) >= rms_sums_smem(32, 32
               "the last column sums take the ring's place");
 
 // flush_columns for one sum a column: a run's sums of the CTA's rows, added in a fixed order and moved to
-// the partial sums pg in binary64.
+// the partial sums pg in binary64, or rounded to dgamma (`only`: there are no others).
 template <int V, int E, int PER, bool RAGGED, int MODE>
-__device__ __forceinline__ void rms_flush(double *pg, const Walk &w, float2 (&dg)[E / 2], const Place<MODE> &p,
-                                          bool first, float *sh) {
+__device__ __forceinline__ void rms_flush(const RmsGradArgs &a, double *pg, const Walk &w, float2 (&dg)[E / 2],
+                                          const Place<MODE> &p, bool first, float *sh) {
+  const bool only = !in_cluster(MODE) && a.parts == nullptr;
   constexpr bool GROUP = in_warps(MODE);
   const int N = (int)w.N;
   const int copies = !GROUP ? (int)blockDim.x / 32 : w.rows;
@@ -574,7 +576,8 @@ __device__ __forceinline__ void rms_flush(double *pg, const Walk &w, float2 (&dg
       t[1] += (double)q[(w + 1) * plane];
     }
     if (copies & 1) t[0] += (double)q[(copies - 1) * plane];
-    pg[c] = first ? t[0] + t[1] : pg[c] + (t[0] + t[1]);
+    if (!only) pg[c] = first ? t[0] + t[1] : pg[c] + (t[0] + t[1]);
+    else if (a.dgamma) store_param(a.dgamma, a.gamma_dt, c, t[0] + t[1]);
   };
 #pragma unroll
   for (int k = 0; k < E; k += PER) {
@@ -710,7 +713,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
     row += w.step;
     out += a.inc_dx;
     if (++run == kRunRows && it + 1 < steps) {
-      rms_flush<V, E, V, RAGGED>(parts, w, dg, p, first, sh);
+      rms_flush<V, E, V, RAGGED>(a, parts, w, dg, p, first, sh);
       first = false;
       run = 0;
     }
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
   // CTA is here, also one that left at the last step.
   cp_async_wait<0>();
   __syncthreads();
-  rms_flush<V, E, E, RAGGED>(parts, w, dg, p, first, reinterpret_cast<float *>(dyn));
+  rms_flush<V, E, E, RAGGED>(a, parts, w, dg, p, first, reinterpret_cast<float *>(dyn));
   if constexpr (CLUSTER) cluster_sync();  // a CTA ends behind what the others send it
 }
 

@@ -159,9 +159,10 @@ def rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, rstd: torch.Tensor, gam
         else:
             gg = _vector(dgamma, "dgamma", N, index, (gamma.dtype,))
     if ws is None:
-        n = _bytes(_SIZE, index, M, N, code)
-        ws = _scratch(n, h.device)
-        wp = ws.data_ptr()
+        n, wp = _bytes(_SIZE, index, M, N, code), None
+        if n > 16:  # (few rows need none)
+            ws = _scratch(n, h.device)
+            wp = ws.data_ptr()
     else:
         wp, n = _workspace(ws, index), ws.numel()
     st = _BACKWARD(

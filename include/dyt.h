@@ -566,6 +566,8 @@ dyt_status dyt_rms_norm_quantize(const void *x, int64_t ldx, const void *residua
  *             NULL: none
  *   dgamma    [N] gamma_dtype, written; NULL: not wanted
  *   dx        may alias h, dy or dh with an equal pitch
+ * Few rows, up to two steps of one CTA, take one launch and no workspace: it may be
+ * NULL where dyt_rms_norm_backward_workspace_bytes gives 16, the least it gives.
  * M * N == 0: dgamma (when N > 0) is set to zero, and no workspace is used.
  */
 size_t dyt_rms_norm_backward_workspace_bytes(int64_t M, int64_t N, dyt_dtype x_dtype);

@@ -120,7 +120,7 @@ WIDTHS = [1, 2, 3, 4, 7, 8, 9, 16, 17, 24, 31, 32, 33, 64, 65, 100, 127, 128, 12
 @pytest.mark.parametrize("N", WIDTHS)
 def test_widths(N, xd):
     _, bwd = check(37, N, xd)
-    assert bwd["kernels"] == 2
+    assert bwd["kernels"] == (1 if bwd["grid"] == 1 else 2)
 
 
 @pytest.mark.parametrize("xd", ["f32", "bf16"])
@@ -198,6 +198,24 @@ def test_many_rows_that_a_cluster_shares(N, xd, pitch):
     torch.cuda.synchronize()
     for got in ((*again, *back), (*other, *obwd)):
         assert all(torch.equal(u, v) for u, v in zip(got, (*want, *grads)))
+
+
+@pytest.mark.parametrize("xd,pd", [("f32", "f32"), ("bf16", "f32"), ("f16", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("N,rows", [(16, 128), (64, 128), (96, 64), (100, 64), (250, 32), (512, 16), (500, 16), (1024, 8),
+                                    (1001, 8), (4096, 2), (8191, 1)])
+def test_few_rows_are_one_ctas(N, rows, xd, pd):
+    """One, a whole step, a row more, two steps, a row beyond them: the last with partial sums."""
+    for M in sorted({1, rows, rows + 1, 2 * rows, 2 * rows + 1}):
+        x, r, dy, gamma = inputs(M, N, xd, pd)
+        rstd = torch.rand(M, device="cuda") + 0.5
+        info = check_backward(x, dy, rstd, gamma, r)
+        if info["grid"] == 1:
+            assert info["kernels"] == 1 and info["workspace_bytes"] == 0
+        else:
+            assert info["kernels"] == 2 and M > rows
+        dx, none = dyt().rms_norm_backward(x.t, dy.t, rstd, gamma, r.t, frozen=True)
+        assert none is None and dyt().dyt_last_launch_info()["kernels"] == 1
+        assert torch.equal(dx, dyt().rms_norm_backward(x.t, dy.t, rstd, gamma, r.t)[0])
 
 
 def test_first_calls_of_a_cluster_inside_a_capture():
@@ -593,7 +611,7 @@ def test_module_captured_with_its_backward():
 
 def test_refusals():
     d = dyt()
-    x = torch.randn(6, 64, device="cuda")
+    x, many = torch.randn(6, 64, device="cuda"), torch.randn(600, 64, device="cuda")
     gamma, rstd = torch.ones(64, device="cuda"), torch.ones(6, device="cuda")
     bad = [lambda: d.rms_norm_forward(x, gamma[:63]), lambda: d.rms_norm_forward(x, gamma.double()),
            lambda: d.rms_norm_forward(x, gamma.cpu()), lambda: d.rms_norm_forward(x.double()),
@@ -610,7 +628,8 @@ def test_refusals():
            lambda: d.rms_norm_backward(x, x, rstd, gamma, x[:, :63]),
            lambda: d.rms_norm_backward(x, x, rstd, dgamma=gamma),
            lambda: d.rms_norm_backward(x, x, rstd, gamma, dgamma=gamma, frozen=True),
-           lambda: d.rms_norm_backward(x, x, rstd, gamma, ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: d.rms_norm_backward(many, many, many[:, 0].contiguous(), gamma,
+                                       ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
            lambda: d.rms_norm_backward(x, x, rstd.double(), gamma)]
     for k, call in enumerate(bad):
         with pytest.raises((ValueError, TypeError, d.DytError)):

@@ -76,7 +76,9 @@ def test_norm_refusals():
     for kw in ({"q": 0}, {"ldq": 7}, {"s": 0}, {"s": A + 2}, {"group": 64}, {"group": -128}, {"group": 1}):
         assert rms_q8(**kw) == 1, kw
     for kw in ({"M": -1}, {"N": -1}, {"ldh": 7}, {"lddy": 7}, {"lddh": 7}, {"lddx": 7}, {"h": 0}, {"dy": 0}, {"dx": 0},
-               {"rstd": 0}, {"ws": 0}, {"ws": A + 8}, {"h": A + 1}, {"dy": A + 2}, {"dh": A + 2}, {"dx": A + 3},
+               {"rstd": 0}, {"ws": 0, "M": 4000},
+               {"ws": 0, "N": 9000, "ldh": 9000, "lddy": 9000, "lddh": 9000, "lddx": 9000},
+               {"ws": 0, "N": 70000, "ldh": 70000, "lddy": 70000, "lddh": 70000, "lddx": 70000}, {"ws": A + 8}, {"h": A + 1}, {"dy": A + 2}, {"dh": A + 2}, {"dx": A + 3},
                {"g": A + 1}, {"dg": A + 2}, {"rstd": A + 1}):
         assert rms_bwd(**kw) == 1, kw
     assert rms_bwd(xd=3) == 2 and rms_bwd(gd=-1) == 2
