@@ -23,6 +23,28 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// v to the place of *p in another CTA's shared memory (which has started, and does not end before a barrier).
+__device__ __forceinline__ void cluster_put(float4 *p, uint32_t cta, float4 v) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(p);
+  asm volatile(
+      "{.reg .u32 r; mapa.shared::cluster.u32 r, %0, %1; st.shared::cluster.v4.f32 [r], {%2, %3, %4, %5};}" ::"r"(at),
+      "r"(cta), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+      : "memory");
+}
+__device__ __forceinline__ void cluster_put(float *p, uint32_t cta, float v) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(p);
+  asm volatile("{.reg .u32 r; mapa.shared::cluster.u32 r, %0, %1; st.shared::cluster.f32 [r], %2;}" ::"r"(at), "r"(cta),
+               "f"(v)
+               : "memory");
+}
+template <typename H>
+__device__ __forceinline__ void cluster_put(H *p, uint32_t cta, H v) {  // 16 bits
+  static_assert(sizeof(H) == 2);
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(p);
+  asm volatile("{.reg .u32 r; mapa.shared::cluster.u32 r, %0, %1; st.shared::cluster.u16 [r], %2;}" ::"r"(at), "r"(cta),
+               "h"(*reinterpret_cast<const unsigned short *>(&v))
+               : "memory");
+}
 
 // Where a row's sums of all the cluster's warps meet: each warp sends its own to every CTA (st.async) and waits for all
 // of them at its CTA's mbarrier. Rows take turns between two places; a warp is at most one row ahead of another, as it

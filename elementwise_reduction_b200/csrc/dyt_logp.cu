@@ -23,11 +23,37 @@ constexpr int kOpLogpForward = 12, kOpLogpBackward = 13;  // dyt_launch_info::op
 struct LogpPlan {
   LossPlan p;
   int together;  // rows that a warp of logp_top_kernel takes at a time
+  int cluster;   // few rows: CTAs that share one (logp_few_kernel), else 0
+  int warps;     // of each
   size_t off_tops, off_taken, bytes;
 };
 
+// Few rows: one kernel, where their clusters are at most so many CTAs, 4 for each of 148 SMs. Measured, in two kernels
+// and in one, bf16 with 20 alternatives: 1 x 131072 8.6 and 8.2 us, 32 x 131072 10.5 and 9.4, 64 x 131072 14.7 and
+// 10.9, 256 x 32000 14.9 and 10.8, but 128 x 131072 (1024 CTAs) without alternatives 11.4 and 12.9, 512 x 32000 18.8
+// and 19.5; a call by the host 20.2 and 16.2.
+constexpr int kFewCtas = 592;
+int few_cluster(int64_t M, int64_t N, size_t es, int *warps) {
+  const int64_t batches = std::max<int64_t>(1, ceil_div(ceil_div(N * (int64_t)es, 16), dyt::loss::kBatch * 32));
+  if (batches > dyt::loss::kFewBatches) return 0;
+  int w = 1, c = 1;
+  while (w < dyt::loss::kFewWarps && w < batches) w <<= 1;
+  while (c < dyt::kMaxCluster && c * w < batches) c <<= 1;
+  *warps = w;
+  return M * c <= kFewCtas ? c : 0;
+}
+
 LogpPlan plan_logp(int64_t M, int64_t N, int top, size_t es, int sms) {
   LogpPlan q = {};
+  q.cluster = few_cluster(M, N, es, &q.warps);
+  if (q.cluster) {
+    q.p.S = q.cluster * q.warps;
+    q.p.block = q.warps * 32;
+    q.p.grid = M * q.cluster;
+    q.p.cta = true;
+    q.bytes = 16;
+    return q;
+  }
   q.p = plan_forward(M, N, es, sms);
   if (top > 0) {
     // as many rows at a time as let the warps take them in one round
@@ -72,19 +98,20 @@ dyt_status dyt_log_probs_forward(const void *logits, int64_t ld, const void *tok
   }
   if (M == 1) ld = N;  // one row has no pitch
   const size_t es = dsize(dtype);
-  if (!logits || (tokens && !logp) || !entropy || !stats || !workspace || (top > 0 && (!top_logp || !top_tokens)) ||
+  if (!logits || (tokens && !logp) || !entropy || !stats || (top > 0 && (!top_logp || !top_tokens)) ||
       !elem_aligned(logits, es) || (tokens && !elem_aligned(tokens, token_bytes)) || !elem_aligned(logp, 4) ||
       !elem_aligned(entropy, 4) || !elem_aligned(top_logp, 4) || !elem_aligned(top_tokens, 8) ||
       !elem_aligned(stats, 8) || !aligned16(workspace))
     return DYT_ERR_INVALID_VALUE;
   const float C = (float)(dyt::loss::kLog2eD / temperature);
-  if (!(C > 0.0f) || std::isinf(C)) return DYT_ERR_INVALID_VALUE;
+  int warps = 0;
+  if (!(C > 0.0f) || std::isinf(C) || (!workspace && !few_cluster(M, N, es, &warps))) return DYT_ERR_INVALID_VALUE;
   int dev = 0, sms = 0;
   st = current_sms(&dev, &sms);
   if (st != DYT_OK) return st;
   const LogpPlan q = plan_logp(M, N, top, es, sms);
   const LossPlan &p = q.p;
-  if (workspace_bytes < q.bytes) return DYT_ERR_WORKSPACE_TOO_SMALL;
+  if (!q.cluster && workspace_bytes < q.bytes) return DYT_ERR_WORKSPACE_TOO_SMALL;
   LogpArgs a = {};
   a.z = logits;
   a.ld = ld;
@@ -103,7 +130,7 @@ dyt_status dyt_log_probs_forward(const void *logits, int64_t ld, const void *tok
   a.S = p.S;
   a.most = p.most;
   a.batches = (int)ceil_div(ceil_div(N * (int64_t)es, 16), dyt::loss::kBatch * 32);
-  a.listed = tokens != nullptr && lists_rows(p, M);
+  a.listed = !q.cluster && tokens != nullptr && lists_rows(p, M);
   a.aligned = N % (16 / (int64_t)es) == 0 && aligned16(logits) && vec_pitch(ld, es);
   a.wide_tokens = token_bytes == 8;
   a.K = top;
@@ -113,6 +140,18 @@ dyt_status dyt_log_probs_forward(const void *logits, int64_t ld, const void *tok
   const cudaStream_t s = (cudaStream_t)stream;
   return with_type(dtype, [&](auto t) -> dyt_status {
     using T = decltype(t);
+    if (q.cluster) {
+      const auto k = top > 0 ? dyt::loss::logp_few_kernel<T, true> : dyt::loss::logp_few_kernel<T, false>;
+      const size_t tops = top > 0 ? (size_t)a.batches * 32 * es : 0;
+      const dyt_status ready = prepare_smem(dev, (const void *)k, (int)tops);
+      if (ready != DYT_OK) return ready;
+      PdlConfig l((unsigned)p.grid, p.block, tops, s);
+      l.cluster((unsigned)q.cluster);
+      const cudaError_t e = cudaLaunchKernelEx(&l.cfg, k, a);
+      if (e != cudaSuccess) return cuda_fail(e);
+      record(kOpLogpForward, &p, (int)(16 / sizeof(T)), 1, 0);
+      return DYT_OK;
+    }
     const auto rows = top > 0 ? dyt::loss::logp_rows_kernel<T, true> : dyt::loss::logp_rows_kernel<T, false>;
     const auto finish = top > 0 ? dyt::loss::logp_top_kernel<T> : dyt::loss::logp_finish_kernel<T>;
     const size_t smem = dyt::loss::rows_smem(p.block);

@@ -20,6 +20,7 @@
 
 #include <type_traits>
 
+#include "dyt_cluster.cuh"
 #include "dyt_loss.cuh"
 
 namespace dyt {
@@ -210,6 +211,18 @@ __device__ __forceinline__ float warp_largest(float v) {
   return r;
 }
 
+// A warp's sums together, in lane 0: one instruction for the largest, and the two sums by halves of the warp, a lane
+// of each half has one.
+__device__ __forceinline__ void lanes_together(Moments &r, float C, int lane) {
+  raise(r, warp_largest(r.m), C);
+  const bool up = (lane & 16) != 0;
+  float sum = (up ? r.t : r.s) + __shfl_xor_sync(0xFFFFFFFFu, up ? r.s : r.t, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  r.t = __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+  r.s = sum;
+}
+
 // Whether a row counts.
 __device__ __forceinline__ bool row_counts(const LogpArgs &a, int64_t row) {
   return a.tokens == nullptr || token_at(a.tokens, a.wide_tokens, row) != a.ignore;
@@ -336,14 +349,7 @@ __global__ void __launch_bounds__(kRowsBlock, 2) logp_rows_kernel(LogpArgs a) {
         const float2 p[1] = {make_float2(first, last)};
         add_values(r, p, C);
       }
-      // one instruction for the largest, and the two sums by halves of the warp: a lane of each half has one
-      raise(r, warp_largest(r.m), C);
-      const bool up = (lane & 16) != 0;
-      float sum = (up ? r.t : r.s) + __shfl_xor_sync(0xFFFFFFFFu, up ? r.s : r.t, 16);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      r.t = __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
-      r.s = sum;
+      lanes_together(r, C, lane);
       if (lane == 0) a.parts[row * a.most + part] = make_float4(r.m, r.s, r.t, 0.0f);
     }
     // The batches of nothing at the end: the ring starts the next items where it stands.
@@ -445,19 +451,19 @@ __device__ __forceinline__ float sort_lanes(float v, int lane, int from) {
   return v;
 }
 
-// A row's vectors and the largest logits of its chunks.
-template <typename T>
+// A row's vectors and the largest logits of its chunks. (SHARED: those are in shared memory.)
+template <typename T, bool SHARED = false>
 struct RowTops {
   static constexpr int V = 16 / (int)sizeof(T);
   const T *z, *tops;
   int head, nb, batches;
   int vecs;  // 16-byte vectors of tops; 0: too few for the warp (less than V batches), taken one by one
-  __device__ __forceinline__ RowTops(const LogpArgs &a, int64_t row) {
+  __device__ __forceinline__ RowTops(const LogpArgs &a, int64_t row, const T *all) {
     z = static_cast<const T *>(a.z) + row * a.ld;
     head = a.aligned ? 0 : head_elems(z, a.N);
     nb = (int)((a.N - head) / V);
     batches = (nb + kBatch * 32 - 1) / (kBatch * 32);
-    tops = static_cast<const T *>(a.tops) + row * a.batches * 32;
+    tops = all;
     vecs = batches * 32 / V;
     if (vecs < 32) vecs = 0;
   }
@@ -466,9 +472,12 @@ struct RowTops {
 #pragma unroll
     for (int u = 0; u < 8; ++u)
       if (i0 + u * 32 + lane < vecs)
-        cp_async16(&b.stage[u][lane], reinterpret_cast<const uint4 *>(tops) + i0 + u * 32 + lane);
-    cp_async_commit();
-    cp_async_wait<0>();
+        if constexpr (SHARED) b.stage[u][lane] = reinterpret_cast<const uint4 *>(tops)[i0 + u * 32 + lane];
+        else cp_async16(&b.stage[u][lane], reinterpret_cast<const uint4 *>(tops) + i0 + u * 32 + lane);
+    if constexpr (!SHARED) {
+      cp_async_commit();
+      cp_async_wait<0>();
+    }
   }
   // The K-th largest of 64 groups' largest logits, two groups a lane: at least K logits are not below it.
   // Leaves the last 8 vectors of tops in the stage.
@@ -513,8 +522,9 @@ struct Bits {
 };
 
 // Candidates among the elements off the vectors (less than 32): those not below v.
-template <typename T>
-__device__ __forceinline__ int off_vectors(const LogpArgs &a, const RowTops<T> &t, float v, Key *keys, int lane) {
+template <typename T, bool SHARED>
+__device__ __forceinline__ int off_vectors(const LogpArgs &a, const RowTops<T, SHARED> &t, float v, Key *keys,
+                                           int lane) {
   const int tail = (int)((a.N - t.head) % RowTops<T>::V);
   const bool off = lane < t.head + tail;
   const uint32_t col = lane < t.head ? (uint32_t)lane : (uint32_t)(a.N - tail + lane - t.head);
@@ -527,8 +537,8 @@ __device__ __forceinline__ int off_vectors(const LogpArgs &a, const RowTops<T> &
 
 // The K largest logits of a row into b.first, in order; returns how many there are (K, but for NaN). -1: there
 // are more candidates than room, as where many logits are equal.
-template <typename T>
-__device__ __forceinline__ int find_best(const LogpArgs &a, const RowTops<T> &t, Best &b, int lane) {
+template <typename T, bool SHARED>
+__device__ __forceinline__ int find_best(const LogpArgs &a, const RowTops<T, SHARED> &t, Best &b, int lane) {
   constexpr int V = RowTops<T>::V;
   using B = Bits<V>;
   const int K = a.K;
@@ -580,10 +590,10 @@ __device__ __forceinline__ int find_best(const LogpArgs &a, const RowTops<T> &t,
 }
 
 // The same where candidates are many: a chunk at a time, all but the K largest dropped whenever there is no room.
-template <typename T>
-__device__ __noinline__ int find_best_of_many(const LogpArgs &a, int64_t row, Best &b, int lane) {
+template <typename T, bool SHARED>
+__device__ __noinline__ int find_best_of_many(const LogpArgs &a, int64_t row, const T *tops, Best &b, int lane) {
   constexpr int V = RowTops<T>::V;
-  const RowTops<T> t(a, row);
+  const RowTops<T, SHARED> t(a, row, tops);
   const int K = a.K;
   Key least = logit_key(t.bound(b, K, lane), 0xFFFFFFFFu);  // of that value at any column
   __syncwarp();
@@ -705,13 +715,32 @@ __global__ void __launch_bounds__(kFinishBlock) logp_finish_kernel(LogpArgs a) {
   }
 }
 
+// A row's alternatives, from its maximum and the log of its sum.
+template <typename T, bool SHARED>
+__device__ __forceinline__ void write_best(const LogpArgs &a, int64_t row, const T *tops, bool counts, double m,
+                                           double s, Best &b, int lane) {
+  int n = 0;
+  if (counts) {
+    n = find_best<T>(a, RowTops<T, SHARED>(a, row, tops), b, lane);
+    if (n < 0) n = find_best_of_many<T, SHARED>(a, row, tops, b, lane);
+  }
+  if (lane < a.K) {
+    const bool found = lane < n;
+    const Key key = found ? b.first[lane] : 0;
+    const float none = counts ? __int_as_float(0x7FC00000) : 0.0f;
+    const int64_t at = row * a.K + lane;
+    a.best[at] = found ? (float)(((double)key_value(key) - m) * a.inv_t - s) : none;
+    a.ids[at] = found ? (long long)key_col(key) : -1;
+  }
+}
+
 constexpr int kTopBlock = 128, kTopCtas = 6;  // CTAs that an SM holds
 // The same with alternatives. A warp takes `a.together` rows at a time: a lane each for their parts and their scalars,
 // all lanes for each row's alternatives. (One row: all lanes for its parts too.)
 // Measured, both kernels: 8192 x 131072 bf16 without alternatives 349 us, with 8 of them 388, with 20 406, with 32 432
-// (4 KB of chunk maxima a row are written and read, and a few chunks read again); 1 x 131072 with 20 8.4. Bound by
-// latency: a row is four trips to memory one after the other (maxima, chunks over the bound, their logits, outputs),
-// with 24 warps an SM to hide them.
+// (4 KB of chunk maxima a row are written and read, and a few chunks read again). Bound by latency: a row is four trips
+// to memory one after the other (maxima, chunks over the bound, their logits, outputs), with 24 warps an SM to hide
+// them.
 template <typename T>
 __global__ void __launch_bounds__(kTopBlock, kTopCtas) logp_top_kernel(const __grid_constant__ LogpArgs a) {
   __shared__ Best best[kTopBlock / 32];
@@ -740,25 +769,99 @@ __global__ void __launch_bounds__(kTopBlock, kTopCtas) logp_top_kernel(const __g
     for (int k = 0; k < rows; ++k) {
       const bool counts = counting >> k & 1u;
       const double m_k = (double)__shfl_sync(0xFFFFFFFFu, mine.m, k), s_k = __shfl_sync(0xFFFFFFFFu, s, k);
-      int n = 0;
-      if (counts) {
-        n = find_best<T>(a, RowTops<T>(a, base + k), b, lane);
-        if (n < 0) n = find_best_of_many<T>(a, base + k, b, lane);
-      }
-      if (lane < a.K) {
-        const bool found = lane < n;
-        const Key key = found ? b.first[lane] : 0;
-        const float none = counts ? __int_as_float(0x7FC00000) : 0.0f;
-        const int64_t at = (base + k) * a.K + lane;
-        a.best[at] = found ? (float)(((double)key_value(key) - m_k) * a.inv_t - s_k) : none;
-        a.ids[at] = found ? (long long)key_col(key) : -1;
-      }
+      const T *tops = static_cast<const T *>(a.tops) + (base + k) * a.batches * 32;
+      write_best<T, false>(a, base + k, tops, counts, m_k, s_k, b, lane);
       __syncwarp();  // (the next row's candidates take their place)
     }
     base += step;
     in = LogpInput();
     if (lane < R && base + lane < a.M) in = logp_input<T>(a, base + lane);
   }
+}
+
+// ---- few rows ---------------------------------------------------------------------------
+
+constexpr int kFewWarps = 8;       // of a CTA
+constexpr int kFewBatches = 256;   // of a row, at most (2 x 500000 binary32, 489: 30.5 us, in two kernels 29.1)
+
+// A row is a cluster's (dyt_cluster.cuh), a batch at a time a warp's; its sums and its chunks' largest logits meet in
+// the first CTA's shared memory, whose first warp finishes the row: one launch, and no workspace. Measured: 1 x 131072
+// bf16 4.4 us, with 20 alternatives 8.2; 7 x 50001 binary32 with 20 10.3. Bound by latency: the batch, the exchange,
+// the chunks over the bound and the ranking one after the other.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kFewWarps * 32) logp_few_kernel(const __grid_constant__ LogpArgs a) {
+  constexpr int V = 16 / (int)sizeof(T), P = V / 2;
+  using IO = VecIO<T, V>;
+  __shared__ float4 parts[kMaxCluster * kFewWarps];
+  __shared__ Best best;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  pdl_prologue();
+  if (TOP && dynamic_smem_bytes() < (size_t)a.batches * 32 * sizeof(T)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const uint32_t rank = cluster_rank(), ctas = cluster_ctas();
+  const int64_t row = blockIdx.x / ctas;
+  T *const tops = reinterpret_cast<T *>(dyn);
+  const float C = a.C;
+  const bool counts = row_counts(a, row);  // (all of the cluster agree)
+  LogpInput in;
+  if (rank == 0 && threadIdx.x == 0) in = logp_input<T>(a, row);
+  Moments r;
+  if (counts) {
+    const RowTops<T, true> t(a, row, tops);
+    const uint4 *zv = reinterpret_cast<const uint4 *>(t.z + t.head);
+    cluster_sync();  // all CTAs have started
+    for (int b = (int)rank * warps + warp; b < t.batches; b += (int)ctas * warps) {
+      const uint4 *src = zv + b * (kBatch * 32) + lane;
+      const int n = t.nb - b * (kBatch * 32);
+      float top;
+      bool done = false;
+      if (n >= kBatch * 32) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) raw[u] = __ldcg(src + u * 32);
+        done = add_batch<T>(r, raw, C, top);
+      }
+      if (!done) {  // (see logp_rows_kernel)
+        top = kNegInf;
+#pragma unroll 1
+        for (int u = 0; u * 32 < n && u < kBatch; ++u) {
+          float2 v[P];
+#pragma unroll
+          for (int i = 0; i < P; ++i) v[i] = f2(kNegInf);
+          if (u * 32 + lane < n) IO::unpack2(__ldcg(src + u * 32), v);
+          top = fmaxf(top, add_values(r, v, C));
+        }
+      }
+      if constexpr (TOP) cluster_put(tops + b * 32 + lane, 0u, from_f32<T>(top));
+    }
+    if (!a.aligned && rank == 0 && warp == 0) {  // the elements off the vectors
+      const int tail = (int)((a.N - t.head) % V);
+      const float2 p[1] = {make_float2(lane < t.head ? to_f32<T>(t.z[lane]) : kNegInf,
+                                       lane < tail ? to_f32<T>(t.z[a.N - tail + lane]) : kNegInf)};
+      add_values(r, p, C);
+    }
+    lanes_together(r, C, lane);
+    if (lane == 0) cluster_put(parts + rank * warps + warp, 0u, make_float4(r.m, r.s, r.t, 0.0f));
+    cluster_sync();
+  }
+  if (rank != 0 || warp != 0) return;
+  Moments mine;
+  if (counts) {
+    for (int i = lane; i < (int)ctas * warps; i += 32) {
+      const float4 p = parts[i];
+      Moments o;
+      o.m = p.x;
+      o.s = p.y;
+      o.t = p.z;
+      mine = join(mine, o, C);
+    }
+    mine = join_lanes(mine, C);
+  }
+  double s = 0.0;
+  if (lane == 0) s = finish_row(a, row, mine, in);
+  if constexpr (TOP)
+    write_best<T, true>(a, row, tops, counts, (double)__shfl_sync(0xFFFFFFFFu, mine.m, 0),
+                        __shfl_sync(0xFFFFFFFFu, s, 0), best, lane);
 }
 
 // ---- backward -------------------------------------------------------------------------

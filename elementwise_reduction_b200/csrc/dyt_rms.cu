@@ -103,8 +103,8 @@ struct BwdPlan {
 
 // Few rows, one or two steps of a CTA, are one CTA's, whose column sums need no others: a launch less, and no
 // workspace. Measured, with a CTA for each row or few and in one CTA: the call, by the host, 16.6 and 12.0 us; the
-// kernels, bf16 with a residual, 1 x 4096 5.8 and 4.6, 4 x 4096 (two steps) 5.9 and 6.4, 40 x 255 binary32 (two) 4.9 and
-// 6.2; three steps, 6 x 4096 6.1 and 7.3, 300 x 64 binary32 5.9 and 9.0.
+// kernels, bf16 with a residual, 1 x 4096 5.8 and 4.6, 4 x 4096 (two steps) 5.9 and 6.4, 40 x 255 binary32 (two) 4.9
+// and 6.2; three steps, 6 x 4096 6.1 and 7.3, 300 x 64 binary32 5.9 and 9.0.
 constexpr int kOneCtaSteps = 2;
 int one_cta_rows(const RowPlan &p) { return (p.ragged && p.L < 8 ? dyt::norm::kBlock / 2 : dyt::norm::kBlock) / p.L; }
 

@@ -58,9 +58,10 @@ def log_probs_forward(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
     _top(top, N)
     ld, code, dev, rows = _pitch(logits, "logits"), _code(logits, "logits"), logits.device, logits.shape[:-1]
     if ws is None:
-        n = _bytes(_SIZE, index, M, N, top, code)
-        ws = _scratch(n, dev)
-        wp = ws.data_ptr()
+        n, wp = _bytes(_SIZE, index, M, N, top, code), None
+        if n > 16:  # (few rows need none)
+            ws = _scratch(n, dev)
+            wp = ws.data_ptr()
     else:
         wp, n = _workspace(ws, index), ws.numel()
     logp = tp = None

@@ -587,7 +587,11 @@ dyt_status dyt_rms_norm_backward(const void *h, int64_t ldh, const void *dy, int
  *   top_tokens[i][k], top_logp[i][k]: column and lp of the k-th largest logit of
  *              the row (k < top); of equal logits the lower column comes first
  *
- * Two kernel launches. The logits are read once, and with alternatives a few
+ * Two kernel launches, or one: few rows (with a cluster of up to 8 CTAs each, at most
+ * 592 CTAs, and rows of at most 1 MB) are finished where they are read, without a
+ * workspace: it may be NULL where dyt_log_probs_workspace_bytes gives 16, the least it
+ * gives. Which it is does not change what is computed, but may the last bits of a row's
+ * sums. The logits are read once, and with alternatives a few
  * pieces of a row (128 bytes each) a second time. Row sums are binary32, the
  * rows' scalar arithmetic binary64, each output rounded once.
  *   logits    [M*N] dtype, row pitch ld, any element alignment

@@ -54,7 +54,7 @@ class Case:
                 R.assert_close(g, w, t, name)
             else:
                 assert name == "logp" or self.top == 0
-        assert info["op"] == 12 and info["kernels"] == 2
+        assert info["op"] == 12 and info["kernels"] == (1 if info["workspace_bytes"] == 0 else 2)
         return got, info
 
     def check_backward(self, got, scale=1.0, out_pitch=None, out_offset=0, da=True, db=True):
@@ -83,6 +83,32 @@ def test_widths(N, dtype):
         got, _ = c.check_forward()
         if top in (0, 5):
             c.check_backward(got, scale=100.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N", [n for n in WIDTHS if n < 20000])
+def test_widths_of_many_rows(N, dtype):
+    c = Case(600, N, dtype, masked=0.2)
+    got, info = c.check_forward()
+    assert info["kernels"] == 2
+    c.check_backward(got)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,top", [(1, 131072, 20), (74, 131072, 32), (75, 131072, 20), (8, 151936, 1),
+                                     (1, 500001, 32), (64, 5000, 20), (592, 1000, 5), (593, 1000, 5), (1, 1, 1), (2, 1048571, 3)])
+def test_few_rows(M, N, top, dtype):
+    """One kernel where the rows' clusters are few, two beyond; rows among them that do not count."""
+    for masked in (0.0, 0.5):
+        c = Case(M, N, dtype, top=top, masked=masked)
+        got, info = c.check_forward()
+        batches = -(-N * c.z.t.element_size() // 4096)
+        ctas = min(8, 1 << max(0, -(-batches // 8) - 1).bit_length())
+        assert info["kernels"] == (1 if batches <= 256 and M * ctas <= 592 else 2)
+        out = Case(M, N, dtype, top=0, masked=masked).check_forward()[0]
+        assert all(torch.equal(got[i], out[i]) for i in (0, 1, 4))  # (with alternatives or without)
+    none = Case(M, N, dtype, top=top, tokens=False)
+    none.check_forward()
 
 
 @pytest.mark.parametrize("M", [1, 2, 5, 64, 65, 1183, 1184, 1185, 5000])
@@ -183,7 +209,8 @@ def test_tokens_outside_the_vocabulary(N):
 
 # ---- equal logits, masks, infinities -------------------------------------------------------------
 
-SHAPES = [(6, 20), (6, 33), (5, 2048), (5, 2049), (4, 12345), (3, 131072), (1500, 4000)]
+SHAPES = [(6, 20), (6, 33), (5, 2048), (5, 2049), (4, 12345), (3, 131072), (1500, 4000),
+          (700, 20), (700, 33), (600, 2049), (600, 12345), (80, 131072)]  # (few rows take a kernel of their own)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -506,7 +533,8 @@ def test_refusals():
            lambda: d.log_probs_forward(z, t, 21), lambda: d.log_probs_forward(z, t, -1),
            lambda: d.log_probs_forward(z, t, temperature=0.0), lambda: d.log_probs_forward(z, t, temperature=NAN),
            lambda: d.log_probs_forward(z[:, :0], t), lambda: d.log_probs_forward(v[0], t),
-           lambda: d.log_probs_forward(z, t, ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: d.log_probs_forward(z.repeat(100, 1), t.repeat(100),
+                                       ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
            lambda: d.log_probs_forward(z, t, ws=v), lambda: d.log_probs_workspace(z, 40),
            lambda: d.log_probs_backward(z, None, st, None, v), lambda: d.log_probs_backward(z, t, st, None, v, v),
            lambda: d.log_probs_backward(z, t, st[:5], v, v), lambda: d.log_probs_backward(z, t, st, v[:5], v),

@@ -201,8 +201,8 @@ def test_many_rows_that_a_cluster_shares(N, xd, pitch):
 
 
 @pytest.mark.parametrize("xd,pd", [("f32", "f32"), ("bf16", "f32"), ("f16", "bf16"), ("bf16", "bf16")])
-@pytest.mark.parametrize("N,rows", [(16, 128), (64, 128), (96, 64), (100, 64), (250, 32), (512, 16), (500, 16), (1024, 8),
-                                    (1001, 8), (4096, 2), (8191, 1)])
+@pytest.mark.parametrize("N,rows", [(16, 128), (64, 128), (96, 64), (100, 64), (250, 32), (512, 16), (500, 16),
+                                    (1024, 8), (1001, 8), (4096, 2), (8191, 1)])
 def test_few_rows_are_one_ctas(N, rows, xd, pd):
     """One, a whole step, a row more, two steps, a row beyond them: the last with partial sums."""
     for M in sorted({1, rows, rows + 1, 2 * rows, 2 * rows + 1}):

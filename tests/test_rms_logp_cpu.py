@@ -78,7 +78,8 @@ def test_norm_refusals():
     for kw in ({"M": -1}, {"N": -1}, {"ldh": 7}, {"lddy": 7}, {"lddh": 7}, {"lddx": 7}, {"h": 0}, {"dy": 0}, {"dx": 0},
                {"rstd": 0}, {"ws": 0, "M": 4000},
                {"ws": 0, "N": 9000, "ldh": 9000, "lddy": 9000, "lddh": 9000, "lddx": 9000},
-               {"ws": 0, "N": 70000, "ldh": 70000, "lddy": 70000, "lddh": 70000, "lddx": 70000}, {"ws": A + 8}, {"h": A + 1}, {"dy": A + 2}, {"dh": A + 2}, {"dx": A + 3},
+               {"ws": 0, "N": 70000, "ldh": 70000, "lddy": 70000, "lddh": 70000, "lddx": 70000},
+               {"ws": A + 8}, {"h": A + 1}, {"dy": A + 2}, {"dh": A + 2}, {"dx": A + 3},
                {"g": A + 1}, {"dg": A + 2}, {"rstd": A + 1}):
         assert rms_bwd(**kw) == 1, kw
     assert rms_bwd(xd=3) == 2 and rms_bwd(gd=-1) == 2
@@ -142,7 +143,7 @@ def logp_bwd(z=A, ld=8, tok=A, tb=8, ignore=-100, stats=A, ent=A, da=A, db=A, T=
 def test_log_probability_refusals():
     nan, inf = float("nan"), float("inf")
     for kw in ({"M": -1}, {"N": -1}, {"N": 0, "ld": 0}, {"ld": 7}, {"tb": 2}, {"tb": 0}, {"z": 0}, {"logp": 0},
-               {"ent": 0}, {"stats": 0}, {"best": 0}, {"ids": 0}, {"ws": 0}, {"ws": A + 8}, {"z": A + 2},
+               {"ent": 0}, {"stats": 0}, {"best": 0}, {"ids": 0}, {"ws": 0, "M": 4000}, {"ws": A + 8}, {"z": A + 2},
                {"tok": A + 4}, {"tok": A + 2, "tb": 4}, {"logp": A + 2}, {"ent": A + 1}, {"best": A + 2},
                {"ids": A + 4}, {"stats": A + 4}, {"top": -1}, {"top": 9}, {"top": 33, "N": 64, "ld": 64}, {"T": 0.0},
                {"T": -1.0}, {"T": nan}, {"T": inf}, {"T": 1e-60}, {"T": 1e300}):
