@@ -96,7 +96,8 @@ def test_widths_of_many_rows(N, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,top", [(1, 131072, 20), (74, 131072, 32), (75, 131072, 20), (8, 151936, 1),
-                                     (1, 500001, 32), (64, 5000, 20), (592, 1000, 5), (593, 1000, 5), (1, 1, 1), (2, 1048571, 3)])
+                                     (1, 500001, 32), (64, 5000, 20), (592, 1000, 5), (593, 1000, 5), (1, 1, 1),
+                                     (2, 1048571, 3)])
 def test_few_rows(M, N, top, dtype):
     """One kernel where the rows' clusters are few, two beyond; rows among them that do not count."""
     for masked in (0.0, 0.5):
