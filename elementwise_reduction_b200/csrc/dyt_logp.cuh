@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) logp_few_kernel(const __grid_c
   using IO = VecIO<T, V>;
   __shared__ float4 parts[kMaxCluster * kFewWarps];
   __shared__ Best best;
-  extern __shared__ __align__(128) unsigned char dyn[];
+  extern __shared__ __align__(16) unsigned char dyn[];
   pdl_prologue();
   if (TOP && dynamic_smem_bytes() < (size_t)a.batches * 32 * sizeof(T)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
