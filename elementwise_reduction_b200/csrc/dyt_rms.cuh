@@ -10,11 +10,12 @@
 // Bound by memory, as layer norm is, and mostly laid out as it: a row is read once
 // into the ring of RowFeed and kept in registers between its sum and its outputs,
 // the same columns of every row in the same lane. The norm is of the sum before it
-// is rounded to the stored residual stream, so y has one rounding. The largest |y|
-// of a row is rstd times the largest |gamma h|, which meets the sum of squares in
-// the one exchange a row takes.
+// is rounded to the stored residual stream, so y has one rounding. The 8-bit output
+// is of the same y, by the quotient that its definition names; where one scale is the
+// whole row's, the largest |y| takes an exchange of its own behind the sum's.
 #pragma once
 
+#include <cfloat>
 #include <type_traits>
 
 #include "dyt_cluster.cuh"
@@ -96,6 +97,25 @@ __device__ __forceinline__ void cut(Walk &w, int first, int cols, int V) {  // V
 __device__ __forceinline__ const void *param_from(const void *p, int dt, int first) {
   return p ? static_cast<const char *>(p) + (int64_t)first * (dt == DYT_F32 ? 4 : 2) : p;
 }
+
+// A group's scale from its largest |y|, and the quotients by it.
+struct Scale {
+  float s, finite, minus;  // the scale, the same but finite (by an infinite one finite values are 0), and about -1 / s
+  __device__ __forceinline__ explicit Scale(float top) {
+    s = max_nan(top, kLeastTop) * (1.0f / kQMax);
+    finite = fminf(s, FLT_MAX);
+    minus = -rcp_approx(s);
+  }
+  // The binary32 nearest to y / s (but for quotients within 2^-21 units of the middle of two), from -y, so that no sign
+  // is turned and -0 stays: the product with 1 / s, corrected by what it leaves of y (P. W. Markstein, IBM J. Res. Dev.
+  // 34, 1990). The product alone is a unit in the last place off for one value in four, and one e4m3 value in 50000 then
+  // lies on the other side of a tie. (It takes 8191 x 1001 fp16 from 10.3 to 10.5 us, 100003 x 255 bf16 from 29.6 to
+  // 31.5; rows of a few KB are bound by memory either way.)
+  __device__ __forceinline__ float2 quotient(float2 minus_y) const {
+    const float2 q = mul2(minus_y, f2(minus));
+    return fma2(fma2(q, f2(finite), minus_y), f2(minus), q);
+  }
+};
 
 // Two values rounded to e4m3 (nearest even, at most 448; NaN stays): a in the low byte.
 __device__ __forceinline__ uint32_t e4m3_pair(float2 v) {
@@ -228,8 +248,9 @@ __device__ __noinline__ void give_up(const RmsArgs &a, int64_t row) {
 // (dyt_cluster.cuh), and a cluster has a fixed share of the rows.
 // Measured with a residual, bf16: 16384 x 4096 80.7 us (6.65 TB/s), 65536 x 1024 80.3 (6.7), 4096 x 20480 by clusters
 // of 2 118 (5.7); without one, 100003 x 255 binary32 32.6 (6.3). 8-bit, with a residual and a scale for 128 columns:
-// 8192 x 8192 72.5 (6.5). Bound by memory; ragged 16-bit rows by instructions, as each element is a load from shared
-// memory and a store of its own: 100003 x 255 bf16 43.4 (4.7), 8191 x 1001 fp16 to 8 bits 9.9 (2.5).
+// 8192 x 8192 73 (6.4); 4096 x 20480, clusters of 2, 109, with a scale a row, whose largest value is a second exchange,
+// 112. Bound by memory; ragged 16-bit rows by instructions, as each element is a load from shared memory and a store of
+// its own: 100003 x 255 bf16 43.4 (4.7), 8191 x 1001 fp16 to 8 bits 10.5 (2.4).
 template <typename T, int E, int MODE, bool RAGGED, bool RES, bool Q>
 __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constant__ RmsArgs a) {
   constexpr bool CLUSTER = in_cluster(MODE), GROUP = in_warps(MODE);
@@ -238,7 +259,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
   constexpr int P = E / 2;
   constexpr int S = kRmsFwdStages, TN = RES ? 2 : 1;
   using Slab = Slabs<T, E, RAGGED, MODE>;
-  __shared__ std::conditional_t<CLUSTER, Meet<float2>, float2[2][kBlock / 32]> red;
+  __shared__ std::conditional_t<CLUSTER, Meet<float>, float[2][2][kBlock / 32]> red;
   __shared__ Steal queue;
   extern __shared__ __align__(128) unsigned char dyn[];
   pdl_prologue();
@@ -289,6 +310,18 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
   const float inv_n = w.inv_n;
   const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31;
   bool lost = false;
+  // CLUSTER: what each of the row's warps has, two for a lane of every warp; NaN once something did not come.
+  int met = 0;
+  auto meet = [&](float v) {
+    const float nan = __int_as_float(0x7FC00000);
+    if constexpr (CLUSTER) {
+      red.put(met, lost ? nan : v, p.lane, p.L);
+      if (!lost) lost = !red.wait(met, p.lane, p.L);
+      const int par = met++ & 1;
+      return lost ? make_float2(nan, nan) : make_float2(red.of[par][wl], red.of[par][wl + 32]);
+    }
+    return make_float2(nan, nan);
+  };
   auto take = [&](int64_t last) {
     if (steal) return queue.take(asked++ & 1u);
     return last + Mine::units() < a.items ? last + Mine::units() : (int64_t)-1;
@@ -330,43 +363,27 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < P; ++i) t[i & 1] = fma2(v[i], v[i], t[i & 1]);
     t[0] = add2(t[0], t[1]);
-    float q = t[0].x + t[0].y, top = 0.0f;
+    float q = t[0].x + t[0].y;
     if (RES && in) store_pairs<T, E, RAGGED>(static_cast<T *>(a.h) + row * a.ldh + col0, v, p, feed, w.NV, N);
-    if constexpr (Q) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) v[i] = mul2(v[i], gam[i]);
-      if (!a.grouped) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) top = max_nan(top, max_nan(fabsf(v[i].x), fabsf(v[i].y)));
-      }
-    }
     q = GROUP ? warp_sum(q) : lanes_sum(q, p.L);
-    if (Q && !a.grouped) top = lanes_max(top, p.seg());
-    if constexpr (GROUP) {
-      const int par = it & 1;
-      if constexpr (CLUSTER) {
-        const float nan = __int_as_float(0x7FC00000);
-        red.put(it, make_float2(lost ? nan : q, top), p.lane, p.L);
-        if (!lost) lost = !red.wait(it, p.lane, p.L);
-        const float2 o = red.of[par][wl], u = red.of[par][wl + 32];
-        q = lost ? nan : warp_sum(o.x + u.x);
-        if (Q && !a.grouped) top = lanes_max(max_nan(o.y, u.y), 32);
-      } else {
-        if (wl == 0) red[par][p.lane / 32] = make_float2(q, top);
-        taken(after);
-        // up to 16 warps, one a lane of each half
-        const float2 o = (wl & 15) < warps ? red[par][wl & 15] : make_float2(0.0f, 0.0f);
-        q = lanes_sum(o.x, 16);
-        if (Q && !a.grouped) top = lanes_max(o.y, 16);
-      }
+    const int par = it & 1;
+    if constexpr (CLUSTER) {
+      const float2 o = meet(q);
+      q = warp_sum(o.x + o.y);
+    } else if constexpr (GROUP) {
+      if (wl == 0) red[par][0][p.lane / 32] = q;
+      taken(after);
+      // up to 16 warps, one a lane of each half
+      q = lanes_sum((wl & 15) < warps ? red[par][0][wl & 15] : 0.0f, 16);
     } else {
       taken(after);
     }
     const float rstd = rsqrtf(fmaf(q, inv_n, a.eps));
     if (a.rstd && p.lane == 0 && in && Mine::rank() == 0) a.rstd[row] = rstd;
-    if constexpr (Q) {
+    const float by = Q ? -rstd : rstd;  // (8 bits: -y, as Scale takes it)
 #pragma unroll
-      for (int i = 0; i < P; ++i) v[i] = mul2(v[i], f2(rstd));
+    for (int i = 0; i < P; ++i) v[i] = mul2(mul2(v[i], f2(by)), gam[i]);
+    if constexpr (Q) {
       if (a.grouped) {
         float tops[Slab::n];
 #pragma unroll
@@ -379,26 +396,34 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
         Slab::join(tops, p);
 #pragma unroll
         for (int s = 0; s < Slab::n; ++s) {
-          tops[s] = max_nan(tops[s], kLeastTop);
+          const Scale c(tops[s]);
           const int g = Slab::group(p, s);
           // (rows in less than a warp: several slabs may write the same value)
           if (in && g < groups && (p.lane & (Slab::lanes(p) - 1)) == 0)
-            a.scale[row * a.groups + col0 / kScaleCols + g] = tops[s] * (1.0f / kQMax);
-          const float inv = kQMax / tops[s];
+            a.scale[row * a.groups + col0 / kScaleCols + g] = c.s;
 #pragma unroll
-          for (int i = s * Slab::W / 2; i < (s + 1) * Slab::W / 2; ++i) v[i] = mul2(v[i], f2(inv));
+          for (int i = s * Slab::W / 2; i < (s + 1) * Slab::W / 2; ++i) v[i] = c.quotient(v[i]);
         }
       } else {
-        top = max_nan(top * rstd, kLeastTop);  // the largest |v|: rounding keeps the order
-        if (p.lane == 0 && in && Mine::rank() == 0) a.scale[row] = top * (1.0f / kQMax);
-        const float inv = kQMax / top;
+        float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = mul2(v[i], f2(inv));
+        for (int i = 0; i < P; ++i) top = max_nan(top, max_nan(fabsf(v[i].x), fabsf(v[i].y)));
+        top = lanes_max(top, p.seg());
+        if constexpr (CLUSTER) {
+          const float2 o = meet(top);
+          top = lanes_max(max_nan(o.x, o.y), 32);
+        } else if constexpr (GROUP) {
+          if (wl == 0) red[par][1][p.lane / 32] = top;
+          __syncthreads();
+          top = lanes_max((wl & 15) < warps ? red[par][1][wl & 15] : 0.0f, 16);
+        }
+        const Scale c(top);
+        if (p.lane == 0 && in && Mine::rank() == 0) a.scale[row] = c.s;
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = c.quotient(v[i]);
       }
       store_bytes<T, E, RAGGED>(static_cast<unsigned char *>(a.y) + row * a.ldy + col0, v, p, feed, w.NV, room, in);
     } else if (in) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) v[i] = mul2(mul2(v[i], f2(rstd)), gam[i]);
       store_pairs<T, E, RAGGED>(static_cast<T *>(a.y) + row * a.ldy + col0, v, p, feed, w.NV, N);
     }
     item = next;
@@ -477,19 +502,24 @@ __global__ void __launch_bounds__(1024) rms_fwd_long_kernel(RmsArgs a) {
       sum_at(c, v);
 #pragma unroll
       for (int e = 0; e < C; ++e) s[0] = fmaf(v[e], v[e], s[0]);
-      if (Q && !a.grouped) {
-        float g[C];
-        gamma_at(c, g);
-#pragma unroll
-        for (int e = 0; e < C; ++e) top = max_nan(top, fabsf(v[e] * g[e]));
-      }
     }
     cta_sum(s, red[0]);
     const float rstd = rsqrtf(fmaf(s[0], a.w.inv_n, a.eps));
-    if (Q && !a.grouped) top = max_nan(cta_max(top, red[1]) * rstd, kLeastTop);
+    if (Q && !a.grouped) {
+#pragma unroll 2
+      for (int64_t c = c0; c < N; c += step) {
+        float v[C], g[C];
+        sum_at(c, v);
+        gamma_at(c, g);
+#pragma unroll
+        for (int e = 0; e < C; ++e) top = max_nan(top, fabsf(v[e] * rstd * g[e]));
+      }
+      top = cta_max(top, red[1]);
+    }
+    const Scale whole(top);
     if (threadIdx.x == 0) {
       if (a.rstd) a.rstd[row] = rstd;
-      if (Q && !a.grouped) a.scale[row] = top * (1.0f / kQMax);
+      if (Q && !a.grouped) a.scale[row] = whole.s;
     }
     // whole warps stay together: a warp's first column decides
     for (int64_t c = c0; c - lane * V < N; c += step) {
@@ -502,29 +532,31 @@ __global__ void __launch_bounds__(1024) rms_fwd_long_kernel(RmsArgs a) {
         for (int b = 0; b < B; ++b)
           if (c + b * 32 < N) store_row<T, V>(h + b * 32, *reinterpret_cast<const float(*)[V]>(v + b * V));
       }
+      const float factor = Q ? -rstd : rstd;  // (8 bits: -y, as Scale takes it)
+#pragma unroll
+      for (int e = 0; e < C; ++e) v[e] = v[e] * factor * g[e];
       if constexpr (!Q) {
         T *y = static_cast<T *>(a.y) + row * a.ldy + c;
-#pragma unroll
-        for (int e = 0; e < C; ++e) v[e] = v[e] * rstd * g[e];
 #pragma unroll
         for (int b = 0; b < B; ++b)
           if (c + b * 32 < N) store_row<T, V>(y + b * 32, *reinterpret_cast<const float(*)[V]>(v + b * V));
       } else {
         unsigned char *y = static_cast<unsigned char *>(a.y) + row * a.ldy + c;
-#pragma unroll
-        for (int e = 0; e < C; ++e) v[e] = v[e] * g[e] * rstd;
-        float t = top;
+        Scale by = whole;
         if (a.grouped) {
-          t = 0.0f;
+          float t = 0.0f;
 #pragma unroll
           for (int e = 0; e < C; ++e) t = max_nan(t, fabsf(v[e]));
-          t = max_nan(lanes_max(t, GL), kLeastTop);
+          by = Scale(lanes_max(t, GL));
           const int64_t grp = c / kScaleCols;
-          if ((lane & (GL - 1)) == 0 && grp < a.groups) a.scale[row * a.groups + grp] = t * (1.0f / kQMax);
+          if ((lane & (GL - 1)) == 0 && grp < a.groups) a.scale[row * a.groups + grp] = by.s;
         }
-        const float inv = kQMax / t;
 #pragma unroll
-        for (int e = 0; e < C; ++e) v[e] *= inv;
+        for (int e = 0; e < C; e += 2) {
+          const float2 q = by.quotient(make_float2(v[e], v[e + 1]));
+          v[e] = q.x;
+          v[e + 1] = q.y;
+        }
 #pragma unroll
         for (int b = 0; b < B; ++b)
           if (c + b * 32 < N) store_e4m3<V>(y + b * 32, *reinterpret_cast<const float(*)[V]>(v + b * V));

@@ -538,7 +538,9 @@ dyt_status dyt_rms_norm_forward(const void *x, int64_t ldx, const void *residual
  *           128; the last group of a row is shorter when N is no multiple)
  *   scale = max(a, 2^-100) / 448        q[i,j] = e4m3(y[i,j] / scale)
  *
- * y is not rounded before. A group that holds a NaN has scale NaN and every q of
+ * y is not rounded to x_dtype before: it is the forward's in binary32, gamma * (h * rstd)
+ * with each product rounded. scale is a product with the rounded 1 / 448, and q the
+ * e4m3 value nearest to the binary32 quotient (ties to even). A group that holds a NaN has scale NaN and every q of
  * it NaN; one whose largest value is infinite has scale infinite, and no finite
  * product stands for it.
  *   group     0 or 128, else DYT_ERR_INVALID_VALUE
