@@ -100,7 +100,8 @@ __device__ __forceinline__ const void *param_from(const void *p, int dt, int fir
 
 // A group's scale from its largest |y|, and the quotients by it.
 struct Scale {
-  float s, finite, minus;  // the scale, the same but finite (by an infinite one finite values are 0), and about -1 / s
+  // The scale, the same but finite (by an infinite one finite values are 0), and about -1 / s.
+  float s, finite, minus;
   __device__ __forceinline__ explicit Scale(float top) {
     s = max_nan(top, kLeastTop) * (1.0f / kQMax);
     finite = fminf(s, FLT_MAX);
@@ -108,8 +109,8 @@ struct Scale {
   }
   // The binary32 nearest to y / s (but for quotients within 2^-21 units of the middle of two), from -y, so that no sign
   // is turned and -0 stays: the product with 1 / s, corrected by what it leaves of y (P. W. Markstein, IBM J. Res. Dev.
-  // 34, 1990). The product alone is a unit in the last place off for one value in four, and one e4m3 value in 50000 then
-  // lies on the other side of a tie. (It takes 8191 x 1001 fp16 from 10.3 to 10.5 us, 100003 x 255 bf16 from 29.6 to
+  // 34, 1990). The product alone is a unit in the last place off for one value in four, and one e4m3 value in 50000
+  // then lies on the other side of a tie. (It takes 8191 x 1001 fp16 from 10.3 to 10.5 us, 100003 x 255 bf16 from 29.6 to
   // 31.5; rows of a few KB are bound by memory either way.)
   __device__ __forceinline__ float2 quotient(float2 minus_y) const {
     const float2 q = mul2(minus_y, f2(minus));
@@ -486,13 +487,15 @@ __global__ void __launch_bounds__(1024) rms_fwd_long_kernel(RmsArgs a) {
         for (int e = 0; e < V; ++e) v[b * V + e] = f[e];
       }
     };
+    // gamma there, 0 past the end too: another column's may be infinite, and 0 times it no number
     auto gamma_at = [&](int64_t c, float (&g)[C]) {
 #pragma unroll
       for (int b = 0; b < B; ++b) {
+        const bool inside = c + b * 32 < N;
         float f[V];
-        load_columns<V>(a.gamma, a.gamma_dt, c + b * 32 < N ? c + b * 32 : 0, 1.0f, f);
+        load_columns<V>(a.gamma, a.gamma_dt, inside ? c + b * 32 : 0, 1.0f, f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[b * V + e] = f[e];
+        for (int e = 0; e < V; ++e) g[b * V + e] = inside ? f[e] : 0.0f;
       }
     };
     float s[1] = {0.0f}, top = 0.0f;

@@ -1,5 +1,6 @@
 """Root-mean-square norm, where its definition leaves one answer: the 8-bit values are the
-rounded quotients of the norm by its scale, bit for bit."""
+rounded quotients of the norm by its scale, bit for bit, and one column's gamma reaches no
+other column's group."""
 from __future__ import annotations
 
 import pytest
@@ -67,3 +68,36 @@ def test_gamma_whose_product_with_the_sum_passes_binary32(N):
         assert torch.isfinite(y).all() and torch.isfinite(scale).all()
         assert_bits(got[1], scale, "scale")
         assert_bits(got[0], q, "q")
+
+
+@pytest.mark.parametrize("value", [INF, NAN])
+@pytest.mark.parametrize("N,xd", [(100, "bf16"), (1000, "f32"), (4100, "f16"), (20000, "bf16"), (20001, "bf16"),
+                                  (40001, "f32"), (40004, "f32"), (65672, "f16"), (70003, "bf16")])
+def test_gamma_that_is_not_finite_keeps_to_its_group(N, xd, value):
+    """The first column's gamma, with a last group of 128 that is not full."""
+    for res in (False, True):
+        x, r, dy, gamma = inputs(7, N, xd, res=res)
+        rt = None if r is None else r.t
+        y0, _, rstd = dyt().rms_norm_forward(x.t, gamma, rt, EPS)
+        q0, s0, _ = dyt().rms_norm_quantize(x.t, gamma, rt, EPS, 128)
+        h = x.t if rt is None else dyt().rms_norm_forward(x.t, gamma, rt, EPS)[1]
+        _, d0 = dyt().rms_norm_backward(h, dy.t, rstd, gamma)
+        bad = gamma.clone()
+        bad[0] = value
+        y, _, again = dyt().rms_norm_forward(x.t, bad, rt, EPS)
+        assert torch.equal(y[:, 1:], y0[:, 1:]) and torch.equal(again, rstd) and not torch.isfinite(y[:, 0]).any()
+        q, s, _ = dyt().rms_norm_quantize(x.t, bad, rt, EPS, 128)
+        assert_bits(s[:, 1:], s0[:, 1:], "scale")
+        assert_bits(q[:, 128:], q0[:, 128:], "q")
+        q1, s1, _ = dyt().rms_norm_quantize(x.t, bad, rt, EPS, 0)
+        if value == INF:  # the group's scale is infinite, and its finite values 0 by it
+            assert torch.isinf(s[:, 0]).all() and torch.isinf(s1).all()
+            assert (q.float()[:, 1:128] == 0).all() and torch.isnan(q.float()[:, 0]).all()
+            assert (q1.float()[:, 1:] == 0).all() and torch.isnan(q1.float()[:, 0]).all()
+        else:
+            assert torch.isnan(s[:, 0]).all() and torch.isnan(q[:, :128].float()).all()
+            assert torch.isnan(s1).all() and torch.isnan(q1.float()).all()
+        dx, dg = dyt().rms_norm_backward(h, dy.t, rstd, bad)
+        assert torch.equal(dg, d0)  # (gamma is no factor of its own gradient)
+        # the row's sum c is not finite, and rstd (g - n c) neither
+        assert not torch.isfinite(dx).any()
