@@ -48,18 +48,17 @@ __device__ __forceinline__ void cluster_put(H *p, uint32_t cta, H v) {  // 16 bi
 
 // Where a row's sums of all the cluster's warps meet: each warp sends its own to every CTA (st.async) and waits for all
 // of them at its CTA's mbarrier. Rows take turns between two places; a warp is at most one row ahead of another, as it
-// has the other's sums of the row before. In shared memory, one for each of a CTA's rows side by
-// side, for V = float or float2.
-template <typename V>
+// has the other's sums of the row before. In shared memory, one for each of a CTA's rows side by side. (The norm's
+// forward takes two steps for a row where its largest value meets too.)
 struct Meet {
   static constexpr int kWarps = 64;               // of a row, at most
   static constexpr int kPolls = 1 << 20;           // of a wait, each waits for a while itself
-  V of[2][kWarps];                         // (0 where there is no warp)
+  float of[2][kWarps];                     // (0 where there is no warp)
   unsigned long long bar[2];
 
   // Lane `lane` of the row's L in this CTA; before any put all threads of the cluster meet.
   __device__ __forceinline__ void init(int lane, int L) {
-    for (int i = lane; i < 2 * kWarps; i += L) of[0][i] = V{};
+    for (int i = lane; i < 2 * kWarps; i += L) of[0][i] = 0.0f;
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_at(i)) : "memory");
@@ -69,23 +68,16 @@ struct Meet {
     }
   }
   // The warp's v (the same in all its lanes) of the row's step `it`.
-  __device__ __forceinline__ void put(int it, V v, int lane, int L) {
+  __device__ __forceinline__ void put(int it, float v, int lane, int L) {
     const uint32_t cta = lane & 31;
     if (cta >= cluster_ctas()) return;
     const int par = it & 1;
     const uint32_t at = (uint32_t)__cvta_generic_to_shared(&of[par][((int)cluster_rank() * L + lane) / 32]);
-    if constexpr (sizeof(V) == 8)
-      asm volatile(
-          "{.reg .u32 r, m; mapa.shared::cluster.u32 r, %0, %2; mapa.shared::cluster.u32 m, %1, %2;"
-          "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [r], {%3, %4}, [m];}" ::"r"(at),
-          "r"(bar_at(par)), "r"(cta), "f"(v.x), "f"(v.y)
-          : "memory");
-    else
-      asm volatile(
-          "{.reg .u32 r, m; mapa.shared::cluster.u32 r, %0, %2; mapa.shared::cluster.u32 m, %1, %2;"
-          "st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [r], %3, [m];}" ::"r"(at),
-          "r"(bar_at(par)), "r"(cta), "f"(v)
-          : "memory");
+    asm volatile(
+        "{.reg .u32 r, m; mapa.shared::cluster.u32 r, %0, %2; mapa.shared::cluster.u32 m, %1, %2;"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [r], %3, [m];}" ::"r"(at),
+        "r"(bar_at(par)), "r"(cta), "f"(v)
+        : "memory");
   }
   // All of step `it` is in of[it & 1]; false: not within the limit.
   __device__ __forceinline__ bool wait(int it, int lane, int L) {
@@ -104,7 +96,7 @@ struct Meet {
  private:
   __device__ __forceinline__ uint32_t bar_at(int i) const { return (uint32_t)__cvta_generic_to_shared(&bar[i]); }
   __device__ __forceinline__ void expect(int i, int L) const {
-    const uint32_t bytes = cluster_ctas() * ((uint32_t)L / 32) * (uint32_t)sizeof(V);
+    const uint32_t bytes = cluster_ctas() * ((uint32_t)L / 32) * (uint32_t)sizeof(float);
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar_at(i)), "r"(bytes) : "memory");
   }
 };

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
   constexpr int P = E / 2;
   constexpr int S = kRmsFwdStages, TN = RES ? 2 : 1;
   using Slab = Slabs<T, E, RAGGED, MODE>;
-  __shared__ std::conditional_t<CLUSTER, Meet<float>, float[2][2][kBlock / 32]> red;
+  __shared__ std::conditional_t<CLUSTER, Meet, float[2][2][kBlock / 32]> red;
   __shared__ Steal queue;
   extern __shared__ __align__(128) unsigned char dyn[];
   pdl_prologue();
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int E = kBwdElems, P = E / 2;
   constexpr int S = rms_bwd_stages<T>(), TN = RES ? 3 : 2;
-  __shared__ std::conditional_t<CLUSTER, Meet<float>[kClusterMost], float[2][kBlock / 32]> red;
+  __shared__ std::conditional_t<CLUSTER, Meet[kClusterMost], float[2][kBlock / 32]> red;
   extern __shared__ __align__(128) unsigned char dyn[];
   pdl_prologue();
   const Place<MODE> p(a.w.L);
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_bwd_kernel(RmsGradArgs a) {
       const int par = it & 1;
       if constexpr (CLUSTER) {
         const float nan = __int_as_float(0x7FC00000);
-        Meet<float> &meet = red[p.mine];
+        Meet &meet = red[p.mine];
         meet.put(it, lost ? nan : c, p.lane, p.L);
         if (!lost) lost = !meet.wait(it, p.lane, p.L);
         c = lost ? nan : warp_sum(meet.of[par][wl] + meet.of[par][wl + 32]);
