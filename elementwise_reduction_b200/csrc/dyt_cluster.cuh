@@ -51,9 +51,9 @@ __device__ __forceinline__ void cluster_put(H *p, uint32_t cta, H v) {  // 16 bi
 // has the other's sums of the row before. In shared memory, one for each of a CTA's rows side by side. (The norm's
 // forward takes two steps for a row where its largest value meets too.)
 struct Meet {
-  static constexpr int kWarps = 64;               // of a row, at most
-  static constexpr int kPolls = 1 << 20;           // of a wait, each waits for a while itself
-  float of[2][kWarps];                     // (0 where there is no warp)
+  static constexpr int kWarps = 64;       // of a row, at most
+  static constexpr int kPolls = 1 << 20;  // of a wait, each waits for a while itself
+  float of[2][kWarps];                    // (0 where there is no warp)
   unsigned long long bar[2];
 
   // Lane `lane` of the row's L in this CTA; before any put all threads of the cluster meet.
@@ -79,17 +79,19 @@ struct Meet {
         "r"(bar_at(par)), "r"(cta), "f"(v)
         : "memory");
   }
-  // All of step `it` is in of[it & 1]; false: not within the limit.
+  // All of step `it` is in of[it & 1]; false: not within the limit. The barrier is then left as it is: its phase has had
+  // the one arrival it counts, and one more before it ends is not defined.
+  template <int POLLS = kPolls>
   __device__ __forceinline__ bool wait(int it, int lane, int L) {
     const int par = it & 1;
     uint32_t done = 0;
-    for (int i = 0; i < kPolls && !done; ++i)
+    for (int i = 0; i < POLLS && !done; ++i)
       asm volatile(
           "{.reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
           : "=r"(done)
           : "r"(bar_at(par)), "r"((uint32_t)it >> 1 & 1u)
           : "memory");
-    if (lane == 0) expect(par, L);
+    if (done && lane == 0) expect(par, L);
     return done != 0;
   }
 

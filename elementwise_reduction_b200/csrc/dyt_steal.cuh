@@ -33,9 +33,10 @@ struct Steal {
   }
   // The index of the CTA whose work is now this one's; -1: none is left (then nothing more may be asked).
   // phase: 0 for the first answer, then 1, 0, ...
+  template <int POLLS = kPolls>
   __device__ __forceinline__ int64_t take(uint32_t phase) const {
     uint32_t done = 0;
-    for (int i = 0; i < kPolls && !done; ++i)
+    for (int i = 0; i < POLLS && !done; ++i)
       asm volatile("{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
                    : "=r"(done)
                    : "r"(bar_at()), "r"(phase)
