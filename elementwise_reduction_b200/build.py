@@ -20,7 +20,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("dyt_api.cu", "dyt_inst_f32.cu", "dyt
                                               "dyt_rms_bf16.cu", "dyt_rms_f16.cu", "dyt_logp.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("dyt_kernels.cuh", "dyt_math.cuh", "dyt_async.cuh", "dyt_finalize.cuh",
                                                   "dyt_select.cuh", "dyt_select_impl.cuh", "dyt_host.h", "dyt_optin.h",
-                                                  "dyt_norm.cuh", "dyt_loss.cuh", "dyt_rows.h", "dyt_steal.cuh",
+                                                  "dyt_capacity.h", "dyt_norm.cuh", "dyt_loss.cuh", "dyt_rows.h", "dyt_steal.cuh",
                                                   "dyt_cluster.cuh", "dyt_rms.cuh", "dyt_rms_select.cuh",
                                                   "dyt_rms_select_impl.cuh", "dyt_loss_plan.h", "dyt_logp.cuh")] + [
     os.path.join(INCLUDE, "dyt.h")]

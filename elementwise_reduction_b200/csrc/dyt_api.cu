@@ -13,6 +13,7 @@
 #include <unordered_map>
 
 #include "dyt.h"
+#include "dyt_capacity.h"
 #include "dyt_finalize.cuh"
 #include "dyt_host.h"
 #include "dyt_optin.h"
@@ -40,7 +41,7 @@ namespace {
 std::mutex g_mu;
 std::unordered_map<int, int> g_sms;                   // device -> SM count
 std::unordered_map<uint64_t, int> g_occ;              // (device, kernel, block) -> CTAs per SM
-std::unordered_map<uint64_t, int> g_clusters;         // (device, kernel, block, cluster) -> clusters at once
+Capacities g_clusters;                                // clusters at once
 SmemOptIn g_smem;                                     // (device, kernel) -> dynamic shared memory opted in
 
 uint64_t kernel_key(int dev, const void *kernel) {
@@ -95,23 +96,10 @@ dyt_status occupancy(int dev, const void *kernel, int block, int *ctas) {
 }
 
 dyt_status cluster_capacity(int dev, const void *kernel, const cudaLaunchConfig_t &cfg, int ctas, int *clusters) {
-  const uint64_t key = (kernel_key(dev, kernel) * 1025u + cfg.blockDim.x) * 17u + (uint64_t)ctas;  // up to 16 CTAs
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    auto it = g_clusters.find(key);
-    if (it != g_clusters.end()) {
-      *clusters = it->second;
-      return DYT_OK;
-    }
-  }
-  int n = 0;
-  cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-  if (e != cudaSuccess) return cuda_fail(e);
-  if (n < 1) n = 1;
-  std::lock_guard<std::mutex> lk(g_mu);
-  g_clusters[key] = n;
-  *clusters = n;
-  return DYT_OK;
+  const int e = g_clusters.get(dev, kernel, cfg.blockDim.x, cfg.dynamicSmemBytes, ctas, clusters, [&](int *n) {
+    return (int)cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+  });
+  return e == (int)cudaSuccess ? DYT_OK : cuda_fail((cudaError_t)e);
 }
 
 // Opt a kernel in to `bytes` of dynamic shared memory, once per device and size.

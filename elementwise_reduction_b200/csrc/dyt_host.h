@@ -23,8 +23,7 @@ void record_info(const dyt_launch_info &i);
 dyt_status current_sms(int *dev_out, int *sms_out);
 // CTAs of `block` threads of a kernel without dynamic shared memory that fit on an SM (cached).
 dyt_status occupancy(int dev, const void *kernel, int block, int *ctas);
-// Clusters of the launch's kernel that run at once (cached by kernel, block and cluster; its shared memory follows
-// from them).
+// Clusters of the launch's kernel that run at once (cached by kernel, block, dynamic shared memory and cluster).
 dyt_status cluster_capacity(int dev, const void *kernel, const cudaLaunchConfig_t &cfg, int ctas, int *clusters);
 // Opt a kernel in to at least `bytes` of dynamic shared memory, once per device and size; safe from any thread.
 dyt_status prepare_smem(int dev, const void *kernel, int bytes);
