@@ -1,11 +1,12 @@
 """Root-mean-square norm, where its definition leaves one answer: the 8-bit values are the
-rounded quotients of the norm by its scale, bit for bit, and one column's gamma reaches no
-other column's group."""
+rounded quotients of the norm by its scale, bit for bit, one column's gamma reaches no
+other column's group, and a row's bits go by its layout alone."""
 from __future__ import annotations
 
 import pytest
 import torch
 
+from tests import rms_helpers as S
 from tests import row_helpers as R
 from tests.rms_helpers import LEAST, QMAX, groups_of
 from tests.test_rms_gpu import EPS, INF, NAN, dyt, inputs
@@ -101,3 +102,43 @@ def test_gamma_that_is_not_finite_keeps_to_its_group(N, xd, value):
         assert torch.equal(dg, d0)  # (gamma is no factor of its own gradient)
         # the row's sum c is not finite, and rstd (g - n c) neither
         assert not torch.isfinite(dx).any()
+
+
+@pytest.mark.parametrize("N,xd", [(100, "bf16"), (255, "f32"), (1000, "bf16"), (1000, "f32"), (4096, "f16"),
+                                  (20000, "bf16")])
+def test_the_same_bits_at_every_offset_of_ragged_rows(N, xd):
+    """Rows 1, 2, ... elements past a 16-byte boundary, and rows an odd pitch apart: spread over lanes alike."""
+    M = 700
+    once = None
+    for offset, pitch in ((1, N), (2, N), (3, N + 8), (3, N + 1), (1, N + 3), (0, N + 5)):
+        x, r, dy, gamma = inputs(M, N, xd, pitch=pitch, offset=offset)
+        fwd = dyt().rms_norm_forward(x.t, gamma, r.t, EPS)
+        assert dyt().dyt_last_launch_info()["shifted"] == 1
+        back = dyt().rms_norm_backward(x.t, dy.t, fwd[2], gamma, r.t)
+        eight = [t.view(torch.uint8) for k in (0, 128) for t in dyt().rms_norm_quantize(x.t, gamma, r.t, EPS, k)[:2]]
+        all_of = (*fwd, *back, *eight)
+        once = once or all_of
+        assert all(torch.equal(a, b) for a, b in zip(once, all_of)), (offset, pitch)
+
+
+@pytest.mark.parametrize("N,xd", [(12288, "bf16"), (20480, "f16"), (9217, "bf16"), (20481, "f16"), (12290, "f32")])
+def test_a_row_alone_and_among_others_backward(N, xd):
+    """Their clusters, and so the order of the row's sum, may differ: both are within the bound, and they are equal in
+    every bit where the launch spreads the row alike."""
+    M = 4000
+    x, r, dy, gamma = inputs(M, N, xd)
+    rstd = dyt().rms_norm_forward(x.t, gamma, r.t, EPS)[2]
+    among, _ = dyt().rms_norm_backward(x.t, dy.t, rstd, gamma, r.t)
+    many = dyt().dyt_last_launch_info()
+    at = [0, 1, 149, 2000, M - 1]
+    exact, tol = S.backward(x.t[at], dy.t[at], rstd[at], gamma, r.t[at])
+    tol = tol[0] + R.half_step(x.t.dtype, exact[0])
+    R.assert_close(among[at], exact[0], tol, "dx among others")
+    for k, n in enumerate(at):
+        row = slice(n, n + 1)
+        alone, _ = dyt().rms_norm_backward(x.t[row], dy.t[row], rstd[row], gamma, r.t[row])
+        one = dyt().dyt_last_launch_info()
+        R.assert_close(alone, exact[0][k:k + 1], tol[k:k + 1], "dx alone")
+        lanes = [(i["col_chunks"], i["block"] // i["row_lanes"]) for i in (one, many)]
+        if lanes[0] == lanes[1]:
+            assert torch.equal(alone, among[row])
