@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(1024) rms_fwd_long_kernel(RmsArgs a) {
         for (int e = 0; e < V; ++e) v[b * V + e] = f[e];
       }
     };
-    // gamma there, 0 past the end too: another column's may be infinite, and 0 times it no number
+    // gamma there; 8 bits: 0 past the end too, where a group's largest value would meet another column's
     auto gamma_at = [&](int64_t c, float (&g)[C]) {
 #pragma unroll
       for (int b = 0; b < B; ++b) {
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(1024) rms_fwd_long_kernel(RmsArgs a) {
         float f[V];
         load_columns<V>(a.gamma, a.gamma_dt, inside ? c + b * 32 : 0, 1.0f, f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[b * V + e] = inside ? f[e] : 0.0f;
+        for (int e = 0; e < V; ++e) g[b * V + e] = inside || !Q ? f[e] : 0.0f;
       }
     };
     float s[1] = {0.0f}, top = 0.0f;

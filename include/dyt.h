@@ -51,15 +51,25 @@
  *   kernel surfaces at the caller's next synchronisation. No call aborts, and
  *   no failure is reported as DYT_OK.
  * - Results are deterministic: the same inputs on the same device give the
- *   same bits (static schedule, fixed reduction order, no atomics in sums).
+ *   same bits (no atomics in sums; the order of every sum is fixed by the call's
+ *   arguments and the device, whichever CTA takes a row and whatever was called
+ *   before).
  * - Every argument error is reported by a status code before anything is
- *   launched. No kernel waits on another grid or device, nor on a CTA that may
- *   not be running; the only waits are hardware completion waits (a thread's
- *   own asynchronous copies, the preceding grid in the stream, the hardware's
- *   answer to a CTA that asks for more work, and, for a root-mean-square norm's
- *   long rows, what the other CTAs of the same thread-block cluster send, which
- *   run together with it). The last two have a limit, after which the rows
- *   concerned are NaN.
+ *   launched.
+ * - No kernel waits on another grid or device, nor on a CTA that may not be
+ *   running. The waits there are: for a thread's own asynchronous copies and
+ *   for the preceding grid in the stream; at the barrier of a thread-block
+ *   cluster, whose CTAs run together (root-mean-square norm: long rows, at a
+ *   kernel's start and end; log probabilities: few rows, before and after a
+ *   row's parts are exchanged), and at those of a CTA; and two with a limit of
+ *   2^20 polls: for the hardware's answer to a CTA that asks for more work
+ *   (root-mean-square norm, forward), and for what the other CTAs of a cluster
+ *   send (its long rows). The hardware lets neither of them run out. If one
+ *   did, the call would still have returned DYT_OK: without the answer, the
+ *   row that it named is not written, and the CTA's own first row, done
+ *   before, is marked by NaN (rstd, and scale or y's first element); without
+ *   the cluster's sums, the cluster's remaining rows become NaN, in the first
+ *   of them at least the columns of the warps that found nothing.
  */
 #ifndef DYT_H_
 #define DYT_H_
@@ -517,10 +527,8 @@ dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *
  *   h         [M*N] x_dtype, row pitch ldh, written: the new residual stream. May
  *             alias x or residual with an equal pitch, as y may, but not y.
  *   rstd      [M] binary32, written for the backward; may be NULL
- * The rows of several warps go to whichever CTA is free, in no fixed order; a
- * row's bits do not depend on it. (Should the hardware leave a CTA's question for
- * a row unanswered, the CTA's own row has NaN for y's first element, rstd or
- * scale.) A row is read once and kept on the SM when N is at most 16384 (16-bit) or
+ * Rows go to whichever CTA is free, in no fixed order; a row's bits do not depend
+ * on it. A row is read once and kept on the SM when N is at most 16384 (16-bit) or
  * 8192 (binary32), and on the SMs of a cluster of 2 or 4 CTAs up to four times as
  * many; longer rows are read twice. Ragged rows are read as there. A row whose sum
  * of squares passes binary32's range has rstd 0. M * N == 0 launches nothing and
