@@ -25,7 +25,7 @@ __device__ __forceinline__ float ex2_approx(float w) {
 }
 
 
-// 1/v for normal v and results (0 for an infinite v).
+// 1/v for normal v and results, within a unit in the last place (0 for an infinite v).
 __device__ __forceinline__ float rcp_approx(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));

@@ -100,22 +100,16 @@ __device__ __forceinline__ const void *param_from(const void *p, int dt, int fir
 
 // A group's scale from its largest |y|, and the quotients by it.
 struct Scale {
-  // The scale, the same but finite (by an infinite one finite values are 0), and about -1 / s.
-  float s, finite, minus;
+  float s, inv, rest;  // the scale, its inverse from below, and what that lacks (both 0 for an infinite scale)
   __device__ __forceinline__ explicit Scale(float top) {
     s = max_nan(top, kLeastTop) * (1.0f / kQMax);
-    finite = fminf(s, FLT_MAX);
-    minus = -rcp_approx(s);
+    inv = rcp_approx(s) * (1.0f - 0x1p-22f);
+    rest = fmaf(-inv, fminf(s, FLT_MAX), 1.0f) * inv;  // (not negative: no sum of it turns a -0)
   }
-  // The binary32 nearest to y / s (but for quotients within 2^-21 units of the middle of two), from -y, so that no sign
-  // is turned and -0 stays: the product with 1 / s, corrected by what it leaves of y (P. W. Markstein, IBM J. Res. Dev.
-  // 34, 1990). The product alone is a unit in the last place off for one value in four, and one e4m3 value in 50000
-  // then lies on the other side of a tie. (It takes 8191 x 1001 fp16 from 10.3 to 10.5 us, 100003 x 255 bf16 from 29.6 to
-  // 31.5; rows of a few KB are bound by memory either way.)
-  __device__ __forceinline__ float2 quotient(float2 minus_y) const {
-    const float2 q = mul2(minus_y, f2(minus));
-    return fma2(fma2(q, f2(finite), minus_y), f2(minus), q);
-  }
+  // The binary32 nearest to y / s (but for quotients within 2^-20 units of the middle of two, and scales over 2^100,
+  // whose rest is subnormal): 1 / s in two parts, 45 bits of it. By one rounded part a value in four is a unit in the
+  // last place off, and one e4m3 value in 50000 lies on the other side of a tie.
+  __device__ __forceinline__ float2 quotient(float2 y) const { return fma2(y, f2(inv), mul2(y, f2(rest))); }
 };
 
 // Two values rounded to e4m3 (nearest even, at most 448; NaN stays): a in the low byte.
@@ -249,9 +243,9 @@ __device__ __noinline__ void give_up(const RmsArgs &a, int64_t row) {
 // (dyt_cluster.cuh), and a cluster has a fixed share of the rows.
 // Measured with a residual, bf16: 16384 x 4096 80.7 us (6.65 TB/s), 65536 x 1024 80.3 (6.7), 4096 x 20480 by clusters
 // of 2 118 (5.7); without one, 100003 x 255 binary32 32.6 (6.3). 8-bit, with a residual and a scale for 128 columns:
-// 8192 x 8192 73 (6.4); 4096 x 20480, clusters of 2, 109, with a scale a row, whose largest value is a second exchange,
-// 112. Bound by memory; ragged 16-bit rows by instructions, as each element is a load from shared memory and a store of
-// its own: 100003 x 255 bf16 43.4 (4.7), 8191 x 1001 fp16 to 8 bits 10.5 (2.4).
+// 8192 x 8192 73 (6.4); 4096 x 20480, clusters of 2, 103, with a scale a row, whose largest value is a second exchange,
+// 106. Bound by memory; ragged 16-bit rows by instructions, as each element is a load from shared memory and a store of
+// its own: 100003 x 255 bf16 43.4 (4.7), 8191 x 1001 fp16 to 8 bits 10.4 (2.4).
 template <typename T, int E, int MODE, bool RAGGED, bool RES, bool Q>
 __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constant__ RmsArgs a) {
   constexpr bool CLUSTER = in_cluster(MODE), GROUP = in_warps(MODE);
@@ -381,9 +375,8 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
     }
     const float rstd = rsqrtf(fmaf(q, inv_n, a.eps));
     if (a.rstd && p.lane == 0 && in && Mine::rank() == 0) a.rstd[row] = rstd;
-    const float by = Q ? -rstd : rstd;  // (8 bits: -y, as Scale takes it)
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = mul2(mul2(v[i], f2(by)), gam[i]);
+    for (int i = 0; i < P; ++i) v[i] = mul2(mul2(v[i], f2(rstd)), gam[i]);
     if constexpr (Q) {
       if (a.grouped) {
         float tops[Slab::n];
@@ -535,9 +528,8 @@ __global__ void __launch_bounds__(1024) rms_fwd_long_kernel(RmsArgs a) {
         for (int b = 0; b < B; ++b)
           if (c + b * 32 < N) store_row<T, V>(h + b * 32, *reinterpret_cast<const float(*)[V]>(v + b * V));
       }
-      const float factor = Q ? -rstd : rstd;  // (8 bits: -y, as Scale takes it)
 #pragma unroll
-      for (int e = 0; e < C; ++e) v[e] = v[e] * factor * g[e];
+      for (int e = 0; e < C; ++e) v[e] = v[e] * rstd * g[e];
       if constexpr (!Q) {
         T *y = static_cast<T *>(a.y) + row * a.ldy + c;
 #pragma unroll

@@ -530,9 +530,9 @@ dyt_status dyt_policy_loss_backward(const void *logits, int64_t ld, const void *
  * Rows go to whichever CTA is free, in no fixed order; a row's bits do not depend
  * on it. A row is read once and kept on the SM when N is at most 16384 (16-bit) or
  * 8192 (binary32), and on the SMs of a cluster of 2 or 4 CTAs up to four times as
- * many; longer rows are read twice. Ragged rows are read as there. A row whose sum
- * of squares passes binary32's range has rstd 0. M * N == 0 launches nothing and
- * writes nothing.
+ * many; longer rows are read twice (8 bits with a scale a row: three times). Ragged
+ * rows are read as there. A row whose sum of squares passes binary32's range has
+ * rstd 0. M * N == 0 launches nothing and writes nothing.
  */
 dyt_status dyt_rms_norm_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *gamma,
                                 float eps, void *y, int64_t ldy, void *h, int64_t ldh, float *rstd, int64_t M,
@@ -548,7 +548,8 @@ dyt_status dyt_rms_norm_forward(const void *x, int64_t ldx, const void *residual
  *
  * y is not rounded to x_dtype before: it is the forward's in binary32, gamma * (h * rstd)
  * with each product rounded. scale is a product with the rounded 1 / 448, and q the
- * e4m3 value nearest to the binary32 quotient (ties to even). A group that holds a NaN has scale NaN and every q of
+ * e4m3 value nearest to the binary32 quotient (ties to even; with a scale over 2^100
+ * that quotient may be a unit in the last place off). A group that holds a NaN has scale NaN and every q of
  * it NaN; one whose largest value is infinite has scale infinite, and no finite
  * product stands for it.
  *   group     0 or 128, else DYT_ERR_INVALID_VALUE
