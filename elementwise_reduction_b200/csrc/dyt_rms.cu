@@ -36,7 +36,9 @@ struct FwdPlan {
 // rows, more of a CTA's time at its ends, gain from the second step on: 9472 x 256 5.3 and 4.5, 18944 x 256 7.1 and
 // 6.5.
 constexpr int kFewSteps = 4;
-constexpr int kNarrowCtas = 6;  // of an SM, as the registers of most of these kernels allow
+// Of an SM. (As the registers of half of these kernels allow; the others have 4 or 5 at once: where there are more CTAs
+// than run, work is taken from those that wait, so that the number only says from when on.)
+constexpr int kNarrowCtas = 6;
 
 // Rows too long for one CTA's registers, and not for four CTAs', are shared by a cluster of 2, 4 or 8 CTAs. A step
 // takes a cluster as long whatever its lanes (1.1 us), so as many threads of the device as can be have a row: `side`

@@ -139,9 +139,9 @@ __device__ __forceinline__ void store_e4m3(unsigned char *p, const float (&f)[V]
 }
 
 // A lane's outputs as e4m3 bytes to the row at `out`, where the row is (`in`). RAGGED: they pass through `room`, the
-// slots that the row came from, where they lie as in their 16-byte chunks of memory. (Single bytes instead, 32 a store:
-// 8191 x 1001 fp16 10.2 us, so 9.9; with a residual 100003 x 700 bf16 133 and 125, 4096 x 20481 254 and 227; but
-// 100003 x 100 31.7 and 34.2.)
+// slots that the row came from, where they lie as in their 16-byte chunks of memory. (Single bytes instead, 32 a store,
+// when both were there: 8191 x 1001 fp16 10.2 us, so 9.9; with a residual 100003 x 700 bf16 133 and 125, 4096 x 20481
+// 254 and 227; but 100003 x 100 31.7 and 34.2. All widths go this way: a second way for the narrow ones is not built.)
 template <typename T, int E, bool RAGGED, int MODE, typename Feed>
 __device__ __forceinline__ void store_bytes(unsigned char *out, const float2 (&f)[E / 2], const Place<MODE> &p,
                                             const Feed &feed, int NV, unsigned char *room, bool in) {
@@ -241,11 +241,11 @@ __device__ __noinline__ void give_up(const RmsArgs &a, int64_t row) {
 // side; several CTAs share an SM, and those that run take the rows of those that were not launched yet
 // (dyt_steal.cuh): an SM gets as many rows as it has time for. With MODE kCluster the row's warps are in several CTAs
 // (dyt_cluster.cuh), and a cluster has a fixed share of the rows.
-// Measured with a residual, bf16: 16384 x 4096 80.7 us (6.65 TB/s), 65536 x 1024 80.3 (6.7), 4096 x 20480 by clusters
-// of 2 118 (5.7); without one, 100003 x 255 binary32 32.6 (6.3). 8-bit, with a residual and a scale for 128 columns:
-// 8192 x 8192 73 (6.4); 4096 x 20480, clusters of 2, 103, with a scale a row, whose largest value is a second exchange,
-// 106. Bound by memory; ragged 16-bit rows by instructions, as each element is a load from shared memory and a store of
-// its own: 100003 x 255 bf16 43.4 (4.7), 8191 x 1001 fp16 to 8 bits 10.4 (2.4).
+// Measured with a residual, bf16: 16384 x 4096 80.5 us (6.65 TB/s), 65536 x 1024 80.2 (6.7), 4096 x 20480 by clusters
+// of 2 117 (5.7); without one, 100003 x 255 binary32 32.4 (6.3). 8-bit, with a residual: 8192 x 8192, a scale for 128
+// columns, 72 (6.5); 4096 x 20480 103 with a scale for 128 columns, and 103 with one a row (with its largest value in
+// the sum's exchange, from gamma h, 92). Bound by memory; ragged 16-bit rows by instructions, as each element is a load
+// from shared memory and a store of its own: 100003 x 255 bf16 44.7 (4.6), 8191 x 1001 fp16 to 8 bits 10.0 (2.5).
 template <typename T, int E, int MODE, bool RAGGED, bool RES, bool Q>
 __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constant__ RmsArgs a) {
   constexpr bool CLUSTER = in_cluster(MODE), GROUP = in_warps(MODE);
@@ -305,15 +305,14 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
   const float inv_n = w.inv_n;
   const int warps = GROUP ? p.L / 32 : 1, wl = (int)threadIdx.x & 31;
   bool lost = false;
-  // CLUSTER: what each of the row's warps has, two for a lane of every warp; NaN once something did not come.
-  int met = 0;
-  auto meet = [&](float v) {
+  // CLUSTER: what each of the row's warps has, two for a lane of every warp; NaN once something did not come. step: 0,
+  // 1, 2, ...
+  auto meet = [&](int step, float v) {
     const float nan = __int_as_float(0x7FC00000);
     if constexpr (CLUSTER) {
-      red.put(met, lost ? nan : v, p.lane, p.L);
-      if (!lost) lost = !red.wait(met, p.lane, p.L);
-      const int par = met++ & 1;
-      return lost ? make_float2(nan, nan) : make_float2(red.of[par][wl], red.of[par][wl + 32]);
+      red.put(step, lost ? nan : v, p.lane, p.L);
+      if (!lost) lost = !red.wait(step, p.lane, p.L);
+      if (!lost) return make_float2(red.of[step & 1][wl], red.of[step & 1][wl + 32]);
     }
     return make_float2(nan, nan);
   };
@@ -363,7 +362,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
     q = GROUP ? warp_sum(q) : lanes_sum(q, p.L);
     const int par = it & 1;
     if constexpr (CLUSTER) {
-      const float2 o = meet(q);
+      const float2 o = meet(Q && !a.grouped ? 2 * it : it, q);
       q = warp_sum(o.x + o.y);
     } else if constexpr (GROUP) {
       if (wl == 0) red[par][0][p.lane / 32] = q;
@@ -404,7 +403,7 @@ __global__ void __launch_bounds__(kBlock, 1) rms_fwd_kernel(const __grid_constan
         for (int i = 0; i < P; ++i) top = max_nan(top, max_nan(fabsf(v[i].x), fabsf(v[i].y)));
         top = lanes_max(top, p.seg());
         if constexpr (CLUSTER) {
-          const float2 o = meet(top);
+          const float2 o = meet(2 * it + 1, top);
           top = lanes_max(max_nan(o.x, o.y), 32);
         } else if constexpr (GROUP) {
           if (wl == 0) red[par][1][p.lane / 32] = top;
@@ -445,8 +444,9 @@ __device__ __forceinline__ float cta_max(float v, float *red) {
 
 // Rows of more columns than 4 CTAs hold: one CTA reads each row twice (the second time mostly from L2), for its sum of
 // squares and for its outputs. A warp takes 32 x C consecutive columns at a time, C = 4 single elements or a vector a
-// lane, which are whole groups of kScaleCols. Measured: 512 x 131072 bf16 with a residual 162 us (3.3 TB/s of what one
-// pass would move); bound by the wait for the sum, during which the CTA writes nothing.
+// lane, which are whole groups of kScaleCols. With a scale a row there is a third reading, for the largest value.
+// Measured: 512 x 131072 bf16 with a residual 161 us (3.3 TB/s of what one pass would move), to 8 bits with a scale a
+// row 232; bound by the wait for the sum, during which the CTA writes nothing.
 template <typename T, int V, bool RES, bool Q>
 __global__ void __launch_bounds__(1024) rms_fwd_long_kernel(RmsArgs a) {
   constexpr int C = V == 1 ? 4 : V;       // a lane's columns of a step
@@ -631,7 +631,7 @@ __device__ __forceinline__ void rms_flush(const RmsGradArgs &a, double *pg, cons
 
 // RES: the stored sum has a gradient of its own, read after the row's sum.
 // A CTA's share of the rows is fixed, so that the column sums are added in the same order every time. Measured: 32768
-// x 8192 bf16 with a residual 318 us (6.75 TB/s), 16384 x 4096 84 (6.4), 100003 x 255 binary32 53 (5.75), 4096 x 16384
+// x 8192 bf16 with a residual 322 us (6.7 TB/s), 16384 x 4096 84 (6.4), 100003 x 255 binary32 53 (5.75), 4096 x 16384
 // bf16 by clusters of 2 88 (6.1), 4096 x 20480 by clusters of 8 120 (5.6). Bound by memory, in clusters by a step's
 // latency, and in short calls by the second kernel (2 to 4 us). Stages of the ring: binary32 2 (3: 100003 x 255 59 us
 // instead of 57, 16384 x 2048 68 instead of 66), 16 bits 3 (4 and 5: 1% more).
