@@ -31,7 +31,8 @@ def rms_norm_forward(x: torch.Tensor, gamma: torch.Tensor | None = None, residua
     is x), the rows' factors in float32 (one kernel launch). x, residual, out and
     residual_out may be row-strided views (dense rows, evenly spaced): no copy is made.
     gamma may have its own dtype, or be left out. residual_out may be residual or x,
-    and so may out, but not the same tensor as residual_out."""
+    and so may out, but not the same tensor as residual_out. (Without a residual, out = x
+    leaves no h: what is returned as h then holds y.)"""
     index = x.get_device()
     if _elsewhere(index, stream):
         with _there(x, stream):
@@ -73,8 +74,8 @@ def rms_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, residu
     """(q, scale, h): the norm as float8_e4m3fn values q that stand for q * scale, and
     the new residual stream h as in rms_norm_forward (one kernel launch). group 0: a
     float32 scale per row ([...]); group 128: one for each 128 columns ([...,
-    ceil(N / 128)]). The largest value of a scale's columns becomes 448. out may be a
-    row-strided view. No gradient: this is the input of an 8-bit product."""
+    ceil(N / 128)]). The largest value of a scale's columns becomes 448; q is the
+    quotient of rms_norm_forward's y, not yet rounded, by its scale. out may be a row-strided view. No gradient: this is the input of an 8-bit product."""
     index = x.get_device()
     if _elsewhere(index, stream):
         with _there(x, stream):
