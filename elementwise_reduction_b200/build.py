@@ -18,12 +18,11 @@ LIB = os.path.join(PKG, "libdyt.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("dyt_api.cu", "dyt_inst_f32.cu", "dyt_inst_bf16.cu", "dyt_inst_f16.cu",
                                               "dyt_norm.cu", "dyt_loss.cu", "dyt_rms.cu", "dyt_rms_f32.cu",
                                               "dyt_rms_bf16.cu", "dyt_rms_f16.cu", "dyt_logp.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("dyt_kernels.cuh", "dyt_math.cuh", "dyt_async.cuh", "dyt_finalize.cuh",
-                                                  "dyt_select.cuh", "dyt_select_impl.cuh", "dyt_host.h", "dyt_optin.h",
-                                                  "dyt_capacity.h", "dyt_norm.cuh", "dyt_loss.cuh", "dyt_rows.h", "dyt_steal.cuh",
-                                                  "dyt_cluster.cuh", "dyt_rms.cuh", "dyt_rms_select.cuh",
-                                                  "dyt_rms_select_impl.cuh", "dyt_loss_plan.h", "dyt_logp.cuh")] + [
-    os.path.join(INCLUDE, "dyt.h")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
+    "dyt_kernels.cuh", "dyt_math.cuh", "dyt_async.cuh", "dyt_finalize.cuh", "dyt_select.cuh", "dyt_select_impl.cuh",
+    "dyt_host.h", "dyt_optin.h", "dyt_capacity.h", "dyt_norm.cuh", "dyt_loss.cuh", "dyt_rows.h", "dyt_steal.cuh",
+    "dyt_cluster.cuh", "dyt_rms.cuh", "dyt_rms_select.cuh", "dyt_rms_select_impl.cuh", "dyt_loss_plan.h",
+    "dyt_logp.cuh")] + [os.path.join(INCLUDE, "dyt.h")]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -79,8 +79,8 @@ struct Meet {
         "r"(bar_at(par)), "r"(cta), "f"(v)
         : "memory");
   }
-  // All of step `it` is in of[it & 1]; false: not within the limit. The barrier is then left as it is: its phase has had
-  // the one arrival it counts, and one more before it ends is not defined.
+  // All of step `it` is in of[it & 1]; false: not within the limit. The barrier is then left as it is: its phase has
+  // had the one arrival it counts, and one more before it ends is not defined.
   template <int POLLS = kPolls>
   __device__ __forceinline__ bool wait(int it, int lane, int L) {
     const int par = it & 1;

@@ -75,7 +75,8 @@ def rms_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, residu
     the new residual stream h as in rms_norm_forward (one kernel launch). group 0: a
     float32 scale per row ([...]); group 128: one for each 128 columns ([...,
     ceil(N / 128)]). The largest value of a scale's columns becomes 448; q is the
-    quotient of rms_norm_forward's y, not yet rounded, by its scale. out may be a row-strided view. No gradient: this is the input of an 8-bit product."""
+    quotient of rms_norm_forward's y, before that is rounded, by its scale. out may be a
+    row-strided view. No gradient: this is the input of an 8-bit product."""
     index = x.get_device()
     if _elsewhere(index, stream):
         with _there(x, stream):
